@@ -425,6 +425,164 @@ typedef struct spec_eagle_tree_args {
 spec_status spec_eagle_tree(const spec_eagle_tree_args* args, int32_t* dev_status, void* stream);
 
 /* ---------------------------------------------------------------------------------------
+ * 8-bit paged KV cache.  (The pages name the cache's upkeep only in passing -- jisaku glossary
+ * "Medusa", section "デプロイと運用上の考慮事項" -- and hold it in the model's type; its tables,
+ * its 8-bit form and the attention over it are this library's own.)
+ *
+ * Pools: k_cache / v_cache hold e4m3 codes (1 sign, 4 exponent, 3 fraction bits, bias 7, no
+ * infinities, 0x7f / 0xff NaN), [num_blocks][Hkv][block_size][d], with one float32 scale for each
+ * block and KV head, k_scale / v_scale [num_blocks][Hkv]: element = code * scale.  Block tables,
+ * block sizes and logical slots are those of the paged bf16 cache (spec_attn_args).  A scale is a
+ * positive finite number within [2^-64, 2^120] (attention reads one outside as the nearer end, one
+ * that is no number as the lower).
+ *
+ * The cache holds a request's prefix only.  A draft tree's K/V rows stay in the model's type in a
+ * buffer of their own, k_tree / v_tree [B][N][Hkv][d], until the round has decided which of them
+ * stay: spec_tree_attention_kv8 reads both, and spec_kv8_append then writes the accepted path's
+ * rows (so that a row that is thrown away never moves a block's scale, and no code is rounded
+ * twice on its way to its slot).  One round, captured or not:
+ *   spec_kv_reserve (room for the tree), spec_tree_attention_kv8 in every layer,
+ *   spec_verify_accept, spec_kv8_append in every layer, spec_kv_reserve (give back the rest).
+ * ------------------------------------------------------------------------------------- */
+
+/* Block tables from request lengths.  Request b holds seq_len[b] slots and is about to write
+ * n_new[b] more (a prompt's rows, a tree's nodes, 0 to shrink): afterwards its table names
+ *   want[b] = ceil((seq_len[b] + n_new[b]) / block_size)
+ * blocks.  free_list is a stack of free block ids, its top at free_list[free_count - 1].  First
+ * every request with n_blocks[b] > want[b] gives back its entries [want[b], n_blocks[b]) (they
+ * become -1): the r-th given back, in order of b, then of the entry, of R in all, goes to
+ * free_list[free_count + R - 1 - r].  Then requests with n_blocks[b] < want[b] take blocks from
+ * the top, in the same order.  So a call that shrinks undoes one that grew, to the bit.  A
+ * request gets all it wants or nothing: it is served while the sum of what the requests up to and
+ * including it want does not exceed the stack.
+ *   slot_map[row_start[b] + j] = block * block_size + offset of slot seq_len[b] + j, j < n_new[b]:
+ *   the pool row a new K/V row is written to; -1 for a request not served and behind the last row.
+ *   row_start[b] = sum of n_new before b (row_start[B] = all rows).
+ * A request with a negative length or count, want[b] > max_blocks, n_blocks[b] outside
+ * [0, max_blocks], too few free blocks, or a block id outside [0, num_blocks) on its way into the
+ * slot map sets SPEC_ERR_CAPACITY; but for the last its table and count stay as they were.  A
+ * free_count outside [0, num_blocks], more blocks given back than the list has room for, or more
+ * than slot_cap rows (slot_map given; else more than 2^31 - 1) set SPEC_ERR_CAPACITY and leave
+ * tables, counts and list as they were; slots are then -1 and row_start 0.  A block belongs to one
+ * table at a time.
+ * Host errors: SPEC_ERR_INVALID_ARGUMENT (sizes < 1, NULL pointers but slot_map / row_start, a
+ * slot_map without row_start, slot_cap < 0), SPEC_ERR_UNSUPPORTED (block_size not 16, 32, 64, 128
+ * or 256, B > SPEC_MAX_RESERVE_BATCH, slot_cap >= 2^31, B * max_blocks >= 2^31). */
+#define SPEC_MAX_RESERVE_BATCH 8192
+
+typedef struct spec_kv_reserve_args {
+  int32_t batch;            /* B, 1..SPEC_MAX_RESERVE_BATCH */
+  int32_t block_size;       /* 16, 32, 64, 128 or 256 */
+  int32_t max_blocks;       /* table entries per request */
+  int32_t num_blocks;       /* blocks of the pool = entries of free_list */
+  int64_t slot_cap;         /* entries of slot_map */
+  const int32_t* seq_len;   /* [B] */
+  const int32_t* n_new;     /* [B] */
+  int32_t* block_table;     /* [B][max_blocks], updated in place */
+  int32_t* n_blocks;        /* [B] blocks held, updated in place */
+  int32_t* free_list;       /* [num_blocks], updated in place */
+  int32_t* free_count;      /* [1], updated in place */
+  int64_t* slot_map;        /* out [slot_cap] or NULL */
+  int32_t* row_start;       /* out [B + 1] or NULL */
+} spec_kv_reserve_args;
+
+spec_status spec_kv_reserve(const spec_kv_reserve_args* args, int32_t* dev_status, void* stream);
+
+/* Append rows to the 8-bit cache, at slots seq_len[b], seq_len[b] + 1, ...  Two sources:
+ *   path == NULL   packed rows k_new / v_new [n_rows][Hkv][d]; request b's are row_start[b] to
+ *                  row_start[b + 1] - 1 (a prompt, or one token per request);
+ *   path != NULL   a tree's rows [B][n_max][Hkv][d]; request b's are path[b][0 .. accept_len[b]]
+ *                  (the outputs of spec_verify_accept).
+ * For every block that rows go to, per KV head, for K and V apart:
+ *   s_new = the smallest 2^e with max |x| <= 448 * 2^e over the new rows' elements, -64 <= e <= 120
+ *           (e = -64 when all are 0; infinities and NaN are left out of the maximum);
+ *   s     = max(s_old, s_new) if the block holds slots below seq_len[b], else s_new;
+ *   codes of the new rows = e4m3(x / s), rounded to nearest, ties to even, infinities and what
+ *           passes 448 to +-448, NaN to NaN;
+ *   codes of the slots below seq_len[b], when s > s_old: e4m3(code * (s_old / s)) -- exact where
+ *           s_old is a power of two and the result is no subnormal code.
+ * Other slots of the block keep what they hold.  new_len[b] = seq_len[b] + rows appended.
+ * Data errors: seq_len[b] < 0 or rows past max_blocks * block_size, row_start that decreases or
+ * leaves [0, n_rows], accept_len[b] outside [0, path_cap) (SPEC_ERR_CAPACITY); path[b] that does not
+ * start at 0 or is not increasing below n_max (SPEC_ERR_BAD_TREE); a table entry outside
+ * [0, num_blocks) among the blocks written (SPEC_ERR_CAPACITY).  new_len[b] is then seq_len[b] and
+ * nothing of the request is written, but for the other blocks of a prompt whose table has a bad
+ * entry.  Requests must not share the blocks they write.
+ * Host errors: SPEC_ERR_INVALID_ARGUMENT, SPEC_ERR_UNSUPPORTED (dtype, head_dim, block_size,
+ * num_blocks * Hkv >= 2^31, too many rows for one grid: about 2^31 * block_size / Hkv). */
+typedef struct spec_kv8_append_args {
+  int32_t dtype;            /* of k_new / v_new: SPEC_DTYPE_BF16 or SPEC_DTYPE_F32 */
+  int32_t batch;            /* B */
+  int32_t num_kv_heads;     /* Hkv */
+  int32_t head_dim;         /* 64 or 128 */
+  int32_t block_size;       /* 16, 32, 64, 128 or 256 */
+  int32_t max_blocks;       /* table entries per request */
+  int32_t num_blocks;       /* blocks per pool */
+  int32_t n_max;            /* path: N, tree nodes per request (1..SPEC_MAX_NODES); else 0 */
+  int32_t path_cap;         /* path: entries per request; else 0 */
+  int32_t reserved0;        /* must be 0 */
+  int64_t n_rows;           /* packed rows: rows of k_new / v_new; else 0 */
+  const void* k_new;
+  const void* v_new;
+  const int32_t* row_start; /* [B + 1], packed rows */
+  const int32_t* path;      /* [B][path_cap] or NULL */
+  const int32_t* accept_len; /* [B], with path */
+  const int32_t* seq_len;   /* [B] */
+  const int32_t* block_table; /* [B][max_blocks] */
+  uint8_t* k_cache;         /* pools, updated in place */
+  uint8_t* v_cache;
+  float* k_scale;           /* [num_blocks][Hkv], updated in place */
+  float* v_scale;
+  int32_t* new_len;         /* out [B] or NULL; not seq_len itself (SPEC_ERR_INVALID_ARGUMENT) */
+} spec_kv8_append_args;
+
+spec_status spec_kv8_append(const spec_kv8_append_args* args, int32_t* dev_status, void* stream);
+
+/* Tree attention over the 8-bit cache: as spec_tree_attention, with the prefix [0, prefix_len[b])
+ * in the pools and node i's own K/V in row i of k_tree / v_tree.  n_max = 1 is decoding of single
+ * tokens.  Products and sums are those of the codes' exact values: q enters as an exact pair of
+ * 8-bit numbers or in 16 bits, the softmax weights as bf16 or better, sums in float32.
+ *   - K/V rows of nodes that a row does not see, of padded nodes and of slots behind the prefix have
+ *     no influence on it, NaN and infinities included.
+ *   - Data errors as for spec_tree_attention: SPEC_ERR_BAD_TREE; SPEC_ERR_CAPACITY for prefix_len
+ *     outside [0, max_blocks * block_size] or a bad table entry among the prefix's blocks.  The
+ *     request's out and lse are then 0, as for padded nodes.
+ * Host errors: SPEC_ERR_INVALID_ARGUMENT, SPEC_ERR_UNSUPPORTED (dtype other than bf16, head_dim,
+ * block_size, n_max > SPEC_MAX_NODES, B * Hkv > 65535, num_blocks * Hkv >= 2^31, max_blocks *
+ * block_size >= 2^31), SPEC_ERR_WORKSPACE_TOO_SMALL. */
+typedef struct spec_attn_kv8_args {
+  int32_t dtype;            /* of q, k_tree, v_tree and out: SPEC_DTYPE_BF16 */
+  int32_t batch;            /* B */
+  int32_t n_max;            /* N, 1..SPEC_MAX_NODES */
+  int32_t num_q_heads;      /* Hq, a multiple of num_kv_heads */
+  int32_t num_kv_heads;     /* Hkv */
+  int32_t head_dim;         /* 64 or 128 */
+  int32_t block_size;       /* 16, 32, 64, 128 or 256 */
+  int32_t max_blocks;       /* table entries per request */
+  int32_t num_blocks;       /* blocks per pool */
+  float scale;              /* softmax scale; <= 0 selects 1/sqrt(head_dim) */
+  const void* q;            /* [B][N][Hq][d] */
+  const void* k_tree;       /* [B][N][Hkv][d] */
+  const void* v_tree;       /* [B][N][Hkv][d] */
+  const uint8_t* k_cache;   /* pools */
+  const uint8_t* v_cache;
+  const float* k_scale;     /* [num_blocks][Hkv] */
+  const float* v_scale;
+  const int32_t* prefix_len; /* [B] */
+  const int32_t* n_nodes;   /* [B] */
+  const int32_t* parent;    /* [B][N] */
+  const int32_t* block_table; /* [B][max_blocks] */
+  void* out;                /* [B][N][Hq][d] */
+  float* lse;               /* [B][N][Hq] natural-log LSE, or NULL */
+} spec_attn_kv8_args;
+
+/* Bytes of workspace (16-byte aligned device memory) for these shapes; 0 on invalid arguments. */
+size_t spec_tree_attention_kv8_workspace(const spec_attn_kv8_args* args);
+
+spec_status spec_tree_attention_kv8(const spec_attn_kv8_args* args, void* workspace, size_t workspace_bytes,
+                                    int32_t* dev_status, void* stream);
+
+/* ---------------------------------------------------------------------------------------
  * One verification round as a single CUDA-graph launch.  (Deployment convenience: the pages
  * describe the round's steps -- parallel tree verification, acceptance, keeping the accepted
  * prefix -- not how they are launched.  At batch 1 the round is a handful of short kernels

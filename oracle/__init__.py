@@ -34,3 +34,4 @@ from .compact import compact_kv  # noqa: F401
 from .medusa import head_topk, cartesian_tuples, pruned_topology, medusa_expand  # noqa: F401
 from .paged import gather_paged, scatter_paged  # noqa: F401
 from .eagle import expand_layer, select_tree  # noqa: F401
+from .kv8 import E4M3, e4m3_encode, block_scale, append_rows, gather_kv8, reserve  # noqa: F401

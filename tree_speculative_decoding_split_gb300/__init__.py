@@ -13,6 +13,9 @@ runs in the library's CUDA kernels; if the library has not been built, every cal
     medusa_topology(...)  -> (parent, rank)       pruned Cartesian topology (host arrays)
     eagle_expand(...)     -> dict of outputs      one layer of a dynamic (EAGLE-2 style) draft tree
     eagle_tree(...)       -> dict of outputs      the tree from all layers' candidates
+    kv_reserve(...)       -> (slot_map, row_start) block tables grown or shrunk from request lengths
+    kv8_append(...)       -> new_len              rows into the 8-bit paged cache
+    tree_attention_kv8(...) -> (out, lse)         tree attention over the 8-bit paged cache
     Round(...)                                    the three verification calls as one graph launch
                                                   (also from host buffers: Round.launch_host)
 """
@@ -95,6 +98,31 @@ class EagleTreeArgs(ctypes.Structure):
                 ("tree_parent", _vp), ("tree_token", _vp), ("n_nodes", _vp), ("node_cand", _vp)]
 
 
+class KvReserveArgs(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("block_size", ctypes.c_int32), ("max_blocks", ctypes.c_int32),
+                ("num_blocks", ctypes.c_int32), ("slot_cap", ctypes.c_int64), ("seq_len", _vp), ("n_new", _vp),
+                ("block_table", _vp), ("n_blocks", _vp), ("free_list", _vp), ("free_count", _vp), ("slot_map", _vp),
+                ("row_start", _vp)]
+
+
+class Kv8AppendArgs(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("batch", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("block_size", ctypes.c_int32), ("max_blocks", ctypes.c_int32),
+                ("num_blocks", ctypes.c_int32), ("n_max", ctypes.c_int32), ("path_cap", ctypes.c_int32),
+                ("reserved0", ctypes.c_int32), ("n_rows", ctypes.c_int64), ("k_new", _vp), ("v_new", _vp),
+                ("row_start", _vp), ("path", _vp), ("accept_len", _vp), ("seq_len", _vp), ("block_table", _vp),
+                ("k_cache", _vp), ("v_cache", _vp), ("k_scale", _vp), ("v_scale", _vp), ("new_len", _vp)]
+
+
+class AttnKv8Args(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("batch", ctypes.c_int32), ("n_max", ctypes.c_int32),
+                ("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("block_size", ctypes.c_int32), ("max_blocks", ctypes.c_int32), ("num_blocks", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("q", _vp), ("k_tree", _vp), ("v_tree", _vp), ("k_cache", _vp),
+                ("v_cache", _vp), ("k_scale", _vp), ("v_scale", _vp), ("prefix_len", _vp), ("n_nodes", _vp),
+                ("parent", _vp), ("block_table", _vp), ("out", _vp), ("lse", _vp)]
+
+
 _lib_handle = None
 
 
@@ -145,6 +173,14 @@ def lib():
         L.spec_eagle_expand.restype = ctypes.c_int32
         L.spec_eagle_tree.argtypes = [ctypes.POINTER(EagleTreeArgs), _vp, _vp]
         L.spec_eagle_tree.restype = ctypes.c_int32
+        L.spec_kv_reserve.argtypes = [ctypes.POINTER(KvReserveArgs), _vp, _vp]
+        L.spec_kv_reserve.restype = ctypes.c_int32
+        L.spec_kv8_append.argtypes = [ctypes.POINTER(Kv8AppendArgs), _vp, _vp]
+        L.spec_kv8_append.restype = ctypes.c_int32
+        L.spec_tree_attention_kv8_workspace.argtypes = [ctypes.POINTER(AttnKv8Args)]
+        L.spec_tree_attention_kv8_workspace.restype = ctypes.c_size_t
+        L.spec_tree_attention_kv8.argtypes = [ctypes.POINTER(AttnKv8Args), _vp, ctypes.c_size_t, _vp, _vp]
+        L.spec_tree_attention_kv8.restype = ctypes.c_int32
         _lib_handle = L
     return _lib_handle
 
@@ -668,3 +704,190 @@ def eagle_tree(score, token, parent, n_max, draft_to_target=None, root_token=Non
     st = _status_buffer(dev_status, dev)
     _check(lib().spec_eagle_tree(ctypes.byref(a), _ptr(st), _stream(stream)), "spec_eagle_tree")
     return out
+
+
+# ---- the 8-bit paged cache ---------------------------------------------------------------------
+
+def _kept_for(stream, *tensors):
+    """Tensors made here for a call on ``stream``: the allocator must not hand their memory out again
+    before that stream is done with it."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def kv_reserve_args(seq_len, n_new, block_table, n_blocks, free_list, free_count, block_size, slot_cap=None,
+                    slot_map=None, row_start=None):
+    """Build the C argument struct for kv_reserve (tensors are validated here); returns (args, slot_map,
+    row_start)."""
+    torch = _torch()
+    _need(block_table, "block_table", torch.int32)
+    dev = block_table.device
+    for name, t in (("seq_len", seq_len), ("n_new", n_new), ("n_blocks", n_blocks), ("free_list", free_list),
+                    ("free_count", free_count)):
+        _need(t, name, torch.int32, dev)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B][max_blocks]")
+    B, max_blocks = block_table.shape
+    if seq_len.numel() != B or n_new.numel() != B or n_blocks.numel() != B or free_count.numel() != 1:
+        raise ValueError("seq_len, n_new and n_blocks must be [B], free_count [1]")
+    if slot_map is None and slot_cap is not None:
+        slot_map = torch.empty(int(slot_cap), dtype=torch.int64, device=dev)
+    if slot_map is not None:
+        _need(slot_map, "slot_map", torch.int64, dev)
+    if row_start is None:
+        row_start = torch.empty(B + 1, dtype=torch.int32, device=dev)
+    _need(row_start, "row_start", torch.int32, dev)
+    if row_start.numel() != B + 1:
+        raise ValueError("row_start must be [B + 1]")
+    slots = slot_map if slot_map is not None and slot_map.numel() > 0 else None
+    a = KvReserveArgs(batch=B, block_size=int(block_size), max_blocks=max_blocks, num_blocks=free_list.numel(),
+                      slot_cap=0 if slots is None else slots.numel(), seq_len=_ptr(seq_len), n_new=_ptr(n_new),
+                      block_table=_ptr(block_table), n_blocks=_ptr(n_blocks), free_list=_ptr(free_list),
+                      free_count=_ptr(free_count), slot_map=_ptr(slots), row_start=_ptr(row_start))
+    return a, slot_map, row_start
+
+
+def kv_reserve(seq_len, n_new, block_table, n_blocks, free_list, free_count, block_size, slot_cap=None, slot_map=None,
+               row_start=None, dev_status=None, stream=None):
+    """Grow or shrink every request's block table to hold ``seq_len + n_new`` slots, from the stack of
+    free blocks, in place (see spec_kv_reserve).  ``slot_cap`` (a bound on the sum of n_new the host
+    knows) or ``slot_map`` asks for the pool row of every new row.  Returns (slot_map, row_start);
+    slot_map is None when neither is given."""
+    torch = _torch()
+    a, slot_map, row_start = kv_reserve_args(seq_len, n_new, block_table, n_blocks, free_list, free_count, block_size,
+                                             slot_cap, slot_map, row_start)
+    with torch.cuda.device(block_table.device):
+        st = _status_buffer(dev_status, block_table.device)
+        _check(lib().spec_kv_reserve(ctypes.byref(a), _ptr(st), _stream(stream)), "spec_kv_reserve")
+        _kept_for(stream, st, slot_map, row_start)
+    return slot_map, row_start
+
+
+def _kv8_pools(k_cache, v_cache, k_scale, v_scale, block_table, B, dev):
+    torch = _torch()
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _need(t, name, torch.float8_e4m3fn, dev)
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise ValueError("pools must be [num_blocks][Hkv][block_size][d]")
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        _need(t, name, torch.float32, dev)
+        if tuple(t.shape) != tuple(k_cache.shape[:2]):
+            raise ValueError(f"{name} must be [num_blocks][Hkv]")
+    return _paged(k_cache, block_table, B, dev)
+
+
+def kv8_append_args(k_new, v_new, k_cache, v_cache, k_scale, v_scale, seq_len, block_table, row_start=None, path=None,
+                    accept_len=None, new_len=None):
+    """Build the C argument struct for kv8_append (tensors are validated here); returns (args, new_len)."""
+    torch = _torch()
+    _need(k_new, "k_new")
+    dev = k_new.device
+    _need(v_new, "v_new", k_new.dtype, dev)
+    _need(seq_len, "seq_len", torch.int32, dev)
+    B = seq_len.numel()
+    bs, max_blocks, nb, Hkv = _kv8_pools(k_cache, v_cache, k_scale, v_scale, block_table, B, dev)
+    d = k_cache.shape[3]
+    if v_new.shape != k_new.shape or tuple(k_new.shape[-2:]) != (Hkv, d):
+        raise ValueError("k_new and v_new must be [...][Hkv][d]")
+    n_max = path_cap = n_rows = 0
+    if path is not None:
+        _need(path, "path", torch.int32, dev)
+        _need(accept_len, "accept_len", torch.int32, dev)
+        if row_start is not None or k_new.dim() != 4 or k_new.shape[0] != B or path.dim() != 2 or \
+                path.shape[0] != B or accept_len.numel() != B:
+            raise ValueError("path [B][path_cap] and accept_len [B] go with rows [B][N][Hkv][d] and no row_start")
+        n_max, path_cap = k_new.shape[1], path.shape[1]
+    else:
+        if row_start is None or accept_len is not None or k_new.dim() != 3:
+            raise ValueError("packed rows [n_rows][Hkv][d] go with row_start [B + 1]")
+        _need(row_start, "row_start", torch.int32, dev)
+        if row_start.numel() != B + 1:
+            raise ValueError("row_start must be [B + 1]")
+        n_rows = k_new.shape[0]
+    if new_len is None:
+        new_len = torch.empty(B, dtype=torch.int32, device=dev)
+    _need(new_len, "new_len", torch.int32, dev)
+    if new_len.numel() != B:
+        raise ValueError("new_len must be [B]")
+    a = Kv8AppendArgs(dtype=_dtype_code(k_new), batch=B, num_kv_heads=Hkv, head_dim=d, block_size=bs,
+                      max_blocks=max_blocks, num_blocks=nb, n_max=n_max, path_cap=path_cap, reserved0=0, n_rows=n_rows,
+                      k_new=_ptr(k_new), v_new=_ptr(v_new), row_start=_ptr(row_start), path=_ptr(path),
+                      accept_len=_ptr(accept_len), seq_len=_ptr(seq_len), block_table=_ptr(block_table),
+                      k_cache=_ptr(k_cache), v_cache=_ptr(v_cache), k_scale=_ptr(k_scale), v_scale=_ptr(v_scale),
+                      new_len=_ptr(new_len))
+    return a, new_len
+
+
+def kv8_append(k_new, v_new, k_cache, v_cache, k_scale, v_scale, seq_len, block_table, row_start=None, path=None,
+               accept_len=None, new_len=None, dev_status=None, stream=None):
+    """Append K/V rows to the 8-bit paged cache in place (see spec_kv8_append): packed rows with
+    ``row_start`` [B + 1], or a tree's rows [B][N][Hkv][d] along ``path`` / ``accept_len`` (the outputs of
+    verify_accept).  Pools are float8_e4m3fn [num_blocks][Hkv][block_size][d], scales float32
+    [num_blocks][Hkv].  Returns new_len."""
+    torch = _torch()
+    a, new_len = kv8_append_args(k_new, v_new, k_cache, v_cache, k_scale, v_scale, seq_len, block_table, row_start,
+                                 path, accept_len, new_len)
+    if k_new.numel() == 0 and path is None:  # no rows at all: no pointer to pass
+        return new_len.copy_(seq_len)
+    with torch.cuda.device(k_new.device):
+        st = _status_buffer(dev_status, k_new.device)
+        _check(lib().spec_kv8_append(ctypes.byref(a), _ptr(st), _stream(stream)), "spec_kv8_append")
+        _kept_for(stream, st, new_len)
+    return new_len
+
+
+def attn_kv8_args(q, k_tree, v_tree, k_cache, v_cache, k_scale, v_scale, prefix_len, n_nodes, parent, block_table,
+                  out=None, lse=None, scale=0.0):
+    """Build the C argument struct for tree_attention_kv8 (tensors are validated here); returns (args, out,
+    lse)."""
+    torch = _torch()
+    _need(q, "q")
+    dev = q.device
+    for name, t in (("k_tree", k_tree), ("v_tree", v_tree)):
+        _need(t, name, q.dtype, dev)
+    for name, t in (("prefix_len", prefix_len), ("n_nodes", n_nodes), ("parent", parent)):
+        _need(t, name, torch.int32, dev)
+    if q.dim() != 4:
+        raise ValueError("q must be [B][N][Hq][d]")
+    B, N, Hq, d = q.shape
+    bs, max_blocks, nb, Hkv = _kv8_pools(k_cache, v_cache, k_scale, v_scale, block_table, B, dev)
+    if k_cache.shape[3] != d or tuple(k_tree.shape) != (B, N, Hkv, d) or v_tree.shape != k_tree.shape:
+        raise ValueError("k_tree and v_tree must be [B][N][Hkv][d], with the pools' d")
+    if tuple(parent.shape) != (B, N) or prefix_len.numel() != B or n_nodes.numel() != B:
+        raise ValueError("parent must be [B][N], prefix_len and n_nodes [B]")
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None:
+        lse = torch.empty((B, N, Hq), dtype=torch.float32, device=dev)
+    _need(out, "out", q.dtype, dev)
+    _need(lse, "lse", torch.float32, dev)
+    if out.shape != q.shape or tuple(lse.shape) != (B, N, Hq):
+        raise ValueError("out must be [B][N][Hq][d] and lse [B][N][Hq]")
+    a = AttnKv8Args(dtype=_dtype_code(q), batch=B, n_max=N, num_q_heads=Hq, num_kv_heads=Hkv, head_dim=d, block_size=bs,
+                    max_blocks=max_blocks, num_blocks=nb, scale=float(scale), q=_ptr(q), k_tree=_ptr(k_tree),
+                    v_tree=_ptr(v_tree), k_cache=_ptr(k_cache), v_cache=_ptr(v_cache), k_scale=_ptr(k_scale),
+                    v_scale=_ptr(v_scale), prefix_len=_ptr(prefix_len), n_nodes=_ptr(n_nodes), parent=_ptr(parent),
+                    block_table=_ptr(block_table), out=_ptr(out), lse=_ptr(lse))
+    return a, out, lse
+
+
+def tree_attention_kv8(q, k_tree, v_tree, k_cache, v_cache, k_scale, v_scale, prefix_len, n_nodes, parent, block_table,
+                       out=None, lse=None, scale=0.0, workspace=None, dev_status=None, stream=None):
+    """Tree attention over the 8-bit paged prefix and the tree's own K/V rows (see
+    spec_tree_attention_kv8); N = 1 is decoding of single tokens.  Returns (out, lse)."""
+    torch = _torch()
+    a, out, lse = attn_kv8_args(q, k_tree, v_tree, k_cache, v_cache, k_scale, v_scale, prefix_len, n_nodes, parent,
+                                block_table, out, lse, scale)
+    L = lib()
+    with torch.cuda.device(q.device):
+        need = L.spec_tree_attention_kv8_workspace(ctypes.byref(a))
+        if need == 0:
+            _check(L.spec_tree_attention_kv8(ctypes.byref(a), None, 0, None, None), "spec_tree_attention_kv8")
+        ws = _workspace(need, q.device, workspace)
+        st = _status_buffer(dev_status, q.device)
+        _check(L.spec_tree_attention_kv8(ctypes.byref(a), _ptr(ws), need, _ptr(st), _stream(stream)),
+               "spec_tree_attention_kv8")
+        _kept_for(stream, ws, st, out, lse)
+    return out, lse

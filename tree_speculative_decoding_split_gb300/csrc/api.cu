@@ -5,69 +5,12 @@
 #include <cstring>
 
 #include "common.cuh"
+#include "host.cuh"
 #include "kernels.cuh"
 
 using namespace spectree;
 
 namespace {
-
-constexpr size_t kAlign = 256;
-
-size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
-
-// Sequential carve-out of a caller-provided workspace (or a pure size count when base is null).
-struct Carver {
-  char* base;
-  size_t off = 0;
-  explicit Carver(void* b) : base(static_cast<char*>(b)) {}
-  template <typename T>
-  T* take(size_t count) {
-    T* p = base ? reinterpret_cast<T*>(base + off) : nullptr;
-    off += align_up(count * sizeof(T));
-    return p;
-  }
-};
-
-int num_sms_current() {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 148;
-  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) return 148;
-  return sms;
-}
-
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// The driver entry point is looked up once per process (immutable after the first call).
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  if (!fn) {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(ptr);
-  }
-  return fn;
-}
-
-// bf16 tensor map with 128-byte swizzle.  dims/box are innermost first; strides (bytes) are for
-// dims 1.. (rank - 1).
-bool make_map_bf16(CUtensorMap* m, const void* ptr, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
-                   const cuuint32_t* box) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return false;
-  cuuint32_t estr[5] = {1, 1, 1, 1, 1};
-  if (rank < 1 || rank > 5) return false;
-  std::memset(m, 0, sizeof(*m));
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(ptr), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Records an optional caller-owned event (cudaEvent_t) on the stream.
 void record(void* event, cudaStream_t stream) {
@@ -75,22 +18,6 @@ void record(void* event, cudaStream_t stream) {
 }
 
 // ---- attention ------------------------------------------------------------------------------
-
-// Paged KV: block size a power of two in [16, 256], kv_capacity = max_blocks * block_size, and
-// pool coordinates that fit the tensor map.
-spec_status check_paged(int bs, int max_blocks, int num_blocks, int Hkv, long long L_cap) {
-  if (bs != 16 && bs != 32 && bs != 64 && bs != 128 && bs != 256) return SPEC_ERR_UNSUPPORTED;
-  if (max_blocks < 1 || num_blocks < 1) return SPEC_ERR_INVALID_ARGUMENT;
-  if ((long long)max_blocks * bs != L_cap) return SPEC_ERR_INVALID_ARGUMENT;
-  if ((long long)num_blocks * Hkv >= 0x7fffffffLL) return SPEC_ERR_UNSUPPORTED;
-  return SPEC_OK;
-}
-
-int log2_of(int x) {
-  int s = 0;
-  while ((1 << s) < x) ++s;
-  return s;
-}
 
 spec_status check_attn(const spec_attn_args* a) {
   if (!a) return SPEC_ERR_INVALID_ARGUMENT;

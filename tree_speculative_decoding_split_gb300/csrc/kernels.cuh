@@ -225,4 +225,75 @@ constexpr int kCompactBufChunks = 2048;  // 32 KB of staged rows (64 bf16 rows o
 void launch_compact_kv(const CompactParams& c, const int32_t* path, const int32_t* accept_len, int B,
                        cudaStream_t stream);
 
+// ---- K7: block tables and slot maps ----------------------------------------------------------
+struct ReserveParams {
+  int B, bs, bs_shift, max_blocks, num_blocks;
+  long long slot_cap;
+  const int32_t* seq_len;
+  const int32_t* n_new;
+  int32_t* table;      // [B][max_blocks]
+  int32_t* n_blocks;   // [B]
+  int32_t* free_list;  // [num_blocks], a stack
+  int32_t* free_count;
+  int64_t* slot_map;   // [slot_cap] or nullptr
+  int32_t* row_start;  // [B + 1] or nullptr
+  int32_t* dev_status;
+};
+cudaError_t launch_kv_reserve(const ReserveParams& p, int num_sms, cudaStream_t stream);
+
+// ---- K8: appending rows to the 8-bit cache ----------------------------------------------------
+struct Kv8AppendParams {
+  int B, Hkv, d, bs, bs_shift, max_blocks, num_blocks;
+  int is_bf16;
+  int N, path_cap;          // tree form
+  long long n_rows;         // packed form
+  const void* k_new;
+  const void* v_new;
+  const int32_t* row_start; // [B + 1] (packed form)
+  const int32_t* path;      // [B][path_cap] or nullptr
+  const int32_t* accept_len;
+  const int32_t* seq_len;
+  const int32_t* table;     // [B][max_blocks]
+  uint8_t* k_cache;         // [num_blocks][Hkv][bs][d]
+  uint8_t* v_cache;
+  float* k_scale;           // [num_blocks][Hkv]
+  float* v_scale;
+  int32_t* new_len;         // [B] or nullptr
+  int32_t* dev_status;
+  int units_per_req;        // tree form: blocks a request's rows can touch
+};
+cudaError_t launch_kv8_append(const Kv8AppendParams& p, cudaStream_t stream);
+// CTAs of the launch (0 when they pass the grid's limit).
+unsigned kv8_append_grid(const Kv8AppendParams& p);
+
+// ---- K9: tree attention over the 8-bit cache --------------------------------------------------
+struct Kv8AttnParams {
+  const uint16_t* q;      // [B][N][Hq][d] bf16
+  const uint16_t* k_tree; // [B][N][Hkv][d] bf16
+  const uint16_t* v_tree;
+  const float* k_scale;   // [num_blocks][Hkv]
+  const float* v_scale;
+  const int32_t* prefix_len;
+  const int32_t* n_nodes;
+  const int32_t* parent;
+  const int32_t* table;   // [B][max_blocks]
+  uint16_t* out;
+  float* lse;
+  float* part_o;          // [B*N*Hq][n_split][d] unnormalised partial rows
+  float2* part_ml;        // [B*N*Hq][n_split] (reference maximum in log2 units, sum); sum < 0 = bad request
+  int32_t* dev_status;
+  int B, N, Hq, Hkv, G, d, bs, bs_shift, max_blocks, num_blocks;
+  long long L_cap;
+  int n_split;            // key splits at most; a request uses as many as its own length fills
+  int n_rt;               // row tiles of (node, head) rows per KV head
+  float scale_log2;
+};
+struct Kv8AttnPlan {
+  int n_split, n_rt;
+};
+Kv8AttnPlan plan_attention_kv8(int B, int N, int G, int Hkv, long long L_cap, int num_sms);
+cudaError_t launch_attention_kv8_rows(const CUtensorMap* tmK, const CUtensorMap* tmV, const Kv8AttnParams& p,
+                                      cudaStream_t stream);
+cudaError_t launch_attention_kv8_merge(const Kv8AttnParams& p, cudaStream_t stream);
+
 }  // namespace spectree

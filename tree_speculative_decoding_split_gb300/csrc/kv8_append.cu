@@ -1,0 +1,285 @@
+// K8: rows into the 8-bit paged cache (spec_kv8_append).
+//
+// A block of one KV head is bs x d elements with one scale s = 2^e, e the smallest with
+// max |x| <= 448 * 2^e; a code is e4m3(x / s).  Both steps need the whole block, which fits the
+// registers of one group of threads: the group loads the block's new rows once, reduces |x| to the
+// maximum, and converts what it holds.  So the rows are read once and the codes written once: HBM-bound.
+// A half-full block keeps its larger scale; its old codes are read only when the scale grows.
+#include "common.cuh"
+#include "kernels.cuh"
+
+namespace spectree {
+
+namespace {
+
+constexpr int kVecs = 4;          // 16-byte source vectors a thread holds (8 where a block needs > 1024 threads)
+constexpr int kMinExp = -64, kMaxExp = 120;
+
+// The exponent of the smallest power of two s with amax <= 448 s (448 = 1.75 * 2^8).
+__device__ __forceinline__ int scale_exp(float amax) {
+  const uint32_t b = __float_as_uint(amax);
+  if ((b >> 23) == 0) return kMinExp;  // zero and what is below 2^-126
+  const int e = (int)(b >> 23) - 127 - 8 + ((b & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  return min(max(e, kMinExp), kMaxExp);
+}
+__device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// Two floats to two e4m3 codes (the first in the low byte), to nearest even, saturating.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t c) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)c));
+  return __half22float2(*reinterpret_cast<__half2*>(&h));
+}
+
+// One 16-byte source vector: 8 bf16 or 4 floats.
+template <bool BF16>
+struct Vec {
+  static constexpr int kElems = BF16 ? 8 : 4;
+  static __device__ __forceinline__ void unpack(const uint4& v, float (&x)[kElems]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (BF16) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      } else {
+        x[i] = __uint_as_float(w[i]);
+      }
+    }
+  }
+};
+
+// kElems codes at `dst` (8 or 4 bytes)
+template <int E>
+__device__ __forceinline__ void store_codes(uint8_t* dst, const float (&x)[E]) {
+  const uint32_t lo = e4m3x2(x[0], x[1]) | (e4m3x2(x[2], x[3]) << 16);
+  if constexpr (E == 8) {
+    const uint32_t hi = e4m3x2(x[4], x[5]) | (e4m3x2(x[6], x[7]) << 16);
+    *reinterpret_cast<uint2*>(dst) = make_uint2(lo, hi);
+  } else {
+    *reinterpret_cast<uint32_t*>(dst) = lo;
+  }
+}
+
+__device__ __forceinline__ int units_before(const int32_t* row_start, int b, int bs_shift) {
+  return (row_start[b] >> bs_shift) + 2 * b;
+}
+
+struct Request {
+  int count;  // rows to append; -1 = refused
+  int err;
+};
+
+// Checks of request b that do not need its table; every thread of the block calls it (barriers inside).
+__device__ __forceinline__ Request check_request(const Kv8AppendParams& p, int b) {
+  Request r = {0, 0};
+  const long long len = p.seq_len[b];
+  int bad = 0;
+  if (p.path) {
+    const int a = p.accept_len[b];
+    if (a < 0 || a >= p.path_cap) {
+      r.err = SPEC_ERR_CAPACITY;
+    } else {
+      r.count = a + 1;
+      const int32_t* pth = p.path + (size_t)b * p.path_cap;
+      for (int j = threadIdx.x; j <= a; j += blockDim.x) {
+        const int v = pth[j];
+        if (v >= p.N || (j == 0 ? v != 0 : v <= pth[j - 1])) bad = 1;
+      }
+    }
+  } else {
+    const int r0 = p.row_start[b], r1 = p.row_start[b + 1];
+    if (r0 < 0 || r1 < r0 || r1 > p.n_rows) r.err = SPEC_ERR_CAPACITY; else r.count = r1 - r0;
+  }
+  if (__syncthreads_or(bad)) r.err = SPEC_ERR_BAD_TREE;
+  if (!r.err && (len < 0 || len + r.count > (long long)p.max_blocks * p.bs)) r.err = SPEC_ERR_CAPACITY;
+  if (r.err) r.count = -1;
+  return r;
+}
+
+// Is a table entry of the blocks that request b's rows go to out of range?  (block-wide)
+__device__ __forceinline__ bool bad_table(const Kv8AppendParams& p, int b, long long len, int count) {
+  int bad = 0;
+  if (count > 0)
+    for (long long j = (len >> p.bs_shift) + threadIdx.x; j <= (len + count - 1) >> p.bs_shift; j += blockDim.x) {
+      const int blk = p.table[(size_t)b * p.max_blocks + j];
+      if (blk < 0 || blk >= p.num_blocks) bad = 1;
+    }
+  return __syncthreads_or(bad);
+}
+
+}  // namespace
+
+// Grid: units x parts.  A unit is one block that rows of a request go to; a part is a run of the unit's
+// 2 * Hkv (K or V, head) blocks of codes, `groups` of TG = blockDim / groups threads each taking one.
+template <bool BF16, int NV>
+__global__ void __launch_bounds__(1024) kv8_append_kernel(const Kv8AppendParams p, int parts, int tg_shift) {
+  constexpr int E = Vec<BF16>::kElems;
+  __shared__ float s_max[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int u = blockIdx.x / parts, part = blockIdx.x - u * parts;
+  // ---- the unit's request and block ----
+  int b, k;  // request, its k-th touched block
+  if (p.path) {
+    b = u / p.units_per_req;
+    k = u - b * p.units_per_req;
+  } else {
+    // units are laid out from floor(row_start / bs) + 2 b, which leaves each request at least as many as
+    // its rows can touch at any offset; 32-way search, one probe per lane
+    int lo = 0, n = p.B;
+    while (n > 1) {
+      const int step = (n + 31) >> 5;
+      const int at = min(lo + lane * step, lo + n - 1);
+      const bool le = lane * step < n && units_before(p.row_start, at, p.bs_shift) <= u;
+      const unsigned m = __ballot_sync(0xffffffffu, le);
+      const int hit = m ? 31 - __clz(m) : 0;
+      const int rest = n - hit * step;
+      lo += hit * step;
+      n = min(step, rest);
+    }
+    b = lo;
+    k = u - units_before(p.row_start, b, p.bs_shift);
+    if (k < 0) return;  // (a row_start that decreases)
+  }
+  const Request rq = check_request(p, b);
+  const int len = p.seq_len[b];
+  const bool lead = k == 0 && part == 0;  // this CTA answers for the request
+  bool bad = false;
+  if (rq.count > 0 && (p.path || lead)) bad = bad_table(p, b, len, rq.count);
+  if (lead && tid == 0) {
+    if (rq.err || bad) set_status(p.dev_status, rq.err ? rq.err : SPEC_ERR_CAPACITY);
+    if (p.new_len) p.new_len[b] = len + (rq.err || bad ? 0 : rq.count);
+  }
+  if (rq.count <= 0 || (p.path && bad)) return;
+  const long long first = ((long long)(len >> p.bs_shift) + k) << p.bs_shift;  // first slot of the block
+  if (first >= (long long)len + rq.count) return;
+  const int held = max(0, (int)(len - first));                       // slots that hold older rows
+  const int end = (int)min((long long)p.bs, len + rq.count - first);  // new rows go to [held, end)
+  const int blk = p.table[(size_t)b * p.max_blocks + (first >> p.bs_shift)];
+  if (blk < 0 || blk >= p.num_blocks) return;  // (the lead CTA has set the status)
+
+  // ---- this group's K or V block of one head ----
+  const int tg = 1 << tg_shift, groups = blockDim.x >> tg_shift;
+  const int item = part * groups + (tid >> tg_shift), t = tid & (tg - 1);
+  const bool live = item < 2 * p.Hkv;
+  const int h = item >> 1;
+  const bool isv = item & 1;
+  const uint8_t* src = static_cast<const uint8_t*>(isv ? p.v_new : p.k_new);
+  const size_t cell = (size_t)blk * p.Hkv + h;
+  uint8_t* codes = (isv ? p.v_cache : p.k_cache) + cell * ((size_t)p.bs * p.d);
+  float* scale = (isv ? p.v_scale : p.k_scale) + cell;
+  const int per_row = p.d / E;        // vectors per row: a power of two
+  const int row_shift = 31 - __clz(per_row);
+  const int row_bytes = p.d * (BF16 ? 2 : 4);
+  uint4 v[NV];
+  float amax = 0.f;
+  const float s_old = live && held ? *scale : 0.f;
+  if (live) {
+    const long long row0 = p.path ? (long long)b * p.N : (long long)p.row_start[b] + (first - len);
+    const int32_t* pth = p.path ? p.path + (size_t)b * p.path_cap + (first - len) : nullptr;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = t + j * tg, r = c >> row_shift, col = c & (per_row - 1);
+      v[j] = make_uint4(0, 0, 0, 0);
+      if (r >= held && r < end) {
+        const long long row = p.path ? row0 + pth[r] : row0 + r;
+        v[j] = __ldcs(reinterpret_cast<const uint4*>(src + ((size_t)row * p.Hkv + h) * row_bytes + col * 16));
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float x[E];
+      Vec<BF16>::unpack(v[j], x);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float a = fabsf(x[e]);
+        amax = fmaxf(amax, a < INFINITY ? a : 0.f);  // NaN and infinities are left out
+      }
+    }
+  }
+  amax = warp_max(amax);
+  if (tg > 32) {
+    if (lane == 0) s_max[warp] = amax;
+    __syncthreads();
+    const int w0 = (tid >> tg_shift) << (tg_shift - 5);
+    amax = 0.f;
+    for (int w = 0; w < (tg >> 5); ++w) amax = fmaxf(amax, s_max[w0 + w]);
+  }
+  if (!live) return;
+  const float s_new = pow2f(scale_exp(amax));
+  const bool grown = held && !(s_old >= s_new);
+  const float s = held && !grown ? s_old : s_new;
+  // x / s: by the reciprocal where s is a power of two (always, unless the caller's own scale stays)
+  const bool exact = (__float_as_uint(s) & 0x7FFFFFu) == 0u && s >= 5.4210108624275222e-20f;  // 2^-64
+  const float inv = exact ? 1.f / s : 0.f;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = t + j * tg, r = c >> row_shift;
+    float x[E];
+    if (r >= held && r < end) {
+      Vec<BF16>::unpack(v[j], x);
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[e] = exact ? x[e] * inv : x[e] / s;
+      store_codes<E>(codes + (size_t)c * E, x);
+    } else if (grown && r < held) {
+      const float ratio = s_old / s;
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(codes + (size_t)c * E);
+#pragma unroll
+      for (int e = 0; e < E; e += 4) {
+        const uint32_t q = w[e / 4];
+        const float2 a = from_e4m3x2(q & 0xFFFFu), z = from_e4m3x2(q >> 16);
+        x[e] = a.x * ratio; x[e + 1] = a.y * ratio; x[e + 2] = z.x * ratio; x[e + 3] = z.y * ratio;
+      }
+      store_codes<E>(codes + (size_t)c * E, x);
+    }
+  }
+  if (t == 0) *scale = s;
+}
+
+namespace {
+
+struct AppendShape {
+  int tg_shift, threads, parts, nv;
+  long long units;
+};
+
+AppendShape append_shape(const Kv8AppendParams& p) {
+  AppendShape s;
+  const int vecs = p.bs * p.d / (p.is_bf16 ? 8 : 4);  // 128 (16 x 64 bf16) to 8192 (256 x 128 fp32)
+  s.nv = vecs > 1024 * kVecs ? 2 * kVecs : kVecs;
+  s.tg_shift = 5;
+  while ((s.nv << s.tg_shift) < vecs) ++s.tg_shift;
+  const int tg = 1 << s.tg_shift;
+  s.threads = tg > 256 ? tg : 256;
+  const int groups = s.threads / tg;
+  s.parts = (2 * p.Hkv + groups - 1) / groups;
+  s.units = p.path ? (long long)p.B * p.units_per_req : (p.n_rows >> p.bs_shift) + 2ll * p.B;
+  return s;
+}
+
+}  // namespace
+
+unsigned kv8_append_grid(const Kv8AppendParams& p) {
+  const AppendShape s = append_shape(p);
+  const long long g = s.units * s.parts;
+  return g > 0x7fffffffLL ? 0u : (unsigned)g;
+}
+
+cudaError_t launch_kv8_append(const Kv8AppendParams& p, cudaStream_t stream) {
+  const AppendShape s = append_shape(p);
+  const unsigned grid = kv8_append_grid(p);
+  if (p.is_bf16)
+    kv8_append_kernel<true, kVecs><<<grid, s.threads, 0, stream>>>(p, s.parts, s.tg_shift);
+  else if (s.nv == kVecs)
+    kv8_append_kernel<false, kVecs><<<grid, s.threads, 0, stream>>>(p, s.parts, s.tg_shift);
+  else
+    kv8_append_kernel<false, 2 * kVecs><<<grid, s.threads, 0, stream>>>(p, s.parts, s.tg_shift);
+  return cudaGetLastError();
+}
+
+}  // namespace spectree
