@@ -3,9 +3,11 @@ and the attention's error bound.
 
 The bound of one output element (attention), against 64 bits, where p are the exact weights:
 * the output's own rounding to bf16: 2^-8 |out| (half a step);
-* each weight enters the product rounded: to bf16 for tree keys (2^-8 of it), else to at least 8
-  significant bits (2^-8 of it) but no finer than 2^-14 of the row's largest weight; so at most
-  2^-8 A + 2^-14 pmax V1, A = sum p |v|, V1 = sum |v| over the keys;
+* each weight enters the product rounded: to bf16 for tree keys (2^-8 of it), else, multiplied by its
+  block's V scale, to at least 8 significant bits (2^-8 of it) but no finer than 2^-14 of the largest such
+  product w of the row (two roundings to multiples of 2^-9 where the largest is 2^7 or more: 2^-16); the
+  product multiplies the code, v / scale; so at most 2^-8 A + 2^-14 w C1, A = sum p |v|, C1 = sum of the
+  prefix's |codes|;
 * a score that is off by dx moves a weight by a factor exp(dx): 2 dx A more.  dx: the query's elements
   are kept to 2^-17 of the row's largest, so |dx| <= scale 2^-17 qmax K1, K1 = max over the keys of
   sum |k|; the float32 sums of at most 256 products add 2^-16 of scale sum |q k| at most;
@@ -100,6 +102,8 @@ def exact(cache, qs, b, scale=0.0):
     k0, v0 = cache.values(b)
     s = scale if scale > 0 else 1 / np.sqrt(d)
     mask = oracle.tree_mask(qs.parent[b], n, L)
+    blocks = cache.table[b][np.arange(L) // cache.bs]
+    slot_vs = cache.vs.astype(np.float64)[blocks].T  # [Hkv][L]
     O, E = np.zeros((N, Hq, d)), np.zeros((N, Hq, d))
     LSE, EL = np.zeros((N, Hq)), np.zeros((N, Hq))
     G = Hq // cache.Hkv
@@ -115,10 +119,12 @@ def exact(cache, qs, b, scale=0.0):
             O[:n, h] = (w @ V) / tot
             LSE[:n, h] = (m + np.log(tot))[:, 0]
             A = (w @ np.abs(V)) / tot
-            V1 = mask.astype(float) @ np.abs(V)
+            vs = slot_vs[g]
+            top = (w[:, :L] * vs).max(1, keepdims=True) if L else np.zeros((n, 1))
+            floor = top * (np.abs(v0[g]) / vs[:, None]).sum(0) if L else 0
             dx = s * (2.0 ** -17 * np.abs(Q).max(1, keepdims=True) * np.abs(K).sum(1).max()
                       + 2.0 ** -16 * (np.abs(Q) @ np.abs(K).T).max(1, keepdims=True))
-            E[:n, h] = 2.0 ** -8 * (np.abs(O[:n, h]) + A) + 2.0 ** -14 * V1 / tot + (2 * dx + 2.0 ** -14) * A
+            E[:n, h] = 2.0 ** -8 * (np.abs(O[:n, h]) + A) + 2.0 ** -14 * floor / tot + (2 * dx + 2.0 ** -14) * A
             EL[:n, h] = dx[:, 0] + 2.0 ** -20 * (np.abs(LSE[:n, h]) + 1)
     return O, LSE, E, EL
 

@@ -62,6 +62,21 @@ def test_any_scale_and_softmax_scale(N):
     K8.check(cache, qs, out, lse, scale=0.03)
 
 
+@pytest.mark.parametrize("N", [1, 3, 60])
+@pytest.mark.parametrize("e", [-50, -30, 100])
+def test_values_far_from_one(N, e):
+    """All of V near 2^e, in the cache and in the tree: the weights keep their precision whatever V's unit."""
+    rng = np.random.default_rng(11)
+    cache = K8.Cache(rng, [300, 47], 1, 128, 32)
+    qs = K8.Queries(rng, 2, N, 4, 1, 128)
+    cache.vs *= np.float32(2.0 ** e)
+    qs.vt_t = qs.vt_t * 2.0 ** e
+    qs.vt = qs.vt_t.double().numpy()
+    out, lse, status = K8.attend(K8.dev(), cache, qs)
+    assert status == 0
+    K8.check(cache, qs, out, lse)
+
+
 @pytest.mark.parametrize("N", [1, 60])
 def test_sharp_and_flat_rows(N):
     """Scores hundreds apart (one key takes all) and queries of zeros (every key the same)."""

@@ -72,20 +72,23 @@ struct RowState {
 };
 
 // y: this lane's four scores of each row (log2 units, V scale included).  Moves the references when a
-// score has run ahead of one, then returns P' and adds it to the sums.
+// score has run ahead of one, then returns P' and adds it to the sums.  `rebase`, at the first prefix keys
+// behind tree keys: references move down as well, as f16 weights need one near their own largest, however
+// small the prefix's V scales are (the tree's bf16 weights bear any).
 template <int NT>
-__device__ __forceinline__ void softmax_step(float (&y)[2][4], RowState& st, float (&o)[NT][4], float inv_vs) {
+__device__ __forceinline__ void softmax_step(float (&y)[2][4], RowState& st, float (&o)[NT][4], float inv_vs,
+                                             bool rebase) {
   float mx[2];
 #pragma unroll
   for (int r = 0; r < 2; ++r) mx[r] = fmaxf(fmaxf(y[r][0], y[r][1]), fmaxf(y[r][2], y[r][3]));
-  if (__any_sync(0xffffffffu, mx[0] > st.m[0] + kLazy || mx[1] > st.m[1] + kLazy)) {
+  if (__any_sync(0xffffffffu, rebase || mx[0] > st.m[0] + kLazy || mx[1] > st.m[1] + kLazy)) {
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       float v = mx[r];
       v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
       v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
       // each row by its own scores alone, so that no row's rounding depends on its neighbours
-      const float mn = v > st.m[r] + kLazy ? v : st.m[r];
+      const float mn = v > st.m[r] + kLazy || (rebase && v > -INFINITY) ? fmaxf(v, st.m[r] - 64.f) : st.m[r];
       const float f = mn == st.m[r] ? 1.f : ex2_approx(st.m[r] - mn);
       st.m[r] = mn;
       st.l[r] *= f;
@@ -130,7 +133,7 @@ __global__ void __launch_bounds__(kWarps * 32)
   long long L;
   int n;
   int err = kv8_counts(p, b, &L, &n);
-  const Kv8Split sp = kv8_split(L, p.n_split);
+  const Kv8Split sp = kv8_split(L, p.n_split, p.unit_shift);
   if (split >= sp.n) return;
   const int row0 = rt * kRowsR, rows = p.N * p.G;
   if (tid == 0) {
@@ -184,8 +187,8 @@ __global__ void __launch_bounds__(kWarps * 32)
   }
   // ---- this warp's boxes: box c0 + warp + 4 i of 16 keys ----
   const int nbox = (int)((L + 15) >> 4);
-  const int c0 = split * sp.steps * 4;
-  const int c1 = min(nbox, c0 + sp.steps * 4);
+  const int c0 = (split * sp.steps) << (p.unit_shift - 4);
+  const int c1 = min(nbox, c0 + (sp.steps << (p.unit_shift - 4)));
   const int mine = c0 + warp < c1 ? (c1 - c0 - warp + kWarps - 1) / kWarps : 0;
   uint8_t* ring = base + warp * (kStagesR * 2 * C::kBox);
   // table entries and scales of 32 boxes at a time, one per lane: `e` for the boxes being requested, `c`
@@ -299,7 +302,7 @@ __global__ void __launch_bounds__(kWarps * 32)
           y[r][nt * 2 + (i & 1)] = see ? c[i] * p.scale_log2 : -INFINITY;
         }
       }
-      softmax_step<NT>(y, st, o, 1.f);
+      softmax_step<NT>(y, st, o, 1.f, false);
       const uint32_t pa[4] = {pack_bf16x2(y[0][0], y[0][1]), pack_bf16x2(y[1][0], y[1][1]),
                               pack_bf16x2(y[0][2], y[0][3]), pack_bf16x2(y[1][2], y[1][3])};
       // V rows 2t, 2t + 1, 2t + 8, 2t + 9 of the chunk, dimensions NT g .. NT g + NT - 1; a row with an
@@ -377,7 +380,7 @@ __global__ void __launch_bounds__(kWarps * 32)
         y[r][nt * 2 + (e & 1)] = kk < left ? fmaf(c[e], qf[r] * ks, lv) : -INFINITY;
       }
     }
-    softmax_step<NT>(y, st, o, inv_vs);
+    softmax_step<NT>(y, st, o, inv_vs, tree && i == 0);
     const uint32_t pa[4] = {pack_f16x2(y[0][0], y[0][1]), pack_f16x2(y[1][0], y[1][1]), pack_f16x2(y[0][2], y[0][3]),
                             pack_f16x2(y[1][2], y[1][3])};
     uint32_t v[4][NT / 4];
@@ -513,7 +516,7 @@ __global__ void __launch_bounds__(256) attn_kv8_merge_kernel(const Kv8AttnParams
   long long L;
   int n;
   kv8_counts(p, b, &L, &n);
-  const Kv8Split sp = kv8_split(L, p.n_split);
+  const Kv8Split sp = kv8_split(L, p.n_split, p.unit_shift);
   if (sp.n == 1) return;  // written by the attention kernel itself
   float M = -INFINITY;
   bool bad = i >= n;
@@ -553,14 +556,38 @@ __global__ void __launch_bounds__(256) attn_kv8_merge_kernel(const Kv8AttnParams
 
 Kv8AttnPlan plan_attention_kv8(int B, int N, int G, int Hkv, long long L_cap, int num_sms) {
   Kv8AttnPlan pl;
-  pl.n_rt = (N * G + kRowsR - 1) / kRowsR;
-  // about four rounds of the three CTAs an SM holds, no split below 256 keys
-  const long long base = (long long)B * Hkv * pl.n_rt;
-  long long want = ((long long)num_sms * 12 + base - 1) / base;
-  const long long most = (L_cap + 255) / 256;
-  if (want > most) want = most;
-  if (want > 64) want = 64;
-  pl.n_split = want < 1 ? 1 : (int)want;
+  const int rows = N * G;
+  if (rows <= kRowsR) {
+    pl.groups = 0;
+    pl.unit_shift = 6;
+    pl.n_rt = 1;
+    // about four rounds of the three CTAs an SM holds, no split below 256 keys
+    const long long base = (long long)B * Hkv;
+    long long want = ((long long)num_sms * 12 + base - 1) / base;
+    const long long most = (L_cap + 255) / 256;
+    if (want > most) want = most;
+    if (want > 64) want = 64;
+    pl.n_split = want < 1 ? 1 : (int)want;
+    return pl;
+  }
+  // two groups of 128 rows per CTA where that still gives every SM work before any splitting
+  const long long units2 = (long long)B * Hkv * ((rows + 255) / 256);
+  pl.groups = rows > 128 && units2 * 2 >= num_sms ? 2 : 1;
+  pl.unit_shift = 7;
+  pl.n_rt = (rows + 128 * pl.groups - 1) / (128 * pl.groups);
+  // splits: the fewest rounds x (tiles + fixed work of a CTA, about kFixed tiles)
+  const long long base = (long long)B * Hkv * pl.n_rt, tiles = (L_cap + 127) / 128;
+  constexpr long long kFixed = 5;
+  long long best = -1;
+  pl.n_split = 1;
+  for (int s = 1; s <= 32 && (s == 1 || (tiles + s - 1) / s >= 2); ++s) {
+    const long long rounds = (base * s + num_sms - 1) / num_sms;
+    const long long cost = rounds * ((tiles + s - 1) / s + kFixed) + (s > 1 ? 3 : 0);
+    if (best < 0 || cost < best) {
+      best = cost;
+      pl.n_split = s;
+    }
+  }
   return pl;
 }
 

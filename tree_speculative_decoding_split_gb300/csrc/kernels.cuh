@@ -285,15 +285,19 @@ struct Kv8AttnParams {
   int B, N, Hq, Hkv, G, d, bs, bs_shift, max_blocks, num_blocks;
   long long L_cap;
   int n_split;            // key splits at most; a request uses as many as its own length fills
+  int unit_shift;         // splits are whole steps of 2^unit_shift keys
   int n_rt;               // row tiles of (node, head) rows per KV head
   float scale_log2;
 };
 struct Kv8AttnPlan {
-  int n_split, n_rt;
+  int n_split, n_rt, unit_shift;
+  int groups;             // 0: the few-rows kernel; 1, 2: groups of 128 rows per CTA of the tensor-core kernel
 };
 Kv8AttnPlan plan_attention_kv8(int B, int N, int G, int Hkv, long long L_cap, int num_sms);
 cudaError_t launch_attention_kv8_rows(const CUtensorMap* tmK, const CUtensorMap* tmV, const Kv8AttnParams& p,
                                       cudaStream_t stream);
+// tm: maps of the K and V pools (boxes of min(bs, 128) rows) and of k_tree and v_tree.
+cudaError_t launch_attention_kv8_tc(const CUtensorMap* tm, const Kv8AttnParams& p, int groups, cudaStream_t stream);
 cudaError_t launch_attention_kv8_merge(const Kv8AttnParams& p, cudaStream_t stream);
 
 }  // namespace spectree

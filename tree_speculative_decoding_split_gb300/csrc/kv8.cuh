@@ -13,16 +13,16 @@ constexpr float kKv8MaxScale = 1.329227995784916e36f;    // 2^120
 
 __device__ __forceinline__ float kv8_clamp_scale(float s) { return fminf(fmaxf(s, kKv8MinScale), kKv8MaxScale); }
 
-// How a request's prefix is cut into splits of whole 64-key steps: as many splits as the launch has, but
-// none shorter than 256 keys.  The merge evaluates the same function.
+// How a request's prefix is cut into splits of whole steps (2^unit_shift keys): as many splits as the launch
+// has, but none shorter than 256 keys.  The merge evaluates the same function.
 struct Kv8Split {
   int n;      // splits in use, >= 1
-  int steps;  // 64-key steps per split
+  int steps;  // steps per split
 };
-__host__ __device__ __forceinline__ Kv8Split kv8_split(long long len, int n_split) {
-  const int total = (int)((len + 63) >> 6);
+__host__ __device__ __forceinline__ Kv8Split kv8_split(long long len, int n_split, int unit_shift) {
+  const int total = (int)((len + (1 << unit_shift) - 1) >> unit_shift);
   int steps = (total + n_split - 1) / n_split;
-  if (steps < 4) steps = 4;
+  if (steps < (256 >> unit_shift)) steps = 256 >> unit_shift;
   Kv8Split s;
   s.steps = steps;
   s.n = total > 0 ? (total + steps - 1) / steps : 1;

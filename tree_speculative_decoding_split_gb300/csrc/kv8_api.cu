@@ -169,11 +169,25 @@ spec_status spec_tree_attention_kv8(const spec_attn_kv8_args* a, void* workspace
   p.n_split = l.plan.n_split; p.n_rt = l.plan.n_rt;
   const float scale = a->scale > 0.f ? a->scale : 1.f / std::sqrt((float)a->head_dim);
   p.scale_log2 = scale * 1.4426950408889634f;
-  CUtensorMap tmK, tmV;
+  p.unit_shift = l.plan.unit_shift;
+  CUtensorMap tm[4];
   const long long heads = (long long)a->num_blocks * a->num_kv_heads;
-  if (!make_map_kv8(&tmK, a->k_cache, p.d, p.bs, heads, 16) || !make_map_kv8(&tmV, a->v_cache, p.d, p.bs, heads, 16))
+  const int box = l.plan.groups == 0 ? 16 : (p.bs < 128 ? p.bs : 128);
+  if (!make_map_kv8(&tm[0], a->k_cache, p.d, p.bs, heads, box) || !make_map_kv8(&tm[1], a->v_cache, p.d, p.bs, heads, box))
     return SPEC_ERR_CUDA;
-  if (launch_attention_kv8_rows(&tmK, &tmV, p, stream) != cudaSuccess) return SPEC_ERR_CUDA;
+  if (l.plan.groups == 0) {
+    if (launch_attention_kv8_rows(&tm[0], &tm[1], p, stream) != cudaSuccess) return SPEC_ERR_CUDA;
+  } else {
+    // the tree's rows as (d, Hkv, N, B): boxes of 64 dimensions of 64 nodes of one head
+    const cuuint64_t dims[4] = {(cuuint64_t)p.d, (cuuint64_t)p.Hkv, (cuuint64_t)p.N, (cuuint64_t)p.B};
+    const cuuint64_t row = (cuuint64_t)p.d * 2;
+    const cuuint64_t strides[3] = {row, row * p.Hkv, row * p.Hkv * p.N};
+    const cuuint32_t tbox[4] = {64, 1, 64, 1};
+    if (!make_map_bf16(&tm[2], a->k_tree, 4, dims, strides, tbox) ||
+        !make_map_bf16(&tm[3], a->v_tree, 4, dims, strides, tbox))
+      return SPEC_ERR_CUDA;
+    if (launch_attention_kv8_tc(tm, p, l.plan.groups, stream) != cudaSuccess) return SPEC_ERR_CUDA;
+  }
   if (p.n_split > 1 && launch_attention_kv8_merge(p, stream) != cudaSuccess) return SPEC_ERR_CUDA;
   return SPEC_OK;
 }
