@@ -4,10 +4,9 @@ and the attention's error bound.
 The bound of one output element (attention), against 64 bits, where p are the exact weights:
 * the output's own rounding to bf16: 2^-8 |out| (half a step);
 * each weight enters the product rounded: to bf16 for tree keys (2^-8 of it), else, multiplied by its
-  block's V scale, to at least 8 significant bits (2^-8 of it) but no finer than 2^-14 of the largest such
-  product w of the row (two roundings to multiples of 2^-9 where the largest is 2^7 or more: 2^-16); the
-  product multiplies the code, v / scale; so at most 2^-8 A + 2^-14 w C1, A = sum p |v|, C1 = sum of the
-  prefix's |codes|;
+  block's V scale, to f16 (2^-11 of it, or 2^-25 in a unit that puts the row's largest such product w at 1/2
+  or above: 2^-24 w); the product multiplies the code, v / scale; so at most 2^-8 A + 2^-20 w C1,
+  A = sum p |v|, C1 = sum of the prefix's |codes| (2^-20 where 2^-24 would do);
 * a score that is off by dx moves a weight by a factor exp(dx): 2 dx A more.  dx: the query's elements
   are kept to 2^-17 of the row's largest, so |dx| <= scale 2^-17 qmax K1, K1 = max over the keys of
   sum |k|; the float32 sums of at most 256 products add 2^-16 of scale sum |q k| at most;
@@ -124,7 +123,8 @@ def exact(cache, qs, b, scale=0.0):
             floor = top * (np.abs(v0[g]) / vs[:, None]).sum(0) if L else 0
             dx = s * (2.0 ** -17 * np.abs(Q).max(1, keepdims=True) * np.abs(K).sum(1).max()
                       + 2.0 ** -16 * (np.abs(Q) @ np.abs(K).T).max(1, keepdims=True))
-            E[:n, h] = 2.0 ** -8 * (np.abs(O[:n, h]) + A) + 2.0 ** -14 * floor / tot + (2 * dx + 2.0 ** -14) * A
+            E[:n, h] = (2.0 ** -8 * np.abs(O[:n, h]) + (2.0 ** -8 + 2.0 ** -14 + 2 * dx) * A
+                        + 2.0 ** -20 * floor / tot)
             EL[:n, h] = dx[:, 0] + 2.0 ** -20 * (np.abs(LSE[:n, h]) + 1)
     return O, LSE, E, EL
 

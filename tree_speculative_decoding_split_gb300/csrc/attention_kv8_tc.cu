@@ -1,26 +1,30 @@
 // K9t: tree attention over the 8-bit paged cache on tcgen05 tensor cores, for many rows per KV head.
 //
-// The codes feed the tensor cores as they lie in the cache.  tcgen05 has no product of a 16-bit with an
-// 8-bit operand, so the 16-bit sides enter as sums of two e4m3 numbers: a number with 8 significant
-// bits is hi + lo, hi its first 4 bits and lo the rest.
-//   Q      scaled per row so that its largest element lies in [128, 256): hi + lo is q to 2^-17 of that;
-//   P      2^(y - m) in [0, 448] (y = score in log2 units with the V scale folded in, as in the
-//          few-rows kernel): hi by truncation, lo = P - hi, together as exact as bf16;
-//   S = Qhi K^T + Qlo K^T and O += Phi V + Plo V, e4m3 x e4m3 at twice the 16-bit rate: the same tensor
-//   time as 16-bit operands, half the bytes from HBM, through L2 and in shared memory, and no key or value
-//   is ever converted.  Accumulation is float32 (measured: 1e-7 relative, as for bf16).
-// The tree's own keys (at most 255, bf16) come first, as bf16 tiles with bf16 Q and P.
+// tcgen05 has no product of a 16-bit with an 8-bit operand.  So
+//   S = Q K^T: the keys' codes feed the tensor cores as they lie, and Q enters as the sum of two e4m3 numbers
+//   (scaled per row so that its largest element lies in [128, 256): hi its first four significant bits, lo the
+//   rest, together q to 2^-17 of that largest): S = Qhi K^T + Qlo K^T at twice the 16-bit rate, the same tensor
+//   time as 16-bit operands.
+//   O += P V: splitting the weights the same way cost more instructions in the softmax (six per pair) than
+//   anything else there, so here the codes of V become f16 instead (exactly, by two warps of their own, once
+//   per tile for all rows), and P = 2^(y - m) is f16 (y: the score in log2 units with the V scale folded in, as
+//   in the few-rows kernel).
+// Accumulation is float32 (measured: 1e-7 relative for e4m3 products, as for bf16).  The tree's own keys (at
+// most 255, bf16) come first, as bf16 tiles with bf16 Q and P.
 //
 // One CTA owns (request, KV head, key split, NG x 128 rows).  Bound: per 128-key tile and 128 rows the
-// tensor pipe takes 512 (S) + 512 (P V) cycles.  To keep it busy the issue order is fixed,
-//   S_a(t)  P V_a(t - 1)  S_b(t)  P V_b(t - 1)  S_a(t + 1) ...
-// so that a group's softmax has a whole round for tile t while both S read-outs hide behind a P V.
-// TMEM (512 columns): O 2 x 128, one S of 128 columns shared by both groups, P 2 x 64 (hi and lo).  With one
-// group: O 128, two S, P 64.
+// tensor pipe takes 512 (S) + 512 (P V) cycles; the two groups fill each other's softmax.  TMEM: O 128
+// columns and S 128 per group, 512 in all with two; P lies over the S it came from, so the issue order per
+// group is  P V(t), S(t + 1)  back to back.  (With one group S has two buffers.)
 //   warp 0     TMA producer: K and V rings of 128-key tiles (one box per block and tensor, issued by as many
 //              lanes), the tile's scales;
-//   warp 1     MMA issuer; warps 2, 3 idle, so that register shares can move between warpgroups;
-//   warps 4..  softmax, four warps per group, a thread owning a row (a TMEM lane): 128 scores in registers.
+//   warp 1     MMA issuer;
+//   warps 2, 3 V tiles to f16;
+//   warps 4..  softmax, eight warps per group: two threads own a row (a TMEM lane), 64 keys of a tile each.
+//              Both use the row's reference; whether one has to move is one barrier's OR per tile.
+// Tried and slower (63-node trees, batch 32 at 4K): P as e4m3 pairs with 128 keys a thread, four warps per
+// group and a row maximum ahead of the weights, 238 us; with one S buffer shared by both groups and all
+// descriptors in uniform registers, 203 us; with two threads per row, 211 us.
 #include "common.cuh"
 #include "kernels.cuh"
 #include "kv8.cuh"
@@ -33,26 +37,30 @@ namespace {
 constexpr int kKT8 = 128;        // keys per prefix tile
 constexpr int kTT = 64;          // keys per tree tile (bf16: the same bytes)
 constexpr int kGR8 = 128;        // rows per group
-constexpr int kKS = 4, kVS = 5;  // ring depths
+constexpr int kKS = 3, kVS = 2;  // ring depths: K codes, V codes
+constexpr int kV16 = 2;          // V tiles in f16
 constexpr int kCS = 8;           // stages of the scales
-constexpr float kHead = 8.75f;   // P <= 2^8.75 < 448
-constexpr float kFresh = 7.f;    // a new reference puts the row's largest P at 2^7
+// A row's reference m is an integer.  It moves when sixteen neighbouring weights sum to more than 2^15, well
+// inside f16; a new one puts the row's largest weight into (1/2, 1].  So rows rarely move (every move costs a
+// pass over O), and a weight is exact to 11 bits or to 2^-24 of the largest.
+constexpr float kTop = 32768.f;
 
 template <int D, int NG>
 struct TcCfg {
-  static constexpr int kThreads = 128 + 128 * NG;
+  static constexpr int kThreads = 128 + 256 * NG;
   static constexpr int kQ = kGR8 * D * 2;      // Q bytes per group: bf16, or e4m3 hi then lo
   static constexpr int kSlot = kKT8 * D;       // ring slot
-  static constexpr int kNB = NG == 2 ? 1 : 2;  // S buffers
-  static constexpr int kColO = 0, kColS = NG * 128, kColP = NG * 128 + kNB * 128;
+  static constexpr int kNB = NG == 2 ? 1 : 2;  // S (and P) buffers per group
+  static constexpr int kColO = 0, kColS = NG * 128;
   static constexpr int kNanc = (kMaxNodes + 1) * kAncWords * 4;
-  static constexpr int kRing = NG * kQ + (kKS + kVS) * kSlot;
+  static constexpr int kTile16 = kKT8 * D * 2; // a V tile in f16
+  static constexpr int kRing = NG * kQ + (kKS + kVS) * kSlot + kV16 * kTile16;
   static constexpr int kSmem = 1024 + kRing + kNanc + kCS * 8 * 16;
   static constexpr int kORow = D * 4 + 16;     // epilogue rows in shared memory, padded
   static_assert(kGR8 * NG * kORow <= kRing, "O staging does not fit");
 };
 
-__device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                           uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
@@ -61,18 +69,8 @@ __device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// A (M x 32 per instruction) in tensor memory: row m in lane m, four consecutive K elements per column.
-__device__ __forceinline__ void umma_e4m3_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                                 uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-// Instruction descriptor, kind::f8f6f4: D fp32, A and B e4m3.
-__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N, int b_mn_major) {
+// Instruction descriptors with type fields 0: D fp32, A and B e4m3 (kind::f8f6f4) or f16 (kind::f16).
+__host__ __device__ constexpr uint32_t idesc_type0_f32(int M, int N, int b_mn_major) {
   return (1u << 4) | ((uint32_t)(b_mn_major ? 1 : 0) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 // Descriptor of an e4m3 tile of D-byte rows, swizzled over 128 (D = 128) or 64 bytes (D = 64); 8-row groups
@@ -90,8 +88,8 @@ template <int D>
 __device__ __forceinline__ uint32_t kv8_off(int r, int ch) {
   return D == 128 ? (uint32_t)(r * 128 + ((ch ^ (r & 7)) << 4)) : (uint32_t)(r * 64 + ((ch ^ ((r >> 1) & 3)) << 4));
 }
-// ... and of chunk ch of row r in a bf16 tile of `rows` rows: halves of 64 columns, 128-byte swizzle.
-__device__ __forceinline__ uint32_t bf16_off(int r, int ch, int rows) {
+// ... and of chunk ch of row r in a 16-bit tile of `rows` rows: halves of 64 columns, 128-byte swizzle.
+__device__ __forceinline__ uint32_t tile16_off(int r, int ch, int rows) {
   return (uint32_t)((ch >> 3) * rows * 128 + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
 }
 
@@ -112,19 +110,35 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-// The tile's constants and the exponentials are ordered (volatile): hoisted ahead of their use they cost more
-// registers than a softmax thread has beside its 128 scores.
-__device__ __forceinline__ float4 lds_f4(const float4* p) {
-  float4 v;
-  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(smem_u32(p)));
-  return v;
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
 }
-__device__ __forceinline__ float ex2_ordered(float x) {
-  float y;
-  asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
+// Two e4m3 codes (the low or high half of `w`) to f16, exactly.
+template <int HALF>
+__device__ __forceinline__ uint32_t kv8_f16x2(uint32_t w) {
+  uint32_t r;
+  if constexpr (HALF == 0)
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(w));
+  else
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(w));
+  return r;
 }
-
+// Named barrier of `count` threads that returns the OR of their predicates.
+__device__ __forceinline__ bool bar_or(int id, int count, bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}\n"
+      : "=r"(r)
+      : "r"(id), "r"(count), "r"((uint32_t)pred)
+      : "memory");
+  return r != 0;
+}
 __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -158,12 +172,14 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
   uint8_t* sQ = base;
   uint8_t* sK = sQ + NG * C::kQ;
   uint8_t* sV = sK + kKS * C::kSlot;
-  uint32_t* s_nanc = reinterpret_cast<uint32_t*>(sV + kVS * C::kSlot);  // [node][word] ancestors-or-self
+  uint8_t* sV16 = sV + kVS * C::kSlot;
+  uint32_t* s_nanc = reinterpret_cast<uint32_t*>(sV16 + kV16 * C::kTile16);  // [node][word] ancestors-or-self
   float4* s_cst = reinterpret_cast<float4*>(s_nanc + (kMaxNodes + 1) * kAncWords);  // [stage][16-key group]
-  __shared__ uint64_t kfull[kKS], kempty[kKS], vfull[kVS], vempty[kVS];
-  // scores ready and read: per group, or with one group per S buffer (else a barrier could be two phases on)
-  constexpr int kSB = NG * C::kNB;
-  __shared__ uint64_t sfull[kSB], sfree[kSB], pfull[NG], ofull[NG], qready[NG];
+  __shared__ uint64_t kfull[kKS], kempty[kKS], vfull[kVS], vempty[kVS], v16full[kV16], v16empty[kV16];
+  // per group, and per buffer where there are two (one barrier could be two phases on)
+  __shared__ uint64_t sfull[NG][C::kNB], pfull[NG][C::kNB], ofull[NG], qready[NG];
+  __shared__ float s_x[NG][2][kGR8];  // a row's threads tell each other their largest score; at the end, their sums
+  __shared__ uint32_t s_w[NG][2][4];  // ... and which of the warp's rows move
   __shared__ uint64_t s_drained;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort, s_bad, s_kissued, s_vissued;
@@ -193,9 +209,6 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
       }
     }
   };
-  // barrier index and parity of step (tile t, group g)
-  auto sbar = [](int t, int g) { return NG == 1 ? t % C::kNB : g; };
-  auto spar = [](int t) { return (uint32_t)((NG == 1 ? t / C::kNB : t) & 1); };
   if (tid == 0) {
     for (int s = 0; s < kKS; ++s) {
       mbar_init(&kfull[s], 1);
@@ -203,16 +216,19 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
     }
     for (int s = 0; s < kVS; ++s) {
       mbar_init(&vfull[s], 1);
-      mbar_init(&vempty[s], 1);
+      mbar_init(&vempty[s], 2);
     }
-    for (int g = 0; g < kSB; ++g) {
-      mbar_init(&sfull[g], 1);
-      mbar_init(&sfree[g], 4);
+    for (int s = 0; s < kV16; ++s) {
+      mbar_init(&v16full[s], 2);
+      mbar_init(&v16empty[s], 1);
     }
     for (int g = 0; g < NG; ++g) {
-      mbar_init(&pfull[g], 4);
+      for (int i = 0; i < C::kNB; ++i) {
+        mbar_init(&sfull[g][i], 1);
+        mbar_init(&pfull[g][i], 8);
+      }
       mbar_init(&ofull[g], 1);
-      mbar_init(&qready[g], 4);
+      mbar_init(&qready[g], 8);
     }
     mbar_init(&s_drained, 1);
     s_abort = 0;
@@ -258,9 +274,9 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  // register shares of the warpgroups (two groups): 88 + 2 x 208 = the 3 x 168 that the block was launched with
+  // register shares of the warpgroups (two groups): 64 + 4 x 104 within the 5 x 96 the block was launched with
   if (warp < 4) {
-    if constexpr (NG == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if constexpr (NG == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == 0) {
     // ---- TMA producer: lane i < 128 / box takes box i of a tile ----
     const int box = min(p.bs, kKT8), nbox = kKT8 / box;
@@ -351,21 +367,30 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
     }
     } else if (warp == 1) {
     // ---- MMA issuer ----
-    if (lane == 0) {
-      constexpr uint32_t idS8 = idesc_e4m3_f32(kGR8, kKT8, 0), idP8 = idesc_e4m3_f32(kGR8, D, 1);
-      constexpr uint32_t idSt = idesc_bf16_f32(kGR8, kTT, 0), idPt = idesc_bf16_f32(kGR8, D, 1);
-      auto issue_s = [&](int t, int g) -> bool {
-        const int u = t * NG + g;
-        if (g == 0 && !mbar_wait_bounded(&kfull[t % kKS], (t / kKS) & 1, &s_abort)) return false;
-        if (t == 0 && !mbar_wait_bounded(&qready[g], 0, &s_abort)) return false;
-        if (t == Tt && Tt > 0 && !mbar_wait_bounded(&qready[g], 1, &s_abort)) return false;
-        if (u >= C::kNB) {
-          const int w = u - C::kNB;  // the step whose scores the buffer holds
-          if (!mbar_wait_bounded(&sfree[sbar(w / NG, w % NG)], spar(w / NG), &s_abort)) return false;
-        }
-        tc_fence_after();
-        const uint32_t ts = tmem + C::kColS + (u % C::kNB) * 128;
-        const uint32_t qa = smem_u32(sQ + g * C::kQ), ka = smem_u32(sK + (t % kKS) * C::kSlot);
+    // The whole warp runs the loop, so that addresses and descriptors stay in uniform registers, and one
+    // elected lane issues: beside two busy softmax warps on the same scheduler, a lane that computed its
+    // descriptors in vector registers took 160 cycles for an MMA of 64.
+    constexpr uint32_t idS8 = idesc_type0_f32(kGR8, kKT8, 0), idP16 = idesc_type0_f32(kGR8, D, 1);
+    constexpr uint32_t idSt = idesc_bf16_f32(kGR8, kTT, 0), idPt = idesc_bf16_f32(kGR8, D, 1);
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint32_t sq0 = __shfl_sync(0xffffffffu, smem_u32(sQ), 0);
+    const uint32_t sk0 = sq0 + NG * C::kQ, sv0 = sk0 + kKS * C::kSlot;
+    const bool leader = elect_one();
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, &s_abort));
+    };
+    int kst = 0;        // ring stage of the next S tile, and its parity
+    uint32_t kph = 0;
+    bool ok = true;
+    auto issue_s = [&](int t, int g) {
+      if (g == 0) ok = ok && wait(&kfull[kst], kph);
+      if (t == 0) ok = ok && wait(&qready[g], 0);
+      if (t == Tt && Tt > 0) ok = ok && wait(&qready[g], 1);
+      if (!ok) return;
+      tc_fence_after();
+      const uint32_t ts = tm + C::kColS + (NG == 2 ? g : t % C::kNB) * 128;
+      const uint32_t qa = sq0 + g * C::kQ, ka = sk0 + kst * C::kSlot;
+      if (leader) {
         if (t < Tt) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
@@ -375,42 +400,59 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {  // hi, then lo
             const int k = kk % (D / 32);
-            umma_e4m3(ts, sdesc_kv8<D>(qa + (kk / (D / 32)) * (kGR8 * D) + k * 32), sdesc_kv8<D>(ka + k * 32), idS8,
-                      kk > 0);
+            umma_f8(ts, sdesc_kv8<D>(qa + (kk / (D / 32)) * (kGR8 * D) + k * 32), sdesc_kv8<D>(ka + k * 32), idS8,
+                    kk > 0);
           }
         }
-        umma_commit(&sfull[sbar(t, g)]);
-        if (g == NG - 1) umma_commit(&kempty[t % kKS]);
-        return true;
-      };
-      auto issue_pv = [&](int t, int g) -> bool {
-        if (g == 0 && !mbar_wait_bounded(&vfull[t % kVS], (t / kVS) & 1, &s_abort)) return false;
-        if (!mbar_wait_bounded(&pfull[g], t & 1, &s_abort)) return false;
-        tc_fence_after();
-        const uint32_t pt = tmem + C::kColP + g * 64, ot = tmem + C::kColO + g * 128;
-        const uint32_t va = smem_u32(sV + (t % kVS) * C::kSlot);
+        umma_commit(&sfull[g][t % C::kNB]);
+        if (g == NG - 1) umma_commit(&kempty[kst]);
+      }
+      if (g == NG - 1 && ++kst == kKS) {
+        kst = 0;
+        kph ^= 1;
+      }
+    };
+    auto issue_pv = [&](int t, int g) {
+      if (g == 0) ok = ok && wait(&v16full[t % kV16], (t / kV16) & 1);
+      ok = ok && wait(&pfull[g][t % C::kNB], (t / C::kNB) & 1);
+      if (!ok) return;
+      tc_fence_after();
+      const uint32_t pt = tm + C::kColS + (NG == 2 ? g : t % C::kNB) * 128, ot = tm + C::kColO + g * 128;
+      if (leader) {
         if (t < Tt) {
+          const uint32_t va = sv0 + (t % kVS) * C::kSlot;
 #pragma unroll
           for (int kk = 0; kk < kTT / 16; ++kk)
-            umma_bf16_tmem_a(ot, pt + kk * 8, sdesc_sw128(va + kk * 16 * 128, kTT * 128, 1024), idPt, t > 0 || kk > 0);
+            umma_bf16_tmem_a(ot, pt + (kk >> 1) * 64 + (kk & 1) * 8, sdesc_sw128(va + kk * 16 * 128, kTT * 128, 1024), idPt,
+                             t > 0 || kk > 0);
         } else {
+          const uint32_t va = sv0 + kVS * C::kSlot + (t % kV16) * C::kTile16;
 #pragma unroll
-          for (int kk = 0; kk < kKT8 / 16; ++kk) {  // hi, then lo
-            const int k = kk % (kKT8 / 32);
-            umma_e4m3_tmem_a(ot, pt + kk * 8, sdesc_kv8<D>(va + k * 32 * D), idP8, t > 0 || kk > 0);
-          }
+          for (int kk = 0; kk < kKT8 / 16; ++kk)  // each half's weights lie over its own scores
+            umma_bf16_tmem_a(ot, pt + (kk >> 2) * 64 + (kk & 3) * 8, sdesc_sw128(va + kk * 16 * 128, kKT8 * 128, 1024),
+                             idP16, t > 0 || kk > 0);
         }
         umma_commit(&ofull[g]);
-        if (g == NG - 1) umma_commit(&vempty[t % kVS]);
-        return true;
-      };
-      bool ok = true;
-      for (int t = 0; t <= T && ok; ++t)
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          if (ok && t < T) ok = issue_s(t, g);
-          if (ok && t > 0) ok = issue_pv(t - 1, g);
+        if (g == NG - 1) {
+          umma_commit(&v16empty[t % kV16]);
+          if (t < Tt) {  // a tree tile's V was read where it landed
+            umma_commit(&vempty[t % kVS]);
+            umma_commit(&vempty[t % kVS]);
+          }
         }
+      }
+    };
+    for (int t = 0; t < C::kNB && t < T; ++t)
+#pragma unroll
+      for (int g = 0; g < NG; ++g) issue_s(t, g);
+    for (int t = 0; t < T && ok; ++t)
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        issue_pv(t, g);
+        // the buffer's next scores follow in the pipe: MMAs of one thread run in their order
+        if (t + C::kNB < T) issue_s(t + C::kNB, g);
+      }
+    if (leader) {
       if (!ok) {
         s_abort = 1;
         set_status(p.dev_status, SPEC_ERR_TIMEOUT);
@@ -418,16 +460,68 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
       umma_commit(&s_drained);  // every MMA of this CTA
       mbar_wait_bounded(&s_drained, 0, nullptr);
     }
+    } else {
+      // ---- V tiles to f16 (warps 2, 3) ----
+      bool ok = true;
+      const int ct = tid - 64;
+      for (int t = 0; t < T; ++t) {
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&vfull[t % kVS], (t / kVS) & 1, &s_abort) &&
+                                         mbar_wait_bounded(&v16empty[t % kV16], ((t / kV16) & 1) ^ 1, &s_abort));
+        if (!ok) break;
+        uint8_t* src = sV + (t % kVS) * C::kSlot;
+        if (t < Tt) {
+          // a tree tile stays bf16; elements that are no finite numbers become 0 and their rows are noted
+          for (int c = ct; c < kTT * (D / 8); c += 64) {
+            const int r = c / (D / 8), key = t * kTT + r;
+            uint4* at = reinterpret_cast<uint4*>(src + tile16_off(r, c % (D / 8), kTT));
+            uint4 x = *at;
+            if (finite2(x.x) && finite2(x.y) && finite2(x.z) && finite2(x.w)) continue;
+            if (key < n) atomicOr(&s_odd[key >> 5], 1u << (key & 31));
+            uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if ((w[j] & 0x7F80u) == 0x7F80u) w[j] &= 0xFFFF0000u;
+              if ((w[j] & 0x7F800000u) == 0x7F800000u) w[j] &= 0xFFFFu;
+            }
+            *at = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        } else {
+          // 16 codes of a row -> two 16-byte chunks of the f16 tile (halves of 64 columns); lanes of the second
+          // half write their two in the other order, so that eight lanes meet eight bank groups.  Slots
+          // behind the prefix may hold anything and become 0.
+          uint8_t* dst = sV16 + (t % kV16) * C::kTile16;
+          const int left = (int)min((long long)kKT8, k1 - (k0 + (long long)(t - Tt) * kKT8));
+#pragma unroll 4
+          for (int c = ct; c < kKT8 * (D / 16); c += 64) {
+            const int r = c / (D / 16), ch = c % (D / 16), swap = (ch >> 2) & 1;
+            uint4 x = *reinterpret_cast<const uint4*>(src + kv8_off<D>(r, ch));
+            if (r >= left) x = make_uint4(0, 0, 0, 0);
+            const uint4 a = make_uint4(kv8_f16x2<0>(x.x), kv8_f16x2<1>(x.x), kv8_f16x2<0>(x.y), kv8_f16x2<1>(x.y));
+            const uint4 e = make_uint4(kv8_f16x2<0>(x.z), kv8_f16x2<1>(x.z), kv8_f16x2<0>(x.w), kv8_f16x2<1>(x.w));
+            *reinterpret_cast<uint4*>(dst + tile16_off(r, 2 * ch + swap, kKT8)) = swap ? e : a;
+            *reinterpret_cast<uint4*>(dst + tile16_off(r, 2 * ch + (swap ^ 1), kKT8)) = swap ? a : e;
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&v16full[t % kV16]);
+          if (t >= Tt) mbar_arrive(&vempty[t % kVS]);
+        }
+      }
+      if (!ok && lane == 0) {
+        s_abort = 1;
+        set_status(p.dev_status, SPEC_ERR_TIMEOUT);
+      }
     }
   } else {
-    if constexpr (NG == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    if constexpr (NG == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
     // ---- softmax ----
-    const int g = (warp - 4) >> 2, q4 = warp & 3;
+    const int g = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1, q4 = warp & 3;
     const int rl = q4 * 32 + lane, rr = g * kGR8 + rl, row = row0 + rr;
-    const int gtid = q4 * 32 + lane;  // thread of the group
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
-    const uint32_t tS = tmem + C::kColS + lane_off, tO = tmem + C::kColO + g * 128 + lane_off;
-    const uint32_t tP = tmem + C::kColP + g * 64 + lane_off;
+    const uint32_t tS = tmem + C::kColS + (NG == 2 ? g : 0) * 128 + lane_off;
+    const uint32_t tO = tmem + C::kColO + g * 128 + lane_off;
     const bool live = row < n * p.G;
     const uint16_t* q = p.q + orow_of(live ? row : row0) * D;
     uint8_t* myQ = sQ + g * C::kQ;
@@ -441,11 +535,10 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
-    // this row as e4m3 hi and lo
+    // this thread's half of its row's dimensions as e4m3 hi and lo
     auto split_q = [&]() {
-      // read twice (the second time from L1 or L2): a row of it beside the scores would not fit the registers
       float mx = 0.f;
-#pragma unroll 8
+#pragma unroll 4
       for (int i = 0; i < D / 8; ++i) {
         const uint4 w = load_q(i);
         const uint32_t x[4] = {w.x, w.y, w.z, w.w};
@@ -456,8 +549,8 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
       const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 100);
       const float up = __uint_as_float((uint32_t)(127 + 7 - e) << 23);  // largest element into [128, 256)
       qf = __uint_as_float((uint32_t)(127 - 7 + e) << 23) * p.scale_log2;
-#pragma unroll 2
-      for (int i = 0; i < D / 16; ++i) {
+#pragma unroll 1
+      for (int i = half * (D / 32); i < (half + 1) * (D / 32); ++i) {
         uint32_t hi[4], lo[4];
         const uint4 w[2] = {load_q(2 * i), load_q(2 * i + 1)};
 #pragma unroll
@@ -474,213 +567,179 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
       }
     };
     if (Tt > 0) {
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) *reinterpret_cast<uint4*>(myQ + bf16_off(rl, i, kGR8)) = load_q(i);
+#pragma unroll 4
+      for (int i = half * (D / 16); i < (half + 1) * (D / 16); ++i)
+        *reinterpret_cast<uint4*>(myQ + tile16_off(rl, i, kGR8)) = load_q(i);
     } else {
       split_q();
     }
     publish(&qready[g]);
 
-    float m = -INFINITY, l = 0.f;  // reference (P = 2^(y - m)) and sum
+    float m = -INFINITY, l = 0.f;  // the row's reference (P = 2^(y - m)), and the sum over this thread's keys
     const uint32_t* anc = s_nanc + (live ? row / p.G : 0) * kAncWords;
+    const int pair = 2 + g * 4 + q4;  // named barrier of the two warps that share rows
     bool ok = true;
-    // Moves the reference up when the tile's largest y has left the range of P; O follows.  At the first tile
-    // behind the tree's (`rebase`) it moves down as well: the tree's weights are bf16 and bear any reference,
-    // but the prefix's must start at the top of e4m3's range, however small its V scales are.
-    auto advance = [&](float top, int t, bool rebase) {
-      const bool need = top > m + kHead || (rebase && top > -INFINITY);
-      if (__any_sync(0xffffffffu, need)) {
-        const float mn = need ? fmaxf(top - kFresh, m - 64.f) : m;
-        const float f = need ? ex2_approx(m - mn) : 1.f;  // 0 when there was none
-        if (t > 0) {
-          if (!wait(&ofull[g], (t - 1) & 1)) return false;
-          tc_fence_after();
+    // Moves the references of the rows that ask for it in either of their threads (`ask`, with the largest of
+    // the thread's scores in `top`); O and the sums follow.  Also down, at the first tile behind the tree's
+    // (`anew`): the tree's weights are bf16 and bear any reference, but the prefix's must start at the top of
+    // f16's range, however small its V scales are.  Each row by its own scores alone.
+    auto move_references = [&](bool ask, bool anew, float top, int t) {
+      s_x[g][half][rl] = top;
+      const uint32_t mine = __ballot_sync(0xffffffffu, ask);
+      if (lane == 0) s_w[g][half][q4] = mine;
+      named_bar_sync(pair, 64);
+      top = fmaxf(top, s_x[g][half ^ 1][rl]);
+      const bool need = (((mine | s_w[g][half ^ 1][q4]) >> lane) & 1u) && top > -INFINITY;
+      const float mn = need ? (anew ? fmaxf(ceilf(top), m - 64.f) : ceilf(top)) : m;
+      const float f = mn == m ? 1.f : ex2_approx(m - mn);  // 0 when there was none
+      named_bar_sync(pair, 64);                            // both have read before either writes again
+      if (t > 0) {  // (these scores follow P V(t - kNB), so this is the phase under way or the one before)
+        if (!wait(&ofull[g], (t - 1) & 1)) return false;
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = half * (D / 64); c < (half + 1) * (D / 64); ++c) {
+          uint32_t o[32];
+          tmem_ld_x32(tO + c * 32, o);
+          tmem_ld_wait();
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld_x32(tO + c * 32, o);
-            tmem_ld_wait();
-#pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-            tmem_st_x32(tO + c * 32, o);
-          }
-          tmem_st_wait();
+          for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+          tmem_st_x32(tO + c * 32, o);
         }
-        l *= f;
-        m = mn;
+        tmem_st_wait();
       }
+      l *= f;
+      m = mn;
       return true;
     };
     for (int t = 0; t < T; ++t) {
-      if (!wait(&sfull[sbar(t, g)], spar(t))) {
+      if (!wait(&sfull[g][t % C::kNB], (t / C::kNB) & 1)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      const uint32_t ts = tS + ((t * NG + g) % C::kNB) * 128;
+      const uint32_t ts = tS + (NG == 2 ? 0 : t % C::kNB) * 128;
       if (t < Tt) {
-        // -- a tree tile: 64 keys, node t * 64 + j --
-        uint32_t s0[32], s1[32];
-        tmem_ld_x32(ts, s0);
-        tmem_ld_x32(ts + 32, s1);
+        // -- a tree tile: 64 keys, this thread's are nodes 64 t + 32 half + j --
+        uint32_t x[32];
+        tmem_ld_x32(ts + half * 32, x);
         tmem_ld_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sfree[sbar(t, g)]);
         if (t == Tt - 1 && T > Tt) {  // the last product with the bf16 queries is done: make room for hi and lo
           split_q();
           publish(&qready[g]);
         }
-        const uint32_t w0 = live ? anc[2 * t] : 0u, w1 = live ? anc[2 * t + 1] : 0u;
-        float v[64], top = -INFINITY;
+        const uint32_t bits = live ? anc[2 * t + half] : 0u;
+        float top = -INFINITY;
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
-          v[j] = (w0 >> j) & 1u ? __uint_as_float(s0[j]) * p.scale_log2 : -INFINITY;
-          v[32 + j] = (w1 >> j) & 1u ? __uint_as_float(s1[j]) * p.scale_log2 : -INFINITY;
-          top = max3(top, v[j], v[32 + j]);
+          const float y = (bits >> j) & 1u ? __uint_as_float(x[j]) * p.scale_log2 : -INFINITY;
+          top = fmaxf(top, y);
+          x[j] = __float_as_uint(y);
         }
-        if (!advance(top, t, false)) {
+        if (bar_or(pair, 64, top > m + 8.f) && !move_references(top > m + 8.f, false, top, t)) {
           ok = false;
           break;
         }
         const float mu = m == -INFINITY ? 0.f : m;
-        uint32_t pk[32];
+        uint32_t pk[16];
         float sum = 0.f;
 #pragma unroll
-        for (int j = 0; j < 64; j += 2) {
-          const float a = ex2_approx(v[j] - mu), c = ex2_approx(v[j + 1] - mu);
+        for (int j = 0; j < 32; j += 2) {
+          const float a = ex2_approx(__uint_as_float(x[j]) - mu), c = ex2_approx(__uint_as_float(x[j + 1]) - mu);
           sum += a + c;
           pk[j / 2] = pack_bf16x2(a, c);
         }
         l += sum;
-        // V elements that are no finite numbers enter as 0 and are noted; both groups do the whole tile, as
-        // each one's product may run before the other has looked
-        if (!wait(&vfull[t % kVS], (t / kVS) & 1)) {
-          ok = false;
-          break;
-        }
-        uint8_t* tv = sV + (t % kVS) * C::kSlot;
-#pragma unroll 1
-        for (int c = gtid; c < kTT * (D / 8); c += kGR8) {
-          const int r = c / (D / 8), key = t * kTT + r;
-          uint4* at = reinterpret_cast<uint4*>(tv + bf16_off(r, c % (D / 8), kTT));
-          uint4 x = *at;
-          if (finite2(x.x) && finite2(x.y) && finite2(x.z) && finite2(x.w)) continue;
-          if (key < n) atomicOr(&s_odd[key >> 5], 1u << (key & 31));
-          uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if ((w[j] & 0x7F80u) == 0x7F80u) w[j] &= 0xFFFF0000u;
-            if ((w[j] & 0x7F800000u) == 0x7F800000u) w[j] &= 0xFFFFu;
-          }
-          *at = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        fence_proxy_async_smem();
-        if (t > 0 && !wait(&ofull[g], (t - 1) & 1)) {
-          ok = false;
-          break;
-        }
-        tmem_st_x32(tP, pk);
+        tmem_st_x16(ts + half * 64, pk);
       } else {
-        // -- a prefix tile: 128 keys in 8 groups of 16, each within one block --
-        uint32_t s[4][32];
+        // -- a prefix tile: this thread's 64 keys are 4 groups of 16, each within one block --
+        const int left = (int)min((long long)kKT8, k1 - (k0 + (long long)(t - Tt) * kKT8)) - half * 64;
+        const float4* cst = s_cst + (t % kCS) * 8 + half * 4;
+        bool anew = t == Tt && t > 0;
+        uint32_t pk[2][16];
+        for (int pass = 0; pass < 2; ++pass) {
+          float part = 0.f, most = 0.f;  // sum of the weights over the V scales; largest sum of sixteen
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld_x32(ts + c * 32, s[c]);
-        tmem_ld_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sfree[sbar(t, g)]);
-        const int left = (int)min((long long)kKT8, k1 - (k0 + (long long)(t - Tt) * kKT8));
-        if (left < kKT8) {
+          for (int c = 0; c < 2; ++c) {
+            uint32_t x[32];
+            tmem_ld_x32(ts + half * 64 + c * 32, x);
+            tmem_ld_wait();
+            if (left < c * 32 + 32) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+              for (int j = 0; j < 32; ++j)
+                if (c * 32 + j >= left) x[j] = 0xFF800000u;
+            }
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (c * 32 + j >= left) s[c][j] = 0xFF800000u;
-          // slots behind the prefix may hold anything: their V rows become 0 (by both groups, as above)
-          if (!wait(&vfull[t % kVS], (t / kVS) & 1)) {
-            ok = false;
+            for (int gr = 0; gr < 2; ++gr) {
+              const float4 k = cst[c * 2 + gr];
+              const float f = k.x * qf, off = k.y - m;
+              const float2 f2 = make_float2(f, f), off2 = make_float2(off, off);
+              float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+              for (int j = gr * 16; j < gr * 16 + 16; j += 2) {
+                float2 w = __ffma2_rn(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), f2, off2);
+                w = make_float2(ex2_approx(w.x), ex2_approx(w.y));
+                sum[(j >> 1) & 1] = __fadd2_rn(sum[(j >> 1) & 1], w);
+                const __half2 h2 = __floats2half2_rn(w.x, w.y);
+                pk[c][j / 2] = *reinterpret_cast<const uint32_t*>(&h2);
+              }
+              const float2 s2 = __fadd2_rn(sum[0], sum[1]);
+              const float s16 = s2.x + s2.y;
+              most = fmaxf(most, s16);
+              part = fmaf(s16, k.z, part);
+            }
+          }
+          if (pass == 1 || !bar_or(pair, 64, anew || most > kTop)) {
+            l += part;
             break;
           }
-          uint8_t* tv = sV + (t % kVS) * C::kSlot;
-          for (int c = left * (D / 16) + gtid; c < kKT8 * (D / 16); c += kGR8)
-            *reinterpret_cast<uint4*>(tv + c * 16) = make_uint4(0, 0, 0, 0);
-          fence_proxy_async_smem();
-        }
-        const float4* cst = s_cst + (t % kCS) * 8;
-        float top = -INFINITY;
-#pragma unroll
-        for (int gr = 0; gr < 8; ++gr) {
-          const uint32_t* x = &s[gr >> 1][(gr & 1) * 16];
-          float a = __uint_as_float(x[0]);
-#pragma unroll
-          for (int j = 1; j < 15; j += 2) a = max3(a, __uint_as_float(x[j]), __uint_as_float(x[j + 1]));
-          a = fmaxf(a, __uint_as_float(x[15]));
-          const float4 c = lds_f4(cst + gr);
-          top = fmaxf(top, fmaf(a, c.x * qf, c.y));
-        }
-        if (!advance(top, t, t == Tt && t > 0)) {
-          ok = false;
-          break;
-        }
-        const float mu = m == -INFINITY ? 0.f : m;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {  // 64 keys at a time
-          uint32_t hi[16], lo[16];
-#pragma unroll
+          // -- a weight may have left f16's range (or there is no reference yet): find the largest scores,
+          // move the references, and take the weights again --
+          float top = -INFINITY;
+#pragma unroll 1
           for (int gr = 0; gr < 4; ++gr) {
-            const uint32_t* x = &s[half * 2 + (gr >> 1)][(gr & 1) * 16];
-            const float4 c = lds_f4(cst + half * 4 + gr);
-            const float f = c.x * qf, off = c.y - mu;
-            const float2 f2 = make_float2(f, f), off2 = make_float2(off, off);
-            float2 sum = make_float2(0.f, 0.f);
+            uint32_t x[16];
+            tmem_ld_x16(ts + half * 64 + gr * 16, x);
+            tmem_ld_wait();
+            float a = -INFINITY;
 #pragma unroll
-            for (int j = 0; j < 16; j += 4) {
-              float2 a = __ffma2_rn(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), f2, off2);
-              float2 e = __ffma2_rn(make_float2(__uint_as_float(x[j + 2]), __uint_as_float(x[j + 3])), f2, off2);
-              a = make_float2(ex2_ordered(a.x), ex2_ordered(a.y));
-              e = make_float2(ex2_ordered(e.x), ex2_ordered(e.y));
-              sum = __fadd2_rn(sum, __fadd2_rn(a, e));
-              const float2 ah = make_float2(head4(a.x), head4(a.y)), eh = make_float2(head4(e.x), head4(e.y));
-              const float2 al = __fadd2_rn(a, make_float2(-ah.x, -ah.y)), el = __fadd2_rn(e, make_float2(-eh.x, -eh.y));
-              hi[gr * 4 + j / 4] = e4m3x4(ah.x, ah.y, eh.x, eh.y);
-              lo[gr * 4 + j / 4] = e4m3x4(al.x, al.y, el.x, el.y);
-            }
-            l = fmaf(sum.x + sum.y, c.z, l);
+            for (int j = 0; j < 16; ++j) a = fmaxf(a, gr * 16 + j < left ? __uint_as_float(x[j]) : -INFINITY);
+            const float4 k = cst[gr];
+            top = fmaxf(top, fmaf(a, k.x * qf, k.y));
           }
-          // P V(t - 1) has read P
-          if (half == 0 && t > 0 && !wait(&ofull[g], (t - 1) & 1)) ok = false;
-          tmem_st_x16(tP + half * 16, hi);
-          tmem_st_x16(tP + 32 + half * 16, lo);
+          if (!move_references(anew || most > kTop, anew, top, t)) ok = false;
         }
         if (!ok) break;
+        tmem_st_x16(ts + half * 64, pk[0]);  // over this thread's own scores
+        tmem_st_x16(ts + half * 64 + 16, pk[1]);
       }
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&pfull[g]);
+      if (lane == 0) mbar_arrive(&pfull[g][t % C::kNB]);
     }
-    const bool fin = ok && wait(&ofull[g], (T - 1) & 1);
+    // in turn: the scores of tile T - 1 follow P V(T - 1 - kNB) only, and a wait two phases ahead returns at once
+    const bool fin = ok && (C::kNB == 1 || T < 2 || wait(&ofull[g], (T - 2) & 1)) && wait(&ofull[g], (T - 1) & 1);
     if (!fin && lane == 0) {
       s_abort = 1;
       set_status(p.dev_status, SPEC_ERR_TIMEOUT);
     }
+    s_x[g][half][rl] = l;
     // every MMA of both groups has completed: Q and the rings are free for the O rows
-    named_bar_sync(1, 128 * NG);
+    named_bar_sync(1, 256 * NG);
+    l += s_x[g][half ^ 1][rl];
     const bool valid = row < rows && fin && !s_abort && !s_bad && (live || sp.n == 1);
+    uint8_t* srow = base + rr * C::kORow;
+    const bool whole = sp.n == 1;
     if (fin) {
       tc_fence_after();
-      uint8_t* srow = base + rr * C::kORow;
-      const bool whole = sp.n == 1;
       const float inv = whole ? (live ? 1.f / l : 0.f) : 1.f;
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
+#pragma unroll 1
+      for (int c = half * (D / 64); c < (half + 1) * (D / 64); ++c) {
         uint32_t o[32];
         tmem_ld_x32(tO + c * 32, o);
         tmem_ld_wait();
-        float x[32];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) x[j] = live ? __uint_as_float(o[j]) * inv : 0.f;
+        for (int j = 0; j < 32; ++j) o[j] = live ? __float_as_uint(__uint_as_float(o[j]) * inv) : 0u;
         if (tree && live) {  // V elements of visible tree keys that are no finite numbers
           for (int w = 0; w < kAncWords; ++w)
             for (uint32_t mask = s_odd[w] & anc[w]; mask; mask &= mask - 1) {
@@ -689,7 +748,7 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
 #pragma unroll
               for (int j = 0; j < 32; ++j) {
                 const float f = __uint_as_float((uint32_t)vt[j] << 16);
-                if (!(fabsf(f) < INFINITY)) x[j] += f;
+                if (!(fabsf(f) < INFINITY)) o[j] = __float_as_uint(__uint_as_float(o[j]) + f);
               }
             }
         }
@@ -697,26 +756,29 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 32; j += 8)
             *reinterpret_cast<uint4*>(srow + (c * 32 + j) * 2) =
-                make_uint4(pack_bf16x2(x[j], x[j + 1]), pack_bf16x2(x[j + 2], x[j + 3]), pack_bf16x2(x[j + 4], x[j + 5]),
-                           pack_bf16x2(x[j + 6], x[j + 7]));
+                make_uint4(pack_bf16x2(__uint_as_float(o[j]), __uint_as_float(o[j + 1])),
+                           pack_bf16x2(__uint_as_float(o[j + 2]), __uint_as_float(o[j + 3])),
+                           pack_bf16x2(__uint_as_float(o[j + 4]), __uint_as_float(o[j + 5])),
+                           pack_bf16x2(__uint_as_float(o[j + 6]), __uint_as_float(o[j + 7])));
         } else {
 #pragma unroll
           for (int j = 0; j < 32; j += 4)
-            *reinterpret_cast<float4*>(srow + (c * 32 + j) * 4) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+            *reinterpret_cast<uint4*>(srow + (c * 32 + j) * 4) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
         }
       }
       if (valid) {
         const size_t o = orow_of(row);
-        if (whole) {
-          if (p.lse) p.lse[o] = live ? (m + log2f(l)) * 0.69314718055994531f : 0.f;
-        } else {
-          p.part_ml[o * p.n_split + split] = make_float2(m, l);
+        const uint32_t bytes = (whole ? D * 2 : D * 4) / 2;
+        uint8_t* dst = whole ? reinterpret_cast<uint8_t*>(p.out + o * D)
+                             : reinterpret_cast<uint8_t*>(p.part_o + (o * p.n_split + split) * D);
+        if (half == 0) {
+          if (!whole)
+            p.part_ml[o * p.n_split + split] = make_float2(m, l);
+          else if (p.lse)
+            p.lse[o] = live ? (m + log2f(l)) * 0.69314718055994531f : 0.f;
         }
         fence_proxy_async_smem();
-        if (whole)
-          store_row_bulk(p.out + o * D, srow, D * 2);
-        else
-          store_row_bulk(p.part_o + (o * p.n_split + split) * D, srow, D * 4);
+        store_row_bulk(dst + half * bytes, srow + half * bytes, bytes);
         store_row_wait();
       }
     }
