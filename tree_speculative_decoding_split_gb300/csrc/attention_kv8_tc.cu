@@ -379,29 +379,34 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, &s_abort));
     };
+    // Descriptors: the upper word is constant per layout, the lower one an address in 16-byte units, so that an
+    // MMA's operands are a base and a constant.
+    const uint32_t q16 = (sq0 & 0x3FFFFu) >> 4, k16 = (sk0 & 0x3FFFFu) >> 4, v16 = (sv0 & 0x3FFFFu) >> 4;
+    const uint64_t hi8 = sdesc_kv8<D>(0), hi16 = sdesc_sw128(0, 0, 1024);
+    const uint64_t hiVt = sdesc_sw128(0, kTT * 128, 1024), hiV = sdesc_sw128(0, kKT8 * 128, 1024);
     int kst = 0;        // ring stage of the next S tile, and its parity
     uint32_t kph = 0;
     bool ok = true;
-    auto issue_s = [&](int t, int g) {
+    // what S(t) of group g needs beside its buffer
+    auto ready_s = [&](int t, int g) {
       if (g == 0) ok = ok && wait(&kfull[kst], kph);
       if (t == 0) ok = ok && wait(&qready[g], 0);
       if (t == Tt && Tt > 0) ok = ok && wait(&qready[g], 1);
-      if (!ok) return;
-      tc_fence_after();
+    };
+    auto issue_s = [&](int t, int g) {
       const uint32_t ts = tm + C::kColS + (NG == 2 ? g : t % C::kNB) * 128;
-      const uint32_t qa = sq0 + g * C::kQ, ka = sk0 + kst * C::kSlot;
+      const uint32_t qa = q16 + g * (C::kQ >> 4), ka = k16 + kst * (C::kSlot >> 4);
       if (leader) {
         if (t < Tt) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            umma_bf16(ts, sdesc_sw128(qa + (kk >> 2) * (kGR8 * 128) + (kk & 3) * 32, 0, 1024),
-                      sdesc_sw128(ka + (kk >> 2) * (kTT * 128) + (kk & 3) * 32, 0, 1024), idSt, kk > 0);
+            umma_bf16(ts, hi16 | (qa + (kk >> 2) * (kGR8 * 8) + (kk & 3) * 2),
+                      hi16 | (ka + (kk >> 2) * (kTT * 8) + (kk & 3) * 2), idSt, kk > 0);
         } else {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {  // hi, then lo
             const int k = kk % (D / 32);
-            umma_f8(ts, sdesc_kv8<D>(qa + (kk / (D / 32)) * (kGR8 * D) + k * 32), sdesc_kv8<D>(ka + k * 32), idS8,
-                    kk > 0);
+            umma_f8(ts, hi8 | (qa + (kk / (D / 32)) * (kGR8 * D / 16) + k * 2), hi8 | (ka + k * 2), idS8, kk > 0);
           }
         }
         umma_commit(&sfull[g][t % C::kNB]);
@@ -413,26 +418,21 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
       }
     };
     auto issue_pv = [&](int t, int g) {
-      if (g == 0) ok = ok && wait(&v16full[t % kV16], (t / kV16) & 1);
-      ok = ok && wait(&pfull[g][t % C::kNB], (t / C::kNB) & 1);
-      if (!ok) return;
-      tc_fence_after();
       const uint32_t pt = tm + C::kColS + (NG == 2 ? g : t % C::kNB) * 128, ot = tm + C::kColO + g * 128;
       if (leader) {
         if (t < Tt) {
-          const uint32_t va = sv0 + (t % kVS) * C::kSlot;
+          const uint32_t va = v16 + (t % kVS) * (C::kSlot >> 4);
 #pragma unroll
           for (int kk = 0; kk < kTT / 16; ++kk)
-            umma_bf16_tmem_a(ot, pt + (kk >> 1) * 64 + (kk & 1) * 8, sdesc_sw128(va + kk * 16 * 128, kTT * 128, 1024), idPt,
-                             t > 0 || kk > 0);
+            umma_bf16_tmem_a(ot, pt + (kk >> 1) * 64 + (kk & 1) * 8, hiVt | (va + kk * 128), idPt, t > 0 || kk > 0);
         } else {
-          const uint32_t va = sv0 + kVS * C::kSlot + (t % kV16) * C::kTile16;
+          const uint32_t va = v16 + (kVS * C::kSlot >> 4) + (t % kV16) * (C::kTile16 >> 4);
 #pragma unroll
           for (int kk = 0; kk < kKT8 / 16; ++kk)  // each half's weights lie over its own scores
-            umma_bf16_tmem_a(ot, pt + (kk >> 2) * 64 + (kk & 3) * 8, sdesc_sw128(va + kk * 16 * 128, kKT8 * 128, 1024),
-                             idP16, t > 0 || kk > 0);
+            umma_bf16_tmem_a(ot, pt + (kk >> 2) * 64 + (kk & 3) * 8, hiV | (va + kk * 128), idP16, t > 0 || kk > 0);
         }
-        umma_commit(&ofull[g]);
+        // (with one S buffer the next scores' commit says so too)
+        if (C::kNB > 1 || t == T - 1) umma_commit(&ofull[g]);
         if (g == NG - 1) {
           umma_commit(&v16empty[t % kV16]);
           if (t < Tt) {  // a tree tile's V was read where it landed
@@ -444,13 +444,24 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
     };
     for (int t = 0; t < C::kNB && t < T; ++t)
 #pragma unroll
-      for (int g = 0; g < NG; ++g) issue_s(t, g);
+      for (int g = 0; g < NG; ++g) {
+        ready_s(t, g);
+        tc_fence_after();
+        if (ok) issue_s(t, g);
+      }
     for (int t = 0; t < T && ok; ++t)
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
+        // everything else first: the weights are what comes last, and the chain waits for them
+        const bool more = t + C::kNB < T;
+        if (g == 0) ok = ok && wait(&v16full[t % kV16], (t / kV16) & 1);
+        if (more) ready_s(t + C::kNB, g);
+        ok = ok && wait(&pfull[g][t % C::kNB], (t / C::kNB) & 1);
+        if (!ok) break;
+        tc_fence_after();
         issue_pv(t, g);
         // the buffer's next scores follow in the pipe: MMAs of one thread run in their order
-        if (t + C::kNB < T) issue_s(t + C::kNB, g);
+        if (more) issue_s(t + C::kNB, g);
       }
     if (leader) {
       if (!ok) {
@@ -486,20 +497,30 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
             *at = make_uint4(w[0], w[1], w[2], w[3]);
           }
         } else {
-          // 16 codes of a row -> two 16-byte chunks of the f16 tile (halves of 64 columns); lanes of the second
-          // half write their two in the other order, so that eight lanes meet eight bank groups.  Slots
-          // behind the prefix may hold anything and become 0.
-          uint8_t* dst = sV16 + (t % kV16) * C::kTile16;
+          // 16 codes of a row -> two 16-byte chunks of the f16 tile (halves of 64 columns).  The lanes of the
+          // second half take the row's neighbour, so that eight lanes meet eight bank groups in every access;
+          // a thread's rows are whole swizzle periods apart, so all its addresses are one base plus a constant.
+          constexpr int kSteps = kKT8 * (D / 16) / 64, kSrcStep = 1024, kDstStep = D == 128 ? 1024 : 2048;
+          const int ch = ct % (D / 16), r0 = ct / (D / 16), r = D == 128 ? r0 ^ (ch >> 2) : r0;
+          const uint8_t* from = src + kv8_off<D>(r, ch);
+          uint8_t* to_a = sV16 + (t % kV16) * C::kTile16 + tile16_off(r, 2 * ch, kKT8);
+          uint8_t* to_b = sV16 + (t % kV16) * C::kTile16 + tile16_off(r, 2 * ch + 1, kKT8);
           const int left = (int)min((long long)kKT8, k1 - (k0 + (long long)(t - Tt) * kKT8));
+          auto convert = [&](int i, uint4 x) {
+            *reinterpret_cast<uint4*>(to_a + i * kDstStep) =
+                make_uint4(kv8_f16x2<0>(x.x), kv8_f16x2<1>(x.x), kv8_f16x2<0>(x.y), kv8_f16x2<1>(x.y));
+            *reinterpret_cast<uint4*>(to_b + i * kDstStep) =
+                make_uint4(kv8_f16x2<0>(x.z), kv8_f16x2<1>(x.z), kv8_f16x2<0>(x.w), kv8_f16x2<1>(x.w));
+          };
+          if (left == kKT8) {
 #pragma unroll 4
-          for (int c = ct; c < kKT8 * (D / 16); c += 64) {
-            const int r = c / (D / 16), ch = c % (D / 16), swap = (ch >> 2) & 1;
-            uint4 x = *reinterpret_cast<const uint4*>(src + kv8_off<D>(r, ch));
-            if (r >= left) x = make_uint4(0, 0, 0, 0);
-            const uint4 a = make_uint4(kv8_f16x2<0>(x.x), kv8_f16x2<1>(x.x), kv8_f16x2<0>(x.y), kv8_f16x2<1>(x.y));
-            const uint4 e = make_uint4(kv8_f16x2<0>(x.z), kv8_f16x2<1>(x.z), kv8_f16x2<0>(x.w), kv8_f16x2<1>(x.w));
-            *reinterpret_cast<uint4*>(dst + tile16_off(r, 2 * ch + swap, kKT8)) = swap ? e : a;
-            *reinterpret_cast<uint4*>(dst + tile16_off(r, 2 * ch + (swap ^ 1), kKT8)) = swap ? a : e;
+            for (int i = 0; i < kSteps; ++i) convert(i, *reinterpret_cast<const uint4*>(from + i * kSrcStep));
+          } else {  // slots behind the prefix may hold anything and become 0
+#pragma unroll 1
+            for (int i = 0; i < kSteps; ++i) {
+              const uint4 x = *reinterpret_cast<const uint4*>(from + i * kSrcStep);
+              convert(i, r + i * (64 / (D / 16)) < left ? x : make_uint4(0, 0, 0, 0));
+            }
           }
         }
         fence_proxy_async_smem();
@@ -593,8 +614,8 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
       const float mn = need ? (anew ? fmaxf(ceilf(top), m - 64.f) : ceilf(top)) : m;
       const float f = mn == m ? 1.f : ex2_approx(m - mn);  // 0 when there was none
       named_bar_sync(pair, 64);                            // both have read before either writes again
-      if (t > 0) {  // (these scores follow P V(t - kNB), so this is the phase under way or the one before)
-        if (!wait(&ofull[g], (t - 1) & 1)) return false;
+      if (t > 0) {  // (these scores came after P V(t - kNB); with one buffer there is nothing to wait for)
+        if (C::kNB > 1 && !wait(&ofull[g], (t - 1) & 1)) return false;
         tc_fence_after();
 #pragma unroll 1
         for (int c = half * (D / 64); c < (half + 1) * (D / 64); ++c) {
@@ -718,7 +739,8 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
       if (lane == 0) mbar_arrive(&pfull[g][t % C::kNB]);
     }
     // in turn: the scores of tile T - 1 follow P V(T - 1 - kNB) only, and a wait two phases ahead returns at once
-    const bool fin = ok && (C::kNB == 1 || T < 2 || wait(&ofull[g], (T - 2) & 1)) && wait(&ofull[g], (T - 1) & 1);
+    const bool fin = ok && (C::kNB == 1 || T < 2 || wait(&ofull[g], (T - 2) & 1)) &&
+                     wait(&ofull[g], C::kNB == 1 ? 0 : (T - 1) & 1);
     if (!fin && lane == 0) {
       s_abort = 1;
       set_status(p.dev_status, SPEC_ERR_TIMEOUT);
