@@ -548,7 +548,7 @@ spec_status spec_kv8_append(const spec_kv8_append_args* args, int32_t* dev_statu
  *     outside [0, max_blocks * block_size] or a bad table entry among the prefix's blocks.  The
  *     request's out and lse are then 0, as for padded nodes.
  * Host errors: SPEC_ERR_INVALID_ARGUMENT, SPEC_ERR_UNSUPPORTED (dtype other than bf16, head_dim,
- * block_size, n_max > SPEC_MAX_NODES, B * Hkv > 65535, num_blocks * Hkv >= 2^31, max_blocks *
+ * block_size, n_max > SPEC_MAX_NODES, Hq / Hkv > 256, B * Hkv > 65535, num_blocks * Hkv >= 2^31, max_blocks *
  * block_size >= 2^31), SPEC_ERR_WORKSPACE_TOO_SMALL. */
 typedef struct spec_attn_kv8_args {
   int32_t dtype;            /* of q, k_tree, v_tree and out: SPEC_DTYPE_BF16 */

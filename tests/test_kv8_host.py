@@ -89,7 +89,7 @@ def _attn(**kw):
 @pytest.mark.parametrize("kw,code", [
     (dict(dtype=0), 2), (dict(batch=0), 1), (dict(n_max=0), 1), (dict(n_max=256), 2), (dict(num_q_heads=7), 1),
     (dict(head_dim=256), 2), (dict(block_size=48), 2), (dict(max_blocks=0), 1), (dict(num_blocks=0), 1),
-    (dict(max_blocks=1 << 27), 2), (dict(batch=40000), 2), (dict(q=None), 1), (dict(k_tree=P + 2), 1),
+    (dict(max_blocks=1 << 27), 2), (dict(batch=40000), 2), (dict(num_q_heads=514), 2), (dict(q=None), 1), (dict(k_tree=P + 2), 1),
     (dict(v_tree=None), 1), (dict(k_cache=None), 1), (dict(v_cache=P + 8), 1), (dict(k_scale=None), 1),
     (dict(v_scale=None), 1), (dict(prefix_len=None), 1), (dict(n_nodes=None), 1), (dict(parent=None), 1),
     (dict(block_table=None), 1), (dict(out=P + 8), 1)])

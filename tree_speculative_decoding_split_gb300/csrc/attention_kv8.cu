@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kWarps * 32)
     if (any) err = SPEC_ERR_BAD_TREE;
   }
   // the final rows of a request that is refused, or of padded nodes; with several splits the merge does it
-  auto orow_of = [&](int row) { return ((size_t)b * p.N + row / p.G) * p.Hq + h * p.G + row % p.G; };
+  auto orow_of = [&](int row) { return kv8_row(p, b, h, row); };
   auto refuse = [&]() {
     for (int c = tid; c < kRowsR * (D / 8); c += blockDim.x) {
       const int row = row0 + c / (D / 8), e = c % (D / 8);
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kWarps * 32)
   if (tree && tid < kRowsR) {
 #pragma unroll
     for (int i = 0; i < kAncWords; ++i) s_anc[tid][i] = 0u;
-    const int i = (row0 + tid) / p.G;
+    const int i = kv8_node(p, row0 + tid);
     if (row0 + tid < rows && i < n)
       for (int a = i; a >= 0; a = s_par[a]) s_anc[tid][a >> 5] |= 1u << (a & 31);
   }

@@ -110,14 +110,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-}
 // Two e4m3 codes (the low or high half of `w`) to f16, exactly.
 template <int HALF>
 __device__ __forceinline__ uint32_t kv8_f16x2(uint32_t w) {
@@ -147,14 +139,6 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-
-__device__ __forceinline__ void store_row_bulk(void* gdst, const void* ssrc, uint32_t bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(gdst), "r"(smem_u32(ssrc)),
-               "r"(bytes)
-               : "memory");
-  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
-__device__ __forceinline__ void store_row_wait() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 
 __device__ __forceinline__ bool finite2(uint32_t w) { return (w & 0x7F80u) != 0x7F80u && (w & 0x7F800000u) != 0x7F800000u; }
 
@@ -194,7 +178,7 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
   const Kv8Split sp = kv8_split(L, p.n_split, p.unit_shift);
   if (split >= sp.n) return;
   const int row0 = rt * kRowsCta, rows = p.N * p.G;
-  auto orow_of = [&](int row) { return ((size_t)b * p.N + row / p.G) * p.Hq + h * p.G + row % p.G; };
+  auto orow_of = [&](int row) { return kv8_row(p, b, h, row); };
   // rows of a refused request or of padded nodes; with several splits the merge writes them
   auto refuse = [&]() {
     for (int c = tid; c < kRowsCta * (D / 8); c += C::kThreads) {
@@ -209,6 +193,17 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
       }
     }
   };
+  // the queries, on their way while the checks run: 16 bytes a lane, whole rows side by side
+  constexpr int kQPer = kRowsCta * (D / 8) / (256 * NG);
+  uint4 qv[kQPer];
+  if (warp >= 4) {
+#pragma unroll
+    for (int k = 0; k < kQPer; ++k) {
+      const int c = tid - 128 + k * 256 * NG, row = row0 + c / (D / 8);
+      qv[k] = make_uint4(0, 0, 0, 0);
+      if (row < rows) qv[k] = *reinterpret_cast<const uint4*>(p.q + orow_of(row) * D + (c % (D / 8)) * 8);
+    }
+  }
   if (tid == 0) {
     for (int s = 0; s < kKS; ++s) {
       mbar_init(&kfull[s], 1);
@@ -266,6 +261,14 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
       for (int j = 0; j < kAncWords; ++j) w[j] = 0u;
       for (int a = i; a >= 0; a = s_par[a]) w[a >> 5] |= 1u << (a & 31);
     }
+  if (warp >= 4) {
+#pragma unroll
+    for (int k = 0; k < kQPer; ++k) {
+      const int c = tid - 128 + k * 256 * NG, rr = c / (D / 8);
+      *reinterpret_cast<uint4*>(sQ + (rr / kGR8) * C::kQ + tile16_off(rr % kGR8, c % (D / 8), kGR8)) = qv[k];
+    }
+    fence_proxy_async_smem();
+  }
   if (warp == 1) {
     tmem_alloc(&s_tmem, 512);
     tmem_relinquish();
@@ -390,8 +393,7 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
     // what S(t) of group g needs beside its buffer
     auto ready_s = [&](int t, int g) {
       if (g == 0) ok = ok && wait(&kfull[kst], kph);
-      if (t == 0) ok = ok && wait(&qready[g], 0);
-      if (t == Tt && Tt > 0) ok = ok && wait(&qready[g], 1);
+      if (t == Tt) ok = ok && wait(&qready[g], 0);
     };
     auto issue_s = [&](int t, int g) {
       const uint32_t ts = tm + C::kColS + (NG == 2 ? g : t % C::kNB) * 128;
@@ -544,60 +546,53 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
     const uint32_t tS = tmem + C::kColS + (NG == 2 ? g : 0) * 128 + lane_off;
     const uint32_t tO = tmem + C::kColO + g * 128 + lane_off;
     const bool live = row < n * p.G;
-    const uint16_t* q = p.q + orow_of(live ? row : row0) * D;
     uint8_t* myQ = sQ + g * C::kQ;
     float qf = 0.f;  // undoes the row's scaling, with the softmax scale in log2 units
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, &s_abort));
     };
-    auto load_q = [&](int ch) { return live ? *reinterpret_cast<const uint4*>(q + ch * 8) : make_uint4(0, 0, 0, 0); };
-    auto publish = [&](uint64_t* bar) {  // shared memory written here is for the tensor cores
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar);
-    };
-    // this thread's half of its row's dimensions as e4m3 hi and lo
+    // this thread's half of its row's dimensions, from bf16 to e4m3 hi and lo in the same place
     auto split_q = [&]() {
+      uint4 w[D / 16];
       float mx = 0.f;
-#pragma unroll 4
-      for (int i = 0; i < D / 8; ++i) {
-        const uint4 w = load_q(i);
-        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        w[i] = *reinterpret_cast<const uint4*>(myQ + tile16_off(rl, half * (D / 16) + i, kGR8));
+        const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           mx = max3(mx, fabsf(__uint_as_float(x[j] << 16)), fabsf(__uint_as_float(x[j] & 0xFFFF0000u)));
       }
+      s_x[g][half][rl] = mx;
+      named_bar_sync(10 + g, 256);  // the group has read what it is about to write over
+      mx = fmaxf(mx, s_x[g][half ^ 1][rl]);
       const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 100);
       const float up = __uint_as_float((uint32_t)(127 + 7 - e) << 23);  // largest element into [128, 256)
       qf = __uint_as_float((uint32_t)(127 - 7 + e) << 23) * p.scale_log2;
-#pragma unroll 1
-      for (int i = half * (D / 32); i < (half + 1) * (D / 32); ++i) {
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
         uint32_t hi[4], lo[4];
-        const uint4 w[2] = {load_q(2 * i), load_q(2 * i + 1)};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint4 v = w[j >> 1];
+          const uint4 v = w[2 * i + (j >> 1)];
           const uint32_t a = (j & 1) ? v.z : v.x, c = (j & 1) ? v.w : v.y;
           const float f[4] = {__uint_as_float(a << 16) * up, __uint_as_float(a & 0xFFFF0000u) * up,
                               __uint_as_float(c << 16) * up, __uint_as_float(c & 0xFFFF0000u) * up};
           hi[j] = e4m3x4(head4(f[0]), head4(f[1]), head4(f[2]), head4(f[3]));
           lo[j] = e4m3x4(f[0] - head4(f[0]), f[1] - head4(f[1]), f[2] - head4(f[2]), f[3] - head4(f[3]));
         }
-        *reinterpret_cast<uint4*>(myQ + kv8_off<D>(rl, i)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(myQ + kGR8 * D + kv8_off<D>(rl, i)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        const int ch = half * (D / 32) + i;
+        *reinterpret_cast<uint4*>(myQ + kv8_off<D>(rl, ch)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(myQ + kGR8 * D + kv8_off<D>(rl, ch)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&qready[g]);
     };
-    if (Tt > 0) {
-#pragma unroll 4
-      for (int i = half * (D / 16); i < (half + 1) * (D / 16); ++i)
-        *reinterpret_cast<uint4*>(myQ + tile16_off(rl, i, kGR8)) = load_q(i);
-    } else {
-      split_q();
-    }
-    publish(&qready[g]);
+    if (Tt == 0) split_q();
 
     float m = -INFINITY, l = 0.f;  // the row's reference (P = 2^(y - m)), and the sum over this thread's keys
-    const uint32_t* anc = s_nanc + (live ? row / p.G : 0) * kAncWords;
+    const uint32_t* anc = s_nanc + (live ? kv8_node(p, row) : 0) * kAncWords;
     const int pair = 2 + g * 4 + q4;  // named barrier of the two warps that share rows
     bool ok = true;
     // Moves the references of the rows that ask for it in either of their threads (`ask`, with the largest of
@@ -644,10 +639,7 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
         uint32_t x[32];
         tmem_ld_x32(ts + half * 32, x);
         tmem_ld_wait();
-        if (t == Tt - 1 && T > Tt) {  // the last product with the bf16 queries is done: make room for hi and lo
-          split_q();
-          publish(&qready[g]);
-        }
+        if (t == Tt - 1 && T > Tt) split_q();  // the last product with the bf16 queries is done
         const uint32_t bits = live ? anc[2 * t + half] : 0u;
         float top = -INFINITY;
 #pragma unroll
@@ -675,7 +667,29 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
         // -- a prefix tile: this thread's 64 keys are 4 groups of 16, each within one block --
         const int left = (int)min((long long)kKT8, k1 - (k0 + (long long)(t - Tt) * kKT8)) - half * 64;
         const float4* cst = s_cst + (t % kCS) * 8 + half * 4;
-        bool anew = t == Tt && t > 0;
+        // the largest of this thread's scores
+        auto largest = [&]() {
+          float top = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            uint32_t x[32];
+            tmem_ld_x32(ts + half * 64 + c * 32, x);
+            tmem_ld_wait();
+#pragma unroll
+            for (int gr = 0; gr < 2; ++gr) {
+              float a = -INFINITY;
+#pragma unroll
+              for (int j = gr * 16; j < gr * 16 + 16; ++j) a = fmaxf(a, c * 32 + j < left ? __uint_as_float(x[j]) : -INFINITY);
+              const float4 k = cst[c * 2 + gr];
+              top = fmaxf(top, fmaf(a, k.x * qf, k.y));
+            }
+          }
+          return top;
+        };
+        if (t == Tt && !move_references(true, true, largest(), t)) {
+          ok = false;
+          break;
+        }
         uint32_t pk[2][16];
         for (int pass = 0; pass < 2; ++pass) {
           float part = 0.f, most = 0.f;  // sum of the weights over the V scales; largest sum of sixteen
@@ -709,25 +723,12 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
               part = fmaf(s16, k.z, part);
             }
           }
-          if (pass == 1 || !bar_or(pair, 64, anew || most > kTop)) {
+          if (pass == 1 || !bar_or(pair, 64, most > kTop)) {
             l += part;
             break;
           }
-          // -- a weight may have left f16's range (or there is no reference yet): find the largest scores,
-          // move the references, and take the weights again --
-          float top = -INFINITY;
-#pragma unroll 1
-          for (int gr = 0; gr < 4; ++gr) {
-            uint32_t x[16];
-            tmem_ld_x16(ts + half * 64 + gr * 16, x);
-            tmem_ld_wait();
-            float a = -INFINITY;
-#pragma unroll
-            for (int j = 0; j < 16; ++j) a = fmaxf(a, gr * 16 + j < left ? __uint_as_float(x[j]) : -INFINITY);
-            const float4 k = cst[gr];
-            top = fmaxf(top, fmaf(a, k.x * qf, k.y));
-          }
-          if (!move_references(anew || most > kTop, anew, top, t)) ok = false;
+          // a weight may have left f16's range: move the references and take the weights again
+          if (!move_references(most > kTop, false, largest(), t)) ok = false;
         }
         if (!ok) break;
         tmem_st_x16(ts + half * 64, pk[0]);  // over this thread's own scores
@@ -788,20 +789,27 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
             *reinterpret_cast<uint4*>(srow + (c * 32 + j) * 4) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
         }
       }
-      if (valid) {
+      if (valid && half == 0) {
         const size_t o = orow_of(row);
-        const uint32_t bytes = (whole ? D * 2 : D * 4) / 2;
-        uint8_t* dst = whole ? reinterpret_cast<uint8_t*>(p.out + o * D)
-                             : reinterpret_cast<uint8_t*>(p.part_o + (o * p.n_split + split) * D);
-        if (half == 0) {
-          if (!whole)
-            p.part_ml[o * p.n_split + split] = make_float2(m, l);
-          else if (p.lse)
-            p.lse[o] = live ? (m + log2f(l)) * 0.69314718055994531f : 0.f;
-        }
-        fence_proxy_async_smem();
-        store_row_bulk(dst + half * bytes, srow + half * bytes, bytes);
-        store_row_wait();
+        if (!whole)
+          p.part_ml[o * p.n_split + split] = make_float2(m, l);
+        else if (p.lse)
+          p.lse[o] = live ? (m + log2f(l)) * 0.69314718055994531f : 0.f;
+      }
+    }
+    // rows leave 16 bytes a lane, a row's lanes side by side
+    named_bar_sync(1, 256 * NG);
+    if (!s_abort && !s_bad) {
+      const int vshift = whole ? (D == 128 ? 4 : 3) : (D == 128 ? 5 : 4), live_rows = whole ? rows : n * p.G;
+      for (int c = tid - 128; c < kRowsCta << vshift; c += 256 * NG) {
+        const int r = c >> vshift, e = c & ((1 << vshift) - 1);
+        if (row0 + r >= live_rows) break;
+        const size_t o = orow_of(row0 + r);
+        const uint4 x = *reinterpret_cast<const uint4*>(base + r * C::kORow + e * 16);
+        if (whole)
+          *reinterpret_cast<uint4*>(p.out + o * D + e * 8) = x;
+        else
+          *reinterpret_cast<uint4*>(p.part_o + (o * p.n_split + split) * D + e * 4) = x;
       }
     }
   }

@@ -285,6 +285,7 @@ struct Kv8AttnParams {
   int B, N, Hq, Hkv, G, d, bs, bs_shift, max_blocks, num_blocks;
   long long L_cap;
   int n_split;            // key splits at most; a request uses as many as its own length fills
+  uint32_t g_magic;       // floor(2^32 / G) + 1 (G > 1): row / G = umulhi(row, g_magic) while row * G < 2^32
   int unit_shift;         // splits are whole steps of 2^unit_shift keys
   int n_rt;               // row tiles of (node, head) rows per KV head
   float scale_log2;

@@ -29,6 +29,15 @@ __host__ __device__ __forceinline__ Kv8Split kv8_split(long long len, int n_spli
   return s;
 }
 
+// Index of row (node row / G, head h G + row % G) of request b in [B][N][Hq].
+__device__ __forceinline__ int kv8_node(const Kv8AttnParams& p, int row) {
+  return p.G == 1 ? row : (int)__umulhi((uint32_t)row, p.g_magic);
+}
+__device__ __forceinline__ size_t kv8_row(const Kv8AttnParams& p, int b, int h, int row) {
+  const int i = kv8_node(p, row);
+  return ((size_t)b * p.N + i) * p.Hq + h * p.G + (row - i * p.G);
+}
+
 // Verdict on request b from its counts alone; `len` is the prefix length every kernel goes on with.
 __device__ __forceinline__ int kv8_counts(const Kv8AttnParams& p, int b, long long* len, int* n) {
   *len = p.prefix_len[b];

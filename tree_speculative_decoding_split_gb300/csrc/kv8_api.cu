@@ -84,6 +84,7 @@ spec_status check_attn_kv8(const spec_attn_kv8_args* a) {
   if (ps != SPEC_OK) return ps;
   if ((long long)a->max_blocks * a->block_size > 0x7fffffffLL - 128) return SPEC_ERR_UNSUPPORTED;
   if ((long long)a->n_max * a->num_q_heads * a->batch > 0x7fffffffLL) return SPEC_ERR_UNSUPPORTED;
+  if (a->num_q_heads / a->num_kv_heads > 256) return SPEC_ERR_UNSUPPORTED;
   if (!a->q || !a->k_tree || !a->v_tree || !a->k_cache || !a->v_cache || !a->k_scale || !a->v_scale || !a->prefix_len ||
       !a->n_nodes || !a->parent || !a->block_table || !a->out)
     return SPEC_ERR_INVALID_ARGUMENT;
@@ -163,6 +164,7 @@ spec_status spec_tree_attention_kv8(const spec_attn_kv8_args* a, void* workspace
   p.part_o = l.part_o; p.part_ml = l.part_ml;
   p.dev_status = dev_status;
   p.B = a->batch; p.N = a->n_max; p.Hq = a->num_q_heads; p.Hkv = a->num_kv_heads; p.G = p.Hq / p.Hkv;
+  p.g_magic = p.G > 1 ? (uint32_t)((1ull << 32) / (uint32_t)p.G) + 1u : 0u;
   p.d = a->head_dim; p.bs = a->block_size; p.bs_shift = log2_of(a->block_size);
   p.max_blocks = a->max_blocks; p.num_blocks = a->num_blocks;
   p.L_cap = (long long)a->max_blocks * a->block_size;
