@@ -25,6 +25,8 @@
 // Tried and slower (63-node trees, batch 32 at 4K): P as e4m3 pairs with 128 keys a thread, four warps per
 // group and a row maximum ahead of the weights, 238 us; with one S buffer shared by both groups and all
 // descriptors in uniform registers, 203 us; with two threads per row, 211 us.
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.cuh"
 #include "kv8.cuh"
@@ -159,9 +161,9 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
   uint8_t* sV16 = sV + kVS * C::kSlot;
   uint32_t* s_nanc = reinterpret_cast<uint32_t*>(sV16 + kV16 * C::kTile16);  // [node][word] ancestors-or-self
   float4* s_cst = reinterpret_cast<float4*>(s_nanc + (kMaxNodes + 1) * kAncWords);  // [stage][16-key group]
-  __shared__ uint64_t kfull[kKS], kempty[kKS], vfull[kVS], vempty[kVS], v16full[kV16], v16empty[kV16];
+  __shared__ uint64_t kfull[kKS], kempty[kKS], vfull[kVS], vempty[kVS], v16empty[kV16];
   // per group, and per buffer where there are two (one barrier could be two phases on)
-  __shared__ uint64_t sfull[NG][C::kNB], pfull[NG][C::kNB], ofull[NG], qready[NG];
+  __shared__ uint64_t sfull[NG][C::kNB], pfull[NG][2], ofull[NG], qready[NG];
   __shared__ float s_x[NG][2][kGR8];  // a row's threads tell each other their largest score; at the end, their sums
   __shared__ uint32_t s_w[NG][2][4];  // ... and which of the warp's rows move
   __shared__ uint64_t s_drained;
@@ -214,14 +216,14 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
       mbar_init(&vempty[s], 2);
     }
     for (int s = 0; s < kV16; ++s) {
-      mbar_init(&v16full[s], 2);
       mbar_init(&v16empty[s], 1);
     }
     for (int g = 0; g < NG; ++g) {
       for (int i = 0; i < C::kNB; ++i) {
         mbar_init(&sfull[g][i], 1);
-        mbar_init(&pfull[g][i], 8);
       }
+      // a tile's weights are there; for group 0 also its V, and the keys of the scores that follow
+      for (int i = 0; i < 2; ++i) mbar_init(&pfull[g][i], g == 0 ? 10 : 8);
       mbar_init(&ofull[g], 1);
       mbar_init(&qready[g], 8);
     }
@@ -379,27 +381,20 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
     const uint32_t sq0 = __shfl_sync(0xffffffffu, smem_u32(sQ), 0);
     const uint32_t sk0 = sq0 + NG * C::kQ, sv0 = sk0 + kKS * C::kSlot;
     const bool leader = elect_one();
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-      return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, &s_abort));
-    };
     // Descriptors: the upper word is constant per layout, the lower one an address in 16-byte units, so that an
     // MMA's operands are a base and a constant.
     const uint32_t q16 = (sq0 & 0x3FFFFu) >> 4, k16 = (sk0 & 0x3FFFFu) >> 4, v16 = (sv0 & 0x3FFFFu) >> 4;
     const uint64_t hi8 = sdesc_kv8<D>(0), hi16 = sdesc_sw128(0, 0, 1024);
     const uint64_t hiVt = sdesc_sw128(0, kTT * 128, 1024), hiV = sdesc_sw128(0, kKT8 * 128, 1024);
-    int kst = 0;        // ring stage of the next S tile, and its parity
-    uint32_t kph = 0;
-    bool ok = true;
-    // what S(t) of group g needs beside its buffer
-    auto ready_s = [&](int t, int g) {
-      if (g == 0) ok = ok && wait(&kfull[kst], kph);
-      if (t == Tt) ok = ok && wait(&qready[g], 0);
+    auto wait = [&](uint64_t* bar, uint32_t parity) {  // (one instruction for the warp: its lanes agree)
+      return mbar_try_wait(bar, parity) || mbar_wait_bounded(bar, parity, &s_abort);
     };
-    auto issue_s = [&](int t, int g) {
+    int kst = 0;  // ring stage of the next S tile
+    auto issue_s = [&](auto tree_tile, int t, int g) {
       const uint32_t ts = tm + C::kColS + (NG == 2 ? g : t % C::kNB) * 128;
       const uint32_t qa = q16 + g * (C::kQ >> 4), ka = k16 + kst * (C::kSlot >> 4);
       if (leader) {
-        if (t < Tt) {
+        if constexpr (tree_tile.value) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
             umma_bf16(ts, hi16 | (qa + (kk >> 2) * (kGR8 * 8) + (kk & 3) * 2),
@@ -414,15 +409,12 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
         umma_commit(&sfull[g][t % C::kNB]);
         if (g == NG - 1) umma_commit(&kempty[kst]);
       }
-      if (g == NG - 1 && ++kst == kKS) {
-        kst = 0;
-        kph ^= 1;
-      }
+      if (g == NG - 1 && ++kst == kKS) kst = 0;
     };
-    auto issue_pv = [&](int t, int g) {
+    auto issue_pv = [&](auto tree_tile, int t, int g) {
       const uint32_t pt = tm + C::kColS + (NG == 2 ? g : t % C::kNB) * 128, ot = tm + C::kColO + g * 128;
       if (leader) {
-        if (t < Tt) {
+        if constexpr (tree_tile.value) {
           const uint32_t va = v16 + (t % kVS) * (C::kSlot >> 4);
 #pragma unroll
           for (int kk = 0; kk < kTT / 16; ++kk)
@@ -437,34 +429,46 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
         if (C::kNB > 1 || t == T - 1) umma_commit(&ofull[g]);
         if (g == NG - 1) {
           umma_commit(&v16empty[t % kV16]);
-          if (t < Tt) {  // a tree tile's V was read where it landed
+          if constexpr (tree_tile.value) {  // a tree tile's V was read where it landed
             umma_commit(&vempty[t % kVS]);
             umma_commit(&vempty[t % kVS]);
           }
         }
       }
     };
-    for (int t = 0; t < C::kNB && t < T; ++t)
+    // P V(t), then the buffer's next scores: MMAs of one thread run in their order
+    auto step = [&](auto pv_tree, auto s_tree, int t) -> bool {
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
-        ready_s(t, g);
+        if (!wait(&pfull[g][t & 1], (t >> 1) & 1)) return false;
+        if (t + C::kNB == Tt && Tt < T && !wait(&qready[g], 0)) return false;
         tc_fence_after();
-        if (ok) issue_s(t, g);
+        issue_pv(pv_tree, t, g);
+        if (t + C::kNB < T) issue_s(s_tree, t + C::kNB, g);
       }
-    for (int t = 0; t < T && ok; ++t)
-#pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        // everything else first: the weights are what comes last, and the chain waits for them
-        const bool more = t + C::kNB < T;
-        if (g == 0) ok = ok && wait(&v16full[t % kV16], (t / kV16) & 1);
-        if (more) ready_s(t + C::kNB, g);
-        ok = ok && wait(&pfull[g][t % C::kNB], (t / C::kNB) & 1);
-        if (!ok) break;
-        tc_fence_after();
-        issue_pv(t, g);
-        // the buffer's next scores follow in the pipe: MMAs of one thread run in their order
-        if (more) issue_s(t + C::kNB, g);
+      return true;
+    };
+    using Yes = std::true_type;
+    using No = std::false_type;
+    auto run = [&]() -> bool {
+      for (int t = 0; t < C::kNB && t < T; ++t) {
+        if (!wait(&kfull[t % kKS], 0)) return false;
+        for (int g = 0; g < NG; ++g) {
+          if (t == Tt && !wait(&qready[g], 0)) return false;
+          tc_fence_after();
+          if (t < Tt) issue_s(Yes(), t, g); else issue_s(No(), t, g);
+        }
       }
+      int t = 0;
+      for (; t < Tt - C::kNB; ++t)
+        if (!step(Yes(), Yes(), t)) return false;
+      for (; t < Tt; ++t)
+        if (!step(Yes(), No(), t)) return false;
+      for (; t < T; ++t)
+        if (!step(No(), No(), t)) return false;
+      return true;
+    };
+    const bool ok = run();
     if (leader) {
       if (!ok) {
         s_abort = 1;
@@ -527,10 +531,15 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&v16full[t % kV16]);
-          if (t >= Tt) mbar_arrive(&vempty[t % kVS]);
+        if (lane == 0 && t >= Tt) mbar_arrive(&vempty[t % kVS]);
+        // with V goes the word that the keys of the next scores are there: the issuer has one wait per group
+        const int tn = t + C::kNB;
+        if (tn < T) {
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(&kfull[tn % kKS], (tn / kKS) & 1, &s_abort));
+          if (!ok) break;
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pfull[0][t & 1]);
       }
       if (!ok && lane == 0) {
         s_abort = 1;
@@ -737,7 +746,7 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&pfull[g][t % C::kNB]);
+      if (lane == 0) mbar_arrive(&pfull[g][t & 1]);
     }
     // in turn: the scores of tile T - 1 follow P V(T - 1 - kNB) only, and a wait two phases ahead returns at once
     const bool fin = ok && (C::kNB == 1 || T < 2 || wait(&ofull[g], (T - 2) & 1)) &&
