@@ -202,9 +202,15 @@ def _check(code, where):
 
 # ---- torch marshalling (torch is used for device memory and streams only) ---------------------
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t):
@@ -707,14 +713,46 @@ def eagle_tree(score, token, parent, n_max, draft_to_target=None, root_token=Non
 
 
 # ---- the 8-bit paged cache ---------------------------------------------------------------------
+# These calls come once per layer and token, so their marshalling is kept short: one test per tensor (the
+# full checks of _need run only where it fails, and say why), plain addresses instead of pointer objects,
+# no status buffer when the caller passes none.
 
-def _kept_for(stream, *tensors):
-    """Tensors made here for a call on ``stream``: the allocator must not hand their memory out again
-    before that stream is done with it."""
-    if stream is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+def _fast(t, name, dtype, device):
+    """_need(t, name, dtype, device), returning the tensor's address."""
+    if getattr(t, "dtype", None) is not dtype or t.device != device or not t.is_contiguous():
+        _need(t, name, dtype, device)
+    return t.data_ptr()
+
+
+class _On:
+    """The device and stream a call goes to: ``stream`` or the device's current one; tensors made by the
+    call are kept from reuse until a stream of the caller's is done with them."""
+    __slots__ = ("guard", "raw", "stream")
+
+    def __init__(self, device, stream):
+        torch = _torch()
+        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+        self.stream = stream
+        self.raw = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+    def keep(self, *tensors):
+        if self.stream is not None:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(self.stream)
+
+
+def _status_ptr(dev_status, device):
+    return None if dev_status is None else _fast(dev_status, "dev_status", _torch().int32, device)
 
 
 def kv_reserve_args(seq_len, n_new, block_table, n_blocks, free_list, free_count, block_size, slot_cap=None,
@@ -723,29 +761,27 @@ def kv_reserve_args(seq_len, n_new, block_table, n_blocks, free_list, free_count
     row_start)."""
     torch = _torch()
     _need(block_table, "block_table", torch.int32)
-    dev = block_table.device
-    for name, t in (("seq_len", seq_len), ("n_new", n_new), ("n_blocks", n_blocks), ("free_list", free_list),
-                    ("free_count", free_count)):
-        _need(t, name, torch.int32, dev)
+    dev, i32 = block_table.device, torch.int32
     if block_table.dim() != 2:
         raise ValueError("block_table must be [B][max_blocks]")
     B, max_blocks = block_table.shape
+    ptr = [_fast(seq_len, "seq_len", i32, dev), _fast(n_new, "n_new", i32, dev), block_table.data_ptr(),
+           _fast(n_blocks, "n_blocks", i32, dev), _fast(free_list, "free_list", i32, dev),
+           _fast(free_count, "free_count", i32, dev)]
     if seq_len.numel() != B or n_new.numel() != B or n_blocks.numel() != B or free_count.numel() != 1:
         raise ValueError("seq_len, n_new and n_blocks must be [B], free_count [1]")
     if slot_map is None and slot_cap is not None:
         slot_map = torch.empty(int(slot_cap), dtype=torch.int64, device=dev)
+    slots = 0
     if slot_map is not None:
-        _need(slot_map, "slot_map", torch.int64, dev)
+        _fast(slot_map, "slot_map", torch.int64, dev)
+        slots = slot_map.numel()
     if row_start is None:
-        row_start = torch.empty(B + 1, dtype=torch.int32, device=dev)
-    _need(row_start, "row_start", torch.int32, dev)
-    if row_start.numel() != B + 1:
+        row_start = torch.empty(B + 1, dtype=i32, device=dev)
+    elif row_start.numel() != B + 1:
         raise ValueError("row_start must be [B + 1]")
-    slots = slot_map if slot_map is not None and slot_map.numel() > 0 else None
-    a = KvReserveArgs(batch=B, block_size=int(block_size), max_blocks=max_blocks, num_blocks=free_list.numel(),
-                      slot_cap=0 if slots is None else slots.numel(), seq_len=_ptr(seq_len), n_new=_ptr(n_new),
-                      block_table=_ptr(block_table), n_blocks=_ptr(n_blocks), free_list=_ptr(free_list),
-                      free_count=_ptr(free_count), slot_map=_ptr(slots), row_start=_ptr(row_start))
+    a = KvReserveArgs(B, int(block_size), max_blocks, free_list.numel(), slots, *ptr,
+                      slot_map.data_ptr() if slots else None, _fast(row_start, "row_start", i32, dev))
     return a, slot_map, row_start
 
 
@@ -755,27 +791,30 @@ def kv_reserve(seq_len, n_new, block_table, n_blocks, free_list, free_count, blo
     free blocks, in place (see spec_kv_reserve).  ``slot_cap`` (a bound on the sum of n_new the host
     knows) or ``slot_map`` asks for the pool row of every new row.  Returns (slot_map, row_start);
     slot_map is None when neither is given."""
-    torch = _torch()
     a, slot_map, row_start = kv_reserve_args(seq_len, n_new, block_table, n_blocks, free_list, free_count, block_size,
                                              slot_cap, slot_map, row_start)
-    with torch.cuda.device(block_table.device):
-        st = _status_buffer(dev_status, block_table.device)
-        _check(lib().spec_kv_reserve(ctypes.byref(a), _ptr(st), _stream(stream)), "spec_kv_reserve")
-        _kept_for(stream, st, slot_map, row_start)
+    dev = block_table.device
+    with _On(dev, stream) as on:
+        _check(lib().spec_kv_reserve(ctypes.byref(a), _status_ptr(dev_status, dev), on.raw), "spec_kv_reserve")
+        on.keep(slot_map, row_start)
     return slot_map, row_start
 
 
 def _kv8_pools(k_cache, v_cache, k_scale, v_scale, block_table, B, dev):
+    """(addresses of the pools and scales), (block_size, max_blocks, num_blocks, Hkv)"""
     torch = _torch()
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _need(t, name, torch.float8_e4m3fn, dev)
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+    f8, f32 = torch.float8_e4m3fn, torch.float32
+    ptr = (_fast(k_cache, "k_cache", f8, dev), _fast(v_cache, "v_cache", f8, dev), _fast(k_scale, "k_scale", f32, dev),
+           _fast(v_scale, "v_scale", f32, dev))
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("pools must be [num_blocks][Hkv][block_size][d]")
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        _need(t, name, torch.float32, dev)
-        if tuple(t.shape) != tuple(k_cache.shape[:2]):
-            raise ValueError(f"{name} must be [num_blocks][Hkv]")
-    return _paged(k_cache, block_table, B, dev)
+    if k_scale.shape != shape[:2] or v_scale.shape != shape[:2]:
+        raise ValueError("k_scale and v_scale must be [num_blocks][Hkv]")
+    _fast(block_table, "block_table", torch.int32, dev)
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [B][max_blocks]")
+    return ptr, (shape[2], block_table.shape[1], shape[0], shape[1])
 
 
 def kv8_append_args(k_new, v_new, k_cache, v_cache, k_scale, v_scale, seq_len, block_table, row_start=None, path=None,
@@ -783,40 +822,32 @@ def kv8_append_args(k_new, v_new, k_cache, v_cache, k_scale, v_scale, seq_len, b
     """Build the C argument struct for kv8_append (tensors are validated here); returns (args, new_len)."""
     torch = _torch()
     _need(k_new, "k_new")
-    dev = k_new.device
-    _need(v_new, "v_new", k_new.dtype, dev)
-    _need(seq_len, "seq_len", torch.int32, dev)
+    dev, i32 = k_new.device, torch.int32
+    new = (k_new.data_ptr(), _fast(v_new, "v_new", k_new.dtype, dev))
+    lens = _fast(seq_len, "seq_len", i32, dev)
     B = seq_len.numel()
-    bs, max_blocks, nb, Hkv = _kv8_pools(k_cache, v_cache, k_scale, v_scale, block_table, B, dev)
+    pools, (bs, max_blocks, nb, Hkv) = _kv8_pools(k_cache, v_cache, k_scale, v_scale, block_table, B, dev)
     d = k_cache.shape[3]
     if v_new.shape != k_new.shape or tuple(k_new.shape[-2:]) != (Hkv, d):
         raise ValueError("k_new and v_new must be [...][Hkv][d]")
     n_max = path_cap = n_rows = 0
     if path is not None:
-        _need(path, "path", torch.int32, dev)
-        _need(accept_len, "accept_len", torch.int32, dev)
-        if row_start is not None or k_new.dim() != 4 or k_new.shape[0] != B or path.dim() != 2 or \
+        if row_start is not None or accept_len is None or k_new.dim() != 4 or k_new.shape[0] != B or path.dim() != 2 or \
                 path.shape[0] != B or accept_len.numel() != B:
             raise ValueError("path [B][path_cap] and accept_len [B] go with rows [B][N][Hkv][d] and no row_start")
+        source = (None, _fast(path, "path", i32, dev), _fast(accept_len, "accept_len", i32, dev))
         n_max, path_cap = k_new.shape[1], path.shape[1]
     else:
-        if row_start is None or accept_len is not None or k_new.dim() != 3:
+        if row_start is None or accept_len is not None or k_new.dim() != 3 or row_start.numel() != B + 1:
             raise ValueError("packed rows [n_rows][Hkv][d] go with row_start [B + 1]")
-        _need(row_start, "row_start", torch.int32, dev)
-        if row_start.numel() != B + 1:
-            raise ValueError("row_start must be [B + 1]")
+        source = (_fast(row_start, "row_start", i32, dev), None, None)
         n_rows = k_new.shape[0]
     if new_len is None:
-        new_len = torch.empty(B, dtype=torch.int32, device=dev)
-    _need(new_len, "new_len", torch.int32, dev)
-    if new_len.numel() != B:
+        new_len = torch.empty(B, dtype=i32, device=dev)
+    elif new_len.numel() != B:
         raise ValueError("new_len must be [B]")
-    a = Kv8AppendArgs(dtype=_dtype_code(k_new), batch=B, num_kv_heads=Hkv, head_dim=d, block_size=bs,
-                      max_blocks=max_blocks, num_blocks=nb, n_max=n_max, path_cap=path_cap, reserved0=0, n_rows=n_rows,
-                      k_new=_ptr(k_new), v_new=_ptr(v_new), row_start=_ptr(row_start), path=_ptr(path),
-                      accept_len=_ptr(accept_len), seq_len=_ptr(seq_len), block_table=_ptr(block_table),
-                      k_cache=_ptr(k_cache), v_cache=_ptr(v_cache), k_scale=_ptr(k_scale), v_scale=_ptr(v_scale),
-                      new_len=_ptr(new_len))
+    a = Kv8AppendArgs(_dtype_code(k_new), B, Hkv, d, bs, max_blocks, nb, n_max, path_cap, 0, n_rows, *new, *source, lens,
+                      block_table.data_ptr(), *pools, _fast(new_len, "new_len", i32, dev))
     return a, new_len
 
 
@@ -826,15 +857,14 @@ def kv8_append(k_new, v_new, k_cache, v_cache, k_scale, v_scale, seq_len, block_
     ``row_start`` [B + 1], or a tree's rows [B][N][Hkv][d] along ``path`` / ``accept_len`` (the outputs of
     verify_accept).  Pools are float8_e4m3fn [num_blocks][Hkv][block_size][d], scales float32
     [num_blocks][Hkv].  Returns new_len."""
-    torch = _torch()
     a, new_len = kv8_append_args(k_new, v_new, k_cache, v_cache, k_scale, v_scale, seq_len, block_table, row_start,
                                  path, accept_len, new_len)
-    if k_new.numel() == 0 and path is None:  # no rows at all: no pointer to pass
-        return new_len.copy_(seq_len)
-    with torch.cuda.device(k_new.device):
-        st = _status_buffer(dev_status, k_new.device)
-        _check(lib().spec_kv8_append(ctypes.byref(a), _ptr(st), _stream(stream)), "spec_kv8_append")
-        _kept_for(stream, st, new_len)
+    dev = k_new.device
+    if k_new.numel() == 0:  # no rows: the pools are not looked at, any address does
+        a.k_new = a.v_new = a.k_cache
+    with _On(dev, stream) as on:
+        _check(lib().spec_kv8_append(ctypes.byref(a), _status_ptr(dev_status, dev), on.raw), "spec_kv8_append")
+        on.keep(new_len)
     return new_len
 
 
@@ -844,32 +874,28 @@ def attn_kv8_args(q, k_tree, v_tree, k_cache, v_cache, k_scale, v_scale, prefix_
     lse)."""
     torch = _torch()
     _need(q, "q")
-    dev = q.device
-    for name, t in (("k_tree", k_tree), ("v_tree", v_tree)):
-        _need(t, name, q.dtype, dev)
-    for name, t in (("prefix_len", prefix_len), ("n_nodes", n_nodes), ("parent", parent)):
-        _need(t, name, torch.int32, dev)
+    dev, dtype, i32 = q.device, q.dtype, torch.int32
     if q.dim() != 4:
         raise ValueError("q must be [B][N][Hq][d]")
     B, N, Hq, d = q.shape
-    bs, max_blocks, nb, Hkv = _kv8_pools(k_cache, v_cache, k_scale, v_scale, block_table, B, dev)
+    tree = (_fast(k_tree, "k_tree", dtype, dev), _fast(v_tree, "v_tree", dtype, dev))
+    pools, (bs, max_blocks, nb, Hkv) = _kv8_pools(k_cache, v_cache, k_scale, v_scale, block_table, B, dev)
     if k_cache.shape[3] != d or tuple(k_tree.shape) != (B, N, Hkv, d) or v_tree.shape != k_tree.shape:
         raise ValueError("k_tree and v_tree must be [B][N][Hkv][d], with the pools' d")
+    counts = (_fast(prefix_len, "prefix_len", i32, dev), _fast(n_nodes, "n_nodes", i32, dev),
+              _fast(parent, "parent", i32, dev))
     if tuple(parent.shape) != (B, N) or prefix_len.numel() != B or n_nodes.numel() != B:
         raise ValueError("parent must be [B][N], prefix_len and n_nodes [B]")
     if out is None:
         out = torch.empty_like(q)
+    elif out.shape != q.shape:
+        raise ValueError("out must be [B][N][Hq][d]")
     if lse is None:
         lse = torch.empty((B, N, Hq), dtype=torch.float32, device=dev)
-    _need(out, "out", q.dtype, dev)
-    _need(lse, "lse", torch.float32, dev)
-    if out.shape != q.shape or tuple(lse.shape) != (B, N, Hq):
-        raise ValueError("out must be [B][N][Hq][d] and lse [B][N][Hq]")
-    a = AttnKv8Args(dtype=_dtype_code(q), batch=B, n_max=N, num_q_heads=Hq, num_kv_heads=Hkv, head_dim=d, block_size=bs,
-                    max_blocks=max_blocks, num_blocks=nb, scale=float(scale), q=_ptr(q), k_tree=_ptr(k_tree),
-                    v_tree=_ptr(v_tree), k_cache=_ptr(k_cache), v_cache=_ptr(v_cache), k_scale=_ptr(k_scale),
-                    v_scale=_ptr(v_scale), prefix_len=_ptr(prefix_len), n_nodes=_ptr(n_nodes), parent=_ptr(parent),
-                    block_table=_ptr(block_table), out=_ptr(out), lse=_ptr(lse))
+    elif tuple(lse.shape) != (B, N, Hq):
+        raise ValueError("lse must be [B][N][Hq]")
+    a = AttnKv8Args(_dtype_code(q), B, N, Hq, Hkv, d, bs, max_blocks, nb, float(scale), q.data_ptr(), *tree, *pools,
+                    *counts, block_table.data_ptr(), _fast(out, "out", dtype, dev), _fast(lse, "lse", torch.float32, dev))
     return a, out, lse
 
 
@@ -877,17 +903,15 @@ def tree_attention_kv8(q, k_tree, v_tree, k_cache, v_cache, k_scale, v_scale, pr
                        out=None, lse=None, scale=0.0, workspace=None, dev_status=None, stream=None):
     """Tree attention over the 8-bit paged prefix and the tree's own K/V rows (see
     spec_tree_attention_kv8); N = 1 is decoding of single tokens.  Returns (out, lse)."""
-    torch = _torch()
     a, out, lse = attn_kv8_args(q, k_tree, v_tree, k_cache, v_cache, k_scale, v_scale, prefix_len, n_nodes, parent,
                                 block_table, out, lse, scale)
-    L = lib()
-    with torch.cuda.device(q.device):
-        need = L.spec_tree_attention_kv8_workspace(ctypes.byref(a))
+    L, dev, ref = lib(), q.device, ctypes.byref(a)
+    with _On(dev, stream) as on:
+        need = L.spec_tree_attention_kv8_workspace(ref)
         if need == 0:
-            _check(L.spec_tree_attention_kv8(ctypes.byref(a), None, 0, None, None), "spec_tree_attention_kv8")
-        ws = _workspace(need, q.device, workspace)
-        st = _status_buffer(dev_status, q.device)
-        _check(L.spec_tree_attention_kv8(ctypes.byref(a), _ptr(ws), need, _ptr(st), _stream(stream)),
+            _check(L.spec_tree_attention_kv8(ref, None, 0, None, None), "spec_tree_attention_kv8")
+        ws = _workspace(need, dev, workspace)
+        _check(L.spec_tree_attention_kv8(ref, ws.data_ptr(), need, _status_ptr(dev_status, dev), on.raw),
                "spec_tree_attention_kv8")
-        _kept_for(stream, ws, st, out, lse)
+        on.keep(ws, out, lse)
     return out, lse
