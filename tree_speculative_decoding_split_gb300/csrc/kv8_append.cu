@@ -4,6 +4,8 @@
 // max |x| <= 448 * 2^e; a code is e4m3(x / s).  Both steps need the whole block, which fits the
 // registers of one group of threads: the group loads the block's new rows once, reduces |x| to the
 // maximum, and converts what it holds.  So the rows are read once and the codes written once: HBM-bound.
+// A CTA goes through the heads of its block one after another with the next one's rows on their way (one
+// head per CTA took 103 us for 35K rows of 8 heads: most of it finding the request, block and scale).
 // A half-full block keeps its larger scale; its old codes are read only when the scale grows.
 #include "common.cuh"
 #include "kernels.cuh"
@@ -13,11 +15,11 @@ namespace spectree {
 namespace {
 
 constexpr int kVecs = 4;          // 16-byte source vectors a thread holds (8 where a block needs > 1024 threads)
+constexpr long long kFillCtas = 152 * 4;
 constexpr int kMinExp = -64, kMaxExp = 120;
 
 // The exponent of the smallest power of two s with amax <= 448 s (448 = 1.75 * 2^8).
-__device__ __forceinline__ int scale_exp(float amax) {
-  const uint32_t b = __float_as_uint(amax);
+__device__ __forceinline__ int scale_exp(uint32_t b) {  // the bits of amax
   if ((b >> 23) == 0) return kMinExp;  // zero and what is below 2^-126
   const int e = (int)(b >> 23) - 127 - 8 + ((b & 0x7FFFFFu) > 0x600000u ? 1 : 0);
   return min(max(e, kMinExp), kMaxExp);
@@ -36,7 +38,8 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t c) {
   return __half22float2(*reinterpret_cast<__half2*>(&h));
 }
 
-// One 16-byte source vector: 8 bf16 or 4 floats.
+// One 16-byte source vector: 8 bf16 or 4 floats.  Magnitudes are compared as bits (a pair of bf16 at a time):
+// their order is that of the numbers, with infinities and NaN on top.
 template <bool BF16>
 struct Vec {
   static constexpr int kElems = BF16 ? 8 : 4;
@@ -52,7 +55,35 @@ struct Vec {
       }
     }
   }
+  // `top` (bf16: two 16-bit maxima) with the vector's magnitudes
+  static __device__ __forceinline__ uint32_t grow(uint32_t top, const uint4& v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (BF16)
+        top = __vmaxu2(top, w[i] & 0x7FFF7FFFu);
+      else
+        top = max(top, w[i] & 0x7FFFFFFFu);
+    }
+    return top;
+  }
+  // the bits of the larger of the two as a float
+  static __device__ __forceinline__ uint32_t bits(uint32_t top) {
+    return BF16 ? max(top << 16, top & 0xFFFF0000u) : top;
+  }
 };
+
+// The bits of the vector's largest finite magnitude, and of `top`.
+template <bool BF16>
+__device__ __noinline__ uint32_t finite_top(uint32_t top, uint4 v) {
+  float x[Vec<BF16>::kElems];
+  Vec<BF16>::unpack(v, x);
+  for (int e = 0; e < Vec<BF16>::kElems; ++e) {
+    const uint32_t b = __float_as_uint(x[e]) & 0x7FFFFFFFu;
+    if (b < 0x7F800000u) top = max(top, b);
+  }
+  return top;
+}
 
 // kElems codes at `dst` (8 or 4 bytes)
 template <int E>
@@ -115,12 +146,12 @@ __device__ __forceinline__ bool bad_table(const Kv8AppendParams& p, int b, long 
 
 }  // namespace
 
-// Grid: units x parts.  A unit is one block that rows of a request go to; a part is a run of the unit's
-// 2 * Hkv (K or V, head) blocks of codes, `groups` of TG = blockDim / groups threads each taking one.
-template <bool BF16, int NV>
-__global__ void __launch_bounds__(1024) kv8_append_kernel(const Kv8AppendParams p, int parts, int tg_shift) {
+// Grid: units x parts.  A unit is one block that rows of a request go to; its items are the 2 * Hkv (head, K
+// or V) blocks of codes; a part is a run of them, which the CTA's groups of TG threads take in turn.
+template <bool BF16, int NV, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv8_append_kernel(const Kv8AppendParams p, int parts, int tg_shift) {
   constexpr int E = Vec<BF16>::kElems;
-  __shared__ float s_max[32];
+  __shared__ uint32_t s_max[2][32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int u = blockIdx.x / parts, part = blockIdx.x - u * parts;
   // ---- the unit's request and block ----
@@ -163,82 +194,120 @@ __global__ void __launch_bounds__(1024) kv8_append_kernel(const Kv8AppendParams 
   const int blk = p.table[(size_t)b * p.max_blocks + (first >> p.bs_shift)];
   if (blk < 0 || blk >= p.num_blocks) return;  // (the lead CTA has set the status)
 
-  // ---- this group's K or V block of one head ----
+  // ---- this thread's vectors: the same places of every item ----
   const int tg = 1 << tg_shift, groups = blockDim.x >> tg_shift;
-  const int item = part * groups + (tid >> tg_shift), t = tid & (tg - 1);
-  const bool live = item < 2 * p.Hkv;
-  const int h = item >> 1;
-  const bool isv = item & 1;
-  const uint8_t* src = static_cast<const uint8_t*>(isv ? p.v_new : p.k_new);
-  const size_t cell = (size_t)blk * p.Hkv + h;
-  uint8_t* codes = (isv ? p.v_cache : p.k_cache) + cell * ((size_t)p.bs * p.d);
-  float* scale = (isv ? p.v_scale : p.k_scale) + cell;
-  const int per_row = p.d / E;        // vectors per row: a power of two
-  const int row_shift = 31 - __clz(per_row);
+  const int t = tid & (tg - 1);
+  const int row_shift = 31 - __clz(p.d / E);  // vectors per row: a power of two
   const int row_bytes = p.d * (BF16 ? 2 : 4);
-  uint4 v[NV];
-  float amax = 0.f;
-  const float s_old = live && held ? *scale : 0.f;
-  if (live) {
-    const long long row0 = p.path ? (long long)b * p.N : (long long)p.row_start[b] + (first - len);
-    const int32_t* pth = p.path ? p.path + (size_t)b * p.path_cap + (first - len) : nullptr;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = t + j * tg, r = c >> row_shift, col = c & (per_row - 1);
-      v[j] = make_uint4(0, 0, 0, 0);
-      if (r >= held && r < end) {
-        const long long row = p.path ? row0 + pth[r] : row0 + r;
-        v[j] = __ldcs(reinterpret_cast<const uint4*>(src + ((size_t)row * p.Hkv + h) * row_bytes + col * 16));
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      float x[E];
-      Vec<BF16>::unpack(v[j], x);
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float a = fabsf(x[e]);
-        amax = fmaxf(amax, a < INFINITY ? a : 0.f);  // NaN and infinities are left out
-      }
-    }
-  }
-  amax = warp_max(amax);
-  if (tg > 32) {
-    if (lane == 0) s_max[warp] = amax;
-    __syncthreads();
-    const int w0 = (tid >> tg_shift) << (tg_shift - 5);
-    amax = 0.f;
-    for (int w = 0; w < (tg >> 5); ++w) amax = fmaxf(amax, s_max[w0 + w]);
-  }
-  if (!live) return;
-  const float s_new = pow2f(scale_exp(amax));
-  const bool grown = held && !(s_old >= s_new);
-  const float s = held && !grown ? s_old : s_new;
-  // x / s: by the reciprocal where s is a power of two (always, unless the caller's own scale stays)
-  const bool exact = (__float_as_uint(s) & 0x7FFFFFu) == 0u && s >= 5.4210108624275222e-20f;  // 2^-64
-  const float inv = exact ? 1.f / s : 0.f;
+  const long long row0 = p.path ? (long long)b * p.N : (long long)p.row_start[b] + (first - len);
+  const int32_t* pth = p.path ? p.path + (size_t)b * p.path_cap + (first - len) : nullptr;
+  int from[NV];  // source row of vector j's place, or -1: no new row there
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int c = t + j * tg, r = c >> row_shift;
-    float x[E];
-    if (r >= held && r < end) {
-      Vec<BF16>::unpack(v[j], x);
-#pragma unroll
-      for (int e = 0; e < E; ++e) x[e] = exact ? x[e] * inv : x[e] / s;
-      store_codes<E>(codes + (size_t)c * E, x);
-    } else if (grown && r < held) {
-      const float ratio = s_old / s;
-      const uint32_t* w = reinterpret_cast<const uint32_t*>(codes + (size_t)c * E);
-#pragma unroll
-      for (int e = 0; e < E; e += 4) {
-        const uint32_t q = w[e / 4];
-        const float2 a = from_e4m3x2(q & 0xFFFFu), z = from_e4m3x2(q >> 16);
-        x[e] = a.x * ratio; x[e + 1] = a.y * ratio; x[e + 2] = z.x * ratio; x[e + 3] = z.y * ratio;
-      }
-      store_codes<E>(codes + (size_t)c * E, x);
-    }
+    const int r = (t + j * tg) >> row_shift;
+    from[j] = r >= held && r < end ? (int)(p.path ? row0 + pth[r] : row0 + r) : -1;
   }
-  if (t == 0) *scale = s;
+  const int items = 2 * p.Hkv, per = (items + parts - 1) / parts;
+  const int i0 = part * per, i1 = min(items, i0 + per);
+  const size_t cell0 = (size_t)blk * p.Hkv;
+  auto scale_of = [&](int item) { return ((item & 1) ? p.v_scale : p.k_scale) + cell0 + (item >> 1); };
+  auto load = [&](int item, uint4 (&v)[NV], float& s_old) {
+    const uint8_t* src = static_cast<const uint8_t*>((item & 1) ? p.v_new : p.k_new) + (size_t)(item >> 1) * row_bytes;
+    const size_t stride = (size_t)p.Hkv * row_bytes;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      v[j] = make_uint4(0, 0, 0, 0);
+      const int col = (t + j * tg) & ((1 << row_shift) - 1);
+      if (item < i1 && from[j] >= 0) v[j] = __ldcs(reinterpret_cast<const uint4*>(src + from[j] * stride + col * 16));
+    }
+    s_old = item < i1 && held ? *scale_of(item) : 0.f;
+  };
+  uint4 next[NV];
+  float s_next;
+  const int mine0 = i0 + (tid >> tg_shift);
+  load(mine0, next, s_next);
+  for (int base = i0, turn = 0; base < i1; base += groups, turn ^= 1) {  // (every thread: barriers inside)
+    const int item = base + (tid >> tg_shift);
+    uint4 v[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) v[j] = next[j];
+    const float s_old = s_next;
+    load(item + groups, next, s_next);
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) top = Vec<BF16>::grow(top, v[j]);
+    top = Vec<BF16>::bits(top);
+    if (top >= 0x7F800000u) {  // NaN and infinities are left out
+      top = 0;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) top = finite_top<BF16>(top, v[j]);
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (tg > 32) {
+      if (lane == 0) s_max[turn][warp] = top;
+      __syncthreads();
+      const int w0 = (tid >> tg_shift) << (tg_shift - 5);
+      top = __reduce_max_sync(0xffffffffu, lane < (tg >> 5) ? s_max[turn][w0 + lane] : 0u);
+    }
+    if (item >= i1) continue;
+    uint8_t* codes = ((item & 1) ? p.v_cache : p.k_cache) + (cell0 + (item >> 1)) * ((size_t)p.bs * p.d);
+    const float s_new = pow2f(scale_exp(top));
+    const bool grown = held && !(s_old >= s_new);
+    const float s = held && !grown ? s_old : s_new;
+    // x / s: by the reciprocal where s is a power of two (always, unless the caller's own scale stays)
+    if ((__float_as_uint(s) & 0x7FFFFFu) == 0u && s >= 5.4210108624275222e-20f &&
+        s <= 1.329227995784916e36f) {  // 2^-64 .. 2^120
+      const float inv = __uint_as_float((254u << 23) - __float_as_uint(s));
+      const float2 inv2 = make_float2(inv, inv);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        if (from[j] < 0) continue;
+        float x[E];
+        Vec<BF16>::unpack(v[j], x);
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          const float2 y = __fmul2_rn(make_float2(x[e], x[e + 1]), inv2);
+          x[e] = y.x;
+          x[e + 1] = y.y;
+        }
+        store_codes<E>(codes + (size_t)(t + j * tg) * E, x);
+      }
+    } else {
+#pragma unroll 1
+      for (int j = 0; j < NV; ++j) {
+        uint4 w = make_uint4(0, 0, 0, 0);
+        int row = -1;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          if (i == j) {
+            w = v[i];
+            row = from[i];
+          }
+        if (row < 0) continue;
+        float x[E];
+        Vec<BF16>::unpack(w, x);
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] = x[e] / s;
+        store_codes<E>(codes + (size_t)(t + j * tg) * E, x);
+      }
+    }
+    if (grown) {  // the old rows' codes in the new scale
+      const float ratio = s_old / s;
+#pragma unroll 1
+      for (int c = t; c < held << row_shift; c += tg) {
+        float x[E];
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(codes + (size_t)c * E);
+#pragma unroll
+        for (int e = 0; e < E; e += 4) {
+          const uint32_t q = w[e / 4];
+          const float2 a = from_e4m3x2(q & 0xFFFFu), z = from_e4m3x2(q >> 16);
+          x[e] = a.x * ratio; x[e + 1] = a.y * ratio; x[e + 2] = z.x * ratio; x[e + 3] = z.y * ratio;
+        }
+        store_codes<E>(codes + (size_t)c * E, x);
+      }
+    }
+    if (t == 0) *scale_of(item) = s;
+  }
 }
 
 namespace {
@@ -256,9 +325,11 @@ AppendShape append_shape(const Kv8AppendParams& p) {
   while ((s.nv << s.tg_shift) < vecs) ++s.tg_shift;
   const int tg = 1 << s.tg_shift;
   s.threads = tg > 256 ? tg : 256;
-  const int groups = s.threads / tg;
-  s.parts = (2 * p.Hkv + groups - 1) / groups;
+  // as many parts per unit as keep every SM busy, down to one for long prompts
+  const int groups = s.threads / tg, most = (2 * p.Hkv + groups - 1) / groups;
   s.units = p.path ? (long long)p.B * p.units_per_req : (p.n_rows >> p.bs_shift) + 2ll * p.B;
+  const long long want = (kFillCtas + s.units - 1) / s.units;
+  s.parts = want < 1 ? 1 : want > most ? most : (int)want;
   return s;
 }
 
@@ -273,12 +344,17 @@ unsigned kv8_append_grid(const Kv8AppendParams& p) {
 cudaError_t launch_kv8_append(const Kv8AppendParams& p, cudaStream_t stream) {
   const AppendShape s = append_shape(p);
   const unsigned grid = kv8_append_grid(p);
-  if (p.is_bf16)
-    kv8_append_kernel<true, kVecs><<<grid, s.threads, 0, stream>>>(p, s.parts, s.tg_shift);
-  else if (s.nv == kVecs)
-    kv8_append_kernel<false, kVecs><<<grid, s.threads, 0, stream>>>(p, s.parts, s.tg_shift);
-  else
-    kv8_append_kernel<false, 2 * kVecs><<<grid, s.threads, 0, stream>>>(p, s.parts, s.tg_shift);
+  auto go = [&](auto kernel) { kernel<<<grid, s.threads, 0, stream>>>(p, s.parts, s.tg_shift); };
+  if (p.is_bf16) {
+    if (s.threads == 256) go(kv8_append_kernel<true, kVecs, 256>);
+    else if (s.threads == 512) go(kv8_append_kernel<true, kVecs, 512>);
+    else go(kv8_append_kernel<true, kVecs, 1024>);
+  } else {
+    if (s.threads == 256) go(kv8_append_kernel<false, kVecs, 256>);
+    else if (s.threads == 512) go(kv8_append_kernel<false, kVecs, 512>);
+    else if (s.nv == kVecs) go(kv8_append_kernel<false, kVecs, 1024>);
+    else go(kv8_append_kernel<false, 2 * kVecs, 1024>);
+  }
   return cudaGetLastError();
 }
 
