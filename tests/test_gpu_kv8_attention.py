@@ -49,6 +49,22 @@ def test_long_prefix_and_chain():
     K8.check(cache, qs, out, lse)
 
 
+@pytest.mark.parametrize("N,G,B,long", [(1, 4, 20, 30000), (1, 8, 150, 20000), (1, 1, 130, 0), (3, 5, 40, 9001),
+                                        (63, 4, 12, 12000), (40, 8, 140, 6001), (255, 4, 3, 5000), (20, 1, 129, 0)])
+def test_one_long_request_among_many(N, G, B, long):
+    """Ragged batches, where the long prefix takes most of the splits; the last request is longer than its table."""
+    rng = np.random.default_rng(B + N)
+    lens = [int(x) for x in rng.integers(0, 90, B)]
+    lens[1] = 1500
+    lens[B // 2] = long
+    cache = K8.Cache(rng, lens, 1, 128, 64, max_len=max(lens) + 64)
+    qs = K8.Queries(rng, B, N, G, 1, 128)
+    out, lse, status = K8.attend(K8.dev(), _with_lens(cache, lens[:-1] + [10 ** 8]), qs)
+    assert status == 7
+    assert not out[-1].any() and not lse[-1].any()
+    K8.check(cache, qs, out, lse, requests=sorted({0, 1, B // 2, B - 2}))
+
+
 @pytest.mark.parametrize("N", [1, 40])
 def test_any_scale_and_softmax_scale(N):
     """Scales that are no powers of two, far apart (2^-20 to 2^20), and a softmax scale of the caller's."""

@@ -146,15 +146,33 @@ __global__ void __launch_bounds__(kWarps * 32, RN == 1 ? 4 : 2)
   __shared__ float s_m[kWarps][kRowsR], s_l[kWarps][kRowsR];
   __shared__ uint32_t s_odd[kAncWords];  // tree keys with an infinity or NaN in their V row
   __shared__ int s_bad;
-  const int rt = blockIdx.x, split = blockIdx.y, bg = blockIdx.z;
-  const int b = bg / p.Hkv, h = bg - b * p.Hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
-  long long L;
-  int n;
-  int err = kv8_counts(p, b, &L, &n);
-  const Kv8Split sp = kv8_split(L, p.n_split, p.unit_shift);
-  if (split >= sp.n) return;
+  Kv8Work sp = kv8_own(p);
+  // queries: row g of every 8-row tile, dimensions [RUN t, RUN t + RUN); they and the tree's links are on their way
+  // while the lengths are read, where they do not hang on them
+  uint4 qv[RN][RUN / 8];
+  int par0 = -1;
+  auto early = [&]() {
+#pragma unroll
+    for (int r = 0; r < RN; ++r) {
+      const int row = sp.rt * kRowsR + g + 8 * r;
+      const bool has = row < p.N * p.G;
+      const uint16_t* qrow = p.q + kv8_row(p, sp.b, sp.h, has ? row : 0) * D + RUN * t;
+#pragma unroll
+      for (int i = 0; i < RUN / 8; ++i)
+        qv[r][i] = has ? *reinterpret_cast<const uint4*>(qrow + 8 * i) : make_uint4(0, 0, 0, 0);
+    }
+    if (tid < p.N) par0 = p.parent[(size_t)sp.b * p.N + tid];
+  };
+  const bool own = sp.b >= 0;
+  if (own) early();
+  sp = kv8_begin(p, sp);
+  if (sp.b < 0) return;
+  if (!own) early();
+  const int b = sp.b, h = sp.h, rt = sp.rt, split = sp.split, n = sp.nodes;
+  const long long L = sp.L;
+  int err = sp.err;
   const int row0 = rt * kRowsR, rows = p.N * p.G;
   auto orow_of = [&](int row) { return kv8_row(p, b, h, row); };
   if (lane == 0) {
@@ -226,21 +244,8 @@ __global__ void __launch_bounds__(kWarps * 32, RN == 1 ? 4 : 2)
     if (lane == 0)
       for (int i = 0; i < pre; ++i) mbar_wait_bounded(&s_full[warp][i], 0, nullptr);
   };
-  // ---- queries: row g of every 8-row tile, dimensions [RUN t, RUN t + RUN)
-  bool has[RN];
-  const uint16_t* qrow[RN];
-  uint4 qv[RN][RUN / 8];
-#pragma unroll
-  for (int r = 0; r < RN; ++r) {
-    const int row = row0 + g + 8 * r;
-    has[r] = row < rows;
-    qrow[r] = p.q + orow_of(has[r] ? row : 0) * D + RUN * t;
-#pragma unroll
-    for (int i = 0; i < RUN / 8; ++i)
-      qv[r][i] = has[r] ? *reinterpret_cast<const uint4*>(qrow[r] + 8 * i) : make_uint4(0, 0, 0, 0);
-  }
   for (int i = tid; i < n; i += blockDim.x) {
-    const int par = p.parent[(size_t)b * p.N + i];
+    const int par = i == tid ? par0 : p.parent[(size_t)b * p.N + i];
     s_par[i] = par;
     if (i == 0 ? par != -1 : (par < 0 || par >= i)) err = SPEC_ERR_BAD_TREE;
   }
@@ -255,7 +260,7 @@ __global__ void __launch_bounds__(kWarps * 32, RN == 1 ? 4 : 2)
         *reinterpret_cast<uint4*>(p.out + o * D + e * 8) = make_uint4(0, 0, 0, 0);
         if (e == 0 && p.lse) p.lse[o] = 0.f;
       } else if (e == 0) {
-        p.part_ml[o * p.n_split + split] = make_float2(0.f, -1.f);
+        p.part_ml[sp.part + (row - row0)] = make_float2(0.f, -1.f);
       }
     }
   };
@@ -342,7 +347,8 @@ __global__ void __launch_bounds__(kWarps * 32, RN == 1 ? 4 : 2)
         const uint4 x1 = in1 ? *reinterpret_cast<const uint4*>(k1 + 8 * i) : z;
 #pragma unroll
         for (int r = 0; r < RN; ++r) {
-          const uint4 q = has[r] ? *reinterpret_cast<const uint4*>(qrow[r] + 8 * i) : z;
+          const int row = row0 + g + 8 * r;
+          const uint4 q = row < rows ? *reinterpret_cast<const uint4*>(p.q + orow_of(row) * D + RUN * t + 8 * i) : z;
           mma_bf16(y[r], x0.x, x1.x, x0.y, x1.y, q.x, q.y);
           mma_bf16(y[r], x0.z, x1.z, x0.w, x1.w, q.z, q.w);
         }
@@ -555,8 +561,8 @@ __global__ void __launch_bounds__(kWarps * 32, RN == 1 ? 4 : 2)
     }
     const size_t orow = orow_of(row);
     if (sp.n > 1) {
-      *reinterpret_cast<float4*>(p.part_o + (orow * p.n_split + split) * D + e * 4) = a;
-      if (e == 0) p.part_ml[orow * p.n_split + split] = make_float2(M, l);
+      *reinterpret_cast<float4*>(p.part_o + (sp.part + rr) * D + e * 4) = a;
+      if (e == 0) p.part_ml[sp.part + rr] = make_float2(M, l);
     } else {
       const float inv = real ? 1.f / l : 0.f;
       uint2 out = make_uint2(0, 0);
@@ -567,53 +573,72 @@ __global__ void __launch_bounds__(kWarps * 32, RN == 1 ? 4 : 2)
   }
 }
 
-// Joins the splits of a row: one warp per output row, lanes over dimensions.
+// Joins the splits of a row: one warp per row of a request that was split, lanes over dimensions.
 template <int D>
 __global__ void __launch_bounds__(256) attn_kv8_merge_kernel(const Kv8AttnParams p) {
   constexpr int EPL = D / 32;
   const int lane = threadIdx.x & 31;
-  const size_t orow = (size_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   pdl_wait();  // first of all: a launch that ended before the attention's would let its successor overtake it
-  if (orow >= (size_t)p.B * p.N * p.Hq) return;
-  const int b = (int)(orow / ((size_t)p.N * p.Hq));
-  const int i = (int)((orow / p.Hq) % p.N);
-  long long L;
-  int n;
-  kv8_counts(p, b, &L, &n);
-  const Kv8Split sp = kv8_split(L, p.n_split, p.unit_shift);
-  if (sp.n == 1) return;  // written by the attention kernel itself
-  float M = -INFINITY;
-  bool bad = i >= n;
-  for (int s = lane; s < sp.n; s += 32) {
-    const float2 ml = bad ? make_float2(0.f, -1.f) : __ldcg(p.part_ml + orow * p.n_split + s);
-    bad |= ml.y < 0.f;
-    M = fmaxf(M, ml.x);
+  const int per_req = p.N * p.Hq;
+  int item = blockIdx.x * 8 + (threadIdx.x >> 5);  // among the rows of the split requests that follow
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int2 cuts = b0 + lane < p.B ? __ldcg(p.used + b0 + lane) : make_int2(1, 0);
+    const unsigned split = __ballot_sync(0xffffffffu, cuts.x > 1);
+    const int items = __popc(split) * per_req;
+    for (; item < items; item += gridDim.x * 8) {
+      const int nth = item / per_req, in_req = item - nth * per_req;
+      unsigned rest = split;
+      for (int j = 0; j < nth; ++j) rest &= rest - 1;
+      const int src = __ffs(rest) - 1, b = b0 + src;
+      const int used = __shfl_sync(0xffffffffu, cuts.x, src), first = __shfl_sync(0xffffffffu, cuts.y, src);
+      const int i = in_req / p.Hq, hq = in_req - i * p.Hq, h = hq / p.G;
+      const size_t orow = (size_t)b * per_req + in_req;
+      // the row's place in the partial results of split s
+      const int row = i * p.G + hq - h * p.G, rt = row / p.rows_cta;
+      auto part = [&](int s) { return kv8_part(p, b, h, rt, s, first) + (row - rt * p.rows_cta); };
+      const int n = p.n_nodes[b];
+      const float2 ml = lane < used && i < n ? __ldcg(p.part_ml + part(lane)) : make_float2(-INFINITY, i < n ? 0.f : -1.f);
+      const bool bad = __any_sync(0xffffffffu, ml.y < 0.f);
+      const float M = warp_max(ml.x);
+      const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
+      const float l = warp_sum(ml.y * f);
+      uint16_t* out = p.out + orow * D + lane * EPL;
+      float acc[EPL];
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) acc[e] = 0.f;
+      for (int s0 = 0; s0 < used && !bad; s0 += 4) {  // four splits' loads at a time
+        float x[4][EPL], w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          w[k] = __shfl_sync(0xffffffffu, f, (s0 + k) & 31);
+          const float* src_o = p.part_o + part(s0 + k) * D + lane * EPL;
+          if (s0 + k < used) {
+            if constexpr (EPL == 4) {
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(src_o));
+              x[k][0] = v.x; x[k][1] = v.y; x[k][2] = v.z; x[k][3] = v.w;
+            } else {
+              const float2 v = __ldcg(reinterpret_cast<const float2*>(src_o));
+              x[k][0] = v.x; x[k][1] = v.y;
+            }
+          } else {
+            w[k] = 0.f;
+#pragma unroll
+            for (int e = 0; e < EPL; ++e) x[k][e] = 0.f;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int e = 0; e < EPL; ++e) acc[e] = fmaf(x[k][e], w[k], acc[e]);
+      }
+      const float inv = bad ? 0.f : 1.f / l;  // (a row that is refused: acc is 0)
+#pragma unroll
+      for (int e = 0; e < EPL; e += 2)
+        *reinterpret_cast<uint32_t*>(out + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+      if (p.lse && lane == 0) p.lse[orow] = bad ? 0.f : (M + log2f(l)) * 0.69314718055994531f;
+    }
+    item -= items;
   }
-  bad = __any_sync(0xffffffffu, bad);
-  M = warp_max(M);
-  uint16_t* out = p.out + orow * D + lane * EPL;
-  if (bad) {
-#pragma unroll
-    for (int e = 0; e < EPL; ++e) out[e] = 0;
-    if (p.lse && lane == 0) p.lse[orow] = 0.f;
-    return;
-  }
-  float l = 0.f, acc[EPL];
-#pragma unroll
-  for (int e = 0; e < EPL; ++e) acc[e] = 0.f;
-  for (int s = 0; s < sp.n; ++s) {
-    const float2 ml = __ldcg(p.part_ml + orow * p.n_split + s);
-    const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
-    l = fmaf(ml.y, f, l);
-    const float* src = p.part_o + (orow * p.n_split + s) * D + lane * EPL;
-#pragma unroll
-    for (int e = 0; e < EPL; ++e) acc[e] = fmaf(__ldcg(src + e), f, acc[e]);
-  }
-  const float inv = 1.f / l;
-#pragma unroll
-  for (int e = 0; e < EPL; e += 2)
-    *reinterpret_cast<uint32_t*>(out + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-  if (p.lse && lane == 0) p.lse[orow] = (M + log2f(l)) * 0.69314718055994531f;
 }
 
 // ---- host side ------------------------------------------------------------------------------
@@ -621,38 +646,44 @@ __global__ void __launch_bounds__(256) attn_kv8_merge_kernel(const Kv8AttnParams
 Kv8AttnPlan plan_attention_kv8(int B, int N, int G, int Hkv, long long L_cap, int num_sms) {
   Kv8AttnPlan pl;
   const int rows = N * G;
+  const long long heads = (long long)B * Hkv;
   if (rows <= 16) {
     pl.groups = 0;
     pl.unit_shift = 6;
     pl.n_rt = 1;
-    // as many CTAs as fit at once (four an SM): 57.8 us for 32 requests at 4K, 59.9 with half or twice as many;
-    // no split below 256 keys
-    const long long base = (long long)B * Hkv;
-    long long want = ((long long)num_sms * 4 + base - 1) / base;
-    const long long most = (L_cap + 255) / 256;
-    if (want > most) want = most;
-    if (want > 64) want = 64;
-    pl.n_split = want < 1 ? 1 : (int)want;
-    return pl;
+    pl.slots = num_sms * 4;  // four CTAs an SM
+    pl.fixed_steps = 2;
+  } else {
+    // two groups of 128 rows per CTA cost little more a key tile than one (each fills the other's waits), so one
+    // is for few rows, and for calls so small that every SM gets less than a few tiles
+    const long long tiles = (L_cap + 127) / 128;
+    pl.groups = rows > 128 && heads * ((rows + 255) / 256) * tiles >= 4 * num_sms ? 2 : 1;
+    pl.unit_shift = 7;
+    pl.n_rt = (rows + 128 * pl.groups - 1) / (128 * pl.groups);
+    pl.slots = num_sms;
+    pl.fixed_steps = 7;
   }
-  // two groups of 128 rows per CTA where that still gives every SM work before any splitting
-  const long long units2 = (long long)B * Hkv * ((rows + 255) / 256);
-  pl.groups = rows > 128 && units2 * 2 >= num_sms ? 2 : 1;
-  pl.unit_shift = 7;
-  pl.n_rt = (rows + 128 * pl.groups - 1) / (128 * pl.groups);
-  // splits: the fewest rounds x (tiles + fixed work of a CTA, about kFixed tiles)
-  const long long base = (long long)B * Hkv * pl.n_rt, tiles = (L_cap + 127) / 128;
-  constexpr long long kFixed = 5;
-  long long best = -1;
-  pl.n_split = 1;
-  for (int s = 1; s <= 32 && (s == 1 || (tiles + s - 1) / s >= 2); ++s) {
-    const long long rounds = (base * s + num_sms - 1) / num_sms;
-    const long long cost = rounds * ((tiles + s - 1) / s + kFixed) + (s > 1 ? 3 : 0);
-    if (best < 0 || cost < best) {
-      best = cost;
-      pl.n_split = s;
-    }
+  pl.rows_cta = pl.groups == 0 ? (rows + 7) / 8 * 8 : 128 * pl.groups;
+  // units, with splits no shorter than 256 keys, kKv8Splits per request at most
+  const long long per = (long long)Hkv * pl.n_rt, ctas = B * per, most = (L_cap + 255) / 256;
+  const long long limit = most < 1 ? 1 : (most < kKv8Splits ? most : kKv8Splits);
+  long long more;
+  if (pl.groups == 0) {
+    // as many CTAs as fit at once (four an SM): 57.8 us for 32 requests at 4K, 59.9 with half or twice as many
+    pl.base = (int)((pl.slots + ctas - 1) / ctas);
+    if (pl.base > limit) pl.base = (int)limit;
+    more = pl.slots / 2 / per + 1;
+  } else {
+    // CTAs for every slot, and up to six where that leaves a split 64 steps of the longest prefixes
+    pl.base = (int)(pl.slots / ctas);
+    pl.base = pl.base < 1 ? 1 : pl.base > limit ? (int)limit : pl.base;
+    more = ctas * (L_cap >> pl.unit_shift) / 64;
+    more = more > 6ll * pl.slots ? 6ll * pl.slots : more < pl.slots ? pl.slots : more;
+    more = (more + per - 1) / per - (long long)B * (pl.base - 1);
+    if (more < 0) more = 0;
   }
+  if (more > B * (limit - pl.base)) more = B * (limit - pl.base);
+  pl.extra = (int)more;
   return pl;
 }
 
@@ -663,7 +694,7 @@ static cudaError_t launch_rows(const CUtensorMap* tmK, const CUtensorMap* tmV, c
   cudaError_t err =
       cudaFuncSetAttribute(attn_kv8_rows_kernel<D, RN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (err != cudaSuccess) return err;
-  attn_kv8_rows_kernel<D, RN><<<dim3(p.n_rt, p.n_split, p.B * p.Hkv), kWarps * 32, C::kSmem, stream>>>(*tmK, *tmV, p);
+  attn_kv8_rows_kernel<D, RN><<<p.n_rt * p.Hkv * (p.B * p.base + p.extra), kWarps * 32, C::kSmem, stream>>>(*tmK, *tmV, p);
   return cudaGetLastError();
 }
 
@@ -675,7 +706,9 @@ cudaError_t launch_attention_kv8_rows(const CUtensorMap* tmK, const CUtensorMap*
 }
 
 cudaError_t launch_attention_kv8_merge(const Kv8AttnParams& p, cudaStream_t stream) {
-  const unsigned blocks = (unsigned)(((size_t)p.B * p.N * p.Hq + 7) / 8);
+  // (which requests are split is known on the device only: as many CTAs as run at once, and their warps go on)
+  const size_t want = ((size_t)p.B * p.N * p.Hq + 7) / 8;
+  const unsigned blocks = (unsigned)(want < 152 * 4 ? want : 152 * 4);
   return p.d == 128 ? launch_dependent(attn_kv8_merge_kernel<128>, dim3(blocks), dim3(256), 0, stream, p)
                     : launch_dependent(attn_kv8_merge_kernel<64>, dim3(blocks), dim3(256), 0, stream, p);
 }

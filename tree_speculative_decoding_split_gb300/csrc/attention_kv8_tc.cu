@@ -171,14 +171,40 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
   __shared__ int s_abort, s_bad, s_kissued, s_vissued;
   __shared__ int s_par[kMaxNodes];
   __shared__ uint32_t s_odd[kAncWords];
-  const int rt = blockIdx.x, split = blockIdx.y, bg = blockIdx.z;
-  const int b = bg / p.Hkv, h = bg - b * p.Hkv;
+  __shared__ int s_any_odd;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  long long L;
-  int n;
-  int err = kv8_counts(p, b, &L, &n);
-  const Kv8Split sp = kv8_split(L, p.n_split, p.unit_shift);
-  if (split >= sp.n) return;
+  __shared__ Kv8Work s_work;
+  Kv8Work sp = kv8_own(p);
+  // the queries (16 bytes a lane, whole rows side by side) and the tree's links, on their way while the lengths are
+  // read and the checks run
+  constexpr int kQPer = kRowsCta * (D / 8) / (256 * NG);
+  uint4 qv[kQPer];
+  int par0 = -1;
+  auto early = [&]() {
+    if (tid < p.N) par0 = p.parent[(size_t)sp.b * p.N + tid];
+    if (warp >= 4) {
+#pragma unroll
+      for (int k = 0; k < kQPer; ++k) {
+        const int c = tid - 128 + k * 256 * NG, row = sp.rt * kRowsCta + c / (D / 8);
+        qv[k] = make_uint4(0, 0, 0, 0);
+        if (row < p.N * p.G)
+          qv[k] = *reinterpret_cast<const uint4*>(p.q + kv8_row(p, sp.b, sp.h, row) * D + (c % (D / 8)) * 8);
+      }
+    }
+  };
+  const bool own = sp.b >= 0;
+  if (own) early();
+  if (warp == 0) {
+    const Kv8Work w = kv8_begin(p, sp);
+    if (lane == 0) s_work = w;
+  }
+  __syncthreads();
+  sp = s_work;
+  if (sp.b < 0) return;
+  if (!own) early();
+  const int b = sp.b, h = sp.h, rt = sp.rt, split = sp.split, n = sp.nodes;
+  const long long L = sp.L;
+  int err = sp.err;
   const int row0 = rt * kRowsCta, rows = p.N * p.G;
   auto orow_of = [&](int row) { return kv8_row(p, b, h, row); };
   // rows of a refused request or of padded nodes; with several splits the merge writes them
@@ -191,21 +217,10 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
         *reinterpret_cast<uint4*>(p.out + o * D + e * 8) = make_uint4(0, 0, 0, 0);
         if (e == 0 && p.lse) p.lse[o] = 0.f;
       } else if (e == 0) {
-        p.part_ml[o * p.n_split + split] = make_float2(0.f, -1.f);
+        p.part_ml[sp.part + (row - row0)] = make_float2(0.f, -1.f);
       }
     }
   };
-  // the queries, on their way while the checks run: 16 bytes a lane, whole rows side by side
-  constexpr int kQPer = kRowsCta * (D / 8) / (256 * NG);
-  uint4 qv[kQPer];
-  if (warp >= 4) {
-#pragma unroll
-    for (int k = 0; k < kQPer; ++k) {
-      const int c = tid - 128 + k * 256 * NG, row = row0 + c / (D / 8);
-      qv[k] = make_uint4(0, 0, 0, 0);
-      if (row < rows) qv[k] = *reinterpret_cast<const uint4*>(p.q + orow_of(row) * D + (c % (D / 8)) * 8);
-    }
-  }
   if (tid == 0) {
     for (int s = 0; s < kKS; ++s) {
       mbar_init(&kfull[s], 1);
@@ -230,25 +245,10 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
     mbar_init(&s_drained, 1);
     s_abort = 0;
     s_bad = 0;
+    s_any_odd = 0;
     s_kissued = 0;
     s_vissued = 0;
     fence_mbar_init();
-  }
-  if (tid < kAncWords) s_odd[tid] = 0u;
-  for (int i = tid; i < n; i += C::kThreads) {
-    const int par = p.parent[(size_t)b * p.N + i];
-    s_par[i] = par;
-    if (i == 0 ? par != -1 : (par < 0 || par >= i)) err = SPEC_ERR_BAD_TREE;
-  }
-  if (__syncthreads_or(err == SPEC_ERR_BAD_TREE)) err = SPEC_ERR_BAD_TREE;
-  if (err) {
-    if (tid == 0 && rt == 0 && split == 0 && h == 0) set_status(p.dev_status, err);
-    refuse();
-    return;
-  }
-  if (row0 >= n * p.G) {
-    if (sp.n == 1) refuse();
-    return;
   }
   // ---- this CTA's tiles: the tree's (in the last split) and then keys [k0, k1) of the prefix ----
   const bool tree = split == sp.n - 1;
@@ -256,68 +256,46 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
   const long long k1 = min(L, k0 + ((long long)sp.steps << p.unit_shift));
   const int Tt = tree ? (n + kTT - 1) / kTT : 0;
   const int T = Tt + (k1 > k0 ? (int)((k1 - k0 + kKT8 - 1) / kKT8) : 0);
-  if (tree)
-    for (int i = tid; i < n; i += C::kThreads) {
-      uint32_t* w = s_nanc + i * kAncWords;
-#pragma unroll
-      for (int j = 0; j < kAncWords; ++j) w[j] = 0u;
-      for (int a = i; a >= 0; a = s_par[a]) w[a >> 5] |= 1u << (a & 31);
-    }
-  if (warp >= 4) {
-#pragma unroll
-    for (int k = 0; k < kQPer; ++k) {
-      const int c = tid - 128 + k * 256 * NG, rr = c / (D / 8);
-      *reinterpret_cast<uint4*>(sQ + (rr / kGR8) * C::kQ + tile16_off(rr % kGR8, c % (D / 8), kGR8)) = qv[k];
-    }
-    fence_proxy_async_smem();
+  // ---- TMA: lane i < 128 / box of warp 0 takes box i of a tile; the first tiles are on their way while the tree is
+  // checked ----
+  const int box = min(p.bs, kKT8), nbox = kKT8 / box;
+  const int out_z = p.num_blocks * p.Hkv;  // behind the map: reads as zeros
+  // slot of this lane's box in prefix tile u, or -1 when it lies behind the split's keys
+  auto slot_of = [&](int u) -> long long {
+    const long long s = k0 + (long long)u * kKT8 + lane * box;
+    return lane < nbox && s < k1 ? s : -1;
+  };
+  auto entry = [&](int u) -> int {
+    const long long s = slot_of(u);
+    return s >= 0 ? p.table[(size_t)b * p.max_blocks + (s >> p.bs_shift)] : -1;
+  };
+  // the block of tile u is loaded two tiles ahead and its scales one tile ahead of its requests
+  int blk0 = -1, blk1 = -1;
+  if (warp == 0) {
+    blk0 = entry(0);
+    blk1 = entry(1);
   }
-  if (warp == 1) {
-    tmem_alloc(&s_tmem, 512);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = s_tmem;
-  // register shares of the warpgroups (two groups): 64 + 4 x 104 within the 5 x 96 the block was launched with
-  if (warp < 4) {
-    if constexpr (NG == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    if (warp == 0) {
-    // ---- TMA producer: lane i < 128 / box takes box i of a tile ----
-    const int box = min(p.bs, kKT8), nbox = kKT8 / box;
-    const int out_z = p.num_blocks * p.Hkv;  // behind the map: reads as zeros
-    // slot of this lane's box in prefix tile u, or -1 when it lies behind the split's keys
-    auto slot_of = [&](int u) -> long long {
-      const long long s = k0 + (long long)u * kKT8 + lane * box;
-      return lane < nbox && s < k1 ? s : -1;
-    };
-    auto entry = [&](int u) -> int {
-      const long long s = slot_of(u);
-      return s >= 0 ? p.table[(size_t)b * p.max_blocks + (s >> p.bs_shift)] : -1;
-    };
-    // the block of tile u is loaded two tiles ahead and its scales one tile ahead of its requests
-    int blk0 = entry(0), blk1 = entry(1);
-    float ks0 = 0.f, vs0 = 0.f;
-    auto scales = [&](int blk, float* ks, float* vs) {
-      *ks = 0.f;
-      *vs = 0.f;
-      if (blk >= 0 && blk < p.num_blocks) {
-        *ks = p.k_scale[(size_t)blk * p.Hkv + h];
-        *vs = p.v_scale[(size_t)blk * p.Hkv + h];
-      }
-    };
-    scales(blk0, &ks0, &vs0);
-    bool ok = true;
-    for (int t = 0; t < T; ++t) {
+  float ks0 = 0.f, vs0 = 0.f;
+  auto scales = [&](int blk, float* ks, float* vs) {
+    *ks = 0.f;
+    *vs = 0.f;
+    if (blk >= 0 && blk < p.num_blocks) {
+      *ks = p.k_scale[(size_t)blk * p.Hkv + h];
+      *vs = p.v_scale[(size_t)blk * p.Hkv + h];
+    }
+  };
+  auto produce = [&](int t0, int t1) -> bool {
+    for (int t = t0; t < t1; ++t) {
       const int ks = t % kKS, vs = t % kVS, u = t - Tt;
       int blk2 = -1;
       float ks1 = 0.f, vs1 = 0.f;
       if (u >= 0) {
+        if (u == 0) scales(blk0, &ks0, &vs0);
         scales(blk1, &ks1, &vs1);
         blk2 = entry(u + 2);
       }
       const bool got = lane == 0 ? mbar_wait_bounded(&kempty[ks], ((t / kKS) & 1) ^ 1, &s_abort) : true;
-      if (!(ok = __shfl_sync(0xffffffffu, got, 0))) break;
+      if (!__shfl_sync(0xffffffffu, got, 0)) return false;
       uint8_t* dk = sK + ks * C::kSlot;
       uint8_t* dv = sV + vs * C::kSlot;
       int y = 0, z = out_z;
@@ -350,7 +328,7 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
         tma_load_3d(dk + lane * box * D, &tmK, &kfull[ks], 0, y, z);
       }
       const bool gotv = lane == 0 ? mbar_wait_bounded(&vempty[vs], ((t / kVS) & 1) ^ 1, &s_abort) : true;
-      if (!(ok = __shfl_sync(0xffffffffu, gotv, 0))) break;
+      if (!__shfl_sync(0xffffffffu, gotv, 0)) return false;
       if (lane == 0) {
         mbar_arrive_expect_tx(&vfull[vs], C::kSlot);
         s_vissued = t + 1;
@@ -366,10 +344,67 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
         vs0 = vs1;
       }
     }
-    if (!ok && lane == 0) {
-      s_abort = 1;
-      set_status(p.dev_status, SPEC_ERR_TIMEOUT);
+    return true;
+  };
+  const int pre = min(T, kVS);
+  if (warp == 0) produce(0, pre);
+  auto drain = [&]() {  // a CTA that leaves early lets them land
+    if (tid == 0)
+      for (int t = 0; t < pre; ++t) {
+        mbar_wait_bounded(&kfull[t], 0, nullptr);
+        mbar_wait_bounded(&vfull[t], 0, nullptr);
+      }
+  };
+  if (tid < kAncWords) s_odd[tid] = 0u;
+  if (const int i = tid; i < n) {  // (there are more threads than nodes)
+    const int par = par0;
+    s_par[i] = par;
+    if (i == 0 ? par != -1 : (par < 0 || par >= i)) err = SPEC_ERR_BAD_TREE;
+  }
+  if (__syncthreads_or(err == SPEC_ERR_BAD_TREE)) err = SPEC_ERR_BAD_TREE;
+  if (err) {
+    if (tid == 0 && rt == 0 && split == 0 && h == 0) set_status(p.dev_status, err);
+    refuse();
+    drain();
+    return;
+  }
+  if (row0 >= n * p.G) {
+    if (sp.n == 1) refuse();
+    drain();
+    return;
+  }
+  if (tree)
+    if (const int i = tid; i < n) {  // (there are more threads than nodes)
+      uint32_t* w = s_nanc + i * kAncWords;
+#pragma unroll
+      for (int j = 0; j < kAncWords; ++j) w[j] = 0u;
+      for (int a = i; a >= 0; a = s_par[a]) w[a >> 5] |= 1u << (a & 31);
     }
+  if (warp >= 4) {
+#pragma unroll
+    for (int k = 0; k < kQPer; ++k) {
+      const int c = tid - 128 + k * 256 * NG, rr = c / (D / 8);
+      *reinterpret_cast<uint4*>(sQ + (rr / kGR8) * C::kQ + tile16_off(rr % kGR8, c % (D / 8), kGR8)) = qv[k];
+    }
+    fence_proxy_async_smem();
+  }
+  if (warp == 1) {
+    tmem_alloc(&s_tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  // register shares of the warpgroups (two groups): 64 + 4 x 104 within the 5 x 96 the block was launched with
+  if (warp < 4) {
+    if constexpr (NG == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp == 0) {
+    // ---- TMA producer, from where the first tiles ended ----
+      if (!produce(pre, T) && lane == 0) {
+        s_abort = 1;
+        set_status(p.dev_status, SPEC_ERR_TIMEOUT);
+      }
     } else if (warp == 1) {
     // ---- MMA issuer ----
     // The whole warp runs the loop, so that addresses and descriptors stay in uniform registers, and one
@@ -493,7 +528,10 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
             uint4* at = reinterpret_cast<uint4*>(src + tile16_off(r, c % (D / 8), kTT));
             uint4 x = *at;
             if (finite2(x.x) && finite2(x.y) && finite2(x.z) && finite2(x.w)) continue;
-            if (key < n) atomicOr(&s_odd[key >> 5], 1u << (key & 31));
+            if (key < n) {
+              atomicOr(&s_odd[key >> 5], 1u << (key & 31));
+              s_any_odd = 1;
+            }
             uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -772,7 +810,7 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
         tmem_ld_wait();
 #pragma unroll
         for (int j = 0; j < 32; ++j) o[j] = live ? __float_as_uint(__uint_as_float(o[j]) * inv) : 0u;
-        if (tree && live) {  // V elements of visible tree keys that are no finite numbers
+        if (tree && live && s_any_odd) {  // V elements of visible tree keys that are no finite numbers
           for (int w = 0; w < kAncWords; ++w)
             for (uint32_t mask = s_odd[w] & anc[w]; mask; mask &= mask - 1) {
               const int key = w * 32 + __ffs(mask) - 1;
@@ -801,7 +839,7 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
       if (valid && half == 0) {
         const size_t o = orow_of(row);
         if (!whole)
-          p.part_ml[o * p.n_split + split] = make_float2(m, l);
+          p.part_ml[sp.part + (row - row0)] = make_float2(m, l);
         else if (p.lse)
           p.lse[o] = live ? (m + log2f(l)) * 0.69314718055994531f : 0.f;
       }
@@ -810,6 +848,7 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
     named_bar_sync(1, 256 * NG);
     if (!s_abort && !s_bad) {
       const int vshift = whole ? (D == 128 ? 4 : 3) : (D == 128 ? 5 : 4), live_rows = whole ? rows : n * p.G;
+#pragma unroll 4
       for (int c = tid - 128; c < kRowsCta << vshift; c += 256 * NG) {
         const int r = c >> vshift, e = c & ((1 << vshift) - 1);
         if (row0 + r >= live_rows) break;
@@ -818,7 +857,7 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
         if (whole)
           *reinterpret_cast<uint4*>(p.out + o * D + e * 8) = x;
         else
-          *reinterpret_cast<uint4*>(p.part_o + (o * p.n_split + split) * D + e * 4) = x;
+          *reinterpret_cast<uint4*>(p.part_o + (sp.part + r) * D + e * 4) = x;
       }
     }
   }
@@ -848,7 +887,7 @@ static cudaError_t launch_tc8(const CUtensorMap* tm, const Kv8AttnParams& p, cud
       cudaFuncSetAttribute(attn_kv8_tc_kernel<D, NG>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (err != cudaSuccess) return err;
   attn_kv8_tc_kernel<D, NG>
-      <<<dim3(p.n_rt, p.n_split, p.B * p.Hkv), C::kThreads, C::kSmem, stream>>>(tm[0], tm[1], tm[2], tm[3], p);
+      <<<p.n_rt * p.Hkv * (p.B * p.base + p.extra), C::kThreads, C::kSmem, stream>>>(tm[0], tm[1], tm[2], tm[3], p);
   return cudaGetLastError();
 }
 

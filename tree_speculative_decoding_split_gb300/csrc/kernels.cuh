@@ -279,19 +279,25 @@ struct Kv8AttnParams {
   const int32_t* table;   // [B][max_blocks]
   uint16_t* out;
   float* lse;
-  float* part_o;          // [B*N*Hq][n_split][d] unnormalised partial rows
-  float2* part_ml;        // [B*N*Hq][n_split] (reference maximum in log2 units, sum); sum < 0 = bad request
+  float* part_o;          // [CTA][row of the CTA][d] unnormalised partial rows
+  float2* part_ml;        // [CTA][row of the CTA] (reference maximum in log2 units, sum); sum < 0 = bad request
+  int2* used;             // [B] splits of the request and the first of its extra units, for the merge; null when no request can be split
   int32_t* dev_status;
   int B, N, Hq, Hkv, G, d, bs, bs_shift, max_blocks, num_blocks;
   long long L_cap;
-  int n_split;            // key splits at most; a request uses as many as its own length fills
+  int base;               // units (Hkv * n_rt CTAs) of the grid per request
+  int extra;              // units behind them, for further splits
+  int rows_cta;           // rows of a CTA
   uint32_t g_magic;       // floor(2^32 / G) + 1 (G > 1): row / G = umulhi(row, g_magic) while row * G < 2^32
   int unit_shift;         // splits are whole steps of 2^unit_shift keys
   int n_rt;               // row tiles of (node, head) rows per KV head
+  float inv_slots;        // 1 / CTAs that run at once
+  int fixed_steps;        // a CTA's work beside its keys, in steps
   float scale_log2;
 };
 struct Kv8AttnPlan {
-  int n_split, n_rt, unit_shift;
+  int base, extra, n_rt, unit_shift, slots, fixed_steps, rows_cta;
+  bool merge() const { return base > 1 || extra > 0; }
   int groups;             // 0: the few-rows kernel; 1, 2: groups of 128 rows per CTA of the tensor-core kernel
 };
 Kv8AttnPlan plan_attention_kv8(int B, int N, int G, int Hkv, long long L_cap, int num_sms);

@@ -78,7 +78,7 @@ spec_status check_attn_kv8(const spec_attn_kv8_args* a) {
   if (a->batch < 1 || a->n_max < 1 || a->num_q_heads < 1 || a->num_kv_heads < 1) return SPEC_ERR_INVALID_ARGUMENT;
   if (a->n_max > SPEC_MAX_NODES) return SPEC_ERR_UNSUPPORTED;
   if (a->num_q_heads % a->num_kv_heads) return SPEC_ERR_INVALID_ARGUMENT;
-  if ((long long)a->batch * a->num_kv_heads > 65535) return SPEC_ERR_UNSUPPORTED;  // grid.z
+  if ((long long)a->batch * a->num_kv_heads > 65535) return SPEC_ERR_UNSUPPORTED;  // keeps the grid and its row offsets within 32 bits
   const spec_status ps = check_paged(a->block_size, a->max_blocks, a->num_blocks, a->num_kv_heads,
                                      (long long)a->max_blocks * a->block_size);
   if (ps != SPEC_OK) return ps;
@@ -97,6 +97,7 @@ spec_status check_attn_kv8(const spec_attn_kv8_args* a) {
 struct AttnKv8Layout {
   float* part_o;
   float2* part_ml;
+  int2* used;
   Kv8AttnPlan plan;
   size_t bytes;
 };
@@ -105,10 +106,12 @@ AttnKv8Layout layout_attn_kv8(const spec_attn_kv8_args* a, void* ws) {
   AttnKv8Layout l;
   l.plan = plan_attention_kv8(a->batch, a->n_max, a->num_q_heads / a->num_kv_heads, a->num_kv_heads,
                               (long long)a->max_blocks * a->block_size, num_sms_current());
-  const size_t rows = l.plan.n_split > 1 ? (size_t)a->batch * a->n_max * a->num_q_heads : 0;
+  const size_t rows = !l.plan.merge() ? 0
+                                      : (size_t)(a->batch * l.plan.base + l.plan.extra) * a->num_kv_heads * l.plan.n_rt * l.plan.rows_cta;
   Carver c(ws);
-  l.part_ml = c.take<float2>(rows * l.plan.n_split + 1);
-  l.part_o = c.take<float>(rows * l.plan.n_split * a->head_dim);
+  l.used = c.take<int2>(a->batch);
+  l.part_ml = c.take<float2>(rows);
+  l.part_o = c.take<float>(rows * a->head_dim);
   l.bytes = c.off;
   return l;
 }
@@ -161,17 +164,19 @@ spec_status spec_tree_attention_kv8(const spec_attn_kv8_args* a, void* workspace
   p.k_scale = a->k_scale; p.v_scale = a->v_scale;
   p.prefix_len = a->prefix_len; p.n_nodes = a->n_nodes; p.parent = a->parent; p.table = a->block_table;
   p.out = static_cast<uint16_t*>(a->out); p.lse = a->lse;
-  p.part_o = l.part_o; p.part_ml = l.part_ml;
+  p.part_o = l.part_o; p.part_ml = l.part_ml; p.used = l.plan.merge() ? l.used : nullptr;
   p.dev_status = dev_status;
   p.B = a->batch; p.N = a->n_max; p.Hq = a->num_q_heads; p.Hkv = a->num_kv_heads; p.G = p.Hq / p.Hkv;
   p.g_magic = p.G > 1 ? (uint32_t)((1ull << 32) / (uint32_t)p.G) + 1u : 0u;
   p.d = a->head_dim; p.bs = a->block_size; p.bs_shift = log2_of(a->block_size);
   p.max_blocks = a->max_blocks; p.num_blocks = a->num_blocks;
   p.L_cap = (long long)a->max_blocks * a->block_size;
-  p.n_split = l.plan.n_split; p.n_rt = l.plan.n_rt;
+  p.base = l.plan.base; p.extra = l.plan.extra; p.rows_cta = l.plan.rows_cta; p.n_rt = l.plan.n_rt;
   const float scale = a->scale > 0.f ? a->scale : 1.f / std::sqrt((float)a->head_dim);
   p.scale_log2 = scale * 1.4426950408889634f;
   p.unit_shift = l.plan.unit_shift;
+  p.inv_slots = 1.f / (float)l.plan.slots;
+  p.fixed_steps = l.plan.fixed_steps;
   CUtensorMap tm[4];
   const long long heads = (long long)a->num_blocks * a->num_kv_heads;
   const int box = l.plan.groups == 0 ? 16 : (p.bs < 128 ? p.bs : 128);
@@ -190,7 +195,7 @@ spec_status spec_tree_attention_kv8(const spec_attn_kv8_args* a, void* workspace
       return SPEC_ERR_CUDA;
     if (launch_attention_kv8_tc(tm, p, l.plan.groups, stream) != cudaSuccess) return SPEC_ERR_CUDA;
   }
-  if (p.n_split > 1 && launch_attention_kv8_merge(p, stream) != cudaSuccess) return SPEC_ERR_CUDA;
+  if (p.used && launch_attention_kv8_merge(p, stream) != cudaSuccess) return SPEC_ERR_CUDA;
   return SPEC_OK;
 }
 
