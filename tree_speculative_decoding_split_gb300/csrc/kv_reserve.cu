@@ -27,25 +27,49 @@ __device__ __forceinline__ int owner_of(const int* start, int n, int x) {
   return lo;
 }
 
-// Inclusive scan of one value per thread over the block; `total` gets the sum.
-template <typename T>
-__device__ __forceinline__ T block_scan(T v, T* s_warp, T* total) {
+// What a thread's requests give back, take and add.
+struct Sums {
+  int rel, need;
+  long long rows;
+};
+// Inclusive scan of one record per thread over the block; `total` gets the sum.
+__device__ __forceinline__ Sums block_scan(Sums v, Sums* s_warp, Sums* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const T u = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += u;
+    const int r = __shfl_up_sync(0xffffffffu, v.rel, o), t = __shfl_up_sync(0xffffffffu, v.need, o);
+    const long long a = __shfl_up_sync(0xffffffffu, v.rows, o);
+    if (lane >= o) {
+      v.rel += r;
+      v.need += t;
+      v.rows += a;
+    }
   }
   if (lane == 31) s_warp[warp] = v;
   __syncthreads();
-  T before = 0, all = 0;
-  for (int w = 0; w < nw; ++w) {
-    if (w < warp) before += s_warp[w];
-    all += s_warp[w];
+  // every warp scans the warps' sums (32 at most)
+  Sums w = lane < nw ? s_warp[lane] : Sums{0, 0, 0};
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int r = __shfl_up_sync(0xffffffffu, w.rel, o), t = __shfl_up_sync(0xffffffffu, w.need, o);
+    const long long a = __shfl_up_sync(0xffffffffu, w.rows, o);
+    if (lane >= o) {
+      w.rel += r;
+      w.need += t;
+      w.rows += a;
+    }
   }
-  __syncthreads();
-  *total = all;
-  return v + before;
+  const int prev = max(warp - 1, 0);
+  const Sums before{__shfl_sync(0xffffffffu, w.rel, prev), __shfl_sync(0xffffffffu, w.need, prev),
+                    __shfl_sync(0xffffffffu, w.rows, prev)};
+  *total = Sums{__shfl_sync(0xffffffffu, w.rel, 31), __shfl_sync(0xffffffffu, w.need, 31),
+                __shfl_sync(0xffffffffu, w.rows, 31)};
+  if (warp > 0) {
+    v.rel += before.rel;
+    v.need += before.need;
+    v.rows += before.rows;
+  }
+  return v;
 }
 
 // The pool row of slot `pos` of request b, or -1 (an unserved request's, or one behind its table).
@@ -68,8 +92,7 @@ __device__ __forceinline__ bool served(const ReserveParams& p, int b, int len, i
 // With `map` (single CTA only) the slot map is written here as well.
 __global__ void __launch_bounds__(1024) kv_reserve_kernel(const ReserveParams p, int map) {
   extern __shared__ int s_plan[];
-  __shared__ long long s_w64[32];
-  __shared__ int s_w32[32];
+  __shared__ Sums s_warp[32];
   const int B = p.B, T = blockDim.x, tid = threadIdx.x;
   int* s_base = s_plan;             // min(held, want): where what is given back or taken begins; -1 = refused
   int* s_rel = s_base + B;          // [B + 1] blocks given back before b
@@ -79,8 +102,8 @@ __global__ void __launch_bounds__(1024) kv_reserve_kernel(const ReserveParams p,
   // ---- scan ----
   const int per = (B + T - 1) / T;
   const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
-  int rel = 0, need = 0, refused = 0;
-  long long rows = 0;
+  int refused = 0;
+  Sums mine{0, 0, 0};
   for (int b = b0; b < b1; ++b) {
     const int len = p.seq_len[b], add = p.n_new[b], held = p.n_blocks[b];
     const long long want = ((long long)len + add + p.bs - 1) >> p.bs_shift;
@@ -91,15 +114,16 @@ __global__ void __launch_bounds__(1024) kv_reserve_kernel(const ReserveParams p,
     s_rel[b] = r;
     s_need[b] = t;
     s_row[b] = max(add, 0);
-    rel += r;
-    need += t;
-    rows += max(add, 0);
+    mine.rel += r;
+    mine.need += t;
+    mine.rows += max(add, 0);
   }
-  int R, A;
-  long long total;
-  int rel0 = block_scan(rel, s_w32, &R) - rel;
-  int need0 = block_scan(need, s_w32, &A) - need;
-  long long row0 = block_scan(rows, s_w64, &total) - rows;
+  Sums all;
+  const Sums incl = block_scan(mine, s_warp, &all);
+  int rel0 = incl.rel - mine.rel, need0 = incl.need - mine.need;
+  long long row0 = incl.rows - mine.rows;
+  const int R = all.rel, A = all.need;
+  const long long total = all.rows;
   const long long row_cap = p.slot_map ? p.slot_cap : 0x7fffffffLL;
   const bool fatal = f < 0 || f > p.num_blocks || (long long)f + R > p.num_blocks || total > row_cap;
   for (int b = b0; b < b1; ++b) {
