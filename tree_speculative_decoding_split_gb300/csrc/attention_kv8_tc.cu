@@ -181,8 +181,8 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
   uint4 qv[kQPer];
   int par0 = -1;
   auto early = [&]() {
-    if (tid < p.N) par0 = p.parent[(size_t)sp.b * p.N + tid];
     if (warp >= 4) {
+      if (tid - 128 < p.N) par0 = p.parent[(size_t)sp.b * p.N + tid - 128];
 #pragma unroll
       for (int k = 0; k < kQPer; ++k) {
         const int c = tid - 128 + k * 256 * NG, row = sp.rt * kRowsCta + c / (D / 8);
@@ -198,30 +198,7 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
     const Kv8Work w = kv8_begin(p, sp);
     if (lane == 0) s_work = w;
   }
-  __syncthreads();
-  sp = s_work;
-  if (sp.b < 0) return;
-  if (!own) early();
-  const int b = sp.b, h = sp.h, rt = sp.rt, split = sp.split, n = sp.nodes;
-  const long long L = sp.L;
-  int err = sp.err;
-  const int row0 = rt * kRowsCta, rows = p.N * p.G;
-  auto orow_of = [&](int row) { return kv8_row(p, b, h, row); };
-  // rows of a refused request or of padded nodes; with several splits the merge writes them
-  auto refuse = [&]() {
-    for (int c = tid; c < kRowsCta * (D / 8); c += C::kThreads) {
-      const int row = row0 + c / (D / 8), e = c % (D / 8);
-      if (row >= rows) continue;
-      const size_t o = orow_of(row);
-      if (sp.n == 1) {
-        *reinterpret_cast<uint4*>(p.out + o * D + e * 8) = make_uint4(0, 0, 0, 0);
-        if (e == 0 && p.lse) p.lse[o] = 0.f;
-      } else if (e == 0) {
-        p.part_ml[sp.part + (row - row0)] = make_float2(0.f, -1.f);
-      }
-    }
-  };
-  if (tid == 0) {
+  if (tid == 32) {
     for (int s = 0; s < kKS; ++s) {
       mbar_init(&kfull[s], 1);
       mbar_init(&kempty[s], 1);
@@ -250,6 +227,30 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
     s_vissued = 0;
     fence_mbar_init();
   }
+  if (warp == 2 && lane < kAncWords) s_odd[lane] = 0u;
+  __syncthreads();
+  sp = s_work;
+  if (sp.b < 0) return;
+  if (!own) early();
+  const int b = sp.b, h = sp.h, rt = sp.rt, split = sp.split, n = sp.nodes;
+  const long long L = sp.L;
+  int err = sp.err;
+  const int row0 = rt * kRowsCta, rows = p.N * p.G;
+  auto orow_of = [&](int row) { return kv8_row(p, b, h, row); };
+  // rows of a refused request or of padded nodes; with several splits the merge writes them
+  auto refuse = [&]() {
+    for (int c = tid; c < kRowsCta * (D / 8); c += C::kThreads) {
+      const int row = row0 + c / (D / 8), e = c % (D / 8);
+      if (row >= rows) continue;
+      const size_t o = orow_of(row);
+      if (sp.n == 1) {
+        *reinterpret_cast<uint4*>(p.out + o * D + e * 8) = make_uint4(0, 0, 0, 0);
+        if (e == 0 && p.lse) p.lse[o] = 0.f;
+      } else if (e == 0) {
+        p.part_ml[sp.part + (row - row0)] = make_float2(0.f, -1.f);
+      }
+    }
+  };
   // ---- this CTA's tiles: the tree's (in the last split) and then keys [k0, k1) of the prefix ----
   const bool tree = split == sp.n - 1;
   const long long k0 = ((long long)split * sp.steps) << p.unit_shift;
@@ -271,10 +272,6 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
   };
   // the block of tile u is loaded two tiles ahead and its scales one tile ahead of its requests
   int blk0 = -1, blk1 = -1;
-  if (warp == 0) {
-    blk0 = entry(0);
-    blk1 = entry(1);
-  }
   float ks0 = 0.f, vs0 = 0.f;
   auto scales = [&](int blk, float* ks, float* vs) {
     *ks = 0.f;
@@ -309,23 +306,21 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
             s_bad = 1;
           }
         }
+      }
+      // the copies first; the barrier's own arrival follows the scales, which the tile's readers need as well
+      if (u < 0) {
+        if (lane < D / 64) tma_load_4d(dk + lane * kTT * 128, &tmKt, &kfull[ks], lane * 64, h, t * kTT, b);
+      } else if (lane < nbox) {
+        tma_load_3d(dk + lane * box * D, &tmK, &kfull[ks], 0, y, z);
         // scales of the box's 16-key groups: K scale, log2 and reciprocal of the V scale
-        if (lane < nbox) {
-          const float sv = kv8_clamp_scale(vs0);
-          const float4 c = make_float4(kv8_clamp_scale(ks0), __log2f(sv), __fdividef(1.f, sv), 0.f);
-          for (int j = 0; j < box / 16; ++j) s_cst[(t % kCS) * 8 + lane * (box / 16) + j] = c;
-        }
+        const float sv = kv8_clamp_scale(vs0);
+        const float4 c = make_float4(kv8_clamp_scale(ks0), __log2f(sv), __fdividef(1.f, sv), 0.f);
+        for (int j = 0; j < box / 16; ++j) s_cst[(t % kCS) * 8 + lane * (box / 16) + j] = c;
       }
       __syncwarp();
       if (lane == 0) {
         mbar_arrive_expect_tx(&kfull[ks], C::kSlot);
         s_kissued = t + 1;
-      }
-      __syncwarp();
-      if (u < 0) {
-        if (lane < D / 64) tma_load_4d(dk + lane * kTT * 128, &tmKt, &kfull[ks], lane * 64, h, t * kTT, b);
-      } else if (lane < nbox) {
-        tma_load_3d(dk + lane * box * D, &tmK, &kfull[ks], 0, y, z);
       }
       const bool gotv = lane == 0 ? mbar_wait_bounded(&vempty[vs], ((t / kVS) & 1) ^ 1, &s_abort) : true;
       if (!__shfl_sync(0xffffffffu, gotv, 0)) return false;
@@ -346,41 +341,31 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
     }
     return true;
   };
-  const int pre = min(T, kVS);
-  if (warp == 0) produce(0, pre);
-  auto drain = [&]() {  // a CTA that leaves early lets them land
-    if (tid == 0)
-      for (int t = 0; t < pre; ++t) {
-        mbar_wait_bounded(&kfull[t], 0, nullptr);
-        mbar_wait_bounded(&vfull[t], 0, nullptr);
+  // While warp 0 asks for the first table entries and the tree's tiles, warp 1 takes the TMEM and warps 4..11 look
+  // at the tree; one barrier joins them.
+  const int pre = min(Tt, kVS);
+  bool bad_tree = err == SPEC_ERR_BAD_TREE;
+  if (warp == 0) {
+    blk0 = entry(0);
+    blk1 = entry(1);
+    produce(0, pre);
+  } else if (warp == 1) {
+    tmem_alloc(&s_tmem, 512);
+    tmem_relinquish();
+  } else if (warp >= 4) {
+    if (warp < 12) {
+      const int i = tid - 128;  // (256 threads, at most 255 nodes)
+      if (i < n) {
+        s_par[i] = par0;
+        bad_tree |= i == 0 ? par0 != -1 : (par0 < 0 || par0 >= i);
       }
-  };
-  if (tid < kAncWords) s_odd[tid] = 0u;
-  if (const int i = tid; i < n) {  // (there are more threads than nodes)
-    const int par = par0;
-    s_par[i] = par;
-    if (i == 0 ? par != -1 : (par < 0 || par >= i)) err = SPEC_ERR_BAD_TREE;
-  }
-  if (__syncthreads_or(err == SPEC_ERR_BAD_TREE)) err = SPEC_ERR_BAD_TREE;
-  if (err) {
-    if (tid == 0 && rt == 0 && split == 0 && h == 0) set_status(p.dev_status, err);
-    refuse();
-    drain();
-    return;
-  }
-  if (row0 >= n * p.G) {
-    if (sp.n == 1) refuse();
-    drain();
-    return;
-  }
-  if (tree)
-    if (const int i = tid; i < n) {  // (there are more threads than nodes)
-      uint32_t* w = s_nanc + i * kAncWords;
+      if (!bar_or(10, 256, bad_tree) && tree && i < n) {  // ancestors-or-self
+        uint32_t* w = s_nanc + i * kAncWords;
 #pragma unroll
-      for (int j = 0; j < kAncWords; ++j) w[j] = 0u;
-      for (int a = i; a >= 0; a = s_par[a]) w[a >> 5] |= 1u << (a & 31);
+        for (int j = 0; j < kAncWords; ++j) w[j] = 0u;
+        for (int a = i; a >= 0; a = s_par[a]) w[a >> 5] |= 1u << (a & 31);
+      }
     }
-  if (warp >= 4) {
 #pragma unroll
     for (int k = 0; k < kQPer; ++k) {
       const int c = tid - 128 + k * 256 * NG, rr = c / (D / 8);
@@ -388,12 +373,20 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
     }
     fence_proxy_async_smem();
   }
-  if (warp == 1) {
-    tmem_alloc(&s_tmem, 512);
-    tmem_relinquish();
-  }
   tc_fence_before();
-  __syncthreads();
+  if (__syncthreads_or(bad_tree)) err = SPEC_ERR_BAD_TREE;
+  if (err || row0 >= n * p.G) {  // refused, or padded nodes only (with several splits the merge zeroes those)
+    if (err && tid == 0 && rt == 0 && split == 0 && h == 0) set_status(p.dev_status, err);
+    if (err || sp.n == 1) refuse();
+    if (tid == 0)  // the copies land first
+      for (int t = 0; t < pre; ++t) {
+        mbar_wait_bounded(&kfull[t], 0, nullptr);
+        mbar_wait_bounded(&vfull[t], 0, nullptr);
+      }
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(s_tmem, 512);
+    return;
+  }
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   // register shares of the warpgroups (two groups): 64 + 4 x 104 within the 5 x 96 the block was launched with

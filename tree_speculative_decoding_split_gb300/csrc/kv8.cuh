@@ -57,10 +57,10 @@ struct Kv8Work {
 //   few-rows kernel: `base` splits, more where one of them would be longer than two even shares of all the steps.  Its
 //   CTAs share the memory's bandwidth, so that it only has to keep one long request from running on alone.  Splits
 //   past base are then no more than slots / (2 * heads) units.
-//   tensor-core kernel, where a CTA's speed is its own: c steps at most, the one of ceil(longest / k), k = 1 .. 32,
-//   that fits the units with the least cost.  With a split's work w = c + fixed, the whole work W and `slots` CTAs at
+//   tensor-core kernel, where a CTA's speed is its own: c steps at most, the one of ceil(longest / k), for 16 numbers k
+//   from 1 to 32, that fits the units with the least cost.  With a split's work w = c + fixed, the whole work W and `slots` CTAs at
 //   once, the cost is the lesser of two upper bounds, whole rounds of CTAs times w and (W - w) / slots + w.  One warp
-//   evaluates it, a lane per k.  Over 128 requests c = ceil(all steps / extra) instead, which always fits.
+//   evaluates it, two lanes per k.  Over 128 requests c = ceil(all steps / extra) instead, which always fits.
 __device__ __forceinline__ int kv8_steps(const Kv8AttnParams& p, int len) {
   return len > 0 && len <= p.L_cap ? (int)(((long long)len + (1 << p.unit_shift) - 1) >> p.unit_shift) : 0;
 }
@@ -75,27 +75,35 @@ __device__ __forceinline__ int kv8_cut(const Kv8AttnParams& p) {
     longest = max(longest, steps);
   }
   total = warp_sum(total);
-  if (p.unit_shift == 6 || p.B > 128) {
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  if (p.unit_shift == 6 || p.B > 128 || longest > 65535) {
     const float share = p.unit_shift == 6 ? 2.f * total * (float)(p.Hkv * p.n_rt) * p.inv_slots : total / (float)p.extra;
     return max(least, (int)fminf(ceilf(share * 1.0001f), 1e9f));
   }
-  longest = __reduce_max_sync(0xffffffffu, longest);
-  const int c = max(least, (longest + lane) / (lane + 1));
+  // two lanes per candidate, each over every other request
+  const int nth = lane >> 1, k = nth < 8 ? nth + 1 : nth < 12 ? 2 * nth - 6 : 4 * nth - 28;
+  const int c = max(least, (longest + k - 1) / k);
   const float rc = __fdividef(1.f, (float)c);
   int units = 0, past = 0;
+  for (int i0 = 0; i0 < p.B; i0 += 32) {
+    const float steps = (float)(i0 + lane < p.B ? kv8_steps(p, p.prefix_len[i0 + lane]) : 0) - 0.5f;
+    const int here = min(32, p.B - i0);
 #pragma unroll 4
-  for (int i = 0; i < p.B; ++i) {  // max(1, ceil(steps / c)); the product is off by one at most
-    const int steps = kv8_steps(p, p.prefix_len[i]);
-    const int q = (int)((float)steps * rc), r = steps - q * c;
-    const int n = max(1, q + (r > 0) + (r > c) - (r <= -c));
-    units += n;
-    past += max(0, n - p.base);
+    for (int i = 0; i < here; i += 2) {
+      // max(1, ceil(steps / c)) - 1, exactly: (steps - 1/2) / c keeps 1 / (2 c) >= 2^-17 from every whole number,
+      // and below 33 its error is less
+      const int n = (int)(__shfl_sync(0xffffffffu, steps, i + (lane & 1)) * rc);
+      units += n;
+      past += max(0, n + 1 - p.base);  // (a lane past the last request holds -1/2: none)
+    }
   }
+  units += __shfl_xor_sync(0xffffffffu, units, 1) + p.B;
+  past += __shfl_xor_sync(0xffffffffu, past, 1);
   const float heads = (float)(p.Hkv * p.n_rt), w = (float)(c + p.fixed_steps);
   const float work = heads * (total + (float)units * (float)p.fixed_steps) * p.inv_slots;
   float cost = fminf(ceilf((float)units * heads * p.inv_slots) * w, work + w * (1.f - p.inv_slots));
   if (units > p.B) cost += 3.f;  // the merge
-  const bool fits = lane == 0 || past <= p.extra;
+  const bool fits = k == 1 || past <= p.extra;
   const uint32_t key = fits ? (__float_as_uint(cost) & ~31u) | (uint32_t)lane : 0xffffffffu;
   return __shfl_sync(0xffffffffu, c, (int)(__reduce_min_sync(0xffffffffu, key) & 31u));
 }
