@@ -175,23 +175,33 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   __shared__ Kv8Work s_work;
   Kv8Work sp = kv8_own(p);
-  // the queries (16 bytes a lane, whole rows side by side) and the tree's links, on their way while the lengths are
-  // read and the checks run
-  constexpr int kQPer = kRowsCta * (D / 8) / (256 * NG);
-  uint4 qv[kQPer];
+  // The queries (16 bytes a lane, whole rows side by side) and the tree's links, on their way while the lengths are
+  // read and the checks run.  As bf16 the queries lie where V tiles in f16 will; the tree's scores are the only ones
+  // to read them there, the prefix's take them from sQ.
+  constexpr int kQPer = kGR8 * (D / 8) / 256;
+  auto q_chunk = [&](int k, int* rr, int* ch) {  // the k-th chunk of this (softmax) thread
+    const int c = ((tid - 128) & 255) + k * 256;
+    *rr = (warp - 4) / 8 * kGR8 + c / (D / 8);
+    *ch = c % (D / 8);
+  };
+  auto q16_at = [&](int rr, int ch) { return sV16 + (rr / kGR8) * C::kQ + tile16_off(rr % kGR8, ch, kGR8); };
   int par0 = -1;
   auto early = [&]() {
-    if (warp >= 4) {
-      if (tid - 128 < p.N) par0 = p.parent[(size_t)sp.b * p.N + tid - 128];
-#pragma unroll
-      for (int k = 0; k < kQPer; ++k) {
-        const int c = tid - 128 + k * 256 * NG, row = sp.rt * kRowsCta + c / (D / 8);
-        qv[k] = make_uint4(0, 0, 0, 0);
-        if (row < p.N * p.G)
-          qv[k] = *reinterpret_cast<const uint4*>(p.q + kv8_row(p, sp.b, sp.h, row) * D + (c % (D / 8)) * 8);
-      }
+    if (warp < 4) return;
+    if (tid - 128 < p.N) par0 = p.parent[(size_t)sp.b * p.N + tid - 128];
+#pragma unroll 2
+    for (int k = 0; k < kQPer; ++k) {
+      int rr, ch;
+      q_chunk(k, &rr, &ch);
+      const int row = sp.rt * kRowsCta + rr;
+      const bool in = row < p.N * p.G;  // (zeros otherwise)
+      const uint16_t* from = p.q + kv8_row(p, sp.b, sp.h, in ? row : 0) * D + ch * 8;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(q16_at(rr, ch))), "l"(from),
+                   "r"(in ? 16 : 0)
+                   : "memory");
     }
   };
+  auto early_done = [&]() { asm volatile("cp.async.wait_all;" ::: "memory"); };
   const bool own = sp.b >= 0;
   if (own) early();
   if (warp == 0) {
@@ -230,7 +240,10 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
   if (warp == 2 && lane < kAncWords) s_odd[lane] = 0u;
   __syncthreads();
   sp = s_work;
-  if (sp.b < 0) return;
+  if (sp.b < 0) {
+    early_done();
+    return;
+  }
   if (!own) early();
   const int b = sp.b, h = sp.h, rt = sp.rt, split = sp.split, n = sp.nodes;
   const long long L = sp.L;
@@ -366,11 +379,7 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
         for (int a = i; a >= 0; a = s_par[a]) w[a >> 5] |= 1u << (a & 31);
       }
     }
-#pragma unroll
-    for (int k = 0; k < kQPer; ++k) {
-      const int c = tid - 128 + k * 256 * NG, rr = c / (D / 8);
-      *reinterpret_cast<uint4*>(sQ + (rr / kGR8) * C::kQ + tile16_off(rr % kGR8, c % (D / 8), kGR8)) = qv[k];
-    }
+    early_done();
     fence_proxy_async_smem();
   }
   tc_fence_before();
@@ -420,7 +429,8 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
     int kst = 0;  // ring stage of the next S tile
     auto issue_s = [&](auto tree_tile, int t, int g) {
       const uint32_t ts = tm + C::kColS + (NG == 2 ? g : t % C::kNB) * 128;
-      const uint32_t qa = q16 + g * (C::kQ >> 4), ka = k16 + kst * (C::kSlot >> 4);
+      const uint32_t qa = (tree_tile.value ? v16 + (kVS * C::kSlot >> 4) : q16) + g * (C::kQ >> 4);
+      const uint32_t ka = k16 + kst * (C::kSlot >> 4);
       if (leader) {
         if constexpr (tree_tile.value) {
 #pragma unroll
@@ -513,6 +523,16 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
         ok = __all_sync(0xffffffffu, mbar_wait_bounded(&vfull[t % kVS], (t / kVS) & 1, &s_abort) &&
                                          mbar_wait_bounded(&v16empty[t % kV16], ((t / kV16) & 1) ^ 1, &s_abort));
         if (!ok) break;
+        // the queries as bf16 are done with: read by their own threads, and by the tree's last scores (waited for
+        // ahead of the word that lets the next ones begin, which would turn the barrier's phase over)
+        if (t == Tt) {
+          for (int g = 0; g < NG && ok; ++g) ok = mbar_wait_bounded(&qready[g], 0, &s_abort);
+        } else if (t == Tt - 1) {
+          for (int g = 0; g < NG && ok; ++g)
+            ok = mbar_wait_bounded(&sfull[g][t % C::kNB], (t / C::kNB) & 1, &s_abort);
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
         uint8_t* src = sV + (t % kVS) * C::kSlot;
         if (t < Tt) {
           // a tree tile stays bf16; elements that are no finite numbers become 0 and their rows are noted
@@ -591,45 +611,41 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, &s_abort));
     };
-    // this thread's half of its row's dimensions, from bf16 to e4m3 hi and lo in the same place
-    auto split_q = [&]() {
-      uint4 w[D / 16];
-      float mx = 0.f;
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        w[i] = *reinterpret_cast<const uint4*>(myQ + tile16_off(rl, half * (D / 16) + i, kGR8));
-        const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          mx = max3(mx, fabsf(__uint_as_float(x[j] << 16)), fabsf(__uint_as_float(x[j] & 0xFFFF0000u)));
-      }
-      s_x[g][half][rl] = mx;
-      named_bar_sync(10 + g, 256);  // the group has read what it is about to write over
-      mx = fmaxf(mx, s_x[g][half ^ 1][rl]);
-      const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 100);
-      const float up = __uint_as_float((uint32_t)(127 + 7 - e) << 23);  // largest element into [128, 256)
-      qf = __uint_as_float((uint32_t)(127 - 7 + e) << 23) * p.scale_log2;
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        uint32_t hi[4], lo[4];
+    // the group's queries from bf16 to e4m3 hi and lo, as they were fetched: D / 8 neighbouring lanes hold a row
+    if (T > Tt) {
+#pragma unroll 1
+      for (int k = 0; k < kQPer; ++k) {
+        int r, ch;
+        q_chunk(k, &r, &ch);
+        const uint4 v = *reinterpret_cast<const uint4*>(q16_at(r, ch));
+        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+        float f[8], mx = 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint4 v = w[2 * i + (j >> 1)];
-          const uint32_t a = (j & 1) ? v.z : v.x, c = (j & 1) ? v.w : v.y;
-          const float f[4] = {__uint_as_float(a << 16) * up, __uint_as_float(a & 0xFFFF0000u) * up,
-                              __uint_as_float(c << 16) * up, __uint_as_float(c & 0xFFFF0000u) * up};
-          hi[j] = e4m3x4(head4(f[0]), head4(f[1]), head4(f[2]), head4(f[3]));
-          lo[j] = e4m3x4(f[0] - head4(f[0]), f[1] - head4(f[1]), f[2] - head4(f[2]), f[3] - head4(f[3]));
+          f[2 * j] = __uint_as_float(x[j] << 16);
+          f[2 * j + 1] = __uint_as_float(x[j] & 0xFFFF0000u);
+          mx = max3(mx, fabsf(f[2 * j]), fabsf(f[2 * j + 1]));
         }
-        const int ch = half * (D / 32) + i;
-        *reinterpret_cast<uint4*>(myQ + kv8_off<D>(rl, ch)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(myQ + kGR8 * D + kv8_off<D>(rl, ch)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+#pragma unroll
+        for (int o = 1; o < D / 8; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 100);
+        const float up = __uint_as_float((uint32_t)(127 + 7 - e) << 23);  // largest element into [128, 256)
+        if (ch == 0) s_x[g][0][r % kGR8] = __uint_as_float((uint32_t)(127 - 7 + e) << 23) * p.scale_log2;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] *= up;
+        uint8_t* to = myQ + kv8_off<D>(r % kGR8, ch >> 1) + (ch & 1) * 8;
+        *reinterpret_cast<uint2*>(to) = make_uint2(e4m3x4(head4(f[0]), head4(f[1]), head4(f[2]), head4(f[3])),
+                                                   e4m3x4(head4(f[4]), head4(f[5]), head4(f[6]), head4(f[7])));
+        *reinterpret_cast<uint2*>(to + kGR8 * D) =
+            make_uint2(e4m3x4(f[0] - head4(f[0]), f[1] - head4(f[1]), f[2] - head4(f[2]), f[3] - head4(f[3])),
+                       e4m3x4(f[4] - head4(f[4]), f[5] - head4(f[5]), f[6] - head4(f[6]), f[7] - head4(f[7])));
       }
       fence_proxy_async_smem();
-      __syncwarp();
+      named_bar_sync(10 + g, 256);
+      qf = s_x[g][0][rl];
       if (lane == 0) mbar_arrive(&qready[g]);
-    };
-    if (Tt == 0) split_q();
+      named_bar_sync(10 + g, 256);  // s_x is free again
+    }
 
     float m = -INFINITY, l = 0.f;  // the row's reference (P = 2^(y - m)), and the sum over this thread's keys
     const uint32_t* anc = s_nanc + (live ? kv8_node(p, row) : 0) * kAncWords;
@@ -679,7 +695,6 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
         uint32_t x[32];
         tmem_ld_x32(ts + half * 32, x);
         tmem_ld_wait();
-        if (t == Tt - 1 && T > Tt) split_q();  // the last product with the bf16 queries is done
         const uint32_t bits = live ? anc[2 * t + half] : 0u;
         float top = -INFINITY;
 #pragma unroll
