@@ -163,7 +163,8 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
   float4* s_cst = reinterpret_cast<float4*>(s_nanc + (kMaxNodes + 1) * kAncWords);  // [stage][16-key group]
   __shared__ uint64_t kfull[kKS], kempty[kKS], vfull[kVS], vempty[kVS], v16empty[kV16];
   // per group, and per buffer where there are two (one barrier could be two phases on)
-  __shared__ uint64_t sfull[NG][C::kNB], pfull[NG][2], ofull[NG], qready[NG];
+  __shared__ uint64_t sfull[NG][C::kNB], pfull[NG][2], ofull[NG];
+  __shared__ float s_qf[NG][kGR8];
   __shared__ float s_x[NG][2][kGR8];  // a row's threads tell each other their largest score; at the end, their sums
   __shared__ uint32_t s_w[NG][2][4];  // ... and which of the warp's rows move
   __shared__ uint64_t s_drained;
@@ -175,134 +176,117 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   __shared__ Kv8Work s_work;
   Kv8Work sp = kv8_own(p);
-  // The queries (16 bytes a lane, whole rows side by side) and the tree's links, on their way while the lengths are
-  // read and the checks run.  As bf16 the queries lie where V tiles in f16 will; the tree's scores are the only ones
-  // to read them there, the prefix's take them from sQ.
-  constexpr int kQPer = kGR8 * (D / 8) / 256;
-  auto q_chunk = [&](int k, int* rr, int* ch) {  // the k-th chunk of this (softmax) thread
-    const int c = ((tid - 128) & 255) + k * 256;
-    *rr = (warp - 4) / 8 * kGR8 + c / (D / 8);
-    *ch = c % (D / 8);
-  };
-  auto q16_at = [&](int rr, int ch) { return sV16 + (rr / kGR8) * C::kQ + tile16_off(rr % kGR8, ch, kGR8); };
-  int par0 = -1;
-  auto early = [&]() {
+  if (warp == 1) {
+    if (lane == 0) {
+      for (int s = 0; s < kKS; ++s) {
+        mbar_init(&kfull[s], 1);
+        mbar_init(&kempty[s], 1);
+      }
+      for (int s = 0; s < kVS; ++s) {
+        mbar_init(&vfull[s], 1);
+        mbar_init(&vempty[s], 2);
+      }
+      for (int s = 0; s < kV16; ++s) mbar_init(&v16empty[s], 1);
+      for (int g = 0; g < NG; ++g) {
+        for (int i = 0; i < C::kNB; ++i) mbar_init(&sfull[g][i], 1);
+        // a tile's weights are there; for group 0 also its V, and the keys of the scores that follow
+        for (int i = 0; i < 2; ++i) mbar_init(&pfull[g][i], g == 0 ? 10 : 8);
+        mbar_init(&ofull[g], 1);
+      }
+      mbar_init(&s_drained, 1);
+      s_abort = 0;
+      s_bad = 0;
+      s_any_odd = 0;
+      s_kissued = 0;
+      s_vissued = 0;
+      fence_mbar_init();
+    }
+  }
+  // The queries, 16 bytes a lane, whole rows side by side, on their way while warp 0 works out the cut (where the
+  // CTA's place in the grid says which).  As bf16 they lie where V tiles in f16 will: only the tree's scores read
+  // them there, the prefix's take them as e4m3 hi and lo from sQ.
+  constexpr int kQPer = kGR8 * (D / 8) / 256, kQStep = 256 / (D / 8);
+  const int q_g = (warp - 4) >> 3, q_r0 = ((tid - 128) & 255) / (D / 8), q_ch = tid % (D / 8);
+  uint8_t* q16 = sV16 + q_g * C::kQ;
+  int par = -1;  // of node tid - 128
+  auto fetch_q = [&]() {
     if (warp < 4) return;
-    if (tid - 128 < p.N) par0 = p.parent[(size_t)sp.b * p.N + tid - 128];
+    if (tid - 128 < p.N) par = p.parent[(size_t)sp.b * p.N + tid - 128];
 #pragma unroll 2
     for (int k = 0; k < kQPer; ++k) {
-      int rr, ch;
-      q_chunk(k, &rr, &ch);
-      const int row = sp.rt * kRowsCta + rr;
+      const int r = q_r0 + k * kQStep, row = sp.rt * kRowsCta + q_g * kGR8 + r;
       const bool in = row < p.N * p.G;  // (zeros otherwise)
-      const uint16_t* from = p.q + kv8_row(p, sp.b, sp.h, in ? row : 0) * D + ch * 8;
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(q16_at(rr, ch))), "l"(from),
-                   "r"(in ? 16 : 0)
+      const uint16_t* from = p.q + kv8_row(p, sp.b, sp.h, in ? row : 0) * D + q_ch * 8;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(q16 + tile16_off(r, q_ch, kGR8))),
+                   "l"(from), "r"(in ? 16 : 0)
                    : "memory");
     }
   };
-  auto early_done = [&]() { asm volatile("cp.async.wait_all;" ::: "memory"); };
+  auto have_q = [&]() { asm volatile("cp.async.wait_all;" ::: "memory"); };
   const bool own = sp.b >= 0;
-  if (own) early();
+  if (own) fetch_q();
   if (warp == 0) {
     const Kv8Work w = kv8_begin(p, sp);
     if (lane == 0) s_work = w;
   }
-  if (tid == 32) {
-    for (int s = 0; s < kKS; ++s) {
-      mbar_init(&kfull[s], 1);
-      mbar_init(&kempty[s], 1);
-    }
-    for (int s = 0; s < kVS; ++s) {
-      mbar_init(&vfull[s], 1);
-      mbar_init(&vempty[s], 2);
-    }
-    for (int s = 0; s < kV16; ++s) {
-      mbar_init(&v16empty[s], 1);
-    }
-    for (int g = 0; g < NG; ++g) {
-      for (int i = 0; i < C::kNB; ++i) {
-        mbar_init(&sfull[g][i], 1);
-      }
-      // a tile's weights are there; for group 0 also its V, and the keys of the scores that follow
-      for (int i = 0; i < 2; ++i) mbar_init(&pfull[g][i], g == 0 ? 10 : 8);
-      mbar_init(&ofull[g], 1);
-      mbar_init(&qready[g], 8);
-    }
-    mbar_init(&s_drained, 1);
-    s_abort = 0;
-    s_bad = 0;
-    s_any_odd = 0;
-    s_kissued = 0;
-    s_vissued = 0;
-    fence_mbar_init();
-  }
-  if (warp == 2 && lane < kAncWords) s_odd[lane] = 0u;
   __syncthreads();
   sp = s_work;
-  if (sp.b < 0) {
-    early_done();
+  if (sp.b < 0) {  // a unit that its request does not use
+    have_q();
     return;
   }
-  if (!own) early();
-  const int b = sp.b, h = sp.h, rt = sp.rt, split = sp.split, n = sp.nodes;
-  const long long L = sp.L;
-  int err = sp.err;
-  const int row0 = rt * kRowsCta, rows = p.N * p.G;
-  auto orow_of = [&](int row) { return kv8_row(p, b, h, row); };
-  // rows of a refused request or of padded nodes; with several splits the merge writes them
-  auto refuse = [&]() {
-    for (int c = tid; c < kRowsCta * (D / 8); c += C::kThreads) {
-      const int row = row0 + c / (D / 8), e = c % (D / 8);
-      if (row >= rows) continue;
-      const size_t o = orow_of(row);
-      if (sp.n == 1) {
-        *reinterpret_cast<uint4*>(p.out + o * D + e * 8) = make_uint4(0, 0, 0, 0);
-        if (e == 0 && p.lse) p.lse[o] = 0.f;
-      } else if (e == 0) {
-        p.part_ml[sp.part + (row - row0)] = make_float2(0.f, -1.f);
-      }
-    }
+  if (!own) fetch_q();
+  // ---- a CTA's tiles: the tree's (in the last split) and then keys [k0, k1) of the prefix ----
+  struct Tiles {
+    bool tree;
+    int b, h;
+    long long k0, k1;
+    int Tt, T;
   };
-  // ---- this CTA's tiles: the tree's (in the last split) and then keys [k0, k1) of the prefix ----
-  const bool tree = split == sp.n - 1;
-  const long long k0 = ((long long)split * sp.steps) << p.unit_shift;
-  const long long k1 = min(L, k0 + ((long long)sp.steps << p.unit_shift));
-  const int Tt = tree ? (n + kTT - 1) / kTT : 0;
-  const int T = Tt + (k1 > k0 ? (int)((k1 - k0 + kKT8 - 1) / kKT8) : 0);
+  auto tiles_of = [&](const Kv8Work& w) {
+    Tiles x;
+    x.tree = w.split == w.n - 1;
+    x.b = w.b;
+    x.h = w.h;
+    x.k0 = ((long long)w.split * w.steps) << p.unit_shift;
+    x.k1 = min(w.L, x.k0 + ((long long)w.steps << p.unit_shift));
+    x.Tt = x.tree ? (w.nodes + kTT - 1) / kTT : 0;
+    x.T = x.Tt + (x.k1 > x.k0 ? (int)((x.k1 - x.k0 + kKT8 - 1) / kKT8) : 0);
+    return x;
+  };
   // ---- TMA: lane i < 128 / box of warp 0 takes box i of a tile; the first tiles are on their way while the tree is
   // checked ----
   const int box = min(p.bs, kKT8), nbox = kKT8 / box;
   const int out_z = p.num_blocks * p.Hkv;  // behind the map: reads as zeros
   // slot of this lane's box in prefix tile u, or -1 when it lies behind the split's keys
-  auto slot_of = [&](int u) -> long long {
-    const long long s = k0 + (long long)u * kKT8 + lane * box;
-    return lane < nbox && s < k1 ? s : -1;
+  auto slot_of = [&](const Tiles& w, int u) -> long long {
+    const long long s = w.k0 + (long long)u * kKT8 + lane * box;
+    return lane < nbox && s < w.k1 ? s : -1;
   };
-  auto entry = [&](int u) -> int {
-    const long long s = slot_of(u);
-    return s >= 0 ? p.table[(size_t)b * p.max_blocks + (s >> p.bs_shift)] : -1;
+  auto entry = [&](const Tiles& w, int u) -> int {
+    const long long s = slot_of(w, u);
+    return s >= 0 ? p.table[(size_t)w.b * p.max_blocks + (s >> p.bs_shift)] : -1;
   };
   // the block of tile u is loaded two tiles ahead and its scales one tile ahead of its requests
   int blk0 = -1, blk1 = -1;
   float ks0 = 0.f, vs0 = 0.f;
-  auto scales = [&](int blk, float* ks, float* vs) {
+  auto scales = [&](const Tiles& w, int blk, float* ks, float* vs) {
     *ks = 0.f;
     *vs = 0.f;
     if (blk >= 0 && blk < p.num_blocks) {
-      *ks = p.k_scale[(size_t)blk * p.Hkv + h];
-      *vs = p.v_scale[(size_t)blk * p.Hkv + h];
+      *ks = p.k_scale[(size_t)blk * p.Hkv + w.h];
+      *vs = p.v_scale[(size_t)blk * p.Hkv + w.h];
     }
   };
-  auto produce = [&](int t0, int t1) -> bool {
+  auto produce = [&](const Tiles& w, int t0, int t1) -> bool {
     for (int t = t0; t < t1; ++t) {
-      const int ks = t % kKS, vs = t % kVS, u = t - Tt;
+      const int ks = t % kKS, vs = t % kVS, u = t - w.Tt;
       int blk2 = -1;
       float ks1 = 0.f, vs1 = 0.f;
       if (u >= 0) {
-        if (u == 0) scales(blk0, &ks0, &vs0);
-        scales(blk1, &ks1, &vs1);
-        blk2 = entry(u + 2);
+        if (u == 0) scales(w, blk0, &ks0, &vs0);
+        scales(w, blk1, &ks1, &vs1);
+        blk2 = entry(w, u + 2);
       }
       const bool got = lane == 0 ? mbar_wait_bounded(&kempty[ks], ((t / kKS) & 1) ^ 1, &s_abort) : true;
       if (!__shfl_sync(0xffffffffu, got, 0)) return false;
@@ -310,11 +294,11 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
       uint8_t* dv = sV + vs * C::kSlot;
       int y = 0, z = out_z;
       if (u >= 0) {
-        const long long s = slot_of(u);
+        const long long s = slot_of(w, u);
         if (s >= 0) {
           if (blk0 >= 0 && blk0 < p.num_blocks) {
             y = (int)(s & (p.bs - 1));
-            z = blk0 * p.Hkv + h;
+            z = blk0 * p.Hkv + w.h;
           } else {
             s_bad = 1;
           }
@@ -322,7 +306,7 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
       }
       // the copies first; the barrier's own arrival follows the scales, which the tile's readers need as well
       if (u < 0) {
-        if (lane < D / 64) tma_load_4d(dk + lane * kTT * 128, &tmKt, &kfull[ks], lane * 64, h, t * kTT, b);
+        if (lane < D / 64) tma_load_4d(dk + lane * kTT * 128, &tmKt, &kfull[ks], lane * 64, w.h, t * kTT, w.b);
       } else if (lane < nbox) {
         tma_load_3d(dk + lane * box * D, &tmK, &kfull[ks], 0, y, z);
         // scales of the box's 16-key groups: K scale, log2 and reciprocal of the V scale
@@ -343,7 +327,7 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
       }
       __syncwarp();
       if (u < 0) {
-        if (lane < D / 64) tma_load_4d(dv + lane * kTT * 128, &tmVt, &vfull[vs], lane * 64, h, t * kTT, b);
+        if (lane < D / 64) tma_load_4d(dv + lane * kTT * 128, &tmVt, &vfull[vs], lane * 64, w.h, t * kTT, w.b);
       } else {
         if (lane < nbox) tma_load_3d(dv + lane * box * D, &tmV, &vfull[vs], 0, y, z);
         blk0 = blk1;
@@ -354,56 +338,106 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
     }
     return true;
   };
-  // While warp 0 asks for the first table entries and the tree's tiles, warp 1 takes the TMEM and warps 4..11 look
-  // at the tree; one barrier joins them.
-  const int pre = min(Tt, kVS);
-  bool bad_tree = err == SPEC_ERR_BAD_TREE;
+  int pre = 0;  // tiles asked for ahead of the barrier
+  bool bad_tree = false;
   if (warp == 0) {
-    blk0 = entry(0);
-    blk1 = entry(1);
-    produce(0, pre);
+    const Tiles w = tiles_of(sp);
+    blk0 = entry(w, 0);
+    blk1 = entry(w, 1);
+    if (!sp.err) pre = min(w.T, kVS);
+    produce(w, 0, pre);
   } else if (warp == 1) {
     tmem_alloc(&s_tmem, 512);
     tmem_relinquish();
+  } else if (warp == 2) {
+    if (lane < kAncWords) s_odd[lane] = 0u;
   } else if (warp >= 4) {
     if (warp < 12) {
       const int i = tid - 128;  // (256 threads, at most 255 nodes)
-      if (i < n) {
-        s_par[i] = par0;
-        bad_tree |= i == 0 ? par0 != -1 : (par0 < 0 || par0 >= i);
+      if (i < sp.nodes) {
+        s_par[i] = par;
+        bad_tree = i == 0 ? par != -1 : (par < 0 || par >= i);
       }
-      if (!bar_or(10, 256, bad_tree) && tree && i < n) {  // ancestors-or-self
+      if (!bar_or(10, 256, bad_tree) && i < sp.nodes) {  // ancestors-or-self
         uint32_t* w = s_nanc + i * kAncWords;
 #pragma unroll
         for (int j = 0; j < kAncWords; ++j) w[j] = 0u;
         for (int a = i; a >= 0; a = s_par[a]) w[a >> 5] |= 1u << (a & 31);
       }
     }
-    early_done();
+    have_q();
+    uint8_t* q8 = sQ + q_g * C::kQ;
+#pragma unroll 2
+    for (int k = 0; k < kQPer; ++k) {  // (this thread's own chunks)
+      const int r = q_r0 + k * kQStep;
+      const uint4 v = *reinterpret_cast<const uint4*>(q16 + tile16_off(r, q_ch, kGR8));
+      const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+      float f[8], mx = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        f[2 * j] = __uint_as_float(x[j] << 16);
+        f[2 * j + 1] = __uint_as_float(x[j] & 0xFFFF0000u);
+        mx = max3(mx, fabsf(f[2 * j]), fabsf(f[2 * j + 1]));
+      }
+#pragma unroll
+      for (int o = 1; o < D / 8; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 100);
+      const float up = __uint_as_float((uint32_t)(127 + 7 - e) << 23);  // largest element into [128, 256)
+      if (q_ch == 0) s_qf[q_g][r] = __uint_as_float((uint32_t)(127 - 7 + e) << 23) * p.scale_log2;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] *= up;
+      uint8_t* to = q8 + kv8_off<D>(r, q_ch >> 1) + (q_ch & 1) * 8;
+      *reinterpret_cast<uint2*>(to) = make_uint2(e4m3x4(head4(f[0]), head4(f[1]), head4(f[2]), head4(f[3])),
+                                                 e4m3x4(head4(f[4]), head4(f[5]), head4(f[6]), head4(f[7])));
+      *reinterpret_cast<uint2*>(to + kGR8 * D) =
+          make_uint2(e4m3x4(f[0] - head4(f[0]), f[1] - head4(f[1]), f[2] - head4(f[2]), f[3] - head4(f[3])),
+                     e4m3x4(f[4] - head4(f[4]), f[5] - head4(f[5]), f[6] - head4(f[6]), f[7] - head4(f[7])));
+    }
     fence_proxy_async_smem();
   }
   tc_fence_before();
-  if (__syncthreads_or(bad_tree)) err = SPEC_ERR_BAD_TREE;
+  bad_tree = __syncthreads_or(bad_tree);
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  const Kv8Work w = s_work;
+  const int b = w.b, h = w.h, rt = w.rt, row0 = rt * kRowsCta, rows = p.N * p.G;
+  auto orow_of = [&](int row) { return kv8_row(p, b, h, row); };
+  // rows of a refused request or of padded nodes; with several splits the merge writes them
+  auto refuse = [&]() {
+    for (int c = tid; c < kRowsCta * (D / 8); c += C::kThreads) {
+      const int row = row0 + c / (D / 8), e = c % (D / 8);
+      if (row >= rows) continue;
+      const size_t o = orow_of(row);
+      if (w.n == 1) {
+        *reinterpret_cast<uint4*>(p.out + o * D + e * 8) = make_uint4(0, 0, 0, 0);
+        if (e == 0 && p.lse) p.lse[o] = 0.f;
+      } else if (e == 0) {
+        p.part_ml[w.part + (row - row0)] = make_float2(0.f, -1.f);
+      }
+    }
+  };
+  const Tiles own_tiles = tiles_of(w);
+  const bool tree = own_tiles.tree;
+  const long long k0 = own_tiles.k0, k1 = own_tiles.k1;
+  const int n = w.nodes, Tt = own_tiles.Tt, T = own_tiles.T;
+  const int err = bad_tree ? SPEC_ERR_BAD_TREE : w.err;
   if (err || row0 >= n * p.G) {  // refused, or padded nodes only (with several splits the merge zeroes those)
-    if (err && tid == 0 && rt == 0 && split == 0 && h == 0) set_status(p.dev_status, err);
-    if (err || sp.n == 1) refuse();
+    if (err && tid == 0 && rt == 0 && w.split == 0 && h == 0) set_status(p.dev_status, err);
+    if (err || w.n == 1) refuse();
     if (tid == 0)  // the copies land first
       for (int t = 0; t < pre; ++t) {
         mbar_wait_bounded(&kfull[t], 0, nullptr);
         mbar_wait_bounded(&vfull[t], 0, nullptr);
       }
-    tc_fence_after();
-    if (warp == 1) tmem_dealloc(s_tmem, 512);
+    if (warp == 1) tmem_dealloc(tmem, 512);
     return;
   }
-  tc_fence_after();
-  const uint32_t tmem = s_tmem;
   // register shares of the warpgroups (two groups): 64 + 4 x 104 within the 5 x 96 the block was launched with
   if (warp < 4) {
     if constexpr (NG == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == 0) {
     // ---- TMA producer, from where the first tiles ended ----
-      if (!produce(pre, T) && lane == 0) {
+      if (!produce(own_tiles, pre, T) && lane == 0) {
         s_abort = 1;
         set_status(p.dev_status, SPEC_ERR_TIMEOUT);
       }
@@ -479,7 +513,6 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         if (!wait(&pfull[g][t & 1], (t >> 1) & 1)) return false;
-        if (t + C::kNB == Tt && Tt < T && !wait(&qready[g], 0)) return false;
         tc_fence_after();
         issue_pv(pv_tree, t, g);
         if (t + C::kNB < T) issue_s(s_tree, t + C::kNB, g);
@@ -492,7 +525,6 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
       for (int t = 0; t < C::kNB && t < T; ++t) {
         if (!wait(&kfull[t % kKS], 0)) return false;
         for (int g = 0; g < NG; ++g) {
-          if (t == Tt && !wait(&qready[g], 0)) return false;
           tc_fence_after();
           if (t < Tt) issue_s(Yes(), t, g); else issue_s(No(), t, g);
         }
@@ -523,11 +555,9 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
         ok = __all_sync(0xffffffffu, mbar_wait_bounded(&vfull[t % kVS], (t / kVS) & 1, &s_abort) &&
                                          mbar_wait_bounded(&v16empty[t % kV16], ((t / kV16) & 1) ^ 1, &s_abort));
         if (!ok) break;
-        // the queries as bf16 are done with: read by their own threads, and by the tree's last scores (waited for
-        // ahead of the word that lets the next ones begin, which would turn the barrier's phase over)
-        if (t == Tt) {
-          for (int g = 0; g < NG && ok; ++g) ok = mbar_wait_bounded(&qready[g], 0, &s_abort);
-        } else if (t == Tt - 1) {
+        // the tree's last scores are done with the bf16 queries (waited for ahead of the word that lets the next ones
+        // begin, which would turn the barrier's phase over)
+        if (t == Tt - 1) {
           for (int g = 0; g < NG && ok; ++g)
             ok = mbar_wait_bounded(&sfull[g][t % C::kNB], (t / C::kNB) & 1, &s_abort);
         }
@@ -606,47 +636,10 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
     const uint32_t tS = tmem + C::kColS + (NG == 2 ? g : 0) * 128 + lane_off;
     const uint32_t tO = tmem + C::kColO + g * 128 + lane_off;
     const bool live = row < n * p.G;
-    uint8_t* myQ = sQ + g * C::kQ;
-    float qf = 0.f;  // undoes the row's scaling, with the softmax scale in log2 units
+    const float qf = s_qf[g][rl];  // undoes the row's scaling, with the softmax scale in log2 units
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, &s_abort));
     };
-    // the group's queries from bf16 to e4m3 hi and lo, as they were fetched: D / 8 neighbouring lanes hold a row
-    if (T > Tt) {
-#pragma unroll 1
-      for (int k = 0; k < kQPer; ++k) {
-        int r, ch;
-        q_chunk(k, &r, &ch);
-        const uint4 v = *reinterpret_cast<const uint4*>(q16_at(r, ch));
-        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-        float f[8], mx = 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          f[2 * j] = __uint_as_float(x[j] << 16);
-          f[2 * j + 1] = __uint_as_float(x[j] & 0xFFFF0000u);
-          mx = max3(mx, fabsf(f[2 * j]), fabsf(f[2 * j + 1]));
-        }
-#pragma unroll
-        for (int o = 1; o < D / 8; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 100);
-        const float up = __uint_as_float((uint32_t)(127 + 7 - e) << 23);  // largest element into [128, 256)
-        if (ch == 0) s_x[g][0][r % kGR8] = __uint_as_float((uint32_t)(127 - 7 + e) << 23) * p.scale_log2;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] *= up;
-        uint8_t* to = myQ + kv8_off<D>(r % kGR8, ch >> 1) + (ch & 1) * 8;
-        *reinterpret_cast<uint2*>(to) = make_uint2(e4m3x4(head4(f[0]), head4(f[1]), head4(f[2]), head4(f[3])),
-                                                   e4m3x4(head4(f[4]), head4(f[5]), head4(f[6]), head4(f[7])));
-        *reinterpret_cast<uint2*>(to + kGR8 * D) =
-            make_uint2(e4m3x4(f[0] - head4(f[0]), f[1] - head4(f[1]), f[2] - head4(f[2]), f[3] - head4(f[3])),
-                       e4m3x4(f[4] - head4(f[4]), f[5] - head4(f[5]), f[6] - head4(f[6]), f[7] - head4(f[7])));
-      }
-      fence_proxy_async_smem();
-      named_bar_sync(10 + g, 256);
-      qf = s_x[g][0][rl];
-      if (lane == 0) mbar_arrive(&qready[g]);
-      named_bar_sync(10 + g, 256);  // s_x is free again
-    }
-
     float m = -INFINITY, l = 0.f;  // the row's reference (P = 2^(y - m)), and the sum over this thread's keys
     const uint32_t* anc = s_nanc + (live ? kv8_node(p, row) : 0) * kAncWords;
     const int pair = 2 + g * 4 + q4;  // named barrier of the two warps that share rows
@@ -805,9 +798,9 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
     // every MMA of both groups has completed: Q and the rings are free for the O rows
     named_bar_sync(1, 256 * NG);
     l += s_x[g][half ^ 1][rl];
-    const bool valid = row < rows && fin && !s_abort && !s_bad && (live || sp.n == 1);
+    const bool valid = row < rows && fin && !s_abort && !s_bad && (live || w.n == 1);
     uint8_t* srow = base + rr * C::kORow;
-    const bool whole = sp.n == 1;
+    const bool whole = w.n == 1;
     if (fin) {
       tc_fence_after();
       const float inv = whole ? (live ? 1.f / l : 0.f) : 1.f;
@@ -847,7 +840,7 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
       if (valid && half == 0) {
         const size_t o = orow_of(row);
         if (!whole)
-          p.part_ml[sp.part + (row - row0)] = make_float2(m, l);
+          p.part_ml[w.part + (row - row0)] = make_float2(m, l);
         else if (p.lse)
           p.lse[o] = live ? (m + log2f(l)) * 0.69314718055994531f : 0.f;
       }
@@ -865,7 +858,7 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
         if (whole)
           *reinterpret_cast<uint4*>(p.out + o * D + e * 8) = x;
         else
-          *reinterpret_cast<uint4*>(p.part_o + (sp.part + r) * D + e * 4) = x;
+          *reinterpret_cast<uint4*>(p.part_o + (w.part + r) * D + e * 4) = x;
       }
     }
   }
