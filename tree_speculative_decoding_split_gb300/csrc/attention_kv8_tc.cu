@@ -565,9 +565,24 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
         if (!ok) break;
         uint8_t* src = sV + (t % kVS) * C::kSlot;
         if (t < Tt) {
-          // a tree tile stays bf16; elements that are no finite numbers become 0 and their rows are noted
-          for (int c = ct; c < kTT * (D / 8); c += 64) {
-            const int r = c / (D / 8), key = t * kTT + r;
+          // a tree tile stays bf16; elements that are no finite numbers become 0 and their rows are noted.  Whether
+          // this thread has any: the sum of all its elements times zero is NaN.
+          constexpr int kChunks = kTT * (D / 8) / 64;
+          __nv_bfloat162 odd = __floats2bfloat162_rn(0.f, 0.f);
+          const __nv_bfloat162 zero = odd;
+#pragma unroll 4
+          for (int i = 0; i < kChunks; ++i) {
+            const int c = ct + i * 64;
+            const uint4 x = *reinterpret_cast<const uint4*>(src + tile16_off(c / (D / 8), c % (D / 8), kTT));
+            odd = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.x), zero, odd);
+            odd = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.y), zero, odd);
+            odd = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.z), zero, odd);
+            odd = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.w), zero, odd);
+          }
+          const bool any = !(__low2float(odd) == 0.f && __high2float(odd) == 0.f);
+#pragma unroll 1
+          for (int i = 0; i < kChunks && any; ++i) {
+            const int c = ct + i * 64, r = c / (D / 8), key = t * kTT + r;
             uint4* at = reinterpret_cast<uint4*>(src + tile16_off(r, c % (D / 8), kTT));
             uint4 x = *at;
             if (finite2(x.x) && finite2(x.y) && finite2(x.z) && finite2(x.w)) continue;
