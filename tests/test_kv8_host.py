@@ -73,7 +73,7 @@ _PATH = dict(path=P, accept_len=P, row_start=None, n_rows=0, n_max=63, path_cap=
     (dict(block_table=None), 1), (dict(k_cache=P + 1), 1), (dict(v_cache=None), 1), (dict(k_scale=None), 1),
     (dict(v_scale=None), 1), (dict(_PATH, accept_len=None), 1), (dict(_PATH, row_start=P), 1), (dict(_PATH, n_rows=3), 1),
     (dict(_PATH, n_max=0), 1), (dict(_PATH, n_max=256), 2), (dict(_PATH, path_cap=0), 1),
-    (dict(n_rows=(1 << 31) - 1, num_kv_heads=64, num_blocks=1 << 20), 2)])
+    (dict(n_rows=(1 << 31) - 1, batch=(1 << 31) - 1), 2)])
 def test_append_refusals(L, kw, code):
     assert L.spec_kv8_append(ctypes.byref(_append(**kw)), None, None) == code
 

@@ -717,11 +717,14 @@ def eagle_tree(score, token, parent, n_max, draft_to_target=None, root_token=Non
 # full checks of _need run only where it fails, and say why), plain addresses instead of pointer objects,
 # no status buffer when the caller passes none.
 
-def _fast(t, name, dtype, device):
-    """_need(t, name, dtype, device), returning the tensor's address."""
-    if getattr(t, "dtype", None) is not dtype or t.device != device or not t.is_contiguous():
-        _need(t, name, dtype, device)
-    return t.data_ptr()
+def _fast(t, name, dtype, device, index):
+    """_need(t, name, dtype, device), returning the tensor's address; index is the device's number."""
+    try:
+        if t.dtype is dtype and t.get_device() == index and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:  # no tensor
+        pass
+    return _need(t, name, dtype, device).data_ptr()
 
 
 class _On:
@@ -730,10 +733,10 @@ class _On:
     __slots__ = ("guard", "raw", "stream")
 
     def __init__(self, device, stream):
-        torch = _torch()
-        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+        torch, index = _torch_module, device.index
+        self.guard = None if torch._C._cuda_getDevice() == index else torch.cuda.device(device)
         self.stream = stream
-        self.raw = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+        self.raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
     def __enter__(self):
         if self.guard is not None:
@@ -751,8 +754,21 @@ class _On:
                     t.record_stream(self.stream)
 
 
+def _launch(fn, name, device, stream, made, *args):
+    """fn(*args, stream) on the device; ``made`` are the tensors that the call has allocated."""
+    cuda, index = _torch_module._C, device.index
+    if stream is None and cuda._cuda_getDevice() == index:
+        code = fn(*args, cuda._cuda_getCurrentRawStream(index))
+    else:
+        with _On(device, stream) as on:
+            code = fn(*args, on.raw)
+            on.keep(*made)
+    if code:
+        raise SpecError(code, name)
+
+
 def _status_ptr(dev_status, device):
-    return None if dev_status is None else _fast(dev_status, "dev_status", _torch().int32, device)
+    return None if dev_status is None else _fast(dev_status, "dev_status", _torch_module.int32, device, device.index)
 
 
 def kv_reserve_args(seq_len, n_new, block_table, n_blocks, free_list, free_count, block_size, slot_cap=None,
@@ -762,26 +778,27 @@ def kv_reserve_args(seq_len, n_new, block_table, n_blocks, free_list, free_count
     torch = _torch()
     _need(block_table, "block_table", torch.int32)
     dev, i32 = block_table.device, torch.int32
-    if block_table.dim() != 2:
+    ix, shape = dev.index, block_table.shape
+    if len(shape) != 2:
         raise ValueError("block_table must be [B][max_blocks]")
-    B, max_blocks = block_table.shape
-    ptr = [_fast(seq_len, "seq_len", i32, dev), _fast(n_new, "n_new", i32, dev), block_table.data_ptr(),
-           _fast(n_blocks, "n_blocks", i32, dev), _fast(free_list, "free_list", i32, dev),
-           _fast(free_count, "free_count", i32, dev)]
+    B, max_blocks = shape
+    ptr = (_fast(seq_len, "seq_len", i32, dev, ix), _fast(n_new, "n_new", i32, dev, ix), block_table.data_ptr(),
+           _fast(n_blocks, "n_blocks", i32, dev, ix), _fast(free_list, "free_list", i32, dev, ix),
+           _fast(free_count, "free_count", i32, dev, ix))
     if seq_len.numel() != B or n_new.numel() != B or n_blocks.numel() != B or free_count.numel() != 1:
         raise ValueError("seq_len, n_new and n_blocks must be [B], free_count [1]")
     if slot_map is None and slot_cap is not None:
         slot_map = torch.empty(int(slot_cap), dtype=torch.int64, device=dev)
     slots = 0
     if slot_map is not None:
-        _fast(slot_map, "slot_map", torch.int64, dev)
+        map_ptr = _fast(slot_map, "slot_map", torch.int64, dev, ix)
         slots = slot_map.numel()
     if row_start is None:
         row_start = torch.empty(B + 1, dtype=i32, device=dev)
     elif row_start.numel() != B + 1:
         raise ValueError("row_start must be [B + 1]")
     a = KvReserveArgs(B, int(block_size), max_blocks, free_list.numel(), slots, *ptr,
-                      slot_map.data_ptr() if slots else None, _fast(row_start, "row_start", i32, dev))
+                      map_ptr if slots else None, _fast(row_start, "row_start", i32, dev, ix))
     return a, slot_map, row_start
 
 
@@ -794,27 +811,28 @@ def kv_reserve(seq_len, n_new, block_table, n_blocks, free_list, free_count, blo
     a, slot_map, row_start = kv_reserve_args(seq_len, n_new, block_table, n_blocks, free_list, free_count, block_size,
                                              slot_cap, slot_map, row_start)
     dev = block_table.device
-    with _On(dev, stream) as on:
-        _check(lib().spec_kv_reserve(ctypes.byref(a), _status_ptr(dev_status, dev), on.raw), "spec_kv_reserve")
-        on.keep(slot_map, row_start)
+    _launch(lib().spec_kv_reserve, "spec_kv_reserve", dev, stream, (slot_map, row_start), ctypes.byref(a),
+            _status_ptr(dev_status, dev))
     return slot_map, row_start
 
 
-def _kv8_pools(k_cache, v_cache, k_scale, v_scale, block_table, B, dev):
-    """(addresses of the pools and scales), (block_size, max_blocks, num_blocks, Hkv)"""
-    torch = _torch()
+def _kv8_pools(k_cache, v_cache, k_scale, v_scale, block_table, B, dev, ix):
+    """(addresses of the pools and scales), (num_blocks, Hkv, block_size, d), max_blocks, address of the table"""
+    torch = _torch_module
     f8, f32 = torch.float8_e4m3fn, torch.float32
-    ptr = (_fast(k_cache, "k_cache", f8, dev), _fast(v_cache, "v_cache", f8, dev), _fast(k_scale, "k_scale", f32, dev),
-           _fast(v_scale, "v_scale", f32, dev))
+    ptr = (_fast(k_cache, "k_cache", f8, dev, ix), _fast(v_cache, "v_cache", f8, dev, ix),
+           _fast(k_scale, "k_scale", f32, dev, ix), _fast(v_scale, "v_scale", f32, dev, ix))
     shape = k_cache.shape
     if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("pools must be [num_blocks][Hkv][block_size][d]")
-    if k_scale.shape != shape[:2] or v_scale.shape != shape[:2]:
+    scales = shape[:2]
+    if k_scale.shape != scales or v_scale.shape != scales:
         raise ValueError("k_scale and v_scale must be [num_blocks][Hkv]")
-    _fast(block_table, "block_table", torch.int32, dev)
-    if block_table.dim() != 2 or block_table.shape[0] != B:
+    table = _fast(block_table, "block_table", torch.int32, dev, ix)
+    rows = block_table.shape
+    if len(rows) != 2 or rows[0] != B:
         raise ValueError("block_table must be [B][max_blocks]")
-    return ptr, (shape[2], block_table.shape[1], shape[0], shape[1])
+    return ptr, shape, rows[1], table
 
 
 def kv8_append_args(k_new, v_new, k_cache, v_cache, k_scale, v_scale, seq_len, block_table, row_start=None, path=None,
@@ -823,31 +841,33 @@ def kv8_append_args(k_new, v_new, k_cache, v_cache, k_scale, v_scale, seq_len, b
     torch = _torch()
     _need(k_new, "k_new")
     dev, i32 = k_new.device, torch.int32
-    new = (k_new.data_ptr(), _fast(v_new, "v_new", k_new.dtype, dev))
-    lens = _fast(seq_len, "seq_len", i32, dev)
+    ix = dev.index
+    new = (k_new.data_ptr(), _fast(v_new, "v_new", k_new.dtype, dev, ix))
+    lens = _fast(seq_len, "seq_len", i32, dev, ix)
     B = seq_len.numel()
-    pools, (bs, max_blocks, nb, Hkv) = _kv8_pools(k_cache, v_cache, k_scale, v_scale, block_table, B, dev)
-    d = k_cache.shape[3]
-    if v_new.shape != k_new.shape or tuple(k_new.shape[-2:]) != (Hkv, d):
+    pools, (nb, Hkv, bs, d), max_blocks, table = _kv8_pools(k_cache, v_cache, k_scale, v_scale, block_table, B, dev, ix)
+    shape = k_new.shape
+    if v_new.shape != shape or shape[-2:] != (Hkv, d):
         raise ValueError("k_new and v_new must be [...][Hkv][d]")
     n_max = path_cap = n_rows = 0
     if path is not None:
-        if row_start is not None or accept_len is None or k_new.dim() != 4 or k_new.shape[0] != B or path.dim() != 2 or \
-                path.shape[0] != B or accept_len.numel() != B:
+        paths = path.shape
+        if row_start is not None or accept_len is None or len(shape) != 4 or shape[0] != B or len(paths) != 2 or \
+                paths[0] != B or accept_len.numel() != B:
             raise ValueError("path [B][path_cap] and accept_len [B] go with rows [B][N][Hkv][d] and no row_start")
-        source = (None, _fast(path, "path", i32, dev), _fast(accept_len, "accept_len", i32, dev))
-        n_max, path_cap = k_new.shape[1], path.shape[1]
+        source = (None, _fast(path, "path", i32, dev, ix), _fast(accept_len, "accept_len", i32, dev, ix))
+        n_max, path_cap = shape[1], paths[1]
     else:
-        if row_start is None or accept_len is not None or k_new.dim() != 3 or row_start.numel() != B + 1:
+        if row_start is None or accept_len is not None or len(shape) != 3 or row_start.numel() != B + 1:
             raise ValueError("packed rows [n_rows][Hkv][d] go with row_start [B + 1]")
-        source = (_fast(row_start, "row_start", i32, dev), None, None)
-        n_rows = k_new.shape[0]
+        source = (_fast(row_start, "row_start", i32, dev, ix), None, None)
+        n_rows = shape[0]
     if new_len is None:
         new_len = torch.empty(B, dtype=i32, device=dev)
     elif new_len.numel() != B:
         raise ValueError("new_len must be [B]")
     a = Kv8AppendArgs(_dtype_code(k_new), B, Hkv, d, bs, max_blocks, nb, n_max, path_cap, 0, n_rows, *new, *source, lens,
-                      block_table.data_ptr(), *pools, _fast(new_len, "new_len", i32, dev))
+                      table, *pools, _fast(new_len, "new_len", i32, dev, ix))
     return a, new_len
 
 
@@ -862,9 +882,8 @@ def kv8_append(k_new, v_new, k_cache, v_cache, k_scale, v_scale, seq_len, block_
     dev = k_new.device
     if k_new.numel() == 0:  # no rows: the pools are not looked at, any address does
         a.k_new = a.v_new = a.k_cache
-    with _On(dev, stream) as on:
-        _check(lib().spec_kv8_append(ctypes.byref(a), _status_ptr(dev_status, dev), on.raw), "spec_kv8_append")
-        on.keep(new_len)
+    _launch(lib().spec_kv8_append, "spec_kv8_append", dev, stream, (new_len,), ctypes.byref(a),
+            _status_ptr(dev_status, dev))
     return new_len
 
 
@@ -874,28 +893,37 @@ def attn_kv8_args(q, k_tree, v_tree, k_cache, v_cache, k_scale, v_scale, prefix_
     lse)."""
     torch = _torch()
     _need(q, "q")
-    dev, dtype, i32 = q.device, q.dtype, torch.int32
-    if q.dim() != 4:
+    dev, dtype, i32, shape = q.device, q.dtype, torch.int32, q.shape
+    ix = dev.index
+    if len(shape) != 4:
         raise ValueError("q must be [B][N][Hq][d]")
-    B, N, Hq, d = q.shape
-    tree = (_fast(k_tree, "k_tree", dtype, dev), _fast(v_tree, "v_tree", dtype, dev))
-    pools, (bs, max_blocks, nb, Hkv) = _kv8_pools(k_cache, v_cache, k_scale, v_scale, block_table, B, dev)
-    if k_cache.shape[3] != d or tuple(k_tree.shape) != (B, N, Hkv, d) or v_tree.shape != k_tree.shape:
+    B, N, Hq, d = shape
+    tree = (_fast(k_tree, "k_tree", dtype, dev, ix), _fast(v_tree, "v_tree", dtype, dev, ix))
+    pools, (nb, Hkv, bs, d_pool), max_blocks, table = _kv8_pools(k_cache, v_cache, k_scale, v_scale, block_table, B, dev,
+                                                                ix)
+    rows = (B, N, Hkv, d)
+    if d_pool != d or k_tree.shape != rows or v_tree.shape != rows:
         raise ValueError("k_tree and v_tree must be [B][N][Hkv][d], with the pools' d")
-    counts = (_fast(prefix_len, "prefix_len", i32, dev), _fast(n_nodes, "n_nodes", i32, dev),
-              _fast(parent, "parent", i32, dev))
-    if tuple(parent.shape) != (B, N) or prefix_len.numel() != B or n_nodes.numel() != B:
+    counts = (_fast(prefix_len, "prefix_len", i32, dev, ix), _fast(n_nodes, "n_nodes", i32, dev, ix),
+              _fast(parent, "parent", i32, dev, ix))
+    if parent.shape != (B, N) or prefix_len.numel() != B or n_nodes.numel() != B:
         raise ValueError("parent must be [B][N], prefix_len and n_nodes [B]")
     if out is None:
         out = torch.empty_like(q)
-    elif out.shape != q.shape:
-        raise ValueError("out must be [B][N][Hq][d]")
+        out_ptr = out.data_ptr()
+    else:
+        out_ptr = _fast(out, "out", dtype, dev, ix)
+        if out.shape != shape:
+            raise ValueError("out must be [B][N][Hq][d]")
     if lse is None:
         lse = torch.empty((B, N, Hq), dtype=torch.float32, device=dev)
-    elif tuple(lse.shape) != (B, N, Hq):
-        raise ValueError("lse must be [B][N][Hq]")
+        lse_ptr = lse.data_ptr()
+    else:
+        lse_ptr = _fast(lse, "lse", torch.float32, dev, ix)
+        if lse.shape != (B, N, Hq):
+            raise ValueError("lse must be [B][N][Hq]")
     a = AttnKv8Args(_dtype_code(q), B, N, Hq, Hkv, d, bs, max_blocks, nb, float(scale), q.data_ptr(), *tree, *pools,
-                    *counts, block_table.data_ptr(), _fast(out, "out", dtype, dev), _fast(lse, "lse", torch.float32, dev))
+                    *counts, table, out_ptr, lse_ptr)
     return a, out, lse
 
 
@@ -906,12 +934,14 @@ def tree_attention_kv8(q, k_tree, v_tree, k_cache, v_cache, k_scale, v_scale, pr
     a, out, lse = attn_kv8_args(q, k_tree, v_tree, k_cache, v_cache, k_scale, v_scale, prefix_len, n_nodes, parent,
                                 block_table, out, lse, scale)
     L, dev, ref = lib(), q.device, ctypes.byref(a)
-    with _On(dev, stream) as on:
+    if _torch_module._C._cuda_getDevice() == dev.index:
         need = L.spec_tree_attention_kv8_workspace(ref)
-        if need == 0:
-            _check(L.spec_tree_attention_kv8(ref, None, 0, None, None), "spec_tree_attention_kv8")
-        ws = _workspace(need, dev, workspace)
-        _check(L.spec_tree_attention_kv8(ref, ws.data_ptr(), need, _status_ptr(dev_status, dev), on.raw),
-               "spec_tree_attention_kv8")
-        on.keep(ws, out, lse)
+    else:  # (it goes by the current device's size)
+        with _torch_module.cuda.device(dev):
+            need = L.spec_tree_attention_kv8_workspace(ref)
+    if need == 0:
+        _check(L.spec_tree_attention_kv8(ref, None, 0, None, None), "spec_tree_attention_kv8")
+    ws = _workspace(need, dev, workspace)
+    _launch(L.spec_tree_attention_kv8, "spec_tree_attention_kv8", dev, stream, (ws, out, lse), ref, ws.data_ptr(), need,
+            _status_ptr(dev_status, dev))
     return out, lse
