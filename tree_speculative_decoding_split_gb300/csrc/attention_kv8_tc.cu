@@ -17,14 +17,21 @@
 // columns and S 128 per group, 512 in all with two; P lies over the S it came from, so the issue order per
 // group is  P V(t), S(t + 1)  back to back.  (With one group S has two buffers.)
 //   warp 0     TMA producer: K and V rings of 128-key tiles (one box per block and tensor, issued by as many
-//              lanes), the tile's scales;
+//              lanes), the tile's scales; first of all it works out the CTA's share of the batch;
 //   warp 1     MMA issuer;
 //   warps 2, 3 V tiles to f16;
 //   warps 4..  softmax, eight warps per group: two threads own a row (a TMEM lane), 64 keys of a tile each.
 //              Both use the row's reference; whether one has to move is one barrier's OR per tile.
-// Tried and slower (63-node trees, batch 32 at 4K): P as e4m3 pairs with 128 keys a thread, four warps per
-// group and a row maximum ahead of the weights, 238 us; with one S buffer shared by both groups and all
-// descriptors in uniform registers, 203 us; with two threads per row, 211 us.
+// Measured (graph replay): 4 trees of 255 nodes, 32 query heads on 8, lengths up to 128K, 1878 us = 1458 TFLOP/s,
+// 0.77 of a large bf16 product's rate; a tile of both groups takes 3.2 K cycles for 2 K of tensor work.  32 trees of
+// 63 nodes at 4K 142 us = 954 TFLOP/s: 256 CTAs on 152 SMs are 1.7 rounds, and about 30 K of a CTA's 140 K cycles go
+// to its first two tiles and its last rows, which nothing overlaps.  8 trees of 127 nodes, d 64, 58 us.
+// Tried and slower (63-node trees, batch 32 at 4K, when this stood at 160 us): P as e4m3 pairs with 128 keys a
+// thread, four warps per group and a row maximum ahead of the weights, 238 us; with one S buffer shared by both groups
+// and all descriptors in uniform registers, 203 us; with two threads per row, 211 us.  Four trees of 255 nodes, at
+// 2112 us: two issuing warps with the V tiles converted by the softmax warps, 2567 us; waits with a suspend-time hint
+// 2942 us, waits that only poll 3144 us.  The tree's tiles eight keys at a time in a rolled loop: 60 us for the 8
+// trees of 127 nodes instead of 57.
 #include <type_traits>
 
 #include "common.cuh"
@@ -142,7 +149,9 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[
       : "memory");
 }
 
-__device__ __forceinline__ bool finite2(uint32_t w) { return (w & 0x7F80u) != 0x7F80u && (w & 0x7F800000u) != 0x7F800000u; }
+__device__ __forceinline__ bool finite2(uint32_t w) {
+  return (w & 0x7F80u) != 0x7F80u && (w & 0x7F800000u) != 0x7F800000u;
+}
 
 }  // namespace
 

@@ -78,7 +78,7 @@ spec_status check_attn_kv8(const spec_attn_kv8_args* a) {
   if (a->batch < 1 || a->n_max < 1 || a->num_q_heads < 1 || a->num_kv_heads < 1) return SPEC_ERR_INVALID_ARGUMENT;
   if (a->n_max > SPEC_MAX_NODES) return SPEC_ERR_UNSUPPORTED;
   if (a->num_q_heads % a->num_kv_heads) return SPEC_ERR_INVALID_ARGUMENT;
-  if ((long long)a->batch * a->num_kv_heads > 65535) return SPEC_ERR_UNSUPPORTED;  // keeps the grid and its row offsets within 32 bits
+  if ((long long)a->batch * a->num_kv_heads > 65535) return SPEC_ERR_UNSUPPORTED;  // CTAs stay within 32 bits
   const spec_status ps = check_paged(a->block_size, a->max_blocks, a->num_blocks, a->num_kv_heads,
                                      (long long)a->max_blocks * a->block_size);
   if (ps != SPEC_OK) return ps;
@@ -106,8 +106,8 @@ AttnKv8Layout layout_attn_kv8(const spec_attn_kv8_args* a, void* ws) {
   AttnKv8Layout l;
   l.plan = plan_attention_kv8(a->batch, a->n_max, a->num_q_heads / a->num_kv_heads, a->num_kv_heads,
                               (long long)a->max_blocks * a->block_size, num_sms_current());
-  const size_t rows = !l.plan.merge() ? 0
-                                      : (size_t)(a->batch * l.plan.base + l.plan.extra) * a->num_kv_heads * l.plan.n_rt * l.plan.rows_cta;
+  const size_t ctas = (size_t)(a->batch * l.plan.base + l.plan.extra) * a->num_kv_heads * l.plan.n_rt;
+  const size_t rows = l.plan.merge() ? ctas * l.plan.rows_cta : 0;
   Carver c(ws);
   l.used = c.take<int2>(a->batch);
   l.part_ml = c.take<float2>(rows);

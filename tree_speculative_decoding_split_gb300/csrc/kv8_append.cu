@@ -6,6 +6,8 @@
 // maximum, and converts what it holds.  So the rows are read once and the codes written once: HBM-bound.
 // A CTA goes through the heads of its block one after another with the next one's rows on their way (one
 // head per CTA took 103 us for 35K rows of 8 heads: most of it finding the request, block and scale).
+// Measured: those rows (bf16, d 128) 52 us = 4.1 TB/s, 0.61 of a plain copy's rate; 328K fp32 rows (d 64) 303 us =
+// 5.5 TB/s, 0.81.  The accepted paths of 32 requests 10.7 us with a cold cache, 6.5 warm: one launch and four loads in a row.
 // A half-full block keeps its larger scale; its old codes are read only when the scale grows.
 #include "common.cuh"
 #include "kernels.cuh"

@@ -6,6 +6,11 @@
 //   r-th given back  -> list[f + R - 1 - r];   a-th taken <- list[f + R - 1 - a]   (f = free, R given back)
 // A taken block may be one given back by another request in the same call, so the two steps are
 // separated by a barrier.
+//
+// Bound: latency.  The tables' changes are a few KB; what takes time is the chain of counts, scan, list, tables and
+// slots.  So small calls are one CTA that writes the slot map as well, and the sums of all three kinds are scanned
+// together (apart, the two calls below took 12.8, 16.9 and 31.2 us).  Measured with a cold cache, a call with its slot map
+// and one without: 10.8 us for one request, 14.8 for 32, 27.1 for 512 prompts with 1 M slots.
 #include "common.cuh"
 #include "kernels.cuh"
 #include "pdl.cuh"
