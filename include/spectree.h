@@ -540,8 +540,10 @@ spec_status spec_kv8_append(const spec_kv8_append_args* args, int32_t* dev_statu
 
 /* Tree attention over the 8-bit cache: as spec_tree_attention, with the prefix [0, prefix_len[b])
  * in the pools and node i's own K/V in row i of k_tree / v_tree.  n_max = 1 is decoding of single
- * tokens.  Products and sums are those of the codes' exact values: q enters as an exact pair of
- * 8-bit numbers or in 16 bits, the softmax weights as bf16 or better, sums in float32.
+ * tokens.  Products and sums are those of the codes' exact values: q enters in 16 bits or as a pair
+ * of 8-bit numbers (exact down to 2^-9 of its row's largest element, below that within 2^-17 of it),
+ * the softmax weights as bf16 or better, sums in float32.  How a prefix is split depends on the
+ * lengths of the whole batch, so the last bits of a row may as well.
  *   - K/V rows of nodes that a row does not see, of padded nodes and of slots behind the prefix have
  *     no influence on it, NaN and infinities included.
  *   - Data errors as for spec_tree_attention: SPEC_ERR_BAD_TREE; SPEC_ERR_CAPACITY for prefix_len
@@ -549,7 +551,7 @@ spec_status spec_kv8_append(const spec_kv8_append_args* args, int32_t* dev_statu
  *     request's out and lse are then 0, as for padded nodes.
  * Host errors: SPEC_ERR_INVALID_ARGUMENT, SPEC_ERR_UNSUPPORTED (dtype other than bf16, head_dim,
  * block_size, n_max > SPEC_MAX_NODES, Hq / Hkv > 256, B * Hkv > 65535, num_blocks * Hkv >= 2^31, max_blocks *
- * block_size >= 2^31), SPEC_ERR_WORKSPACE_TOO_SMALL. */
+ * block_size >= 2^31 - 128), SPEC_ERR_WORKSPACE_TOO_SMALL. */
 typedef struct spec_attn_kv8_args {
   int32_t dtype;            /* of q, k_tree, v_tree and out: SPEC_DTYPE_BF16 */
   int32_t batch;            /* B */
