@@ -502,12 +502,13 @@ spec_status spec_kv_reserve(const spec_kv_reserve_args* args, int32_t* dev_statu
  *   codes of the slots below seq_len[b], when s > s_old: e4m3(code * (s_old / s)) -- exact where
  *           s_old is a power of two and the result is no subnormal code.
  * Other slots of the block keep what they hold.  new_len[b] = seq_len[b] + rows appended.
- * Data errors: seq_len[b] < 0 or rows past max_blocks * block_size, row_start that decreases or
- * leaves [0, n_rows], accept_len[b] outside [0, path_cap) (SPEC_ERR_CAPACITY); path[b] that does not
- * start at 0 or is not increasing below n_max (SPEC_ERR_BAD_TREE); a table entry outside
- * [0, num_blocks) among the blocks written (SPEC_ERR_CAPACITY).  new_len[b] is then seq_len[b] and
- * nothing of the request is written, but for the other blocks of a prompt whose table has a bad
- * entry.  Requests must not share the blocks they write.
+ * Data errors: seq_len[b] < 0 or rows past max_blocks * block_size, accept_len[b] outside
+ * [0, path_cap) (SPEC_ERR_CAPACITY); path[b] that does not start at 0 or is not increasing below
+ * n_max (SPEC_ERR_BAD_TREE); a table entry outside [0, num_blocks) among the blocks written
+ * (SPEC_ERR_CAPACITY).  new_len[b] is then seq_len[b] and nothing of the request is written, but for
+ * the other blocks of a prompt whose table has a bad entry.  A row_start that decreases or leaves
+ * [0, n_rows] anywhere (SPEC_ERR_CAPACITY) refuses every request of the call.  Requests must not share
+ * the blocks they write.
  * Host errors: SPEC_ERR_INVALID_ARGUMENT, SPEC_ERR_UNSUPPORTED (dtype, head_dim, block_size,
  * num_blocks * Hkv >= 2^31, too many rows for one grid: about 2^31 * block_size / Hkv). */
 typedef struct spec_kv8_append_args {

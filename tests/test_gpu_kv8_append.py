@@ -145,7 +145,42 @@ def test_appending_twice_is_the_same():
         assert torch.equal(c[n].view(torch.uint8) if "cache" in n else c[n], first[n]), n
 
 
-@pytest.mark.parametrize("kind,code", [("table", 7), ("len", 7), ("negative", 7), ("rows", 7), ("past", 7)])
+@pytest.mark.parametrize("rows", [[0, 5, 4, 44], [0, 5, 200, 65], [0, 60, 10, 20], [-1, 5, 25, 65], [0, 5, 25, 66], [9, 8, 7, 6],
+                                  [0, 1 << 30, -(1 << 31), 65]])
+def test_rows_out_of_order_refuse_the_call(rows):
+    """Nothing is written and no length moves, whichever request's range is the bad one."""
+    dev = K8.dev()
+    rng = np.random.default_rng(8)
+    start = [3, 10, 0]
+    cache = K8.Cache(rng, [48, 48, 48], 2, 64, 16)
+    c, kw = _device(cache, dev)
+    rk, _ = _rows(rng, (65, 2, 64), torch.bfloat16, 3)
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    new = st.kv8_append(rk.to(dev), rk.to(dev), seq_len=torch.tensor(start, dtype=torch.int32, device=dev),
+                        row_start=torch.tensor(rows, dtype=torch.int32, device=dev), dev_status=status, **kw)
+    _compare(cache, c)
+    assert int(status.item()) == 7 and new.tolist() == start
+
+
+def test_rows_ahead_of_and_behind_the_requests():
+    """Packed rows that belong to no request are not looked at."""
+    dev = K8.dev()
+    rng = np.random.default_rng(9)
+    start, rs = [3, 17, 0], [70, 75, 75, 119]
+    cache = K8.Cache(rng, [48, 48, 48], 2, 128, 16)
+    c, kw = _device(cache, dev)
+    rk, k = _rows(rng, (200, 2, 128), torch.bfloat16, 3)
+    rk[:70] = float("nan")
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    new = st.kv8_append(rk.to(dev), rk.to(dev), seq_len=torch.tensor(start, dtype=torch.int32, device=dev),
+                        row_start=torch.tensor(rs, dtype=torch.int32, device=dev), dev_status=status, **kw)
+    for b in range(3):
+        _oracle_append(cache, b, k[rs[b]: rs[b + 1]], k[rs[b]: rs[b + 1]], start[b])
+    _compare(cache, c)
+    assert int(status.item()) == 0 and new.tolist() == [8, 17, 44]
+
+
+@pytest.mark.parametrize("kind,code", [("table", 7), ("len", 7), ("negative", 7)])
 def test_bad_packed_requests(kind, code):
     dev = K8.dev()
     rng = np.random.default_rng(3)
@@ -159,10 +194,6 @@ def test_bad_packed_requests(kind, code):
         seq[1] = 29
     if kind == "negative":
         seq[1] = -1
-    if kind == "rows":
-        rs = np.array([0, 5, 4, 44], np.int32)  # request 1's rows decrease; request 2's are 4..43
-    if kind == "past":
-        rs = np.array([0, 5, 200, 65], np.int32)
     c, kw = _device(cache, dev)
     rk, k = _rows(rng, (65, 2, 64), torch.bfloat16, 3)
     status = torch.zeros(1, dtype=torch.int32, device=dev)
@@ -174,12 +205,9 @@ def test_bad_packed_requests(kind, code):
     _oracle_append(cache, 0, k[:5], k[:5], start[0])
     if kind in ("len", "negative"):
         _oracle_append(cache, 2, k[25:], k[25:], start[2])
-    if kind == "rows":
-        _oracle_append(cache, 2, k[4:44], k[4:44], start[2])
-    if kind in ("table", "past"):  # the others as they should be; request 1's blocks are not compared
-        if kind == "table":
-            _oracle_append(cache, 2, k[25:], k[25:], start[2])
-        mine = [b for b in cache.table[0] if b >= 0] + ([b for b in cache.table[2] if b >= 0] if kind == "table" else [])
+    if kind == "table":  # the others as they should be; request 1's blocks are not compared
+        _oracle_append(cache, 2, k[25:], k[25:], start[2])
+        mine = [b for b in cache.table[0] if b >= 0] + [b for b in cache.table[2] if b >= 0]
         got = c["k_cache"].view(torch.uint8).cpu().numpy()
         for blk in mine:
             assert np.array_equal(got[blk] & 127 == 127, cache.k[blk] & 127 == 127)

@@ -126,8 +126,7 @@ __device__ __forceinline__ Request check_request(const Kv8AppendParams& p, int b
       }
     }
   } else {
-    const int r0 = p.row_start[b], r1 = p.row_start[b + 1];
-    if (r0 < 0 || r1 < r0 || r1 > p.n_rows) r.err = SPEC_ERR_CAPACITY; else r.count = r1 - r0;
+    r.count = p.row_start[b + 1] - p.row_start[b];
   }
   if (__syncthreads_or(bad)) r.err = SPEC_ERR_BAD_TREE;
   if (!r.err && (len < 0 || len + r.count > (long long)p.max_blocks * p.bs)) r.err = SPEC_ERR_CAPACITY;
@@ -177,7 +176,20 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv8_append_kernel(con
     }
     b = lo;
     k = u - units_before(p.row_start, b, p.bs_shift);
-    if (k < 0) return;  // (a row_start that decreases)
+    // a row_start that decreases or leaves its range would share units out wrongly: the whole call is refused
+    int bad = 0;
+    for (int i = tid; i < p.B; i += THREADS) {
+      const int r = p.row_start[i], next = p.row_start[i + 1];
+      bad |= r < 0 || next < r || next > p.n_rows;
+    }
+    if (__syncthreads_or(bad)) {
+      if (tid == 0 && part == 0 && u < p.B) {
+        set_status(p.dev_status, SPEC_ERR_CAPACITY);
+        if (p.new_len) p.new_len[u] = p.seq_len[u];
+      }
+      return;
+    }
+    if (k < 0) return;  // (rows ahead of the first request's)
   }
   const Request rq = check_request(p, b);
   const int len = p.seq_len[b];
