@@ -232,3 +232,31 @@ def test_repeats_and_streams_agree_to_the_bit(N):
         ws = torch.full((1 << 26,), 0xFF, dtype=torch.uint8, device=dev)  # NaN bytes: nothing of it may be read unwritten
         again, lse2, _ = K8.attend(dev, cache, qs, workspace=ws)
     assert np.array_equal(out, again) and np.array_equal(lse, lse2)
+
+
+@pytest.mark.parametrize("N", [1, 40])
+def test_calls_on_two_streams_at_once(N):
+    dev = K8.dev()
+    rng = np.random.default_rng(12)
+    sides = [torch.cuda.Stream(), torch.cuda.Stream()]
+    calls, want = [], []
+    for i in range(2):
+        cache = K8.Cache(rng, [3000 + i, 200, 900], 2, 128, 32)
+        qs = K8.Queries(rng, 3, N, 8, 2, 128)
+        out, lse, status = K8.attend(dev, cache, qs)
+        assert status == 0
+        c = cache.device(dev)
+        lens = torch.tensor(cache.lens, dtype=torch.int32, device=dev)
+        rest = [torch.from_numpy(x).to(dev) for x in (qs.n_nodes, qs.parent)]
+        calls.append((qs.q_t.to(dev), qs.kt_t.to(dev), qs.vt_t.to(dev), c["k_cache"], c["v_cache"], c["k_scale"],
+                      c["v_scale"], lens, *rest, c["block_table"]))
+        want.append(torch.from_numpy(out))
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i, side in enumerate(sides):
+            got[i].append(st.tree_attention_kv8(*calls[i], stream=side)[0])
+    torch.cuda.synchronize()
+    for i in range(2):
+        for out in got[i]:
+            assert torch.equal(out.double().cpu(), want[i])
