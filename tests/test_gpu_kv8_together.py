@@ -154,3 +154,81 @@ def test_decoding_rounds(N, G, Hkv, d, bs, prompts):
         graph.replay()
         accepted += loop.check()
     assert accepted > 0 or N == 1
+
+
+def _plain(rng, N=3):
+    """Arguments of a plain attention and append call."""
+    dev = K8.dev()
+    cache = K8.Cache(rng, [70, 5], 2, 128, 16, max_len=96)
+    qs = K8.Queries(rng, 2, N, 4, 2, 128)
+    c = cache.device(dev)
+    pools = [c["k_cache"], c["v_cache"], c["k_scale"], c["v_scale"]]
+    lens = torch.tensor(cache.lens, dtype=torch.int32, device=dev)
+    attend = [qs.q_t.to(dev), qs.kt_t.to(dev), qs.vt_t.to(dev), *pools, lens, torch.from_numpy(qs.n_nodes).to(dev),
+              torch.from_numpy(qs.parent).to(dev), c["block_table"]]
+    append = [attend[1], attend[2], *pools, lens, c["block_table"]]
+    path = dict(path=torch.tensor([[0, -1, -1]] * 2, dtype=torch.int32, device=dev),
+                accept_len=torch.zeros(2, dtype=torch.int32, device=dev))
+    return attend, append, path
+
+
+def test_both_ways_of_marshalling_agree():
+    """A plain call goes through the native marshalling, one with a stream, a workspace or a scale that is no float
+    through the interpreted one: the same answers, and given outputs come back themselves."""
+    attend, append, path = _plain(np.random.default_rng(1))
+    native = st._native()
+    order = attend[:7] + [attend[10]] + attend[7:10]
+    assert native.attend(*order, None, None, 0.1, None) is not None
+    out, lse = st.tree_attention_kv8(*attend, scale=1.0)
+    here = torch.cuda.current_stream()
+    ws = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
+    for kw in (dict(stream=here), dict(workspace=ws), dict(scale=1)):
+        again = st.tree_attention_kv8(*attend, **{"scale": 1.0, **kw})
+        torch.cuda.synchronize()
+        assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+    mine = torch.empty_like(out), torch.empty_like(lse)
+    back = st.tree_attention_kv8(*attend, scale=1.0, out=mine[0], lse=mine[1])
+    assert back[0] is mine[0] and back[1] is mine[1] and torch.equal(mine[0], out) and torch.equal(mine[1], lse)
+    states = []
+    for kw in (dict(), dict(stream=here), dict(new_len=torch.empty(2, dtype=torch.int32, device="cuda"))):
+        pools = [x.clone() for x in append[2:6]]
+        new_len = st.kv8_append(*append[:2], *pools, *append[6:], **path, **kw)
+        torch.cuda.synchronize()
+        assert new_len.tolist() == [71, 6] and kw.get("new_len", new_len) is new_len
+        states.append(pools)
+    for pools in states[1:]:
+        for a, b in zip(pools, states[0]):
+            assert torch.equal(a.view(torch.uint8) if a.dim() == 4 else a, b.view(torch.uint8) if b.dim() == 4 else b)
+
+
+@pytest.mark.parametrize("i,change,error", [
+    (0, lambda t: t.float(), TypeError), (0, lambda t: t.transpose(1, 2), ValueError), (1, lambda t: t[:, :2], ValueError),
+    (1, lambda t: t[:, :2].contiguous(), ValueError), (2, lambda t: t.half(), TypeError), (3, lambda t: t.cpu(), ValueError),
+    (4, lambda t: t[:-1], ValueError), (5, lambda t: t.double(), TypeError), (6, lambda t: t[:, :1], ValueError),
+    (7, lambda t: t.long(), TypeError), (8, lambda t: t[:1], ValueError), (9, lambda t: t[:, :2].contiguous(), ValueError),
+    (10, lambda t: t[0], ValueError), (7, lambda t: t.tolist(), TypeError)])
+def test_refused_tensors(i, change, error):
+    attend, append, path = _plain(np.random.default_rng(2))
+    attend[i] = change(attend[i])
+    with pytest.raises(error):
+        st.tree_attention_kv8(*attend)
+    where = {1: 0, 2: 1, 3: 2, 4: 3, 5: 4, 6: 5, 7: 6, 10: 7}.get(i)
+    if where is not None and i != 1:
+        append[where] = attend[i]
+        with pytest.raises((error, AttributeError)):
+            st.kv8_append(*append, **path)
+
+
+def test_refusals_by_the_library():
+    attend, append, path = _plain(np.random.default_rng(3))
+    pools = [torch.zeros((4, 2, 48, 128), dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)] * 2
+    scales = [torch.ones((4, 2), device="cuda")] * 2
+    with pytest.raises(st.SpecError, match="UNSUPPORTED"):
+        st.tree_attention_kv8(*attend[:3], *pools, *scales, *attend[7:])
+    with pytest.raises(st.SpecError, match="UNSUPPORTED"):
+        st.kv8_append(*append[:2], *pools, *scales, *append[6:], **path)
+    i = torch.zeros(2, dtype=torch.int32, device="cuda")
+    with pytest.raises(st.SpecError, match="UNSUPPORTED"):
+        st.kv_reserve(i, i, i.view(2, 1).clone(), i.clone(), i.clone(), i[:1].clone(), 48)
+    with pytest.raises(ValueError):
+        st.kv_reserve(i[:1], i, i.view(2, 1).clone(), i.clone(), i.clone(), i[:1].clone(), 16)

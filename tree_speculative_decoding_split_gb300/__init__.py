@@ -2,7 +2,8 @@
 
 Thin ctypes binding of ``libspectree.so`` (C ABI in ``include/spectree.h``).  This module only
 marshals arguments: it checks tensor placement, dtype and contiguity, carves nothing itself,
-and passes raw device pointers plus the current CUDA stream.  Every step of the computation
+and passes raw device pointers plus the current CUDA stream (for the 8-bit cache's calls, which come
+once per layer and token, in native code: ``csrc/marshal.cpp``).  Every step of the computation
 runs in the library's CUDA kernels; if the library has not been built, every call raises.
 
     tree_attention(...)   -> (out, lse)          one attention layer over the draft tree
@@ -21,6 +22,7 @@ runs in the library's CUDA kernels; if the library has not been built, every cal
 """
 
 import ctypes
+import importlib.util
 import os
 
 from ._build import LIB as _LIB_PATH
@@ -713,9 +715,39 @@ def eagle_tree(score, token, parent, n_max, draft_to_target=None, root_token=Non
 
 
 # ---- the 8-bit paged cache ---------------------------------------------------------------------
-# These calls come once per layer and token, so their marshalling is kept short: one test per tensor (the
-# full checks of _need run only where it fails, and say why), plain addresses instead of pointer objects,
-# no status buffer when the caller passes none.
+# These calls come once per layer and token, so their marshalling is native (csrc/marshal.cpp) for the plain
+# call: contiguous tensors of the current device, on its current stream, no workspace of the caller's.  Any
+# other call, and every one that is refused, goes through the functions below, which say why.  They too are
+# kept short: one test per tensor (the full checks of _need run only where it fails), plain addresses instead
+# of pointer objects, no status buffer when the caller passes none.
+
+_marshal = None
+
+
+def _native():
+    """The native marshalling, with the library's entry points handed over."""
+    global _marshal
+    if _marshal is None:
+        _torch()
+        path = os.path.join(os.path.dirname(_LIB_PATH), "spectree_marshal.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with tree_speculative_decoding_split_gb300.build()")
+        spec = importlib.util.spec_from_file_location("spectree_marshal", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        L = lib()
+        module.bind(*(ctypes.cast(fn, _vp).value for fn in (L.spec_kv_reserve, L.spec_kv8_append,
+                                                            L.spec_tree_attention_kv8_workspace,
+                                                            L.spec_tree_attention_kv8)))
+        _marshal = module
+    return _marshal
+
+
+def _answer(r, name):
+    if r.__class__ is int:
+        raise SpecError(r, name)
+    return r
+
 
 def _fast(t, name, dtype, device, index):
     """_need(t, name, dtype, device), returning the tensor's address; index is the device's number."""
@@ -808,6 +840,11 @@ def kv_reserve(seq_len, n_new, block_table, n_blocks, free_list, free_count, blo
     free blocks, in place (see spec_kv_reserve).  ``slot_cap`` (a bound on the sum of n_new the host
     knows) or ``slot_map`` asks for the pool row of every new row.  Returns (slot_map, row_start);
     slot_map is None when neither is given."""
+    if stream is None:
+        r = (_marshal or _native()).reserve(seq_len, n_new, block_table, n_blocks, free_list, free_count, block_size,
+                                            slot_cap, slot_map, row_start, dev_status)
+        if r is not None:
+            return _answer(r, "spec_kv_reserve")
     a, slot_map, row_start = kv_reserve_args(seq_len, n_new, block_table, n_blocks, free_list, free_count, block_size,
                                              slot_cap, slot_map, row_start)
     dev = block_table.device
@@ -877,6 +914,11 @@ def kv8_append(k_new, v_new, k_cache, v_cache, k_scale, v_scale, seq_len, block_
     ``row_start`` [B + 1], or a tree's rows [B][N][Hkv][d] along ``path`` / ``accept_len`` (the outputs of
     verify_accept).  Pools are float8_e4m3fn [num_blocks][Hkv][block_size][d], scales float32
     [num_blocks][Hkv].  Returns new_len."""
+    if stream is None:
+        r = (_marshal or _native()).append(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_table, seq_len,
+                                           row_start, path, accept_len, new_len, dev_status)
+        if r is not None:
+            return _answer(r, "spec_kv8_append")
     a, new_len = kv8_append_args(k_new, v_new, k_cache, v_cache, k_scale, v_scale, seq_len, block_table, row_start,
                                  path, accept_len, new_len)
     dev = k_new.device
@@ -931,6 +973,11 @@ def tree_attention_kv8(q, k_tree, v_tree, k_cache, v_cache, k_scale, v_scale, pr
                        out=None, lse=None, scale=0.0, workspace=None, dev_status=None, stream=None):
     """Tree attention over the 8-bit paged prefix and the tree's own K/V rows (see
     spec_tree_attention_kv8); N = 1 is decoding of single tokens.  Returns (out, lse)."""
+    if stream is None and workspace is None:
+        r = (_marshal or _native()).attend(q, k_tree, v_tree, k_cache, v_cache, k_scale, v_scale, block_table, prefix_len,
+                                           n_nodes, parent, out, lse, scale, dev_status)
+        if r is not None:
+            return _answer(r, "spec_tree_attention_kv8")
     a, out, lse = attn_kv8_args(q, k_tree, v_tree, k_cache, v_cache, k_scale, v_scale, prefix_len, n_nodes, parent,
                                 block_table, out, lse, scale)
     L, dev, ref = lib(), q.device, ctypes.byref(a)

@@ -1,8 +1,9 @@
 """Builds libspectree.so (the CUDA kernels and the C ABI) in-tree for sm_103a.
 
 Each .cu file is compiled in parallel with nvcc, then linked into
-``tree_speculative_decoding_split_gb300/lib/libspectree.so``.  A stamp of the sources and flags
-lets an unchanged tree skip the rebuild.
+``tree_speculative_decoding_split_gb300/lib/libspectree.so``.  Beside it stands ``spectree_marshal.so``,
+the native part of the Python binding (host code, against the installed torch).  A stamp of the
+sources and flags lets an unchanged tree skip the rebuild.
 """
 
 import concurrent.futures as cf
@@ -11,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libspectree.so")
+MARSHAL = os.path.join(LIBDIR, "spectree_marshal.so")
 BUILD = os.path.join(PKG, "_build")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -36,22 +39,40 @@ def _sources():
 
 
 def _stamp():
+    import torch
     h = hashlib.sha256()
     files = _sources() + sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h")))
-    files.append(os.path.join(INCLUDE, "spectree.h"))
+    files += [os.path.join(INCLUDE, "spectree.h"), os.path.join(CSRC, "marshal.cpp")]
     for f in files:
         h.update(f.encode())
         h.update(open(f, "rb").read())
     h.update(" ".join(ARCH + FLAGS).encode())
-    h.update(os.uname().machine.encode())
+    h.update(f"{os.uname().machine} {torch.__version__} {sys.version}".encode())
     return h.hexdigest()
 
 
+def _marshal():
+    """Compile spectree_marshal.so."""
+    import torch
+    home = os.path.dirname(torch.__file__)
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    tmp = MARSHAL + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(home, "include"),
+           "-isystem", os.path.join(cuda, "include"), os.path.join(CSRC, "marshal.cpp"), "-o", tmp,
+           "-L", os.path.join(home, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on marshal.cpp:\n{r.stderr}")
+    os.replace(tmp, MARSHAL)
+
+
 def build(verbose=False, force=False):
-    """Compile and link libspectree.so; returns its path."""
+    """Compile and link libspectree.so and spectree_marshal.so; returns the former's path."""
     stamp_file = os.path.join(LIBDIR, ".stamp")
     stamp = _stamp()
-    if not force and os.path.exists(LIB) and os.path.exists(stamp_file) and open(stamp_file).read() == stamp:
+    made = all(os.path.exists(f) for f in (LIB, MARSHAL, stamp_file))
+    if not force and made and open(stamp_file).read() == stamp:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     os.makedirs(LIBDIR, exist_ok=True)
@@ -68,8 +89,10 @@ def build(verbose=False, force=False):
         return obj
 
     srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
+        marshal = ex.submit(_marshal)
         objs = list(ex.map(compile_one, srcs))
+        marshal.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc] + ARCH + ["-shared", "-cudart", "static", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
