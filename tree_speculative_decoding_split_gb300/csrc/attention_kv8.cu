@@ -169,6 +169,8 @@ __global__ void __launch_bounds__(kWarps * 32, RN == 1 ? 4 : 2)
     }
     if (tid < p.N) par0 = p.parent[(size_t)sp.b * p.N + tid];
   };
+  pdl_wait();  // what comes before in the stream may still be ending: nothing of it is read ahead of this
+  pdl_launch_dependents();  // the merge may be launched
   const bool own = sp.b >= 0;
   if (own) early();
   sp = kv8_begin(p, sp);
@@ -703,8 +705,7 @@ static cudaError_t launch_rows(const CUtensorMap* tmK, const CUtensorMap* tmV, c
       cudaFuncSetAttribute(attn_kv8_rows_kernel<D, RN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (err != cudaSuccess) return err;
   const unsigned grid = (unsigned)(p.n_rt * p.Hkv * (p.B * p.base + p.extra));
-  attn_kv8_rows_kernel<D, RN><<<grid, kWarps * 32, C::kSmem, stream>>>(*tmK, *tmV, p);
-  return cudaGetLastError();
+  return launch_dependent(attn_kv8_rows_kernel<D, RN>, dim3(grid), dim3(kWarps * 32), C::kSmem, stream, *tmK, *tmV, p);
 }
 
 cudaError_t launch_attention_kv8_rows(const CUtensorMap* tmK, const CUtensorMap* tmV, const Kv8AttnParams& p,

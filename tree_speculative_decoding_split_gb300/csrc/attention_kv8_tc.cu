@@ -37,6 +37,7 @@
 #include "common.cuh"
 #include "kernels.cuh"
 #include "kv8.cuh"
+#include "pdl.cuh"
 #include "tc_ptx.cuh"
 
 namespace spectree {
@@ -211,6 +212,8 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
       fence_mbar_init();
     }
   }
+  pdl_wait();  // what comes before in the stream may still be ending: nothing of it is read ahead of this
+  pdl_launch_dependents();  // the merge may be launched
   // The queries, 16 bytes a lane, whole rows side by side, on their way while warp 0 works out the cut (where the
   // CTA's place in the grid says which).  As bf16 they lie where V tiles in f16 will: only the tree's scores read
   // them there, the prefix's take them as e4m3 hi and lo from sQ.
@@ -911,9 +914,8 @@ static cudaError_t launch_tc8(const CUtensorMap* tm, const Kv8AttnParams& p, cud
   cudaError_t err =
       cudaFuncSetAttribute(attn_kv8_tc_kernel<D, NG>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (err != cudaSuccess) return err;
-  attn_kv8_tc_kernel<D, NG>
-      <<<p.n_rt * p.Hkv * (p.B * p.base + p.extra), C::kThreads, C::kSmem, stream>>>(tm[0], tm[1], tm[2], tm[3], p);
-  return cudaGetLastError();
+  return launch_dependent(attn_kv8_tc_kernel<D, NG>, dim3((unsigned)(p.n_rt * p.Hkv * (p.B * p.base + p.extra))),
+                          dim3(C::kThreads), C::kSmem, stream, tm[0], tm[1], tm[2], tm[3], p);
 }
 
 cudaError_t launch_attention_kv8_tc(const CUtensorMap* tm, const Kv8AttnParams& p, int groups, cudaStream_t stream) {

@@ -11,6 +11,7 @@
 // A half-full block keeps its larger scale; its old codes are read only when the scale grows.
 #include "common.cuh"
 #include "kernels.cuh"
+#include "pdl.cuh"
 
 namespace spectree {
 
@@ -155,6 +156,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv8_append_kernel(con
   __shared__ uint32_t s_max[2][32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int u = blockIdx.x / parts, part = blockIdx.x - u * parts;
+  pdl_wait();  // what comes before in the stream may still be ending: nothing of it is read ahead of this
   // ---- the unit's request and block ----
   int b, k;  // request, its k-th touched block
   if (p.path) {
@@ -358,7 +360,10 @@ unsigned kv8_append_grid(const Kv8AppendParams& p) {
 cudaError_t launch_kv8_append(const Kv8AppendParams& p, cudaStream_t stream) {
   const AppendShape s = append_shape(p);
   const unsigned grid = kv8_append_grid(p);
-  auto go = [&](auto kernel) { kernel<<<grid, s.threads, 0, stream>>>(p, s.parts, s.tg_shift); };
+  cudaError_t err = cudaSuccess;
+  auto go = [&](auto kernel) {
+    err = launch_dependent(kernel, dim3(grid), dim3(s.threads), 0, stream, p, s.parts, s.tg_shift);
+  };
   if (p.is_bf16) {
     if (s.threads == 256) go(kv8_append_kernel<true, kVecs, 256>);
     else if (s.threads == 512) go(kv8_append_kernel<true, kVecs, 512>);
@@ -369,7 +374,7 @@ cudaError_t launch_kv8_append(const Kv8AppendParams& p, cudaStream_t stream) {
     else if (s.nv == kVecs) go(kv8_append_kernel<false, kVecs, 1024>);
     else go(kv8_append_kernel<false, 2 * kVecs, 1024>);
   }
-  return cudaGetLastError();
+  return err;
 }
 
 }  // namespace spectree

@@ -103,6 +103,8 @@ __global__ void __launch_bounds__(1024) kv_reserve_kernel(const ReserveParams p,
   int* s_rel = s_base + B;          // [B + 1] blocks given back before b
   int* s_need = s_rel + B + 1;      // [B + 1] blocks taken before b
   int* s_row = s_need + B + 1;      // [B + 1] new rows before b
+  pdl_wait();  // what comes before in the stream may still be ending: nothing of it is read ahead of this
+  pdl_launch_dependents();  // the slot map's kernel may be launched
   const int f = *p.free_count;
   // ---- scan ----
   const int per = (B + T - 1) / T;
@@ -247,13 +249,15 @@ cudaError_t launch_kv_reserve(const ReserveParams& p, int num_sms, cudaStream_t 
   cfg.blockDim = dim3(small ? 512 : 1024);
   cfg.dynamicSmemBytes = plan;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = small ? 1 : 8;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   err = cudaLaunchKernelEx(&cfg, kv_reserve_kernel, p, small ? 1 : 0);
   if (err != cudaSuccess || small || !p.slot_map || p.slot_cap == 0) return err;
   const long long want = (p.slot_cap + 256 * kRowsPerThread - 1) / (256 * kRowsPerThread);
