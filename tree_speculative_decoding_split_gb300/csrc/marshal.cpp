@@ -116,7 +116,7 @@ bool pools(Call& c, PyObject* const* o, int64_t batch, Pools* p) {
 
 bool fits(std::initializer_list<int64_t> sizes) {
   for (const int64_t s : sizes)
-    if (s > INT32_MAX) return false;
+    if (s < 0 || s > INT32_MAX) return false;
   return true;
 }
 
