@@ -79,6 +79,21 @@ inline bool make_map_kv8(CUtensorMap* m, const void* pool, int d, int bs, long l
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Packed K/V rows [n_rows][Hkv][d] in bf16 or float32: boxes of `box_rows` rows of one head, dense.
+inline bool make_map_rows(CUtensorMap* m, const void* rows, bool bf16, int d, int Hkv, long long n_rows, int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)Hkv, (cuuint64_t)n_rows};
+  const cuuint64_t row = (cuuint64_t)d * (bf16 ? 2 : 4);
+  const cuuint64_t strides[2] = {row, row * Hkv};
+  const cuuint32_t box[3] = {(cuuint32_t)d, 1, (cuuint32_t)box_rows};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  std::memset(m, 0, sizeof(*m));
+  return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void*>(rows), dims,
+            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Paged KV: block size a power of two in [16, 256], kv_capacity = max_blocks * block_size, and

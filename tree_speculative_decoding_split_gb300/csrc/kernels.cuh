@@ -262,7 +262,9 @@ struct Kv8AppendParams {
   int32_t* dev_status;
   int units_per_req;        // tree form: blocks a request's rows can touch
 };
-cudaError_t launch_kv8_append(const Kv8AppendParams& p, cudaStream_t stream);
+// tm: maps of k_new and v_new (boxes of a block's rows of one head) where kv8_append_boxes says so, else null.
+cudaError_t launch_kv8_append(const CUtensorMap* tm, const Kv8AppendParams& p, cudaStream_t stream);
+bool kv8_append_boxes(const Kv8AppendParams& p);
 // CTAs of the launch (0 when they pass the grid's limit).
 unsigned kv8_append_grid(const Kv8AppendParams& p);
 

@@ -140,7 +140,13 @@ spec_status spec_kv8_append(const spec_kv8_append_args* a, int32_t* dev_status, 
   if (st != SPEC_OK) return st;
   const Kv8AppendParams p = append_params(a, dev_status);
   if (kv8_append_grid(p) == 0) return SPEC_ERR_UNSUPPORTED;
-  return launch_kv8_append(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+  CUtensorMap tm[2];
+  const bool boxes = kv8_append_boxes(p);
+  if (boxes && (!make_map_rows(&tm[0], p.k_new, p.is_bf16, p.d, p.Hkv, p.n_rows, p.bs) ||
+                !make_map_rows(&tm[1], p.v_new, p.is_bf16, p.d, p.Hkv, p.n_rows, p.bs)))
+    return SPEC_ERR_CUDA;
+  return launch_kv8_append(boxes ? tm : nullptr, p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SPEC_OK
+                                                                                                    : SPEC_ERR_CUDA;
 }
 
 size_t spec_tree_attention_kv8_workspace(const spec_attn_kv8_args* a) {

@@ -19,6 +19,7 @@ namespace {
 
 constexpr int kVecs = 4;          // 16-byte source vectors a thread holds (8 where a block needs > 1024 threads)
 constexpr long long kFillCtas = 152 * 4;
+constexpr int kStages = 3;        // rounds of items in shared memory
 constexpr int kMinExp = -64, kMaxExp = 120;
 
 // The exponent of the smallest power of two s with amax <= 448 s (448 = 1.75 * 2^8).
@@ -150,9 +151,17 @@ __device__ __forceinline__ bool bad_table(const Kv8AppendParams& p, int b, long 
 
 // Grid: units x parts.  A unit is one block that rows of a request go to; its items are the 2 * Hkv (head, K
 // or V) blocks of codes; a part is a run of them, which the CTA's groups of TG threads take in turn.
-template <bool BF16, int NV, int THREADS>
-__global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv8_append_kernel(const Kv8AppendParams p, int parts, int tg_shift) {
+// TMA: the packed rows of an item come as one box into a ring in shared memory, kStages rounds ahead, instead of one
+// round ahead into registers.
+template <bool BF16, int NV, int THREADS, bool TMA>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS)
+    kv8_append_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                      const Kv8AppendParams p, int parts, int tg_shift) {
   constexpr int E = Vec<BF16>::kElems;
+  constexpr int kStageBytes = THREADS * NV * 16;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = TMA ? reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127)) : nullptr;
+  __shared__ uint64_t s_full[kStages];
   __shared__ uint32_t s_max[2][32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int u = blockIdx.x / parts, part = blockIdx.x - u * parts;
@@ -241,14 +250,47 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv8_append_kernel(con
   uint4 next[NV];
   float s_next;
   const int mine0 = i0 + (tid >> tg_shift);
-  load(mine0, next, s_next);
+  const int item_bytes = NV * 16 << tg_shift;
+  auto fetch = [&](int base, int stage) {  // one thread: the boxes of a round's items
+    const int n = min(groups, i1 - base);
+    mbar_arrive_expect_tx(&s_full[stage], (uint32_t)(n * item_bytes));
+    for (int g = 0; g < n; ++g)
+      tma_load_3d(ring + stage * kStageBytes + g * item_bytes, (base + g) & 1 ? &tmV : &tmK, &s_full[stage], 0,
+                  (base + g) >> 1, (int)(row0));
+  };
+  if constexpr (TMA) {
+    if (tid == 0) {
+      for (int i = 0; i < kStages; ++i) mbar_init(&s_full[i], 1);
+      fence_mbar_init();
+      for (int i = 0; i < kStages && i0 + i * groups < i1; ++i) fetch(i0 + i * groups, i);
+    }
+    __syncthreads();
+    s_next = mine0 < i1 && held ? *scale_of(mine0) : 0.f;
+  } else {
+    load(mine0, next, s_next);
+  }
+  int stage = 0, phase = 0;
   for (int base = i0, turn = 0; base < i1; base += groups, turn ^= 1) {  // (every thread: barriers inside)
     const int item = base + (tid >> tg_shift);
     uint4 v[NV];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) v[j] = next[j];
     const float s_old = s_next;
-    load(item + groups, next, s_next);
+    if constexpr (TMA) {
+      if (!mbar_wait_bounded(&s_full[stage], phase, nullptr)) {
+        set_status(p.dev_status, SPEC_ERR_TIMEOUT);
+        if (tid == 0)  // the copies in flight land first
+          for (int i = 0; i < kStages; ++i) mbar_wait_bounded(&s_full[i], i >= stage ? phase : phase ^ 1, nullptr);
+        return;  // (every thread: all wait for the same)
+      }
+      const uint4* box = reinterpret_cast<const uint4*>(ring + stage * kStageBytes + (tid >> tg_shift) * item_bytes);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) v[j] = from[j] >= 0 ? box[t + j * tg] : make_uint4(0, 0, 0, 0);
+      const int ahead = item + groups;
+      s_next = ahead < i1 && held ? *scale_of(ahead) : 0.f;
+    } else {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) v[j] = next[j];
+      load(item + groups, next, s_next);
+    }
     uint32_t top = 0;
 #pragma unroll
     for (int j = 0; j < NV; ++j) top = Vec<BF16>::grow(top, v[j]);
@@ -259,9 +301,18 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv8_append_kernel(con
       for (int j = 0; j < NV; ++j) top = finite_top<BF16>(top, v[j]);
     }
     top = __reduce_max_sync(0xffffffffu, top);
-    if (tg > 32) {
+    if (TMA || tg > 32) {
       if (lane == 0) s_max[turn][warp] = top;
       __syncthreads();
+      if constexpr (TMA) {  // the round has been read: its place is free
+        if (tid == 0 && base + kStages * groups < i1) fetch(base + kStages * groups, stage);
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+    }
+    if (tg > 32) {
       const int w0 = (tid >> tg_shift) << (tg_shift - 5);
       top = __reduce_max_sync(0xffffffffu, lane < (tg >> 5) ? s_max[turn][w0 + lane] : 0u);
     }
@@ -357,24 +408,35 @@ unsigned kv8_append_grid(const Kv8AppendParams& p) {
   return g > 0x7fffffffLL ? 0u : (unsigned)g;
 }
 
-cudaError_t launch_kv8_append(const Kv8AppendParams& p, cudaStream_t stream) {
+cudaError_t launch_kv8_append(const CUtensorMap* tm, const Kv8AppendParams& p, cudaStream_t stream) {
   const AppendShape s = append_shape(p);
   const unsigned grid = kv8_append_grid(p);
+  static const CUtensorMap none = {};
   cudaError_t err = cudaSuccess;
-  auto go = [&](auto kernel) {
-    err = launch_dependent(kernel, dim3(grid), dim3(s.threads), 0, stream, p, s.parts, s.tg_shift);
+  auto go = [&](auto kernel, size_t smem = 0) {
+    if (smem) err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (err == cudaSuccess)
+      err = launch_dependent(kernel, dim3(grid), dim3(s.threads), smem, stream, tm ? tm[0] : none, tm ? tm[1] : none, p,
+                             s.parts, s.tg_shift);
   };
+  constexpr size_t kRing = 128 + (size_t)kStages * 256 * kVecs * 16;
   if (p.is_bf16) {
-    if (s.threads == 256) go(kv8_append_kernel<true, kVecs, 256>);
-    else if (s.threads == 512) go(kv8_append_kernel<true, kVecs, 512>);
-    else go(kv8_append_kernel<true, kVecs, 1024>);
+    if (s.threads == 256) {
+      if (tm) go(kv8_append_kernel<true, kVecs, 256, true>, kRing);
+      else go(kv8_append_kernel<true, kVecs, 256, false>);
+    } else if (s.threads == 512) go(kv8_append_kernel<true, kVecs, 512, false>);
+    else go(kv8_append_kernel<true, kVecs, 1024, false>);
   } else {
-    if (s.threads == 256) go(kv8_append_kernel<false, kVecs, 256>);
-    else if (s.threads == 512) go(kv8_append_kernel<false, kVecs, 512>);
-    else if (s.nv == kVecs) go(kv8_append_kernel<false, kVecs, 1024>);
-    else go(kv8_append_kernel<false, 2 * kVecs, 1024>);
+    if (s.threads == 256) {
+      if (tm) go(kv8_append_kernel<false, kVecs, 256, true>, kRing);
+      else go(kv8_append_kernel<false, kVecs, 256, false>);
+    } else if (s.threads == 512) go(kv8_append_kernel<false, kVecs, 512, false>);
+    else if (s.nv == kVecs) go(kv8_append_kernel<false, kVecs, 1024, false>);
+    else go(kv8_append_kernel<false, 2 * kVecs, 1024, false>);
   }
   return err;
 }
+
+bool kv8_append_boxes(const Kv8AppendParams& p) { return !p.path && p.n_rows > 0 && append_shape(p).threads == 256; }
 
 }  // namespace spectree
