@@ -162,6 +162,33 @@ def test_rows_out_of_order_refuse_the_call(rows):
     assert int(status.item()) == 7 and new.tolist() == start
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("bs,d", [(16, 128), (64, 64), (128, 128), (256, 128), (256, 64)])
+def test_tokens_and_a_prompt_in_one_call(dtype, bs, d):
+    """One row for most requests, none for some, a prompt of several blocks for one: a block may have more new rows
+    than the call's average suggests."""
+    dev = K8.dev()
+    rng = np.random.default_rng(bs * d)
+    B, Hkv = 40, 3
+    start = [int(x) for x in rng.integers(0, 2 * bs, B)]
+    add = [1] * B
+    add[3], add[7], add[20] = 0, 2 * bs + 5, 11
+    cache = K8.Cache(rng, [a + n for a, n in zip(start, add)], Hkv, d, bs)
+    c, kw = _device(cache, dev)
+    rk, k = _rows(rng, (sum(add), Hkv, d), dtype, 7)
+    rv, v = _rows(rng, (sum(add), Hkv, d), dtype, 7)
+    rk[4, 1, 5] = float("inf")
+    k[4, 1, 5] = np.inf
+    rs = np.concatenate([[0], np.cumsum(add)]).astype(np.int32)
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    new = st.kv8_append(rk.to(dev), rv.to(dev), seq_len=torch.tensor(start, dtype=torch.int32, device=dev),
+                        row_start=torch.from_numpy(rs).to(dev), dev_status=status, **kw)
+    for b in range(B):
+        _oracle_append(cache, b, k[rs[b]: rs[b + 1]], v[rs[b]: rs[b + 1]], start[b])
+    _compare(cache, c)
+    assert int(status.item()) == 0 and new.tolist() == [a + n for a, n in zip(start, add)]
+
+
 def test_rows_ahead_of_and_behind_the_requests():
     """Packed rows that belong to no request are not looked at."""
     dev = K8.dev()

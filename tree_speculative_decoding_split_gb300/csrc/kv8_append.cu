@@ -1,13 +1,14 @@
 // K8: rows into the 8-bit paged cache (spec_kv8_append).
 //
 // A block of one KV head is bs x d elements with one scale s = 2^e, e the smallest with
-// max |x| <= 448 * 2^e; a code is e4m3(x / s).  Both steps need the whole block, which fits the
-// registers of one group of threads: the group loads the block's new rows once, reduces |x| to the
+// max |x| <= 448 * 2^e; a code is e4m3(x / s).  Both steps need all of a block's new rows, which fit the
+// registers of one group of threads: the group loads them once, reduces |x| to the
 // maximum, and converts what it holds.  So the rows are read once and the codes written once: HBM-bound.
-// A CTA goes through the heads of its block one after another with the next one's rows on their way (one
-// head per CTA took 103 us for 35K rows of 8 heads: most of it finding the request, block and scale).
-// Measured: those rows (bf16, d 128) 52 us = 4.1 TB/s, 0.61 of a plain copy's rate; 328K fp32 rows (d 64) 303 us =
-// 5.5 TB/s, 0.81.  The accepted paths of 32 requests 10.7 us with a cold cache, 6.5 warm: one launch and four loads in a row.
+// A CTA goes through the heads of its block one after another (one head per CTA took 103 us for 35K rows of 8 heads:
+// most of it finding the request, block and scale); long runs of rows come by TMA, three rounds ahead.
+// Measured: 8 prompts of 35K rows together (bf16, 8 heads, d 128) 41.5 us = 5.2 TB/s, 0.76 of a plain copy's rate;
+// 328K fp32 rows (d 64) 262 us = 6.4 TB/s, 0.94 (one round ahead into registers: 51.7 and 303 us).  The accepted
+// paths of 32 requests 10.7 us with a cold cache, 6.5 warm: one launch and four loads in a row.
 // A half-full block keeps its larger scale; its old codes are read only when the scale grows.
 #include "common.cuh"
 #include "kernels.cuh"
@@ -219,31 +220,36 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
   const int blk = p.table[(size_t)b * p.max_blocks + (first >> p.bs_shift)];
   if (blk < 0 || blk >= p.num_blocks) return;  // (the lead CTA has set the status)
 
-  // ---- this thread's vectors: the same places of every item ----
+  // ---- this thread's vectors: the same places of every item, counted from the first new row.  Where a group cannot
+  // hold all of a block's (a prompt among single tokens), the others are read twice. ----
   const int tg = 1 << tg_shift, groups = blockDim.x >> tg_shift;
   const int t = tid & (tg - 1);
   const int row_shift = 31 - __clz(p.d / E);  // vectors per row: a power of two
   const int row_bytes = p.d * (BF16 ? 2 : 4);
   const long long row0 = p.path ? (long long)b * p.N : (long long)p.row_start[b] + (first - len);
   const int32_t* pth = p.path ? p.path + (size_t)b * p.path_cap + (first - len) : nullptr;
-  int from[NV];  // source row of vector j's place, or -1: no new row there
+  const int start = held << row_shift, vecs = (end - held) << row_shift;
+  auto source = [&](int q) {  // source row of vector q, or -1 behind the last new row
+    const int r = held + (q >> row_shift);
+    return q < vecs ? (int)(p.path ? row0 + pth[r] : row0 + r) : -1;
+  };
+  int from[NV];
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int r = (t + j * tg) >> row_shift;
-    from[j] = r >= held && r < end ? (int)(p.path ? row0 + pth[r] : row0 + r) : -1;
-  }
+  for (int j = 0; j < NV; ++j) from[j] = source(t + j * tg);
   const int items = 2 * p.Hkv, per = (items + parts - 1) / parts;
   const int i0 = part * per, i1 = min(items, i0 + per);
   const size_t cell0 = (size_t)blk * p.Hkv;
+  auto vector = [&](int item, int q, int row) {
+    const uint8_t* src = static_cast<const uint8_t*>((item & 1) ? p.v_new : p.k_new) + (size_t)(item >> 1) * row_bytes;
+    const int col = q & ((1 << row_shift) - 1);
+    return __ldcs(reinterpret_cast<const uint4*>(src + row * ((size_t)p.Hkv * row_bytes) + col * 16));
+  };
   auto scale_of = [&](int item) { return ((item & 1) ? p.v_scale : p.k_scale) + cell0 + (item >> 1); };
   auto load = [&](int item, uint4 (&v)[NV], float& s_old) {
-    const uint8_t* src = static_cast<const uint8_t*>((item & 1) ? p.v_new : p.k_new) + (size_t)(item >> 1) * row_bytes;
-    const size_t stride = (size_t)p.Hkv * row_bytes;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       v[j] = make_uint4(0, 0, 0, 0);
-      const int col = (t + j * tg) & ((1 << row_shift) - 1);
-      if (item < i1 && from[j] >= 0) v[j] = __ldcs(reinterpret_cast<const uint4*>(src + from[j] * stride + col * 16));
+      if (item < i1 && from[j] >= 0) v[j] = vector(item, t + j * tg, from[j]);
     }
     s_old = item < i1 && held ? *scale_of(item) : 0.f;
   };
@@ -283,7 +289,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
       }
       const uint4* box = reinterpret_cast<const uint4*>(ring + stage * kStageBytes + (tid >> tg_shift) * item_bytes);
 #pragma unroll
-      for (int j = 0; j < NV; ++j) v[j] = from[j] >= 0 ? box[t + j * tg] : make_uint4(0, 0, 0, 0);
+      for (int j = 0; j < NV; ++j) v[j] = from[j] >= 0 ? box[start + t + j * tg] : make_uint4(0, 0, 0, 0);
       const int ahead = item + groups;
       s_next = ahead < i1 && held ? *scale_of(ahead) : 0.f;
     } else {
@@ -300,6 +306,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
 #pragma unroll
       for (int j = 0; j < NV; ++j) top = finite_top<BF16>(top, v[j]);
     }
+    if constexpr (!TMA)
+      if (item < i1)
+#pragma unroll 1
+        for (int q = t + NV * tg; q < vecs; q += tg) top = finite_top<BF16>(top, vector(item, q, source(q)));
     top = __reduce_max_sync(0xffffffffu, top);
     if (TMA || tg > 32) {
       if (lane == 0) s_max[turn][warp] = top;
@@ -337,7 +347,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
           x[e] = y.x;
           x[e + 1] = y.y;
         }
-        store_codes<E>(codes + (size_t)(t + j * tg) * E, x);
+        store_codes<E>(codes + (size_t)(start + t + j * tg) * E, x);
       }
     } else {
 #pragma unroll 1
@@ -355,9 +365,18 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
         Vec<BF16>::unpack(w, x);
 #pragma unroll
         for (int e = 0; e < E; ++e) x[e] = x[e] / s;
-        store_codes<E>(codes + (size_t)(t + j * tg) * E, x);
+        store_codes<E>(codes + (size_t)(start + t + j * tg) * E, x);
       }
     }
+    if constexpr (!TMA)
+#pragma unroll 1
+      for (int q = t + NV * tg; q < vecs; q += tg) {
+        float x[E];
+        Vec<BF16>::unpack(vector(item, q, source(q)), x);
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] = x[e] / s;
+        store_codes<E>(codes + (size_t)(start + q) * E, x);
+      }
     if (grown) {  // the old rows' codes in the new scale
       const float ratio = s_old / s;
 #pragma unroll 1
@@ -381,13 +400,25 @@ namespace {
 
 struct AppendShape {
   int tg_shift, threads, parts, nv;
+  bool boxes;  // packed rows by TMA
   long long units;
 };
 
 AppendShape append_shape(const Kv8AppendParams& p) {
   AppendShape s;
-  const int vecs = p.bs * p.d / (p.is_bf16 ? 8 : 4);  // 128 (16 x 64 bf16) to 8192 (256 x 128 fp32)
+  // A group holds a block's new rows: of a path, all there can be; of packed rows a whole block, or, where the
+  // requests have few on average (tokens, one each), about as many as that.  One row for each of 512 requests (bf16,
+  // d 128, blocks of 64): 17.5 us, as whole blocks by TMA 34, into registers 40; 16 rows each: by TMA 36, into
+  // registers 44.  (fp32, blocks of 256, one row each: 17.5 and 261.)
+  long long rows = p.bs;
+  if (p.path) rows = p.path_cap < p.N ? p.path_cap : p.N;
+  else if (p.n_rows < (long long)p.B * p.bs / 8) rows = (p.n_rows + p.B - 1) / p.B;
+  const bool whole = rows >= p.bs;
+  int fit = 1;
+  while (fit < rows && fit < p.bs) fit <<= 1;
+  const int vecs = fit * p.d / (p.is_bf16 ? 8 : 4);  // up to 8192 (256 x 128 fp32)
   s.nv = vecs > 1024 * kVecs ? 2 * kVecs : kVecs;
+  s.boxes = !p.path && whole && p.n_rows > 0 && s.nv == kVecs;
   s.tg_shift = 5;
   while ((s.nv << s.tg_shift) < vecs) ++s.tg_shift;
   const int tg = 1 << s.tg_shift;
@@ -419,24 +450,35 @@ cudaError_t launch_kv8_append(const CUtensorMap* tm, const Kv8AppendParams& p, c
       err = launch_dependent(kernel, dim3(grid), dim3(s.threads), smem, stream, tm ? tm[0] : none, tm ? tm[1] : none, p,
                              s.parts, s.tg_shift);
   };
-  constexpr size_t kRing = 128 + (size_t)kStages * 256 * kVecs * 16;
+  const size_t ring = 128 + (size_t)kStages * s.threads * kVecs * 16;
   if (p.is_bf16) {
     if (s.threads == 256) {
-      if (tm) go(kv8_append_kernel<true, kVecs, 256, true>, kRing);
+      if (tm) go(kv8_append_kernel<true, kVecs, 256, true>, ring);
       else go(kv8_append_kernel<true, kVecs, 256, false>);
-    } else if (s.threads == 512) go(kv8_append_kernel<true, kVecs, 512, false>);
-    else go(kv8_append_kernel<true, kVecs, 1024, false>);
+    } else if (s.threads == 512) {
+      if (tm) go(kv8_append_kernel<true, kVecs, 512, true>, ring);
+      else go(kv8_append_kernel<true, kVecs, 512, false>);
+    } else {
+      if (tm) go(kv8_append_kernel<true, kVecs, 1024, true>, ring);
+      else go(kv8_append_kernel<true, kVecs, 1024, false>);
+    }
   } else {
     if (s.threads == 256) {
-      if (tm) go(kv8_append_kernel<false, kVecs, 256, true>, kRing);
+      if (tm) go(kv8_append_kernel<false, kVecs, 256, true>, ring);
       else go(kv8_append_kernel<false, kVecs, 256, false>);
-    } else if (s.threads == 512) go(kv8_append_kernel<false, kVecs, 512, false>);
-    else if (s.nv == kVecs) go(kv8_append_kernel<false, kVecs, 1024, false>);
-    else go(kv8_append_kernel<false, 2 * kVecs, 1024, false>);
+    } else if (s.threads == 512) {
+      if (tm) go(kv8_append_kernel<false, kVecs, 512, true>, ring);
+      else go(kv8_append_kernel<false, kVecs, 512, false>);
+    } else if (s.nv == kVecs) {
+      if (tm) go(kv8_append_kernel<false, kVecs, 1024, true>, ring);
+      else go(kv8_append_kernel<false, kVecs, 1024, false>);
+    } else {
+      go(kv8_append_kernel<false, 2 * kVecs, 1024, false>);
+    }
   }
   return err;
 }
 
-bool kv8_append_boxes(const Kv8AppendParams& p) { return !p.path && p.n_rows > 0 && append_shape(p).threads == 256; }
+bool kv8_append_boxes(const Kv8AppendParams& p) { return append_shape(p).boxes; }
 
 }  // namespace spectree
