@@ -71,7 +71,7 @@ __device__ __forceinline__ int kv8_cut(const Kv8AttnParams& p) {
   const int least = 256 >> p.unit_shift, lane = threadIdx.x & 31;
   float total = 0.f;
   int longest = 1;
-#pragma unroll 1
+#pragma unroll 4
   for (int i = lane; i < p.B; i += 32) {
     const int steps = kv8_steps(p, p.prefix_len[i]);
     total += (float)steps;
