@@ -682,7 +682,7 @@ Kv8AttnPlan plan_attention_kv8(int B, int N, int G, int Hkv, long long L_cap, in
     // as many CTAs as fit at once (four an SM): 57.8 us for 32 requests at 4K, 59.9 with half or twice as many
     pl.base = (int)((pl.slots + ctas - 1) / ctas);
     if (pl.base > limit) pl.base = (int)limit;
-    more = pl.slots / 2 / per + 1;
+    more = pl.slots * 2ll / 3 / per + 1;
   } else {
     // CTAs for every slot, and up to six where that leaves a split 64 steps of the longest prefixes
     pl.base = (int)(pl.slots / ctas);

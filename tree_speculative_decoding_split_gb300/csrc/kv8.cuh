@@ -54,9 +54,10 @@ struct Kv8Work {
 // for 32 requests took 62-66 us instead of 56), and behind them `extra` units for the splits past `base`, in the
 // requests' order.  CTAs without a split end at once.
 // The lengths are on the device, so every CTA works out the same cut from them:
-//   few-rows kernel: `base` splits, more where one of them would be longer than two even shares of all the steps.  Its
+//   few-rows kernel: `base` splits, more where one of them would be longer than 1.5 even shares of all the steps.  Its
 //   CTAs share the memory's bandwidth, so that it only has to keep one long request from running on alone.  Splits
-//   past base are then no more than slots / (2 * heads) units.
+//   past base are then no more than slots / (1.5 * heads) units.  (31 requests of 2K and one of 128K: 118 us, at two
+//   shares 132; at one share the 32 requests of 2K to 6K take 68 us instead of 57.)
 //   tensor-core kernel, where a CTA's speed is its own: c steps at most, the one of ceil(longest / k), for 16 numbers k
 //   from 1 to 32, that fits the units with the least cost.  With a split's work w = c + fixed, the whole work W and
 //   `slots` CTAs at once, the cost is the lesser of two upper bounds, whole rounds of CTAs times w and
@@ -80,7 +81,7 @@ __device__ __forceinline__ int kv8_cut(const Kv8AttnParams& p) {
   total = warp_sum(total);
   longest = __reduce_max_sync(0xffffffffu, longest);
   if (p.unit_shift == 6 || p.B > 128 || longest > 65535) {
-    const float share = p.unit_shift == 6 ? 2.f * total * (float)(p.Hkv * p.n_rt) * p.inv_slots : total / (float)p.extra;
+    const float share = p.unit_shift == 6 ? 1.5f * total * (float)(p.Hkv * p.n_rt) * p.inv_slots : total / (float)p.extra;
     return max(least, (int)fminf(ceilf(share * 1.0001f), 1e9f));
   }
   // two lanes per candidate, each over every other request
