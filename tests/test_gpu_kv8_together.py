@@ -232,3 +232,36 @@ def test_refusals_by_the_library():
         st.kv_reserve(i, i, i.view(2, 1).clone(), i.clone(), i.clone(), i[:1].clone(), 48)
     with pytest.raises(ValueError):
         st.kv_reserve(i[:1], i, i.view(2, 1).clone(), i.clone(), i.clone(), i[:1].clone(), 16)
+
+
+@pytest.mark.parametrize("N", [1, 40])
+def test_graphs_that_share_a_workspace(N):
+    """Two captured calls with one workspace of the caller's, replayed in turn after other lengths have been written:
+    the answers of eager calls."""
+    dev = K8.dev()
+    rng = np.random.default_rng(4 + N)
+    ws = torch.empty(1 << 27, dtype=torch.uint8, device=dev)
+    calls, outs, graphs = [], [], []
+    for lens in ([2600, 31], [64, 5000, 700]):
+        cache = K8.Cache(rng, lens, 2, 128, 32)
+        qs = K8.Queries(rng, len(lens), N, 8, 2, 128)
+        c = cache.device(dev)
+        calls.append([qs.q_t.to(dev), qs.kt_t.to(dev), qs.vt_t.to(dev), c["k_cache"], c["v_cache"], c["k_scale"], c["v_scale"],
+                      torch.tensor(lens, dtype=torch.int32, device=dev), torch.from_numpy(qs.n_nodes).to(dev),
+                      torch.from_numpy(qs.parent).to(dev), c["block_table"]])
+    for call in calls:
+        st.tree_attention_kv8(*call, workspace=ws)
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(st.tree_attention_kv8(*call, workspace=ws))
+    for shorter in (0, 7, 29):
+        for call in calls:
+            call[7].sub_(shorter)
+        want = [st.tree_attention_kv8(*call) for call in calls]
+        for _ in range(3):
+            for g in graphs:
+                g.replay()
+        torch.cuda.synchronize()
+        for (out, lse), (o, e) in zip(want, outs):
+            assert torch.equal(out, o) and torch.equal(lse, e)
