@@ -679,8 +679,11 @@ Kv8AttnPlan plan_attention_kv8(int B, int N, int G, int Hkv, long long L_cap, in
   const long long limit = most < 1 ? 1 : (most < kKv8Splits ? most : kKv8Splits);
   long long more;
   if (pl.groups == 0) {
-    // as many CTAs as fit at once (four an SM): 57.8 us for 32 requests at 4K, 59.9 with half or twice as many
-    pl.base = (int)((pl.slots + ctas - 1) / ctas);
+    // one round of CTAs (four an SM) where splits are fine enough to fill it, else at least one and a half: just over
+    // one leaves the second almost empty.  1.0 rounds and up against 1.5 and up: 32 requests of 2K to 6K 67 and 62 us, 48
+    // of 4K 97 and 80, 20 of 8K 93 and 72, 4 of 32K (19 or 29 splits) 62 and 68.
+    pl.base = (int)(pl.slots / ctas);
+    if (pl.base < 4) pl.base = (int)((pl.slots * 3ll / 2 + ctas - 1) / ctas);
     if (pl.base > limit) pl.base = (int)limit;
     more = pl.slots * 2ll / 3 / per + 1;
   } else {

@@ -56,8 +56,8 @@ struct Kv8Work {
 // The lengths are on the device, so every CTA works out the same cut from them:
 //   few-rows kernel: `base` splits, more where one of them would be longer than 1.5 even shares of all the steps.  Its
 //   CTAs share the memory's bandwidth, so that it only has to keep one long request from running on alone.  Splits
-//   past base are then no more than slots / (1.5 * heads) units.  (31 requests of 2K and one of 128K: 118 us, at two
-//   shares 132; at one share the 32 requests of 2K to 6K take 68 us instead of 57.)
+//   past base are then no more than slots / (1.5 * heads) units.  (31 requests of 2K and one of 128K take a tenth less
+//   than at two shares; at one share the 32 requests of 2K to 6K take 68 us instead of 57.)
 //   tensor-core kernel, where a CTA's speed is its own: c steps at most, the one of ceil(longest / k), for 16 numbers k
 //   from 1 to 32, that fits the units with the least cost.  With a split's work w = c + fixed, the whole work W and
 //   `slots` CTAs at once, the cost is the lesser of two upper bounds, whole rounds of CTAs times w and
@@ -140,7 +140,8 @@ __device__ __forceinline__ Kv8Work kv8_begin(const Kv8AttnParams& p, Kv8Work w) 
   int c = 0x3fffffff, first = 0;
   w.L = own ? p.prefix_len[w.b] : 0;
   w.nodes = own ? p.n_nodes[w.b] : 0;
-  if (p.extra > 0 || (p.unit_shift == 7 && p.base > 1)) {
+  // (a request of 256 keys or fewer has one split whatever the others are)
+  if ((p.extra > 0 || (p.unit_shift == 7 && p.base > 1)) && !(own && w.L <= 256)) {
     c = kv8_cut(p);
     if (!own) {
       const int heads = p.Hkv * p.n_rt, idx = blockIdx.x - p.B * p.base * heads, unit = idx / heads;
