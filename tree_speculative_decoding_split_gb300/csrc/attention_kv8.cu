@@ -687,11 +687,13 @@ Kv8AttnPlan plan_attention_kv8(int B, int N, int G, int Hkv, long long L_cap, in
     if (pl.base > limit) pl.base = (int)limit;
     more = pl.slots * 2ll / 3 / per + 1;
   } else {
-    // CTAs for every slot, and up to six where that leaves a split 64 steps of the longest prefixes
+    // CTAs for every slot, and up to six where the requests fill the slots by themselves and that leaves a split 64
+    // steps of the longest prefixes (those that are not used cost a microsecond or two a round)
     pl.base = (int)(pl.slots / ctas);
     pl.base = pl.base < 1 ? 1 : pl.base > limit ? (int)limit : pl.base;
     more = ctas * (L_cap >> pl.unit_shift) / 64;
-    more = more > 6ll * pl.slots ? 6ll * pl.slots : more < pl.slots ? pl.slots : more;
+    more = more > 6ll * pl.slots ? 6ll * pl.slots : more;
+    if (more < pl.slots || pl.base > 1) more = pl.slots;
     more = (more + per - 1) / per - (long long)B * (pl.base - 1);
     if (more < 0) more = 0;
   }
