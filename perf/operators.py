@@ -251,7 +251,7 @@ def _reserve(table, n_blocks, free, free_count, seq_len, n_new, bs):
     free.copy_(longer[:num])
     top = free_count + released
     # blocks taken come off its top, in the order of the requests; all that a request wants, or none
-    ok = (torch.cumsum(need, 0) <= top) | (need == 0)
+    ok = torch.cumsum(need, 0) <= top
     taken = ok[:, None] & (col >= n_blocks[:, None]) & (col < want[:, None])
     at = (top - 1 - (need_start[:, None] + col - n_blocks[:, None])).clamp(0, num - 1)
     table.copy_(torch.where(taken, free[at.long()], torch.where(gone, -1, table)))
