@@ -32,6 +32,7 @@
 // 2112 us: two issuing warps with the V tiles converted by the softmax warps, 2567 us; waits with a suspend-time hint
 // 2942 us, waits that only poll 3144 us.  The tree's tiles eight keys at a time in a rolled loop: 60 us for the 8
 // trees of 127 nodes instead of 57.
+#include <cfloat>
 #include <type_traits>
 
 #include "common.cuh"
@@ -756,7 +757,7 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
 #pragma unroll
               for (int j = gr * 16; j < gr * 16 + 16; ++j) a = fmaxf(a, c * 32 + j < left ? __uint_as_float(x[j]) : -INFINITY);
               const float4 k = cst[c * 2 + gr];
-              top = fmaxf(top, fmaf(a, k.x * qf, k.y));
+              top = fmaxf(top, fmaf(a, fmaxf(k.x * qf, FLT_MIN), k.y));
             }
           }
           return top;
@@ -781,7 +782,9 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
 #pragma unroll
             for (int gr = 0; gr < 2; ++gr) {
               const float4 k = cst[c * 2 + gr];
-              const float f = k.x * qf, off = k.y - m;
+              // (never 0, as a row of zeros or a block of zeros would have it: the -inf of a slot behind the prefix
+              // has to stay one, and what is below 2^-126 moves no score)
+              const float f = fmaxf(k.x * qf, FLT_MIN), off = k.y - m;
               const float2 f2 = make_float2(f, f), off2 = make_float2(off, off);
               float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
