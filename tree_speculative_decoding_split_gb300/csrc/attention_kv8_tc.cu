@@ -665,13 +665,14 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
     const uint32_t tO = tmem + C::kColO + g * 128 + lane_off;
     const bool live = row < n * p.G;
     const float qf = s_qf[g][rl];  // undoes the row's scaling, with the softmax scale in log2 units
+    // The pair's barriers below have no limit, and either warp's waits may give up.  So no warp leaves the tiles
+    // early: it says that it gave up, and goes through the rest with its pair (no wait takes long then), for nothing.
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-      return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, &s_abort));
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, &s_abort))) s_abort = 1;
     };
     float m = -INFINITY, l = 0.f;  // the row's reference (P = 2^(y - m)), and the sum over this thread's keys
     const uint32_t* anc = s_nanc + (live ? kv8_node(p, row) : 0) * kAncWords;
     const int pair = 2 + g * 4 + q4;  // named barrier of the two warps that share rows
-    bool ok = true;
     // Moves the references of the rows that ask for it in either of their threads (`ask`, with the largest of
     // the thread's scores in `top`); O and the sums follow.  Also down, at the first tile behind the tree's
     // (`anew`): the tree's weights are bf16 and bear any reference, but the prefix's must start at the top of
@@ -687,7 +688,7 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
       const float f = mn == m ? 1.f : ex2_approx(m - mn);  // 0 when there was none
       named_bar_sync(pair, 64);                            // both have read before either writes again
       if (t > 0) {  // (these scores came after P V(t - kNB); with one buffer there is nothing to wait for)
-        if (C::kNB > 1 && !wait(&ofull[g], (t - 1) & 1)) return false;
+        if (C::kNB > 1) wait(&ofull[g], (t - 1) & 1);
         tc_fence_after();
 #pragma unroll 1
         for (int c = half * (D / 64); c < (half + 1) * (D / 64); ++c) {
@@ -702,13 +703,9 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
       }
       l *= f;
       m = mn;
-      return true;
     };
     for (int t = 0; t < T; ++t) {
-      if (!wait(&sfull[g][t % C::kNB], (t / C::kNB) & 1)) {
-        ok = false;
-        break;
-      }
+      wait(&sfull[g][t % C::kNB], (t / C::kNB) & 1);
       tc_fence_after();
       const uint32_t ts = tS + (NG == 2 ? 0 : t % C::kNB) * 128;
       if (t < Tt) {
@@ -724,10 +721,7 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
           top = fmaxf(top, y);
           x[j] = __float_as_uint(y);
         }
-        if (bar_or(pair, 64, top > m + 8.f) && !move_references(top > m + 8.f, false, top, t)) {
-          ok = false;
-          break;
-        }
+        if (bar_or(pair, 64, top > m + 8.f)) move_references(top > m + 8.f, false, top, t);
         const float mu = m == -INFINITY ? 0.f : m;
         uint32_t pk[16];
         float sum = 0.f;
@@ -762,10 +756,7 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
           }
           return top;
         };
-        if (t == Tt && !move_references(true, true, largest(), t)) {
-          ok = false;
-          break;
-        }
+        if (t == Tt) move_references(true, true, largest(), t);
         uint32_t pk[2][16];
         for (int pass = 0; pass < 2; ++pass) {
           float part = 0.f, most = 0.f;  // sum of the weights over the V scales; largest sum of sixteen
@@ -806,9 +797,8 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
             break;
           }
           // a weight may have left f16's range: move the references and take the weights again
-          if (!move_references(most > kTop, false, largest(), t)) ok = false;
+          move_references(most > kTop, false, largest(), t);
         }
-        if (!ok) break;
         tmem_st_x16(ts + half * 64, pk[0]);  // over this thread's own scores
         tmem_st_x16(ts + half * 64 + 16, pk[1]);
       }
@@ -818,12 +808,10 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
       if (lane == 0) mbar_arrive(&pfull[g][t & 1]);
     }
     // in turn: the scores of tile T - 1 follow P V(T - 1 - kNB) only, and a wait two phases ahead returns at once
-    const bool fin = ok && (C::kNB == 1 || T < 2 || wait(&ofull[g], (T - 2) & 1)) &&
-                     wait(&ofull[g], C::kNB == 1 ? 0 : (T - 1) & 1);
-    if (!fin && lane == 0) {
-      s_abort = 1;
-      set_status(p.dev_status, SPEC_ERR_TIMEOUT);
-    }
+    if (C::kNB > 1 && T >= 2) wait(&ofull[g], (T - 2) & 1);
+    wait(&ofull[g], C::kNB == 1 ? 0 : (T - 1) & 1);
+    const bool fin = __all_sync(0xffffffffu, *static_cast<volatile int*>(&s_abort) == 0);
+    if (!fin && lane == 0) set_status(p.dev_status, SPEC_ERR_TIMEOUT);
     s_x[g][half][rl] = l;
     // every MMA of both groups has completed: Q and the rings are free for the O rows
     named_bar_sync(1, 256 * NG);
