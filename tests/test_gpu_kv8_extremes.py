@@ -4,6 +4,7 @@ smallest and largest numbers."""
 import numpy as np
 import pytest
 
+import oracle
 import kv8_helpers as K8
 import kv8_strict
 
@@ -36,3 +37,80 @@ def test_rows_of_zeros(N, G, slots, d, bs):
     assert status == 0
     assert np.isfinite(out).all() and np.isfinite(lse).all()
     kv8_strict.check(cache, qs, out, lse)
+
+
+@pytest.mark.parametrize("N,G,slots", FORMS)
+@pytest.mark.parametrize("e,ke", [(22, 0), (27, 0), (31, 0), (60, 0), (104, 0), (120, 0), (126, -56), (127, -58), (20, 90)])
+def test_large_queries(N, G, slots, e, ke):
+    """Queries near 2^e and K scales near 2^ke, so that scores run from 2^26 to 2^124: one key takes a row's whole
+    weight.  Request 0: a key each row points to.  Request 1: every score negative, the first key's least.
+
+    The winner's score leads by more than half of itself, its error is 2^-13 of it at most (kv8_strict takes the
+    same bound from kv8_helpers), so every other weight is 0 and the row is the winner's V row, which is exact in bf16."""
+    rng = np.random.default_rng(N + e)
+    d, lens = 128, [300, 3]
+    cache = K8.Cache(rng, lens, 1, d, 64, max_len=slots)
+    sign = rng.choice([-1.0, 1.0], (300, d))
+    cache.k[cache.table[0, : 5]] = oracle.e4m3_encode(np.concatenate([sign * 64, np.zeros((20, d))]).reshape(5, 1, 64, d))
+    cache.k[cache.table[1, 0], 0, :3] = oracle.e4m3_encode(sign[0] * np.array([[64], [104], [120]]))
+    cache.ks[:] = 2.0 ** (ke - 6)
+    qs = K8.Queries(rng, 2, N, G, 1, d)
+    winner = rng.integers(0, 300, (N, G))
+    qs.q_t, qs.q = K8.bf16(np.stack([sign[winner], np.broadcast_to(-sign[0], (N, G, d))]) *
+                           rng.uniform(1, 1.9, (2, N, G, d)) * 2.0 ** e)
+    qs.kt_t, qs.kt = K8.bf16(np.stack([rng.standard_normal((N, 1, d)) * 0.1, np.broadcast_to(sign[0] * 2, (N, 1, d))]) * 2.0 ** ke)
+    out, lse, status = K8.attend(K8.dev(), cache, qs)
+    assert status == 0
+    v0, v1 = (cache.values(b)[1][0] for b in range(2))
+    assert np.array_equal(out[0], v0[winner])
+    assert np.array_equal(out[1], np.broadcast_to(v1[0], out[1].shape))
+    kv8_strict.check(cache, qs, out, lse)
+
+
+@pytest.mark.parametrize("N,G,slots", FORMS)
+@pytest.mark.parametrize("e", [0, 30])
+def test_rows_keep_their_bits_beside_large_ones(N, G, slots, e):
+    """A head's rows are the same to the bit whatever the other heads' scores are."""
+    rng = np.random.default_rng(N)
+    cache = K8.Cache(rng, [300, 77], 1, 128, 64, max_len=slots)
+    qs = K8.Queries(rng, 2, N, 2 * G, 1, 128)
+    qs.q_t *= 2.0 ** e
+    out, lse, _ = K8.attend(K8.dev(), cache, qs)
+    qs.q_t[:, :, ::2] *= 2.0 ** 60
+    again, lse2, status = K8.attend(K8.dev(), cache, qs)
+    assert status == 0 and np.isfinite(again).all()
+    assert np.array_equal(out[:, :, 1::2], again[:, :, 1::2]) and np.array_equal(lse[:, :, 1::2], lse2[:, :, 1::2])
+    assert not np.array_equal(lse[:, :, ::2], lse2[:, :, ::2])
+
+
+@pytest.mark.parametrize("N,G,slots", FORMS)
+@pytest.mark.parametrize("e", range(24, 36))
+def test_scores_a_few_steps_apart(N, G, slots, e):
+    """Two keys whose scores, near 2^e in log2 units, differ by none to some float32 steps, the larger one later or in
+    the tree: whichever weighs more, the row lies between their two V rows."""
+    rng = np.random.default_rng(e)
+    cache = K8.Cache(rng, [300, 130], 1, 128, 64, max_len=slots)
+    cache.k[cache.table[0, :5]] = 0
+    cache.k[cache.table[1, :3]] = 0
+    one, two, minus = oracle.e4m3_encode(np.array([64.0, 128.0, -128.0]))
+    cache.ks[:] = 2.0 ** -6
+    for b, (first, second) in enumerate([(3, 290), (127, 128)]):
+        for slot in (first, second):
+            cache.k[cache.table[b, slot // 64], 0, slot % 64, 0] = one
+        cache.k[cache.table[b, second // 64], 0, second % 64, 1] = two
+        cache.v[cache.table[b, second // 64], 0, second % 64] = minus
+        cache.v[cache.table[b, first // 64], 0, first % 64] = two
+    cache.vs[:] = 2.0 ** -6
+    qs = K8.Queries(rng, 2, N, G, 1, 128)
+    q = np.zeros((2, N, G, 128))
+    q[..., 0] = 2.0 ** e * rng.uniform(5.6, 11.2, (2, N, G))          # times log2(e) / sqrt(128): 2^e * (0.7 .. 1.4)
+    q[..., 1] = q[..., 0] * 2.0 ** rng.integers(-26, -17, (2, N, G))  # half a step to 256 of them
+    qs.q_t, qs.q = K8.bf16(q)
+    kt = np.zeros((2, N, 1, 128))
+    kt[:, ::2, :, 0] = 1
+    kt[:, ::2, :, 2] = 2.0 ** -20
+    qs.kt_t, qs.kt = K8.bf16(kt)
+    qs.vt_t, qs.vt = K8.bf16(np.full((2, N, 1, 128), 1.5))
+    out, lse, status = K8.attend(K8.dev(), cache, qs)
+    assert status == 0
+    assert np.isfinite(lse).all() and (np.abs(out) <= 2).all()

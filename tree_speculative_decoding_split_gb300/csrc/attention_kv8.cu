@@ -98,7 +98,7 @@ __device__ __forceinline__ void softmax_step(float (&y)[RN][4], RowState<RN>& st
 #pragma unroll
   for (int n = 0; n < RN; ++n)
 #pragma unroll
-    for (int r = 0; r < 2; ++r) ahead = ahead || fmaxf(y[n][r], y[n][2 + r]) > st.m[n][r] + kLazy;
+    for (int r = 0; r < 2; ++r) ahead = ahead || fmaxf(y[n][r], y[n][2 + r]) - st.m[n][r] > kLazy;
   if (__any_sync(0xffffffffu, ahead)) {
 #pragma unroll
     for (int n = 0; n < RN; ++n)
@@ -109,7 +109,8 @@ __device__ __forceinline__ void softmax_step(float (&y)[RN][4], RowState<RN>& st
         for (int s = 4; s < 32; s <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, s));
         // each row by its own scores alone, so that no row's rounding depends on its neighbours
         const float m = st.m[n][r];
-        const float mn = v > m + kLazy || (rebase && v > -INFINITY) ? fmaxf(v, m - 64.f) : m;
+        // (down by 64 at most, also where 64 is less than a step of m)
+        const float mn = v - m > kLazy || (rebase && v > -INFINITY) ? fmaxf(v, __fsub_ru(m, 64.f)) : m;
         const float f = mn == m ? 1.f : ex2_approx(m - mn);
         st.m[n][r] = mn;
         st.l[n][r] *= f;
@@ -307,8 +308,9 @@ __global__ void __launch_bounds__(kWarps * 32, RN == 1 ? 4 : 2)
     }
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    // exponent of 2^(4 - floor(log2 mx)), kept where the factor and its reciprocal are normal numbers
-    const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 100);
+    // the factor 2^(4 - floor(log2 mx)) and its reciprocal are normal numbers up to the exponent 128 of an infinity; at
+    // the lower end mx counts as 2^-100 at least
+    const int e = max((int)(__float_as_uint(mx) >> 23) - 127, -100);
     const float up = __uint_as_float((uint32_t)(127 + 4 - e) << 23);
     const float down = __uint_as_float((uint32_t)(127 - 4 + e) << 23) * p.scale_log2;
     qf[r][0] = __shfl_sync(0xffffffffu, down, 8 * t);

@@ -394,7 +394,9 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
       }
 #pragma unroll
       for (int o = 1; o < D / 8; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 100);
+      // (both powers of two below are normal numbers up to the exponent 128 of an infinity; at the lower end a row's
+      // largest element counts as 2^-100 at least)
+      const int e = max((int)(__float_as_uint(mx) >> 23) - 127, -100);
       const float up = __uint_as_float((uint32_t)(127 + 7 - e) << 23);  // largest element into [128, 256)
       if (q_ch == 0) s_qf[q_g][r] = __uint_as_float((uint32_t)(127 - 7 + e) << 23) * p.scale_log2;
 #pragma unroll
@@ -676,7 +678,8 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
     // Moves the references of the rows that ask for it in either of their threads (`ask`, with the largest of
     // the thread's scores in `top`); O and the sums follow.  Also down, at the first tile behind the tree's
     // (`anew`): the tree's weights are bf16 and bear any reference, but the prefix's must start at the top of
-    // f16's range, however small its V scales are.  Each row by its own scores alone.
+    // f16's range, however small its V scales are.  Each row by its own scores alone.  Returns whether this row's
+    // was asked for.
     auto move_references = [&](bool ask, bool anew, float top, int t) {
       s_x[g][half][rl] = top;
       const uint32_t mine = __ballot_sync(0xffffffffu, ask);
@@ -684,10 +687,12 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
       named_bar_sync(pair, 64);
       top = fmaxf(top, s_x[g][half ^ 1][rl]);
       const bool need = (((mine | s_w[g][half ^ 1][q4]) >> lane) & 1u) && top > -INFINITY;
-      const float mn = need ? (anew ? fmaxf(ceilf(top), m - 64.f) : ceilf(top)) : m;
+      // (down by 64 at most, also where 64 is less than a step of m, and never down otherwise)
+      const float mn = need ? fmaxf(ceilf(top), anew ? __fsub_ru(m, 64.f) : m) : m;
       const float f = mn == m ? 1.f : ex2_approx(m - mn);  // 0 when there was none
       named_bar_sync(pair, 64);                            // both have read before either writes again
-      if (t > 0) {  // (these scores came after P V(t - kNB); with one buffer there is nothing to wait for)
+      // (these scores came after P V(t - kNB); with one buffer there is nothing to wait for)
+      if (t > 0 && __any_sync(0xffffffffu, mn != m)) {
         if (C::kNB > 1) wait(&ofull[g], (t - 1) & 1);
         tc_fence_after();
 #pragma unroll 1
@@ -703,6 +708,7 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
       }
       l *= f;
       m = mn;
+      return need;
     };
     for (int t = 0; t < T; ++t) {
       wait(&sfull[g][t % C::kNB], (t / C::kNB) & 1);
@@ -735,11 +741,51 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
         tmem_st_x16(ts + half * 64, pk);
       } else {
         // -- a prefix tile: this thread's 64 keys are 4 groups of 16, each within one block --
-        const int left = (int)min((long long)kKT8, k1 - (k0 + (long long)(t - Tt) * kKT8)) - half * 64;
         const float4* cst = s_cst + (t % kCS) * 8 + half * 4;
-        // the largest of this thread's scores
-        auto largest = [&]() {
-          float top = -INFINITY;
+        // Weights of sixteen keys, 2^(f y + off); returns their sum.
+        auto weigh = [&](const uint32_t* y, float f, float off, uint32_t* to) {
+          const float2 f2 = make_float2(f, f), off2 = make_float2(off, off);
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int j = 0; j < 16; j += 2) {
+            float2 w = __ffma2_rn(make_float2(__uint_as_float(y[j]), __uint_as_float(y[j + 1])), f2, off2);
+            w = make_float2(ex2_approx(w.x), ex2_approx(w.y));
+            sum[(j >> 1) & 1] = __fadd2_rn(sum[(j >> 1) & 1], w);
+            const __half2 h2 = __floats2half2_rn(w.x, w.y);
+            to[j / 2] = *reinterpret_cast<const uint32_t*>(&h2);
+          }
+          const float2 s2 = __fadd2_rn(sum[0], sum[1]);
+          return s2.x + s2.y;
+        };
+        const int keys = (int)min((long long)kKT8, k1 - (k0 + (long long)(t - Tt) * kKT8));
+        float part = 0.f, most = 0.f;  // sum of the weights over the V scales; largest sum of sixteen
+        bool slow = t == Tt || keys < kKT8;
+        if (!slow) {
+          uint32_t pk[2][16];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t x[32];
+            tmem_ld_x32(ts + half * 64 + c * 32, x);
+            tmem_ld_wait();
+#pragma unroll
+            for (int gr = 0; gr < 2; ++gr) {
+              const float4 k = cst[c * 2 + gr];
+              const float s16 = weigh(x + gr * 16, k.x * qf, k.y - m, pk[c] + gr * 8);
+              most = fmaxf(most, s16);
+              part = fmaf(s16, k.z, part);
+            }
+          }
+          slow = bar_or(pair, 64, most > kTop);
+          if (!slow) {
+            tmem_st_x16(ts + half * 64, pk[0]);  // over this thread's own scores
+            tmem_st_x16(ts + half * 64 + 16, pk[1]);
+          }
+        }
+        if (slow) {
+          // The references move ahead of the weights: in the first tile, where one has shown to lie too low, and where
+          // slots lie behind the prefix.
+          const int left = keys - half * 64;
+          float top = -INFINITY;  // the largest of this thread's scores
 #pragma unroll 1
           for (int c = 0; c < 2; ++c) {
             uint32_t x[32];
@@ -751,56 +797,45 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
 #pragma unroll
               for (int j = gr * 16; j < gr * 16 + 16; ++j) a = fmaxf(a, c * 32 + j < left ? __uint_as_float(x[j]) : -INFINITY);
               const float4 k = cst[c * 2 + gr];
-              top = fmaxf(top, fmaf(a, fmaxf(k.x * qf, FLT_MIN), k.y));
+              if (a > -INFINITY) top = fmaxf(top, __fmaf_rd(a, k.x * qf, k.y));
             }
           }
-          return top;
-        };
-        if (t == Tt) move_references(true, true, largest(), t);
-        uint32_t pk[2][16];
-        for (int pass = 0; pass < 2; ++pass) {
-          float part = 0.f, most = 0.f;  // sum of the weights over the V scales; largest sum of sixteen
-#pragma unroll
+          const bool asked = move_references(t == Tt || (keys < kKT8 ? top - m > 8.f : most > kTop), t == Tt, top, t);
+          // A row whose scores pass 2^23 asks for this wherever its largest comes up: m is y rounded down, so up to a step
+          // of m below the product that the weights above take exactly.  Here its y is rounded as that of m was.
+          const bool far = (asked || keys < kKT8) && fabsf(m) >= 0x1p23f, any_far = __any_sync(0xffffffffu, far);
+          part = 0.f;
+#pragma unroll 1
           for (int c = 0; c < 2; ++c) {
-            uint32_t x[32];
+            uint32_t x[32], pk[16];
             tmem_ld_x32(ts + half * 64 + c * 32, x);
             tmem_ld_wait();
-            if (left < c * 32 + 32) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (c * 32 + j >= left) x[j] = 0xFF800000u;
-            }
 #pragma unroll
             for (int gr = 0; gr < 2; ++gr) {
               const float4 k = cst[c * 2 + gr];
-              // (never 0, as a row of zeros or a block of zeros would have it: the -inf of a slot behind the prefix
-              // has to stay one, and what is below 2^-126 moves no score)
-              const float f = fmaxf(k.x * qf, FLT_MIN), off = k.y - m;
-              const float2 f2 = make_float2(f, f), off2 = make_float2(off, off);
-              float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+              // (never 0, as a row of zeros or a block of zeros would have it: the -inf of a slot behind the prefix has
+              // to stay one, and what is below 2^-126 moves no score)
+              float f = fmaxf(k.x * qf, FLT_MIN), off = k.y - m;
+              if (any_far) {
 #pragma unroll
-              for (int j = gr * 16; j < gr * 16 + 16; j += 2) {
-                float2 w = __ffma2_rn(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), f2, off2);
-                w = make_float2(ex2_approx(w.x), ex2_approx(w.y));
-                sum[(j >> 1) & 1] = __fadd2_rn(sum[(j >> 1) & 1], w);
-                const __half2 h2 = __floats2half2_rn(w.x, w.y);
-                pk[c][j / 2] = *reinterpret_cast<const uint32_t*>(&h2);
+                for (int j = gr * 16; j < gr * 16 + 16; ++j) {
+                  const float y = __uint_as_float(x[j]);
+                  x[j] = __float_as_uint(far ? __fadd_rn(__fmaf_rd(y, f, k.y), -m) : __fmaf_rn(y, f, off));
+                }
+                f = 1.f;
+                off = 0.f;
               }
-              const float2 s2 = __fadd2_rn(sum[0], sum[1]);
-              const float s16 = s2.x + s2.y;
-              most = fmaxf(most, s16);
-              part = fmaf(s16, k.z, part);
+              if (left < c * 32 + gr * 16 + 16) {
+#pragma unroll
+                for (int j = gr * 16; j < gr * 16 + 16; ++j)
+                  if (c * 32 + j >= left) x[j] = 0xFF800000u;
+              }
+              part = fmaf(weigh(x + gr * 16, f, off, pk + gr * 8), k.z, part);
             }
+            tmem_st_x16(ts + half * 64 + c * 16, pk);
           }
-          if (pass == 1 || !bar_or(pair, 64, most > kTop)) {
-            l += part;
-            break;
-          }
-          // a weight may have left f16's range: move the references and take the weights again
-          move_references(most > kTop, false, largest(), t);
         }
-        tmem_st_x16(ts + half * 64, pk[0]);  // over this thread's own scores
-        tmem_st_x16(ts + half * 64 + 16, pk[1]);
+        l += part;
       }
       tmem_st_wait();
       tc_fence_before();
