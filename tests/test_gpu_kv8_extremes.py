@@ -1,5 +1,7 @@
 """Tree attention over the 8-bit cache at the ends of what its inputs may hold: rows of zeros, rows next to bf16's
-smallest and largest numbers."""
+smallest and largest numbers, table entries out of range."""
+
+import time
 
 import numpy as np
 import pytest
@@ -114,3 +116,23 @@ def test_scores_a_few_steps_apart(N, G, slots, e):
     out, lse, status = K8.attend(K8.dev(), cache, qs)
     assert status == 0
     assert np.isfinite(lse).all() and (np.abs(out) <= 2).all()
+
+
+@pytest.mark.parametrize("N", [1, 40])
+def test_bad_table_entries_are_reported_as_such(N):
+    """Bad entries anywhere among many requests' blocks: each time the status says so, no call takes as long as a wait
+    that gives up would, and the other requests' rows are as they should be."""
+    rng = np.random.default_rng(N)
+    lens = [int(x) for x in rng.integers(200, 3000, 96)]
+    cache = K8.Cache(rng, lens, 2, 128, 16)
+    for b in range(0, len(lens), 2):
+        cache.table[b, rng.integers(0, -(-lens[b] // 16))] = [-1, cache.k.shape[0], 1 << 30, -(1 << 31)][b // 2 % 4]
+    qs = K8.Queries(rng, len(lens), N, 4, 2, 128)
+    for turn in range(10):
+        began = time.perf_counter()
+        out, lse, status = K8.attend(K8.dev(), cache, qs)
+        took = time.perf_counter() - began
+        assert status == 7
+        assert not out[::2].any() and not lse[::2].any()
+        assert turn == 0 or took < 0.9  # (a wait gives up after a second)
+    kv8_strict.check(cache, qs, out, lse, requests=[1, 33, 95])

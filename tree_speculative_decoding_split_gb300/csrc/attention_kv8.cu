@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kWarps * 32, RN == 1 ? 4 : 2)
   __shared__ uint32_t s_anc[kRowsR][kAncWords];
   __shared__ float s_m[kWarps][kRowsR], s_l[kWarps][kRowsR];
   __shared__ uint32_t s_odd[kAncWords];  // tree keys with an infinity or NaN in their V row
-  __shared__ int s_bad;
+  __shared__ int s_bad, s_abort;  // a table entry out of range; a wait that gave up
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
   Kv8Work sp = kv8_own(p);
@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kWarps * 32, RN == 1 ? 4 : 2)
     for (int s = 0; s < kStagesR; ++s) mbar_init(&s_full[warp][s], 1);
     fence_mbar_init();
   }
-  if (tid == 0) s_bad = 0;
+  if (tid == 0) s_bad = s_abort = 0;
   if (tid < kAncWords) s_odd[tid] = 0u;
   // ---- this warp's boxes: box c0 + warp + 4 i of 16 keys.  Their first table entries, scales and copies are on
   // their way while the tree is checked.
@@ -408,12 +408,14 @@ __global__ void __launch_bounds__(kWarps * 32, RN == 1 ? 4 : 2)
   // ---- the prefix ----
   turn();
   bool ok = true;
-  for (int i = 0; i < mine; ++i) {
+  int i = 0;
+  for (; i < mine; ++i) {
     const int s = i % kStagesR;
     if ((i & 31) == 0 && i > 0) turn();  // (the requests have moved on to this batch kStagesR boxes ago)
     const float ks = __shfl_sync(0xffffffffu, ks_c, i & 31);
     const float lv = __shfl_sync(0xffffffffu, lv_c, i & 31), inv_vs = __shfl_sync(0xffffffffu, iv_c, i & 31);
-    if (!mbar_wait_bounded(&s_full[warp][s], (i / kStagesR) & 1, &s_bad)) {
+    // (the lanes leave together: what follows is the whole warp's)
+    if (!__all_sync(0xffffffffu, mbar_wait_bounded(&s_full[warp][s], (i / kStagesR) & 1, &s_abort))) {
       ok = false;
       break;
     }
@@ -491,18 +493,16 @@ __global__ void __launch_bounds__(kWarps * 32, RN == 1 ? 4 : 2)
       for (int r = 0; r < RN; ++r) mma_f16(o[r][j], a0, a1, a2, a3, pb[r][0], pb[r][1]);
     }
   }
-  if (!ok) {
-    s_bad = 1;
-    if (lane == 0) {
-      set_status(p.dev_status, SPEC_ERR_TIMEOUT);
-      // let the copies in flight land (again with a limit) before shared memory goes
-      for (int s = 0; s < kStagesR && s < mine; ++s)
-        for (int ph = 0; ph < 2; ++ph) mbar_wait_bounded(&s_full[warp][s], ph, nullptr);
-    }
+  if (!ok && lane == 0) {
+    set_status(p.dev_status, SPEC_ERR_TIMEOUT);
+    s_abort = 1;
+    // the boxes that have been asked for and not been seen land first (again with a limit)
+    for (int j = i; j < min(mine, i + kStagesR); ++j)
+      mbar_wait_bounded(&s_full[warp][j % kStagesR], (j / kStagesR) & 1, nullptr);
   }
   if (__any_sync(0xffffffffu, bad) && lane == 0) {
-    s_bad = 1;
     set_status(p.dev_status, SPEC_ERR_CAPACITY);
+    s_bad = 1;
   }
   // ---- join the four warps' states ----
 #pragma unroll
@@ -517,7 +517,7 @@ __global__ void __launch_bounds__(kWarps * 32, RN == 1 ? 4 : 2)
       }
     }
   __syncthreads();  // every box has landed and been read: the ring's memory is free
-  if (s_bad) {
+  if (s_bad || s_abort) {
     refuse();
     return;
   }
