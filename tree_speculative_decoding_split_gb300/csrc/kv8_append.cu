@@ -164,6 +164,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
   uint8_t* ring = TMA ? reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127)) : nullptr;
   __shared__ uint64_t s_full[kStages];
   __shared__ uint32_t s_max[2][32];
+  __shared__ int s_gave_up;  // a wait for a box has passed its limit
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int u = blockIdx.x / parts, part = blockIdx.x - u * parts;
   pdl_wait();  // what comes before in the stream may still be ending: nothing of it is read ahead of this
@@ -257,7 +258,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
   float s_next;
   const int mine0 = i0 + (tid >> tg_shift);
   const int item_bytes = NV * 16 << tg_shift;
+  int asked = 0;  // rounds
   auto fetch = [&](int base, int stage) {  // one thread: the boxes of a round's items
+    ++asked;
     const int n = min(groups, i1 - base);
     mbar_arrive_expect_tx(&s_full[stage], (uint32_t)(n * item_bytes));
     for (int g = 0; g < n; ++g)
@@ -266,6 +269,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
   };
   if constexpr (TMA) {
     if (tid == 0) {
+      s_gave_up = 0;
       for (int i = 0; i < kStages; ++i) mbar_init(&s_full[i], 1);
       fence_mbar_init();
       for (int i = 0; i < kStages && i0 + i * groups < i1; ++i) fetch(i0 + i * groups, i);
@@ -281,12 +285,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     uint4 v[NV];
     const float s_old = s_next;
     if constexpr (TMA) {
-      if (!mbar_wait_bounded(&s_full[stage], phase, nullptr)) {
-        set_status(p.dev_status, SPEC_ERR_TIMEOUT);
-        if (tid == 0)  // the copies in flight land first
-          for (int i = 0; i < kStages; ++i) mbar_wait_bounded(&s_full[i], i >= stage ? phase : phase ^ 1, nullptr);
-        return;  // (every thread: all wait for the same)
-      }
+      // A thread that gives up stays with the others, whose warp's and block's steps follow: behind the barrier all know,
+      // and the rounds that are left ask for nothing, wait for nothing and write nothing.
+      if (!mbar_wait_bounded(&s_full[stage], phase, &s_gave_up)) s_gave_up = 1;
       const uint4* box = reinterpret_cast<const uint4*>(ring + stage * kStageBytes + (tid >> tg_shift) * item_bytes);
 #pragma unroll
       for (int j = 0; j < NV; ++j) v[j] = from[j] >= 0 ? box[start + t + j * tg] : make_uint4(0, 0, 0, 0);
@@ -315,7 +316,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
       if (lane == 0) s_max[turn][warp] = top;
       __syncthreads();
       if constexpr (TMA) {  // the round has been read: its place is free
-        if (tid == 0 && base + kStages * groups < i1) fetch(base + kStages * groups, stage);
+        if (tid == 0 && base + kStages * groups < i1 && !s_gave_up) fetch(base + kStages * groups, stage);
         if (++stage == kStages) {
           stage = 0;
           phase ^= 1;
@@ -326,7 +327,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
       const int w0 = (tid >> tg_shift) << (tg_shift - 5);
       top = __reduce_max_sync(0xffffffffu, lane < (tg >> 5) ? s_max[turn][w0 + lane] : 0u);
     }
-    if (item >= i1) continue;
+    if (item >= i1 || (TMA && s_gave_up)) continue;
     uint8_t* codes = ((item & 1) ? p.v_cache : p.k_cache) + (cell0 + (item >> 1)) * ((size_t)p.bs * p.d);
     const float s_new = pow2f(scale_exp(top));
     const bool grown = held && !(s_old >= s_new);
@@ -394,6 +395,12 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     }
     if (t == 0) *scale_of(item) = s;
   }
+  if constexpr (TMA)
+    if (tid == 0 && s_gave_up) {
+      set_status(p.dev_status, SPEC_ERR_TIMEOUT);
+      for (int i = 0; i < kStages; ++i)  // what is in flight lands first (again with a limit)
+        if (asked > i) mbar_wait_bounded(&s_full[(asked - 1 - i) % kStages], ((asked - 1 - i) / kStages) & 1, nullptr);
+    }
 }
 
 namespace {
