@@ -462,11 +462,11 @@ spec_status spec_eagle_tree(const spec_eagle_tree_args* args, int32_t* dev_statu
  * [0, max_blocks], too few free blocks, or a block id outside [0, num_blocks) on its way into the
  * slot map sets SPEC_ERR_CAPACITY; but for the last its table and count stay as they were.  A
  * free_count outside [0, num_blocks], more blocks given back than the list has room for, or more
- * than slot_cap rows (slot_map given; else more than 2^31 - 1) set SPEC_ERR_CAPACITY and leave
- * tables, counts and list as they were; slots are then -1 and row_start 0.  A block belongs to one
+ * than slot_cap rows (slot_map given, 0 entries included; else more than 2^31 - 1) set SPEC_ERR_CAPACITY
+ * and leave tables, counts and list as they were; slots are then -1 and row_start 0.  A block belongs to one
  * table at a time.
  * Host errors: SPEC_ERR_INVALID_ARGUMENT (sizes < 1, NULL pointers but slot_map / row_start, a
- * slot_map without row_start, slot_cap < 0), SPEC_ERR_UNSUPPORTED (block_size not 16, 32, 64, 128
+ * slot_map without row_start or, with entries, not 16-byte aligned, slot_cap < 0), SPEC_ERR_UNSUPPORTED (block_size not 16, 32, 64, 128
  * or 256, B > SPEC_MAX_RESERVE_BATCH, slot_cap >= 2^31, B * max_blocks >= 2^31). */
 #define SPEC_MAX_RESERVE_BATCH 8192
 

@@ -821,7 +821,7 @@ def kv_reserve_args(seq_len, n_new, block_table, n_blocks, free_list, free_count
         raise ValueError("seq_len, n_new and n_blocks must be [B], free_count [1]")
     if slot_map is None and slot_cap is not None:
         slot_map = torch.empty(int(slot_cap), dtype=torch.int64, device=dev)
-    slots = 0
+    slots, map_ptr = 0, None
     if slot_map is not None:
         map_ptr = _fast(slot_map, "slot_map", torch.int64, dev, ix)
         slots = slot_map.numel()
@@ -829,8 +829,10 @@ def kv_reserve_args(seq_len, n_new, block_table, n_blocks, free_list, free_count
         row_start = torch.empty(B + 1, dtype=i32, device=dev)
     elif row_start.numel() != B + 1:
         raise ValueError("row_start must be [B + 1]")
-    a = KvReserveArgs(B, int(block_size), max_blocks, free_list.numel(), slots, *ptr,
-                      map_ptr if slots else None, _fast(row_start, "row_start", i32, dev, ix))
+    start_ptr = _fast(row_start, "row_start", i32, dev, ix)
+    if slot_map is not None and slots == 0:  # an empty tensor has no address; any other says that there is a map
+        map_ptr = start_ptr
+    a = KvReserveArgs(B, int(block_size), max_blocks, free_list.numel(), slots, *ptr, map_ptr, start_ptr)
     return a, slot_map, row_start
 
 
@@ -838,8 +840,8 @@ def kv_reserve(seq_len, n_new, block_table, n_blocks, free_list, free_count, blo
                row_start=None, dev_status=None, stream=None):
     """Grow or shrink every request's block table to hold ``seq_len + n_new`` slots, from the stack of
     free blocks, in place (see spec_kv_reserve).  ``slot_cap`` (a bound on the sum of n_new the host
-    knows) or ``slot_map`` asks for the pool row of every new row.  Returns (slot_map, row_start);
-    slot_map is None when neither is given."""
+    knows) or ``slot_map`` asks for the pool row of every new row; more rows than it has entries (none
+    allow no row) refuse the call.  Returns (slot_map, row_start); slot_map is None when neither is given."""
     if stream is None:
         r = (_marshal or _native()).reserve(seq_len, n_new, block_table, n_blocks, free_list, free_count, block_size,
                                             slot_cap, slot_map, row_start, dev_status)

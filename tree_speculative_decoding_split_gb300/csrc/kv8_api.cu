@@ -23,7 +23,7 @@ spec_status check_reserve(const spec_kv_reserve_args* a) {
     return SPEC_ERR_UNSUPPORTED;
   if (!a->seq_len || !a->n_new || !a->block_table || !a->n_blocks || !a->free_list || !a->free_count)
     return SPEC_ERR_INVALID_ARGUMENT;
-  if (a->slot_map && (!a->row_start || !aligned16(a->slot_map))) return SPEC_ERR_INVALID_ARGUMENT;
+  if (a->slot_map && (!a->row_start || (a->slot_cap > 0 && !aligned16(a->slot_map)))) return SPEC_ERR_INVALID_ARGUMENT;
   return SPEC_OK;
 }
 

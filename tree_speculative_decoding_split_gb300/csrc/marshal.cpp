@@ -194,7 +194,9 @@ PyObject* reserve(PyObject*, PyObject* const* o, Py_ssize_t n) {
     a.n_blocks = ptr<int32_t>(held);
     a.free_list = ptr<int32_t>(list);
     a.free_count = ptr<int32_t>(count);
-    a.slot_map = a.slot_cap ? ptr<int64_t>(map) : nullptr;
+    if (map && a.slot_cap > 0) a.slot_map = ptr<int64_t>(map);
+    // an empty tensor has no address; any other says that there is a map, and nothing is written to it
+    if (map && a.slot_cap == 0) a.slot_map = reinterpret_cast<int64_t*>(ptr<int32_t>(start));
     a.row_start = ptr<int32_t>(start);
     const spec_status st = g_reserve(&a, status, c.stream());
     if (st != SPEC_OK) return PyLong_FromLong(st);
