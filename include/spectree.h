@@ -502,7 +502,7 @@ spec_status spec_kv_reserve(const spec_kv_reserve_args* args, int32_t* dev_statu
  *   codes of the slots below seq_len[b], when s > s_old: e4m3(code * (s_old / s)) -- exact where
  *           s_old is a power of two and the result is no subnormal code.
  * Other slots of the block keep what they hold.  new_len[b] = seq_len[b] + rows appended.
- * Data errors: seq_len[b] < 0 or rows past max_blocks * block_size, accept_len[b] outside
+ * Data errors: seq_len[b] < 0, rows past max_blocks * block_size or 2^31 - 1 slots, accept_len[b] outside
  * [0, path_cap) (SPEC_ERR_CAPACITY); path[b] that does not start at 0 or is not increasing below
  * n_max (SPEC_ERR_BAD_TREE); a table entry outside [0, num_blocks) among the blocks written
  * (SPEC_ERR_CAPACITY).  new_len[b] is then seq_len[b] and nothing of the request is written, but for

@@ -132,7 +132,8 @@ __device__ __forceinline__ Request check_request(const Kv8AppendParams& p, int b
     r.count = p.row_start[b + 1] - p.row_start[b];
   }
   if (__syncthreads_or(bad)) r.err = SPEC_ERR_BAD_TREE;
-  if (!r.err && (len < 0 || len + r.count > (long long)p.max_blocks * p.bs)) r.err = SPEC_ERR_CAPACITY;
+  // (lengths are 32-bit numbers, whatever the table has room for)
+  if (!r.err && (len < 0 || len + r.count > min((long long)p.max_blocks * p.bs, 0x7fffffffLL))) r.err = SPEC_ERR_CAPACITY;
   if (r.err) r.count = -1;
   return r;
 }
