@@ -498,7 +498,8 @@ spec_status spec_kv_reserve(const spec_kv_reserve_args* args, int32_t* dev_statu
  *           (e = -64 when all are 0; infinities and NaN are left out of the maximum);
  *   s     = max(s_old, s_new) if the block holds slots below seq_len[b], else s_new;
  *   codes of the new rows = e4m3(x / s), rounded to nearest, ties to even, infinities and what
- *           passes 448 to +-448, NaN to NaN;
+ *           passes 448 to +-448, NaN to NaN (the quotient in float32: rounded twice where a scale of
+ *           the caller's own that is no power of two stays);
  *   codes of the slots below seq_len[b], when s > s_old: e4m3(code * (s_old / s)) -- exact where
  *           s_old is a power of two and the result is no subnormal code.
  * Other slots of the block keep what they hold.  new_len[b] = seq_len[b] + rows appended.
