@@ -544,8 +544,8 @@ spec_status spec_kv8_append(const spec_kv8_append_args* args, int32_t* dev_statu
  * in the pools and node i's own K/V in row i of k_tree / v_tree.  n_max = 1 is decoding of single
  * tokens.  Products and sums are those of the codes' exact values: q enters in 16 bits or as a pair
  * of 8-bit numbers (exact down to 2^-9 of its row's largest element, below that within 2^-17 of it;
- * the largest counts as 2^-100 at least), the softmax weights as bf16 (of the tree's keys) or f16, sums
- * in float32.  Scores, and the product of a row's largest element, the softmax scale and a K scale,
+ * the largest counts as 2^-100 at least), the softmax weights as f16, those of the tree's keys as a pair
+ * of bf16 numbers, sums in float32.  Scores, and the product of a row's largest element, the softmax scale and a K scale,
  * have to lie within float32.  How a prefix is split depends on the lengths of the whole batch, so the
  * last bits of a row may as well.
  *   - K/V rows of nodes that a row does not see, of padded nodes and of slots behind the prefix have

@@ -136,3 +136,23 @@ def test_bad_table_entries_are_reported_as_such(N):
         assert not out[::2].any() and not lse[::2].any()
         assert turn == 0 or took < 0.9  # (a wait gives up after a second)
     kv8_strict.check(cache, qs, out, lse, requests=[1, 33, 95])
+
+
+@pytest.mark.parametrize("N,G,slots", [(3, 4, 64), (16, 1, 64), (8, 2, 64), (20, 1, 64), (63, 4, 64), (255, 3, 64), (40, 8, 10000)])
+@pytest.mark.parametrize("d", [128, 64])
+def test_weights_of_the_trees_keys(N, G, slots, d):
+    """With no prefix the tree's keys hold all the weight, and what is rounded to bf16 is the output alone: 2^-8 of it
+    (half a step), beside the weights' pair of bf16 numbers (2^-16 of each: 2^-16 A, A = sum p |v|), the exponentials
+    (2^-20 A) and float32 scores and sums over at most 255 keys (2^-14 A, as derived in kv8_helpers)."""
+    rng = np.random.default_rng(N + d)
+    cache = K8.Cache(rng, [0, 0, 0], 1, d, 16, max_len=slots)
+    qs = K8.Queries(rng, 3, N, G, 1, d, spread=0.5)
+    out, lse, status = K8.attend(K8.dev(), cache, qs)
+    assert status == 0
+    for b in range(3):
+        O = K8.exact(cache, qs, b)[0]
+        mask = oracle.tree_mask(qs.parent[b], N, 0)
+        x = np.where(mask[:, None], np.einsum("nhd,kd->nhk", qs.q[b], qs.kt[b, :, 0]) / np.sqrt(d), -np.inf)
+        w = np.exp(x - x.max(2, keepdims=True))
+        A = np.einsum("nhk,kd->nhd", w / w.sum(2, keepdims=True), np.abs(qs.vt[b, :, 0]))
+        assert kv8_strict.within(out[b], O, 2.0 ** -8 * np.abs(O) + (2.0 ** -16 + 2.0 ** -20 + 2.0 ** -14) * A).all()

@@ -370,37 +370,48 @@ __global__ void __launch_bounds__(kWarps * 32, RN == 1 ? 4 : 2)
           y[r][i] = see ? y[r][i] * p.scale_log2 : -INFINITY;
         }
       softmax_step<RN, NT>(y, st, o, 1.f, false);
-      // V rows 2t, 2t + 1, 2t + 8, 2t + 9 of the chunk, dimensions 2 NT g .. 2 NT g + 2 NT - 1; an element that
-      // is no finite number enters as 0 and is added at the end, to the rows that see it only
-      uint32_t v[4][NT];
+      // The weights as bf16, and what that rounding leaves: together to 2^-16 of them, as a short prefix leaves most to
+      // the tree.
+      uint32_t pb[RN][4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int key = j0 + 2 * t + (k & 1) + (k >> 1) * 8;
-        bool fin = true;
+      for (int r = 0; r < RN; ++r) {
+        const uint32_t h0 = pack_bf16x2(y[r][0], y[r][1]), h1 = pack_bf16x2(y[r][2], y[r][3]);
+        pb[r][0] = transpose8(h0);
+        pb[r][1] = transpose8(h1);
+        pb[r][2] = transpose8(pack_bf16x2(y[r][0] - bf16_lo(h0), y[r][1] - bf16_hi(h0)));
+        pb[r][3] = transpose8(pack_bf16x2(y[r][2] - bf16_lo(h1), y[r][3] - bf16_hi(h1)));
+      }
+      // V rows 2t, 2t + 1, 2t + 8, 2t + 9 of the chunk, dimensions 2 NT g .. 2 NT g + 2 NT - 1, eight at a time; an
+      // element that is no finite number enters as 0 and is added at the end, to the rows that see it only
 #pragma unroll
-        for (int i = 0; i < NT / 4; ++i) {
+      for (int i = 0; i < NT / 4; ++i) {
+        uint32_t v[4][4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int key = j0 + 2 * t + (k & 1) + (k >> 1) * 8;
           uint4 x = z;
           if (key < n)
             x = *reinterpret_cast<const uint4*>(p.v_tree + (((size_t)b * p.N + key) * p.Hkv + h) * D + 2 * NT * g + 8 * i);
-          v[k][4 * i] = x.x; v[k][4 * i + 1] = x.y; v[k][4 * i + 2] = x.z; v[k][4 * i + 3] = x.w;
-          fin = fin && bf16_pair_finite(x.x) && bf16_pair_finite(x.y) && bf16_pair_finite(x.z) && bf16_pair_finite(x.w);
-        }
-        if (!fin) {
-          atomicOr(&s_odd[key >> 5], 1u << (key & 31));
+          v[k][0] = x.x; v[k][1] = x.y; v[k][2] = x.z; v[k][3] = x.w;
+          if (!(bf16_pair_finite(x.x) && bf16_pair_finite(x.y) && bf16_pair_finite(x.z) && bf16_pair_finite(x.w))) {
+            atomicOr(&s_odd[key >> 5], 1u << (key & 31));
 #pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            if ((v[k][i] & 0x7F80u) == 0x7F80u) v[k][i] &= 0xFFFF0000u;
-            if ((v[k][i] & 0x7F800000u) == 0x7F800000u) v[k][i] &= 0xFFFFu;
+            for (int e = 0; e < 4; ++e) {
+              if ((v[k][e] & 0x7F80u) == 0x7F80u) v[k][e] &= 0xFFFF0000u;
+              if ((v[k][e] & 0x7F800000u) == 0x7F800000u) v[k][e] &= 0xFFFFu;
+            }
           }
         }
-      }
 #pragma unroll
-      for (int r = 0; r < RN; ++r) {
-        const uint32_t b0 = transpose8(pack_bf16x2(y[r][0], y[r][1])), b1 = transpose8(pack_bf16x2(y[r][2], y[r][3]));
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t a0 = __byte_perm(v[0][j], v[1][j], 0x5410), a1 = __byte_perm(v[0][j], v[1][j], 0x7632);
+          const uint32_t a2 = __byte_perm(v[2][j], v[3][j], 0x5410), a3 = __byte_perm(v[2][j], v[3][j], 0x7632);
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
-          mma_bf16(o[r][j], __byte_perm(v[0][j], v[1][j], 0x5410), __byte_perm(v[0][j], v[1][j], 0x7632),
-                   __byte_perm(v[2][j], v[3][j], 0x5410), __byte_perm(v[2][j], v[3][j], 0x7632), b0, b1);
+          for (int r = 0; r < RN; ++r) {
+            mma_bf16(o[r][4 * i + j], a0, a1, a2, a3, pb[r][0], pb[r][1]);
+            mma_bf16(o[r][4 * i + j], a0, a1, a2, a3, pb[r][2], pb[r][3]);
+          }
+        }
       }
     }
   }

@@ -505,7 +505,10 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
           const uint32_t va = v16 + (t % kVS) * (C::kSlot >> 4);
 #pragma unroll
           for (int kk = 0; kk < kTT / 16; ++kk)
-            umma_bf16_tmem_a(ot, pt + (kk >> 1) * 64 + (kk & 1) * 8, hiVt | (va + kk * 128), idPt, t > 0 || kk > 0);
+#pragma unroll
+            for (int part = 0; part < 2; ++part)  // the weights' two parts
+              umma_bf16_tmem_a(ot, pt + (kk >> 1) * 64 + part * 16 + (kk & 1) * 8, hiVt | (va + kk * 128), idPt,
+                               t > 0 || kk > 0 || part > 0);
         } else {
           const uint32_t va = v16 + (kVS * C::kSlot >> 4) + (t % kV16) * (C::kTile16 >> 4);
 #pragma unroll
@@ -736,9 +739,17 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
           const float a = ex2_approx(__uint_as_float(x[j]) - mu), c = ex2_approx(__uint_as_float(x[j + 1]) - mu);
           sum += a + c;
           pk[j / 2] = pack_bf16x2(a, c);
+          x[j] = __float_as_uint(a);
+          x[j + 1] = __float_as_uint(c);
         }
         l += sum;
         tmem_st_x16(ts + half * 64, pk);
+        // ... and what that rounding left: together the weights to 2^-16 of them, as a short prefix leaves most to the tree
+#pragma unroll
+        for (int j = 0; j < 32; j += 2)
+          pk[j / 2] = pack_bf16x2(__uint_as_float(x[j]) - __uint_as_float(pk[j / 2] << 16),
+                                  __uint_as_float(x[j + 1]) - __uint_as_float(pk[j / 2] & 0xFFFF0000u));
+        tmem_st_x16(ts + half * 64 + 16, pk);
       } else {
         // -- a prefix tile: this thread's 64 keys are 4 groups of 16, each within one block --
         const float4* cst = s_cst + (t % kCS) * 8 + half * 4;
