@@ -10,7 +10,8 @@
 //   per tile for all rows), and P = 2^(y - m) is f16 (y: the score in log2 units with the V scale folded in, as
 //   in the few-rows kernel).
 // Accumulation is float32 (measured: 1e-7 relative for e4m3 products, as for bf16).  The tree's own keys (at
-// most 255, bf16) come first, as bf16 tiles with bf16 Q and P.
+// most 255, bf16) come first, as bf16 tiles with bf16 Q and P as a pair of bf16 numbers (to 2^-16; single ones made
+// the output of a row that the tree outweighs 0.0022 wrong instead of 0.0017, and are four tiles' work at most).
 //
 // One CTA owns (request, KV head, key split, NG x 128 rows).  Bound: per 128-key tile and 128 rows the
 // tensor pipe takes 512 (S) + 512 (P V) cycles; the two groups fill each other's softmax.  TMEM: O 128
@@ -21,11 +22,13 @@
 //   warp 1     MMA issuer;
 //   warps 2, 3 V tiles to f16;
 //   warps 4..  softmax, eight warps per group: two threads own a row (a TMEM lane), 64 keys of a tile each.
-//              Both use the row's reference; whether one has to move is one barrier's OR per tile.
-// Measured (graph replay): 4 trees of 255 nodes, 32 query heads on 8, lengths up to 128K, 1878 us = 1458 TFLOP/s,
-// 0.77 of a large bf16 product's rate; a tile of both groups takes 3.2 K cycles for 2 K of tensor work.  32 trees of
-// 63 nodes at 4K 142 us = 954 TFLOP/s: 256 CTAs on 152 SMs are 1.7 rounds, and about 30 K of a CTA's 140 K cycles go
-// to its first two tiles and its last rows, which nothing overlaps.  8 trees of 127 nodes, d 64, 58 us.
+//              Both use the row's reference; whether one has to move is one barrier's OR per tile.  Moving it
+//              and masking the tile that ends the prefix have loops of their own, which leaves the tiles' own short
+//              (4 trees of 255 nodes 1880 -> 1840 us).
+// Measured (graph replay): 4 trees of 255 nodes, 64 query heads on 8, lengths up to 128K, 1843 us = 1486 TFLOP/s,
+// 0.78 of a large bf16 product's rate; a tile of both groups takes 3.1 K cycles for 2 K of tensor work.  32 trees of
+// 63 nodes at 4K 141 us = 957 TFLOP/s: 256 CTAs on 152 SMs are 1.7 rounds, and about 30 K of a CTA's 140 K cycles go
+// to its first two tiles and its last rows, which nothing overlaps.  8 trees of 127 nodes, d 64, 62 us.
 // Tried and slower (63-node trees, batch 32 at 4K, when this stood at 160 us): P as e4m3 pairs with 128 keys a
 // thread, four warps per group and a row maximum ahead of the weights, 238 us; with one S buffer shared by both groups
 // and all descriptors in uniform registers, 203 us; with two threads per row, 211 us.  Four trees of 255 nodes, at
@@ -770,7 +773,24 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
         };
         const int keys = (int)min((long long)kKT8, k1 - (k0 + (long long)(t - Tt) * kKT8));
         float part = 0.f, most = 0.f;  // sum of the weights over the V scales; largest sum of sixteen
-        bool slow = t == Tt || keys < kKT8;
+        if (keys < kKT8) {  // slots behind the prefix may hold anything: their scores become -inf where they lie
+          const int left = keys - half * 64;
+#pragma unroll 1
+          for (int c = left < 32 ? 0 : 1; c < 2; ++c) {
+            uint32_t x[32];
+            tmem_ld_x32(ts + half * 64 + c * 32, x);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (c * 32 + j >= left) x[j] = 0xFF800000u;
+            tmem_st_x32(ts + half * 64 + c * 32, x);
+          }
+          tmem_st_wait();
+        }
+        // The factor of a score is never 0, as a row of zeros or a block of zeros would have it: -inf has to stay one (and
+        // what is below 2^-126 moves no score).
+        auto factor = [&](const float4& k) { return fmaxf(k.x * qf, FLT_MIN); };
+        bool slow = t == Tt;
         if (!slow) {
           uint32_t pk[2][16];
 #pragma unroll
@@ -781,7 +801,7 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
 #pragma unroll
             for (int gr = 0; gr < 2; ++gr) {
               const float4 k = cst[c * 2 + gr];
-              const float s16 = weigh(x + gr * 16, k.x * qf, k.y - m, pk[c] + gr * 8);
+              const float s16 = weigh(x + gr * 16, factor(k), k.y - m, pk[c] + gr * 8);
               most = fmaxf(most, s16);
               part = fmaf(s16, k.z, part);
             }
@@ -793,9 +813,7 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
           }
         }
         if (slow) {
-          // The references move ahead of the weights: in the first tile, where one has shown to lie too low, and where
-          // slots lie behind the prefix.
-          const int left = keys - half * 64;
+          // the references move ahead of the weights: in the first tile, and where one has shown to lie too low
           float top = -INFINITY;  // the largest of this thread's scores
 #pragma unroll 1
           for (int c = 0; c < 2; ++c) {
@@ -806,15 +824,15 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
             for (int gr = 0; gr < 2; ++gr) {
               float a = -INFINITY;
 #pragma unroll
-              for (int j = gr * 16; j < gr * 16 + 16; ++j) a = fmaxf(a, c * 32 + j < left ? __uint_as_float(x[j]) : -INFINITY);
+              for (int j = gr * 16; j < gr * 16 + 16; ++j) a = fmaxf(a, __uint_as_float(x[j]));
               const float4 k = cst[c * 2 + gr];
-              if (a > -INFINITY) top = fmaxf(top, __fmaf_rd(a, k.x * qf, k.y));
+              top = fmaxf(top, __fmaf_rd(a, factor(k), k.y));
             }
           }
-          const bool asked = move_references(t == Tt || (keys < kKT8 ? top - m > 8.f : most > kTop), t == Tt, top, t);
+          const bool asked = move_references(t == Tt || most > kTop, t == Tt, top, t);
           // A row whose scores pass 2^23 asks for this wherever its largest comes up: m is y rounded down, so up to a step
           // of m below the product that the weights above take exactly.  Here its y is rounded as that of m was.
-          const bool far = (asked || keys < kKT8) && fabsf(m) >= 0x1p23f, any_far = __any_sync(0xffffffffu, far);
+          const bool far = asked && fabsf(m) >= 0x1p23f, any_far = __any_sync(0xffffffffu, far);
           part = 0.f;
 #pragma unroll 1
           for (int c = 0; c < 2; ++c) {
@@ -824,9 +842,7 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
 #pragma unroll
             for (int gr = 0; gr < 2; ++gr) {
               const float4 k = cst[c * 2 + gr];
-              // (never 0, as a row of zeros or a block of zeros would have it: the -inf of a slot behind the prefix has
-              // to stay one, and what is below 2^-126 moves no score)
-              float f = fmaxf(k.x * qf, FLT_MIN), off = k.y - m;
+              float f = factor(k), off = k.y - m;
               if (any_far) {
 #pragma unroll
                 for (int j = gr * 16; j < gr * 16 + 16; ++j) {
@@ -835,11 +851,6 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
                 }
                 f = 1.f;
                 off = 0.f;
-              }
-              if (left < c * 32 + gr * 16 + 16) {
-#pragma unroll
-                for (int j = gr * 16; j < gr * 16 + 16; ++j)
-                  if (c * 32 + j >= left) x[j] = 0xFF800000u;
               }
               part = fmaf(weigh(x + gr * 16, f, off, pk + gr * 8), k.z, part);
             }
