@@ -13,9 +13,10 @@
 // cores need to be busy: the kernel is bound by HBM.  What matters is bytes in flight, so every warp
 // runs its own ring of TMA boxes of 16 keys and its own softmax state over every fourth box of the
 // split, without any barrier between warps; the four states are joined at the end.
+// The tree's weights enter their product as a pair of bf16 numbers (to 2^-16 of them), the prefix's as f16.
 // Measured: 32 requests of 4 rows over 2K to 6K keys (8 KV heads, d 128) 57 us = 4.7 TB/s of codes, 0.69 of a plain
 // copy's rate; one request at 2K 18.9 us with a cold cache, 14.6 warm, most of it latency (two launches, and three
-// loads that hang on one another ahead of the first keys).  With two 8-row tiles the registers (234) leave two CTAs
+// loads that hang on one another ahead of the first keys).  With two 8-row tiles the registers (246) leave two CTAs
 // an SM; three with a few spilled take as long, four twice as long.
 #include "common.cuh"
 #include "kernels.cuh"
@@ -667,13 +668,14 @@ Kv8AttnPlan plan_attention_kv8(int B, int N, int G, int Hkv, long long L_cap, in
   Kv8AttnPlan pl;
   const int rows = N * G;
   const long long heads = (long long)B * Hkv;
-  // Sixteen rows or fewer: 32 requests of 16 rows at 4K take 88 us here (d 64: 56) and 130 (110) on the tensor-core
+  // Sixteen rows or fewer: 32 requests of 16 rows at 4K take 87 us here (d 64: 58) and 130 (110) on the tensor-core
   // kernel; one at 2K 23.7 and 21.7.
   if (rows <= 16) {
     pl.groups = 0;
     pl.unit_shift = 6;
     pl.n_rt = 1;
-    pl.slots = num_sms * 4;  // four CTAs an SM
+    // four CTAs an SM, as 8 rows have them (with 16 two or three fit: the plan is then for more than run at once)
+    pl.slots = num_sms * 4;
     pl.fixed_steps = 2;
   } else {
     // Two groups of 128 rows per CTA cost little more a key tile than one (each fills the other's waits), so one

@@ -24,10 +24,10 @@
 //   warps 4..  softmax, eight warps per group: two threads own a row (a TMEM lane), 64 keys of a tile each.
 //              Both use the row's reference; whether one has to move is one barrier's OR per tile.  Moving it
 //              and masking the tile that ends the prefix have loops of their own, which leaves the tiles' own short
-//              (4 trees of 255 nodes 1880 -> 1840 us).
-// Measured (graph replay): 4 trees of 255 nodes, 64 query heads on 8, lengths up to 128K, 1843 us = 1486 TFLOP/s,
-// 0.78 of a large bf16 product's rate; a tile of both groups takes 3.1 K cycles for 2 K of tensor work.  32 trees of
-// 63 nodes at 4K 141 us = 957 TFLOP/s: 256 CTAs on 152 SMs are 1.7 rounds, and about 30 K of a CTA's 140 K cycles go
+//              (4 trees of 255 nodes 1880 -> 1861 us).
+// Measured (graph replay): 4 trees of 255 nodes, 64 query heads on 8, lengths up to 128K, 1861 us = 1471 TFLOP/s,
+// 0.77 of a large bf16 product's rate; a tile of both groups takes 3.2 K cycles for 2 K of tensor work.  32 trees of
+// 63 nodes at 4K 142 us = 954 TFLOP/s: 256 CTAs on 152 SMs are 1.7 rounds, and about 30 K of a CTA's 140 K cycles go
 // to its first two tiles and its last rows, which nothing overlaps.  8 trees of 127 nodes, d 64, 62 us.
 // Tried and slower (63-node trees, batch 32 at 4K, when this stood at 160 us): P as e4m3 pairs with 128 keys a
 // thread, four warps per group and a row maximum ahead of the weights, 238 us; with one S buffer shared by both groups

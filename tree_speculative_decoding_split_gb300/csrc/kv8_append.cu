@@ -6,7 +6,7 @@
 // maximum, and converts what it holds.  So the rows are read once and the codes written once: HBM-bound.
 // A CTA goes through the heads of its block one after another (one head per CTA took 103 us for 35K rows of 8 heads:
 // most of it finding the request, block and scale); long runs of rows come by TMA, three rounds ahead.
-// Measured: 8 prompts of 35K rows together (bf16, 8 heads, d 128) 41.5 us = 5.2 TB/s, 0.76 of a plain copy's rate;
+// Measured: 8 prompts of 35K rows together (bf16, 8 heads, d 128) 43 us = 5.0 TB/s, 0.73 of a plain copy's rate;
 // 328K fp32 rows (d 64) 262 us = 6.4 TB/s, 0.94 (one round ahead into registers: 51.7 and 303 us).  The accepted
 // paths of 32 requests 10.7 us with a cold cache, 6.5 warm: one launch and four loads in a row.
 // A half-full block keeps its larger scale; its old codes are read only when the scale grows.

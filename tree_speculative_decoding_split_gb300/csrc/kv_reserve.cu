@@ -10,7 +10,7 @@
 // Bound: latency.  The tables' changes are a few KB; what takes time is the chain of counts, scan, list, tables and
 // slots.  So small calls are one CTA that writes the slot map as well, and the sums of all three kinds are scanned
 // together (apart, the two calls below took 12.8, 16.9 and 31.2 us).  Measured with a cold cache, a call with its slot map
-// and one without: 10.8 us for one request, 14.8 for 32, 27.1 for 512 prompts with 1 M slots.
+// and one without: 10.7 us for one request, 14.8 for 32, 26.4 for 512 prompts with 1 M slots.
 #include "common.cuh"
 #include "kernels.cuh"
 #include "pdl.cuh"
