@@ -1,12 +1,12 @@
 """Tree attention over the 8-bit cache at the ends of what its inputs may hold: rows of zeros, rows next to bf16's
 smallest and largest numbers, table entries out of range."""
 
-import time
-
 import numpy as np
 import pytest
+import torch
 
 import oracle
+import tree_speculative_decoding_split_gb300 as st
 import kv8_helpers as K8
 import kv8_strict
 
@@ -128,13 +128,21 @@ def test_bad_table_entries_are_reported_as_such(N):
     for b in range(0, len(lens), 2):
         cache.table[b, rng.integers(0, -(-lens[b] // 16))] = [-1, cache.k.shape[0], 1 << 30, -(1 << 31)][b // 2 % 4]
     qs = K8.Queries(rng, len(lens), N, 4, 2, 128)
+    dev, c = K8.dev(), cache.device(K8.dev())
+    args = [qs.q_t.to(dev), qs.kt_t.to(dev), qs.vt_t.to(dev), c["k_cache"], c["v_cache"], c["k_scale"], c["v_scale"],
+            torch.tensor(lens, dtype=torch.int32, device=dev), torch.from_numpy(qs.n_nodes).to(dev),
+            torch.from_numpy(qs.parent).to(dev), c["block_table"]]
+    began, ended = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
     for turn in range(10):
-        began = time.perf_counter()
-        out, lse, status = K8.attend(K8.dev(), cache, qs)
-        took = time.perf_counter() - began
-        assert status == 7
+        status = torch.zeros(1, dtype=torch.int32, device=dev)
+        began.record()
+        out, lse = st.tree_attention_kv8(*args, dev_status=status)
+        ended.record()
+        torch.cuda.synchronize()
+        out, lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+        assert int(status.item()) == 7
         assert not out[::2].any() and not lse[::2].any()
-        assert turn == 0 or took < 0.9  # (a wait gives up after a second)
+        assert turn == 0 or began.elapsed_time(ended) < 500  # ms (a wait gives up after a second)
     kv8_strict.check(cache, qs, out, lse, requests=[1, 33, 95])
 
 
