@@ -589,6 +589,215 @@ spec_status spec_tree_attention_kv8(const spec_attn_kv8_args* args, void* worksp
                                     int32_t* dev_status, void* stream);
 
 /* ---------------------------------------------------------------------------------------
+ * From prompts to the cache.  (The pages take the prompt's keys and values as given -- qiita guide,
+ * section "並列検証": the candidates are scored behind a cached prefix; how the prefix is made, and
+ * how rows get their positions, is this library's own.)
+ *
+ * Packed prompt rows: request b's rows are row_start[b] .. row_start[b + 1] - 1 of arrays with
+ * n_rows rows (row_start as spec_kv_reserve writes it; requests without rows are fine, and so are
+ * rows in front of the first and behind the last request, which no call reads or writes).  A
+ * row_start that decreases or leaves [0, n_rows] anywhere sets SPEC_ERR_CAPACITY and the call
+ * writes no rows.  Rows of heads [n_rows][H][d] may be views of wider rows (one projection's q, k
+ * and v): the heads of a row lie together, and *_stride elements lie between rows.  Strides are
+ * multiples of 16 bytes and at least H * d.
+ *
+ *   spec_rope_positions      positions of prompt rows and of tree nodes, once per step
+ *   spec_rope                rotary positions of q and k, per layer
+ *   spec_prompt_attention    causal attention over the prompts
+ *   spec_prompt_key_weights  what the last queries of each prompt attend to
+ *   spec_kv_keep             the rows that a budget leaves, packed for spec_kv8_append
+ * ------------------------------------------------------------------------------------- */
+
+/* Host-side helper (no GPU): rotary frequencies f_i, i < rot_dim / 2, as turns[i] = f_i / (2 pi) in
+ * units of 2^-64 turns per position (rounded down), from theta_i = base^(-2 i / rot_dim):
+ *   NONE    f = theta
+ *   LINEAR  f = theta / factor
+ *   BASE    f with base * factor^(rot_dim / (rot_dim - 2)) in the place of base (rot_dim > 2)
+ *   BANDS   by the turns r = original_len * theta / (2 pi) that a frequency makes over the trained
+ *           length: theta for r >= high, theta / factor for r <= low, in between the two weighted by
+ *           (r - low) / (high - low)
+ *   RAMP    theta and theta / factor weighted linearly in i: theta up to the (real) index i_high at which r = high,
+ *           theta / factor from the index i_low at which r = low on, both held to [0, rot_dim / 2 - 1]
+ *           after rounding i_high down and i_low up (i_low at least 0.001 behind i_high)
+ * SPEC_ERR_INVALID_ARGUMENT: turns NULL, rot_dim < 2 or odd, base <= 1, factor <= 0, and for BANDS and
+ * RAMP original_len < 1 or not 0 < low < high; numbers that are not finite.  SPEC_ERR_UNSUPPORTED:
+ * an unknown kind, a frequency of half a turn or more. */
+#define SPEC_ROPE_NONE 0
+#define SPEC_ROPE_LINEAR 1
+#define SPEC_ROPE_BASE 2
+#define SPEC_ROPE_BANDS 3
+#define SPEC_ROPE_RAMP 4
+
+spec_status spec_rope_table(int32_t rot_dim, double base, int32_t kind, double factor, int64_t original_len, double low,
+                            double high, int64_t* turns);
+
+/* Positions of rows.  Packed rows (row_start != NULL): positions[row_start[b] + j] = pos0[b] + j.
+ * Trees (parent != NULL): positions[b][i] = pos0[b] + depth of node i, -1 for padded nodes.
+ * Data errors: pos0[b] < 0 or a position past 2^31 - 1 (SPEC_ERR_CAPACITY), a bad tree
+ * (SPEC_ERR_BAD_TREE): the request's positions are then -1.
+ * Host errors: SPEC_ERR_INVALID_ARGUMENT (sizes < 1, NULL pointers, both forms or none),
+ * SPEC_ERR_UNSUPPORTED (n_max > SPEC_MAX_NODES, n_rows >= 2^31, B > SPEC_MAX_RESERVE_BATCH for rows). */
+typedef struct spec_rope_positions_args {
+  int32_t batch;            /* B */
+  int32_t n_max;            /* trees: N; else 0 */
+  int64_t n_rows;           /* packed rows: entries of positions; else 0 */
+  const int32_t* pos0;      /* [B] position of a request's first row or root */
+  const int32_t* row_start; /* [B + 1] or NULL */
+  const int32_t* parent;    /* [B][N] or NULL */
+  const int32_t* n_nodes;   /* [B], with parent */
+  int32_t* positions;       /* out [n_rows] or [B][N] */
+} spec_rope_positions_args;
+
+spec_status spec_rope_positions(const spec_rope_positions_args* args, int32_t* dev_status, void* stream);
+
+/* Rotary positions.  For every row r with positions[r] >= 0, every head of q and k and every pair
+ * (x, y) of its first rot_dim channels, with a = 2 pi * (positions[r] * turns[i] mod 2^64) / 2^64:
+ *   x' = amplitude (x cos a - y sin a),  y' = amplitude (x sin a + y cos a)
+ * HALF pairs channel i with i + rot_dim / 2, INTERLEAVED 2 i with 2 i + 1.  Channels from rot_dim on
+ * are passed on as they are.  The angle's fraction of a turn is exact in 32 bits at any position; cos,
+ * sin and the products are float32, rounded once to the rows' type.  Rows with a negative
+ * position are not written.  q_out == q (k_out == k) with equal strides works in place; outputs
+ * that overlap an input in another way are not supported.
+ * Host errors: SPEC_ERR_INVALID_ARGUMENT (sizes < 1, NULL pointers, strides or addresses that are no
+ * multiple of 16 bytes or too short, an amplitude that is not finite), SPEC_ERR_UNSUPPORTED (dtype,
+ * layout, head_dim or rot_dim no multiple of 16, head_dim > 256, rot_dim > head_dim, n_rows >= 2^31,
+ * more than 65535 heads). */
+#define SPEC_ROPE_HALF 0
+#define SPEC_ROPE_INTERLEAVED 1
+
+typedef struct spec_rope_args {
+  int32_t dtype;            /* of q, k and the outputs: SPEC_DTYPE_BF16 or SPEC_DTYPE_F32 */
+  int32_t layout;           /* SPEC_ROPE_HALF or SPEC_ROPE_INTERLEAVED */
+  int32_t num_q_heads;      /* Hq */
+  int32_t num_k_heads;      /* Hkv */
+  int32_t head_dim;
+  int32_t rot_dim;
+  int64_t n_rows;
+  int64_t q_stride;         /* elements between rows */
+  int64_t k_stride;
+  int64_t q_out_stride;
+  int64_t k_out_stride;
+  float amplitude;          /* 1 unless a scaling asks for another */
+  int32_t reserved0;        /* must be 0 */
+  const void* q;
+  const void* k;
+  const int32_t* positions; /* [n_rows] */
+  const int64_t* turns;     /* [rot_dim / 2] as spec_rope_table makes them */
+  void* q_out;
+  void* k_out;
+} spec_rope_args;
+
+spec_status spec_rope(const spec_rope_args* args, void* stream);
+
+/* Causal attention over packed prompts.  For row i of a request, query head h, g = h / (Hq / Hkv):
+ *   out[i][h] = sum_{j <= i} softmax_j(scale * q[i][h] . k[j][g]) v[j][g]
+ *   lse[i][h] = ln sum_{j <= i} exp(scale * q[i][h] . k[j][g])        (j over the same request's rows)
+ * Products of bf16 numbers, sums in float32; the softmax weights enter the second product as bf16 (off
+ * by 2^-8 of themselves at most, as the output's own rounding), their sum as float32.  Keys that a row does not see
+ * have no influence on it, NaN and infinities included.
+ * Host errors: SPEC_ERR_INVALID_ARGUMENT, SPEC_ERR_UNSUPPORTED (dtype other than bf16, head_dim other
+ * than 64 or 128, Hq / Hkv > 128, n_rows >= 2^31 - 256, B > SPEC_MAX_RESERVE_BATCH, strides of 2^38 elements or more),
+ * SPEC_ERR_WORKSPACE_TOO_SMALL. */
+typedef struct spec_prompt_attn_args {
+  int32_t dtype;            /* SPEC_DTYPE_BF16 */
+  int32_t batch;            /* B */
+  int32_t num_q_heads;      /* Hq, a multiple of num_kv_heads */
+  int32_t num_kv_heads;     /* Hkv */
+  int32_t head_dim;         /* 64 or 128 */
+  float scale;              /* softmax scale; <= 0 selects 1/sqrt(head_dim) */
+  int64_t n_rows;
+  int64_t q_stride;         /* elements between rows */
+  int64_t k_stride;
+  int64_t v_stride;
+  const void* q;            /* [n_rows][Hq][d] */
+  const void* k;            /* [n_rows][Hkv][d] */
+  const void* v;            /* [n_rows][Hkv][d] */
+  const int32_t* row_start; /* [B + 1] */
+  void* out;                /* [n_rows][Hq][d], contiguous */
+  float* lse;               /* [n_rows][Hq] or NULL */
+} spec_prompt_attn_args;
+
+/* Bytes of workspace (16-byte aligned device memory) for these shapes; 0 on invalid arguments. */
+size_t spec_prompt_attention_workspace(const spec_prompt_attn_args* args);
+
+spec_status spec_prompt_attention(const spec_prompt_attn_args* args, void* workspace, size_t workspace_bytes,
+                                  int32_t* dev_status, void* stream);
+
+/* The attention weight that each key gets from the last `window` rows of its own request (all of them
+ * where there are fewer), summed over these rows and over the query heads that share the key's head:
+ *   weight[g][j] = sum_{i >= j, i in window} sum_{h in group g} exp(scale * q[i][h] . k[j][g] - lse[i][h])
+ * in float32, the terms added in an order of their own that does not change from call to call; rows
+ * outside of the requests keep what they hold.  lse is spec_prompt_attention's; only the window's rows
+ * of q and lse are read.
+ * Host errors and workspace as for spec_prompt_attention, and window < 1. */
+typedef struct spec_key_weights_args {
+  int32_t dtype;            /* SPEC_DTYPE_BF16 */
+  int32_t batch;            /* B */
+  int32_t num_q_heads;      /* Hq, a multiple of num_kv_heads */
+  int32_t num_kv_heads;     /* Hkv */
+  int32_t head_dim;         /* 64 or 128 */
+  float scale;              /* softmax scale; <= 0 selects 1/sqrt(head_dim) */
+  int32_t window;           /* >= 1 */
+  int32_t reserved0;        /* must be 0 */
+  int64_t n_rows;
+  int64_t q_stride;         /* elements between rows */
+  int64_t k_stride;
+  const void* q;            /* [n_rows][Hq][d] */
+  const void* k;            /* [n_rows][Hkv][d] */
+  const float* lse;         /* [n_rows][Hq] */
+  const int32_t* row_start; /* [B + 1] */
+  float* weight;            /* out [Hkv][n_rows] */
+} spec_key_weights_args;
+
+size_t spec_prompt_key_weights_workspace(const spec_key_weights_args* args);
+
+spec_status spec_prompt_key_weights(const spec_key_weights_args* args, void* workspace, size_t workspace_bytes,
+                                    int32_t* dev_status, void* stream);
+
+/* The rows of each prompt that a budget leaves, per KV head.  Request b with n rows keeps n_keep[b] =
+ * min(n, budget) of them for every KV head: all of them if n <= budget, else its first `first` and last
+ * `last` rows and, of the others, those with the largest weight[g][.] (equal weights by the lower row, -0 =
+ * +0; NaN ranks below -inf).  They are written in the prompt's order:
+ *   keep_start[b] = sum of n_keep before b;  for s < n_keep[b], at row keep_start[b] + s and head g:
+ *   index = the row's number within its request, k_out / v_out = its K and V.
+ * Rows of the outputs behind keep_start[B] keep what they hold.  n_keep and keep_start are the n_new and
+ * row_start with which spec_kv_reserve and spec_kv8_append admit the rows; rows behind the budget never
+ * reach the cache.  (K rows carry their positions, so what follows goes on from the prompt's full length.)
+ * Data errors: a bad row_start, or more than rows_out rows kept (SPEC_ERR_CAPACITY): n_keep and
+ * keep_start are then 0 and no row is written.
+ * Host errors: SPEC_ERR_INVALID_ARGUMENT (sizes < 1, first or last < 0, first + last > budget, NULL
+ * pointers, strides or addresses that are no multiple of 16 bytes or too short), SPEC_ERR_UNSUPPORTED (dtype,
+ * head_dim, n_rows or rows_out >= 2^31, B > SPEC_MAX_RESERVE_BATCH, B * Hkv >= 2^27), SPEC_ERR_WORKSPACE_TOO_SMALL. */
+typedef struct spec_kv_keep_args {
+  int32_t dtype;            /* of k, v: SPEC_DTYPE_BF16 or SPEC_DTYPE_F32 */
+  int32_t batch;            /* B */
+  int32_t num_kv_heads;     /* Hkv */
+  int32_t head_dim;         /* 64 or 128 */
+  int32_t budget;           /* >= 1 */
+  int32_t first;
+  int32_t last;
+  int32_t reserved0;        /* must be 0 */
+  int64_t n_rows;
+  int64_t rows_out;         /* rows of the outputs */
+  int64_t k_stride;         /* elements between rows */
+  int64_t v_stride;
+  const void* k;            /* [n_rows][Hkv][d] */
+  const void* v;            /* [n_rows][Hkv][d] */
+  const float* weight;      /* [Hkv][n_rows] */
+  const int32_t* row_start; /* [B + 1] */
+  void* k_out;              /* out [rows_out][Hkv][d], contiguous */
+  void* v_out;
+  int32_t* index;           /* out [rows_out][Hkv] */
+  int32_t* keep_start;      /* out [B + 1] */
+  int32_t* n_keep;          /* out [B] */
+} spec_kv_keep_args;
+
+size_t spec_kv_keep_workspace(const spec_kv_keep_args* args);
+
+spec_status spec_kv_keep(const spec_kv_keep_args* args, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                         void* stream);
+
+/* ---------------------------------------------------------------------------------------
  * One verification round as a single CUDA-graph launch.  (Deployment convenience: the pages
  * describe the round's steps -- parallel tree verification, acceptance, keeping the accepted
  * prefix -- not how they are launched.  At batch 1 the round is a handful of short kernels

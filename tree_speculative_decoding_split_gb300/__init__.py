@@ -17,6 +17,8 @@ runs in the library's CUDA kernels; if the library has not been built, every cal
     kv_reserve(...)       -> (slot_map, row_start) block tables grown or shrunk from request lengths
     kv8_append(...)       -> new_len              rows into the 8-bit paged cache
     tree_attention_kv8(...) -> (out, lse)         tree attention over the 8-bit paged cache
+    rope_table, rope_positions, rope, prompt_attention, prompt_key_weights, kv_keep
+                                                  prompts on their way to the cache (``_prompt``)
     Round(...)                                    the three verification calls as one graph launch
                                                   (also from host buffers: Round.launch_host)
 """
@@ -183,6 +185,7 @@ def lib():
         L.spec_tree_attention_kv8_workspace.restype = ctypes.c_size_t
         L.spec_tree_attention_kv8.argtypes = [ctypes.POINTER(AttnKv8Args), _vp, ctypes.c_size_t, _vp, _vp]
         L.spec_tree_attention_kv8.restype = ctypes.c_int32
+        _prompt.declare(L)
         _lib_handle = L
     return _lib_handle
 
@@ -739,6 +742,9 @@ def _native():
         module.bind(*(ctypes.cast(fn, _vp).value for fn in (L.spec_kv_reserve, L.spec_kv8_append,
                                                             L.spec_tree_attention_kv8_workspace,
                                                             L.spec_tree_attention_kv8)))
+        module.bind_prompt(*(ctypes.cast(fn, _vp).value for fn in (
+            L.spec_rope_positions, L.spec_rope, L.spec_prompt_attention_workspace, L.spec_prompt_attention,
+            L.spec_prompt_key_weights_workspace, L.spec_prompt_key_weights, L.spec_kv_keep_workspace, L.spec_kv_keep)))
         _marshal = module
     return _marshal
 
@@ -994,3 +1000,11 @@ def tree_attention_kv8(q, k_tree, v_tree, k_cache, v_cache, k_scale, v_scale, pr
     _launch(L.spec_tree_attention_kv8, "spec_tree_attention_kv8", dev, stream, (ws, out, lse), ref, ws.data_ptr(), need,
             _status_ptr(dev_status, dev))
     return out, lse
+
+
+# ---- prompts on their way to the cache ---------------------------------------------------------
+
+from . import _prompt  # noqa: E402
+from ._prompt import (ROPE_KINDS, ROPE_LAYOUTS, KeyWeightsArgs, KvKeepArgs, PromptAttnArgs, RopeArgs,  # noqa: E402, F401
+                      RopePositionsArgs, key_weights_args, kv_keep, kv_keep_args, prompt_attention, prompt_attn_args,
+                      prompt_key_weights, rope, rope_args, rope_positions, rope_positions_args, rope_table)

@@ -1,0 +1,291 @@
+// K13: the rows of each prompt that a budget leaves in the cache.
+//
+// Three kernels: the counts and their sums (one CTA), the choice, and the copying of the chosen rows.
+//
+// The choice is a radix selection.  Weights become 32-bit keys in their order; three passes of 11, 11 and 10 bits
+// count the keys that share what is known of the threshold, and the bin in which the budget runs out is the
+// threshold's next piece.  Then a row stays if its key is above the threshold, or equal to it and among the first of
+// the equal ones; warps walk disjoint stretches in order, so a row's place is the number of rows that stay before
+// it, counted by ballots.  One cluster works on a request and KV head: its CTAs hold the keys in shared memory (one
+// read of the weights; stretches past 40960 keys per CTA are read again in each pass) and add their
+// counts through distributed shared memory.  All counts are integers: no order of additions changes the result.
+//
+// The copy reads and writes every kept row once, with 16-byte accesses, four rows of K and V in flight per thread.
+
+#include "pdl.cuh"
+#include "prompt.cuh"
+#include "tc_ptx.cuh"
+#include "topk.cuh"
+
+namespace spectree {
+
+namespace {
+
+constexpr int kThreads = 1024;
+constexpr int kWarps = kThreads / 32;
+constexpr int kHeld = 40960;        // keys a CTA holds
+constexpr int kCopyThreads = 256;
+constexpr int kCopies = 4;          // (row, head)s per thread
+
+__global__ void __launch_bounds__(kThreads) keep_counts_kernel(const KeepParams p) {
+  __shared__ long long s_warp[kWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_wait();
+  pdl_launch_dependents();
+  bool ok = row_start_ok(p.row_start, p.B, p.n_rows);
+  const int per = (p.B + kThreads - 1) / kThreads;
+  const int b0 = tid * per, b1 = b0 + per < p.B ? b0 + per : p.B;
+  auto kept = [&](int b) {
+    const int n = p.row_start[b + 1] - p.row_start[b];
+    return n < p.budget ? n : p.budget;
+  };
+  long long mine = 0;
+  if (ok)
+    for (int b = b0; b < b1; ++b) mine += kept(b);
+  long long v = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += y;
+  }
+  if (lane == 31) s_warp[warp] = v;
+  __syncthreads();
+  long long before = v - mine, total = 0;
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += s_warp[w];
+    total += s_warp[w];
+  }
+  ok = ok && total <= p.rows_out;
+  if (!ok && tid == 0) set_status(p.dev_status, SPEC_ERR_CAPACITY);
+  for (int b = b0; b < b1; ++b) {
+    const int n = ok ? kept(b) : 0;
+    p.n_keep[b] = n;
+    p.keep_start[b] = ok ? (int)before : 0;
+    before += n;
+  }
+  if (tid == 0) p.keep_start[p.B] = ok ? (int)total : 0;
+}
+
+__device__ __forceinline__ int cluster_ld(const int* at, uint32_t rank) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(cluster_addr(at, rank)) : "memory");
+  return v;
+}
+
+struct SelectShared {
+  int part[4][2048];    // a pass's counts, by warp & 3
+  int bins[3][2048];    // their sums, one set per pass (other CTAs read them)
+  int warp_sum[kWarps];
+  int totals[2];        // keys above and at the threshold
+  int warp_n[kWarps][2];
+  int bin, left;
+};
+
+__global__ void __launch_bounds__(kThreads, 1) keep_select_kernel(const KeepParams p, int32_t* source, int cluster) {
+  extern __shared__ __align__(16) uint8_t s_raw[];
+  SelectShared& s = *reinterpret_cast<SelectShared*>(s_raw);
+  uint32_t* s_key = reinterpret_cast<uint32_t*>(s_raw + sizeof(SelectShared));  // [kHeld]
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = cluster > 1 ? (int)cluster_rank() : 0;
+  const int seg = blockIdx.x / cluster;
+  const int b = seg / p.Hkv, g = seg % p.Hkv;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int keep = p.n_keep[b];
+  if (keep == 0) return;  // (the whole cluster)
+  const int r0 = p.row_start[b], n = p.row_start[b + 1] - r0;
+  const long long out0 = p.keep_start[b];
+  auto put = [&](int place, int j) {
+    const long long at = (out0 + place) * p.Hkv + g;
+    p.index[at] = j;
+    source[at] = r0 + j;
+  };
+  if (n <= p.budget) {
+    for (long long j = (long long)rank * kThreads + tid; j < n; j += (long long)cluster * kThreads) put((int)j, (int)j);
+    return;
+  }
+  if (rank == 0) {
+    for (int j = tid; j < p.first; j += kThreads) put(j, j);
+    for (int j = tid; j < p.last; j += kThreads) put(p.budget - p.last + j, n - p.last + j);
+  }
+  int left = p.budget - p.first - p.last;  // rows to choose
+  if (left == 0) return;
+  // candidates [first, n - last); this CTA's are [c0, c1)
+  const int cands = n - p.first - p.last;
+  const int per = (int)(((long long)cands + cluster - 1) / cluster);
+  const long long lo = (long long)rank * per, hi = lo + per < cands ? lo + per : cands;
+  const int mine = hi > lo ? (int)(hi - lo) : 0;
+  const float* weight = p.weight + (size_t)g * p.n_rows + r0 + p.first + (mine ? lo : 0);
+  auto key_at = [&](int i) { return i < kHeld ? s_key[i] : order_u(weight[i]); };
+  uint32_t known = 0;  // the threshold's upper bits
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
+    const int bits = pass == 2 ? 10 : 11;
+    for (int i = tid; i < 4 * 2048; i += kThreads) (&s.part[0][0])[i] = 0;
+    __syncthreads();
+    int* part = s.part[warp & 3];
+    for (int i = tid; i < mine; i += kThreads) {
+      uint32_t key;
+      if (pass == 0) {
+        key = order_u(weight[i]);
+        if (i < kHeld) s_key[i] = key;
+      } else {
+        key = key_at(i);
+      }
+      if (pass == 0 || (key >> (shift + bits)) == known) atomicAdd(&part[(key >> shift) & ((1u << bits) - 1)], 1);
+    }
+    __syncthreads();
+    for (int i = tid; i < 2048; i += kThreads) s.bins[pass][i] = s.part[0][i] + s.part[1][i] + s.part[2][i] + s.part[3][i];
+    if (cluster > 1)
+      cluster_sync_all();
+    else
+      __syncthreads();
+    // the bin, from above, in which the rows to choose run out; thread t looks at bins 2047 - 2 t and 2046 - 2 t
+    int x[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int bin = 2047 - 2 * tid - e;
+      x[e] = 0;
+      if (cluster > 1) {
+        for (int r = 0; r < cluster; ++r) x[e] += cluster_ld(&s.bins[pass][bin], (uint32_t)r);
+      } else {
+        x[e] = s.bins[pass][bin];
+      }
+    }
+    int v = x[0] + x[1];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += y;
+    }
+    if (lane == 31) s.warp_sum[warp] = v;
+    __syncthreads();
+    int above = v - x[0] - x[1];
+    for (int w = 0; w < warp; ++w) above += s.warp_sum[w];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      if (above < left && above + x[e] >= left) {
+        s.bin = 2047 - 2 * tid - e;
+        s.left = left - above;
+      }
+      above += x[e];
+    }
+    __syncthreads();
+    known = (known << bits) | (uint32_t)s.bin;
+    left = s.left;
+    __syncthreads();
+  }
+  // `known` is the threshold, `left` the number of keys equal to it that stay.  Warps walk stretches of 32 w keys.
+  const int stretch = ((mine + kWarps - 1) / kWarps + 31) & ~31;
+  const int w0 = warp * stretch < mine ? warp * stretch : mine, w1 = w0 + stretch < mine ? w0 + stretch : mine;
+  int above = 0, equal = 0;
+  for (int i = w0; i < w1; i += 32) {
+    const uint32_t key = i + lane < w1 ? key_at(i + lane) : 0u;
+    above += __popc(__ballot_sync(0xffffffffu, i + lane < w1 && key > known));
+    equal += __popc(__ballot_sync(0xffffffffu, i + lane < w1 && key == known));
+  }
+  if (lane == 0) {
+    s.warp_n[warp][0] = above;
+    s.warp_n[warp][1] = equal;
+  }
+  __syncthreads();
+  if (tid < 2) {
+    int sum = 0;
+    for (int w = 0; w < kWarps; ++w) sum += s.warp_n[w][tid];
+    s.totals[tid] = sum;
+  }
+  above = equal = 0;
+  if (cluster > 1) {
+    cluster_sync_all();
+    for (int r = 0; r < rank; ++r) {
+      above += cluster_ld(&s.totals[0], (uint32_t)r);
+      equal += cluster_ld(&s.totals[1], (uint32_t)r);
+    }
+  }
+  for (int w = 0; w < warp; ++w) {
+    above += s.warp_n[w][0];
+    equal += s.warp_n[w][1];
+  }
+  const uint32_t below = (1u << lane) - 1u;
+  for (int i = w0; i < w1; i += 32) {
+    const uint32_t key = i + lane < w1 ? key_at(i + lane) : 0u;
+    const uint32_t up = __ballot_sync(0xffffffffu, i + lane < w1 && key > known);
+    const uint32_t eq = __ballot_sync(0xffffffffu, i + lane < w1 && key == known);
+    const int eq_before = equal + __popc(eq & below);
+    const bool is_eq = (eq >> lane) & 1u;
+    if (((up >> lane) & 1u) || (is_eq && eq_before < left)) {
+      const int place = above + __popc(up & below) + (eq_before < left ? eq_before : left);
+      put(p.first + place, p.first + (int)lo + i + lane);
+    }
+    above += __popc(up);
+    equal += __popc(eq);
+  }
+  if (cluster > 1) cluster_sync_all();  // no CTA leaves while another may still read its counts
+}
+
+// Copies K and V of every kept (row, head): `vecs` lanes of 16 bytes per row.
+__global__ void __launch_bounds__(kCopyThreads) keep_copy_kernel(const KeepParams p, const int32_t* source, int vecs) {
+  pdl_wait();
+  const long long units = (long long)p.keep_start[p.B] * p.Hkv;
+  const int per_block = kCopyThreads / vecs;  // units side by side
+  const int lane = threadIdx.x % vecs, at = threadIdx.x / vecs;
+  const long long u0 = (long long)blockIdx.x * per_block * kCopies + at;
+  uint4 kv[kCopies][2];
+#pragma unroll
+  for (int f = 0; f < kCopies; ++f) {
+    const long long u = u0 + (long long)f * per_block;
+    if (u < units) {
+      const long long row = source[u];
+      const int g = (int)(u % p.Hkv);
+      kv[f][0] = *reinterpret_cast<const uint4*>(p.k + row * p.k_stride + (size_t)g * p.row_bytes + lane * 16);
+      kv[f][1] = *reinterpret_cast<const uint4*>(p.v + row * p.v_stride + (size_t)g * p.row_bytes + lane * 16);
+    }
+  }
+#pragma unroll
+  for (int f = 0; f < kCopies; ++f) {
+    const long long u = u0 + (long long)f * per_block;
+    if (u < units) {
+      *reinterpret_cast<uint4*>(p.k_out + (size_t)u * p.row_bytes + lane * 16) = kv[f][0];
+      *reinterpret_cast<uint4*>(p.v_out + (size_t)u * p.row_bytes + lane * 16) = kv[f][1];
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_kv_keep(const KeepParams& p, int32_t* source, int num_sms, cudaStream_t stream) {
+  cudaError_t err = launch_dependent(keep_counts_kernel, dim3(1), dim3(kThreads), 0, stream, p);
+  if (err != cudaSuccess) return err;
+  if (p.n_rows == 0 || p.rows_out == 0) return cudaSuccess;
+  // CTAs per request and head: as many as there are SMs for, and 2048 rows for each.
+  const long long segs = (long long)p.B * p.Hkv;
+  int cluster = 1;
+  while (cluster < 8 && segs * cluster * 2 <= num_sms && (long long)cluster * 2 * 2048 <= p.n_rows) cluster *= 2;
+  err = cudaFuncSetAttribute(keep_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)sizeof(SelectShared) + kHeld * 4);
+  if (err != cudaSuccess) return err;
+  const long long longest = p.n_rows < kHeld ? p.n_rows : kHeld;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(segs * cluster));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = sizeof(SelectShared) + (size_t)longest * 4;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  err = cudaLaunchKernelEx(&cfg, keep_select_kernel, p, source, cluster);
+  if (err != cudaSuccess) return err;
+  const int vecs = p.row_bytes / 16;
+  const long long per_block = (long long)(kCopyThreads / vecs) * kCopies;
+  const long long most = p.rows_out < p.n_rows ? p.rows_out : p.n_rows;  // a request keeps no more rows than it has
+  const long long blocks = (most * p.Hkv + per_block - 1) / per_block;
+  return launch_dependent(keep_copy_kernel, dim3((unsigned)blocks), dim3(kCopyThreads), 0, stream, p, source, vecs);
+}
+
+}  // namespace spectree

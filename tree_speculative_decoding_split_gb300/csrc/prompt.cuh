@@ -1,0 +1,131 @@
+// Parameters, device helpers and launches of the kernels that take prompts to the cache: positions and their
+// rotation, causal attention over packed prompts, key weights and the rows kept for a budget.
+#pragma once
+
+#include "common.cuh"
+
+namespace spectree {
+
+// ---- K10: positions, rotation -----------------------------------------------------------------
+struct PositionsParams {
+  int B, N;
+  long long n_rows;
+  const int32_t* pos0;       // [B]
+  const int32_t* row_start;  // [B + 1] (packed rows) or nullptr
+  const int32_t* parent;     // [B][N] (trees) or nullptr
+  const int32_t* n_nodes;
+  int32_t* positions;        // [n_rows] or [B][N]
+  int32_t* dev_status;
+};
+cudaError_t launch_rope_positions(const PositionsParams& p, cudaStream_t stream);
+
+struct RopeParams {
+  int is_bf16, interleaved, Hq, Hk, d, rot;
+  long long n_rows;
+  long long q_stride, k_stride, q_out_stride, k_out_stride;
+  float amplitude;
+  const void* q;
+  const void* k;
+  const int32_t* positions;
+  const int64_t* turns;
+  void* q_out;
+  void* k_out;
+};
+cudaError_t launch_rope(const RopeParams& p, int num_sms, cudaStream_t stream);
+
+// ---- the plan of a call over packed rows -------------------------------------------------------
+// A work item: `tokens` rows of one request from row `tok` on; the kernels take every KV head of it.
+struct PromptItem {
+  int r0;   // the request's first row
+  int n;    // its rows
+  int tok;  // the item's first row, counted in the request
+  int pad;
+};
+// Cuts [from(n), n) of every request into pieces of `step` rows and lists them; count[0] = items, 0 for a bad
+// row_start (SPEC_ERR_CAPACITY).  by_work: the items with the most keys behind them first.
+struct PlanParams {
+  int B, step, by_work;
+  long long n_rows;
+  const int32_t* row_start;
+  PromptItem* items;
+  int32_t* count;
+  int32_t* dev_status;
+};
+// Items that a plan can hold at most.
+inline long long plan_items(long long n_rows, int B, int step) { return n_rows / step + (B < n_rows ? B : n_rows); }
+cudaError_t launch_prompt_plan(const PlanParams& p, cudaStream_t stream);
+
+// ---- K11: causal attention over packed prompts --------------------------------------------------
+struct PromptAttnParams {
+  int Hq, Hkv, G, tg;       // tg: rows of a request per 128-row group (128 / G)
+  float scale, scale_log2;
+  const PromptItem* items;
+  const int32_t* count;
+  const uint16_t* v;        // for keys with infinities
+  long long v_stride;
+  uint16_t* out;            // [n_rows][Hq][d]
+  float* lse;               // [n_rows][Hq] or nullptr
+  int32_t* dev_status;
+};
+cudaError_t launch_prompt_attention(int d, const CUtensorMap* tmQ, const CUtensorMap* tmK, const CUtensorMap* tmV,
+                                    const PromptAttnParams& p, int grid, cudaStream_t stream);
+
+// ---- K12: key weights -----------------------------------------------------------------------------
+constexpr int kWeightKeys = 256;  // keys per item
+struct KeyWeightsParams {
+  int Hq, Hkv, G, tc;       // tc: rows of the window per chunk (128 / G)
+  int window;
+  float scale_log2;
+  long long n_rows;
+  const PromptItem* items;
+  const int32_t* count;
+  const float* lse;         // [n_rows][Hq]
+  float* weight;            // [Hkv][n_rows]
+  int32_t* dev_status;
+};
+cudaError_t launch_key_weights(int d, const CUtensorMap* tmQ, const CUtensorMap* tmK, const KeyWeightsParams& p, int grid,
+                               cudaStream_t stream);
+
+// ---- K13: rows kept for a budget -------------------------------------------------------------------
+struct KeepParams {
+  int B, Hkv, row_bytes;    // row_bytes: of one head's row
+  int budget, first, last;
+  long long n_rows, rows_out;
+  long long k_stride, v_stride;  // bytes between rows
+  const uint8_t* k;
+  const uint8_t* v;
+  const float* weight;
+  const int32_t* row_start;
+  uint8_t* k_out;
+  uint8_t* v_out;
+  int32_t* index;
+  int32_t* keep_start;
+  int32_t* n_keep;
+  int32_t* dev_status;
+};
+// source: [rows_out][Hkv] numbers of the chosen rows, handed from the choice to the copy.
+cudaError_t launch_kv_keep(const KeepParams& p, int32_t* source, int num_sms, cudaStream_t stream);
+
+// Is row_start an ascending walk within [0, n_rows]?  All threads of the block call it; the verdict is the same in all.
+__device__ __forceinline__ bool row_start_ok(const int32_t* row_start, int B, long long n_rows) {
+  int bad = 0;
+  for (int b = threadIdx.x; b < B; b += blockDim.x) {
+    const int lo = row_start[b], hi = row_start[b + 1];
+    bad |= lo < 0 || hi < lo || hi > n_rows;
+  }
+  return !__syncthreads_or(bad);
+}
+
+// The request that row `r` belongs to: the last b in [lo, hi) with row_start[b] <= r.
+__device__ __forceinline__ int request_of(const int32_t* row_start, int lo, int hi, long long r) {
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (row_start[mid] <= r)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+}  // namespace spectree
