@@ -36,6 +36,7 @@ namespace {
 constexpr int kKeys = 128;        // keys per tile
 constexpr int kRows = 128;        // rows per group
 constexpr int kThreads = 384;
+constexpr int kBarTurn = 1, kBarP = 3;  // named barriers: an issuer's turn, a group's P written
 constexpr float kRescale = 8.f;   // log2
 constexpr float kExact = 262144.f;  // 2^18: maxima from here on, in log2 units, take differences ahead of the scale
 
@@ -48,18 +49,21 @@ struct PromptCfg {
   static constexpr int kColS = 0, kColO = 256;
 };
 
-// The registers of a launch, 384 x 168, shared out anew: the softmax threads hold a row of 128 scores each.
-// 128 x 88 + 256 x 208 = 384 x 168.
-constexpr int kRegsLaunch = 168, kRegsIssue = 88, kRegsSoftmax = 208;
-static_assert(128 * kRegsIssue + 256 * kRegsSoftmax <= kThreads * kRegsLaunch, "more registers than the launch has");
-
-template <int N>
-__device__ __forceinline__ void regs_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+// mbar_wait_bounded with all but the first try out of line: a wait that is over costs the issuing threads a few instructions.
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, int* abort) { return mbar_wait_bounded(bar, parity, abort); }
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* abort) {
+  return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort);
 }
-template <int N>
-__device__ __forceinline__ void regs_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+// A 128-byte-swizzle K-major operand's descriptor, the address apart: base plus (address >> 4) in the lower word.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint64_t desc(uint32_t lo) { return ((uint64_t)kDescHi << 32) | lo; }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ void named_arrive(int id, int count) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
 __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -68,10 +72,107 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+// tmem_ld_wait, with the registers that it is for: nothing is taken from them ahead of it.
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&a)[4][32]) {
+  tmem_ld_wait();
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+#pragma unroll
+    for (int j = 0; j < 32; j += 16)
+      asm volatile("" : "+r"(a[c][j]), "+r"(a[c][j + 1]), "+r"(a[c][j + 2]), "+r"(a[c][j + 3]), "+r"(a[c][j + 4]),
+                   "+r"(a[c][j + 5]), "+r"(a[c][j + 6]), "+r"(a[c][j + 7]), "+r"(a[c][j + 8]), "+r"(a[c][j + 9]),
+                   "+r"(a[c][j + 10]), "+r"(a[c][j + 11]), "+r"(a[c][j + 12]), "+r"(a[c][j + 13]), "+r"(a[c][j + 14]),
+                   "+r"(a[c][j + 15]));
+}
 
-// Does a word hold a bf16 infinity or NaN, in its lower or upper half?
-__device__ __forceinline__ bool special_lo(uint32_t w) { return (w & 0x7f80u) == 0x7f80u; }
-__device__ __forceinline__ bool special_hi(uint32_t w) { return (w & 0x7f800000u) == 0x7f800000u; }
+// A tile's weights in two passes over its scores, of which a row sees those up to key `lim`: the maximum, with what is
+// there brought to it where it has grown by more than 2^8 (with_o: O holds something; the commit behind the scores says
+// that it is complete), then P over the scores that have been read.  Where the maximum is so large that its product
+// with the scale would be rounded by whole units, differences are taken ahead of the scale.  Returns the row's maximum
+// (in the scores' units) and sum.  Out of line and in loops: it runs once or twice an item, and cold code costs more
+// than its instructions.
+template <int D>
+__device__ __noinline__ float2 tile_again(uint32_t tS, uint32_t tO, int lim, bool with_o, float2 ml, float scale_log2) {
+  float top = -INFINITY;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    uint32_t s[32];
+    tmem_ld_x32(tS + c * 32, s);
+    tmem_ld_wait();
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (c * 32 + j <= lim) top = fmaxf(top, __uint_as_float(s[j]));
+  }
+  const bool need = (top - ml.x) * scale_log2 > kRescale;  // the first finite maximum among them
+  if (__any_sync(0xffffffffu, need)) {
+    const float f = need ? exp2f((ml.x - top) * scale_log2) : 1.f;
+    if (with_o) {
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        tmem_ld_x32(tO + c * 32, o);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+        tmem_st_x32(tO + c * 32, o);
+      }
+    }
+    if (need) ml = make_float2(top, ml.y * f);
+  }
+  const float ref = ml.x == -INFINITY ? 0.f : ml.x;
+  const bool far = fabsf(ref * scale_log2) >= kExact;
+  const float shift = far ? 0.f : ref * scale_log2, before = far ? ref : 0.f;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    uint32_t s[32], pk[16];
+    tmem_ld_x32(tS + c * 32, s);
+    tmem_ld_wait();
+    float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+      float w[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        w[e] = ex2_approx(fmaf(__uint_as_float(s[j + e]) - before, scale_log2, -shift));
+        if (c * 32 + j + e > lim) w[e] = 0.f;
+      }
+      sum = __fadd2_rn(sum, make_float2(w[0], w[1]));
+      pk[j / 2] = pack_bf16x2(w[0], w[1]);
+    }
+    ml.y += sum.x + sum.y;
+    tmem_st_x16(tS + c * 16, pk);
+  }
+  tmem_st_wait();
+  return ml;
+}
+
+// The upper bits of a word's halves that are a bf16 infinity or NaN (exponent all ones); the word without these.
+__device__ __forceinline__ uint32_t specials(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
+__device__ __forceinline__ uint32_t clean(uint32_t w) {
+  const uint32_t bad = specials(w);
+  return w & ~((bad & 0x80000000u ? 0xffff0000u : 0u) | (bad & 0x8000u ? 0xffffu : 0u));
+}
+
+// Of four threads, each with four pieces: thread i's piece j becomes thread j's piece i.
+__device__ __forceinline__ void transpose4(uint32_t (&y)[4][4], int lane) {
+#pragma unroll
+  for (int step = 1; step < 4; step <<= 1) {
+    const bool up = lane & step;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i & step) continue;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? y[i][e] : y[i | step][e], step);
+        if (up)
+          y[i][e] = got;
+        else
+          y[i | step][e] = got;
+      }
+    }
+  }
+}
+constexpr uint32_t kNoRow = 0xffffffffu;
 
 // An item as every role sees it.
 struct Work {
@@ -123,10 +224,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint64_t empty[kStages];    // tile read by every MMA
   __shared__ uint64_t qfull[2], qempty[2];
   __shared__ uint64_t sfull[2];        // S computed (and everything issued before it)
-  __shared__ uint64_t pfull[2];        // P written
   __shared__ uint64_t ofull[2];        // O complete
   __shared__ uint64_t ofree[2];        // O read
-  __shared__ uint64_t drained;
+  __shared__ uint64_t drained[2];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort, s_special;
 
@@ -135,18 +235,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&held[s], 1);
-      mbar_init(&empty[s], 1);
-      mbar_init(&guarded[s], 2);
+      mbar_init(&empty[s], 2);
+      mbar_init(&guarded[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&qfull[a], 1);
       mbar_init(&qempty[a], 1);
       mbar_init(&sfull[a], 1);
-      mbar_init(&pfull[a], 4);
       mbar_init(&ofull[a], 1);
+      mbar_init(&drained[a], 1);
       mbar_init(&ofree[a], 4);
     }
-    mbar_init(&drained, 1);
     s_abort = 0;
     s_special = 0;
     fence_mbar_init();
@@ -161,10 +260,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = s_tmem;
   pdl_wait();  // the plan
   const int total = p.count[0] * p.Hkv;
-  auto work_at = [&](int at) { return work_of(p, p.items[at / p.Hkv], at % p.Hkv); };
+  // This CTA's items one by one, the next one's entry fetched while the current one is under way.
+  int u = 0, at = item_index(0, total);
+  PromptItem entry = at >= 0 ? p.items[at / p.Hkv] : PromptItem{};
+  auto take = [&](Work& w) -> bool {
+    if (at < 0) return false;
+    w = work_of(p, entry, at % p.Hkv);
+    at = item_index(++u, total);
+    if (at >= 0) entry = p.items[at / p.Hkv];
+    return true;
+  };
 
   if (warp < 4) {
-    regs_dec<kRegsIssue>();
     if (warp == 0) {
       // ---- TMA producer ----
       if (lane == 0) {
@@ -205,8 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++qround[a];
           return true;
         };
-        for (int u = 0, at; ok && (at = item_index(u, total)) >= 0; ++u) {
-          const Work w = work_at(at);
+        for (Work w; ok && take(w);) {
           ok = queries(w, 0) && tile(&tmK, w, 0, false) && queries(w, 1);
           for (int t = 0; ok && t < w.all; ++t) {
             ok = tile(&tmV, w, t, t >= w.edge);
@@ -225,92 +331,95 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (qround[a]) mbar_wait_bounded(&qfull[a], (qround[a] - 1) & 1, nullptr);
         }
       }
-    } else if (warp == 1) {
-      // ---- MMA issuer ----
-      if (lane == 0) {
-        constexpr uint32_t idS = idesc_bf16_f32(kRows, kKeys, 0);
-        constexpr uint32_t idP = idesc_bf16_f32(kRows, D, 1);
-        uint32_t at_load = 0;          // loads before the item's first tile; K(t) is load 2 t, V(t) 2 t + 1 of an item
-        uint32_t f_phase = 0, g_phase = 0;  // per stage: parity of the next phase of full and guarded
-        uint32_t q_n[2] = {0, 0}, p_n[2] = {0, 0}, o_n[2] = {0, 0};
-        bool ok = true;
-        auto landed = [&](uint32_t load, bool guard) {
-          const int st = load % kStages;
-          const uint32_t parity = ((guard ? g_phase : f_phase) >> st) & 1;
-          if (guard)
-            g_phase ^= 1u << st;
-          else
-            f_phase ^= 1u << st;
-          return mbar_wait_bounded(guard ? &guarded[st] : &full[st], parity, &s_abort);
-        };
-        auto scores = [&](uint32_t load, int a) {
-          tc_fence_after();
-          const uint32_t qa = smem_u32(sQ + a * C::kQ), ka = smem_u32(sKV + (load % kStages) * C::kTile);
+    } else if (warp < 3) {
+      // ---- MMA issuer of group a: the whole warp waits, one lane issues ----
+      const int a = warp - 1;
+      constexpr uint32_t idS = idesc_bf16_f32(kRows, kKeys, 0);
+      constexpr uint32_t idP = idesc_bf16_f32(kRows, D, 1);
+      const uint32_t q_lo = (smem_u32(sQ + a * C::kQ) >> 4), kv_lo = (smem_u32(sKV) >> 4);
+      const uint32_t v_mn = ((kKeys * 128) >> 4) << 16;  // V (MN-major): the distance of its two halves of d
+      const uint32_t tS = tmem + C::kColS + a * kKeys, tO = tmem + C::kColO + a * D;
+      int st = 0;                          // stage of the next load
+      uint32_t f_phase = 0, g_phase = 0;   // per stage: parity of the next phase of full and guarded
+      uint32_t q_n = 0;
+      bool ok = true;
+      // The next load has landed (and been looked over); its stage.
+      auto landed = [&](bool guard) -> int {
+        uint32_t& phase = guard ? g_phase : f_phase;
+        const int at = st;
+        ok = ok && wait(guard ? &guarded[at] : &full[at], (phase >> at) & 1, &s_abort);
+        phase ^= 1u << at;
+        st = at + 1 == kStages ? 0 : at + 1;
+        return at;
+      };
+      auto arrive = [&](uint64_t* bar) {
+        if (lane == 0) mbar_arrive(bar);
+      };
+      auto scores = [&](int k) {
+        const uint32_t k_lo = kv_lo + k * (C::kTile >> 4);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            umma_bf16(tmem + C::kColS + a * kKeys, sdesc_sw128(qa + (kk >> 2) * (kRows * 128) + (kk & 3) * 32, 0, 1024),
-                      sdesc_sw128(ka + (kk >> 2) * (kKeys * 128) + (kk & 3) * 32, 0, 1024), idS, kk > 0);
-          umma_commit(&sfull[a]);
-        };
-        for (int u = 0, at; ok && (at = item_index(u, total)) >= 0; ++u) {
-          const Work w = work_at(at);
-          ok = landed(at_load, false);
-#pragma unroll
-          for (int a = 0; a < 2; ++a) {
-            if (!ok || w.tiles[a] == 0) continue;
-            ok = mbar_wait_bounded(&qfull[a], q_n[a]++ & 1, &s_abort);
-            if (!ok) continue;
-            scores(at_load, a);
-            if (w.tiles[a] == 1) umma_commit(&qempty[a]);
-          }
-          if (ok) umma_commit(&empty[at_load % kStages]);
-          for (int t = 0; ok && t < w.all; ++t) {
-            const uint32_t lv = at_load + 2 * t + 1, lk = lv + 1;
-            const int sv = lv % kStages;
-            ok = landed(lv, t >= w.edge);
-            bool next = false;             // K(t + 1) has been waited for
-            const uint32_t va = smem_u32(sKV + sv * C::kTile);
-#pragma unroll
-            for (int a = 0; a < 2; ++a) {
-              if (!ok || t >= w.tiles[a]) continue;
-              if (t == 0) ok = mbar_wait_bounded(&ofree[a], (o_n[a]++ & 1) ^ 1, &s_abort);
-              ok = ok && mbar_wait_bounded(&pfull[a], p_n[a]++ & 1, &s_abort);
-              if (!ok) continue;
-              tc_fence_after();
-#pragma unroll
-              for (int kk = 0; kk < kKeys / 16; ++kk)
-                umma_bf16_tmem_a(tmem + C::kColO + a * D, tmem + C::kColS + a * kKeys + kk * 8,
-                                 sdesc_sw128(va + kk * 2048, kKeys * 128, 1024), idP, (t > 0 || kk > 0) ? 1u : 0u);
-              if (t + 1 < w.tiles[a]) {
-                ok = next || landed(lk, false);
-                next = true;
-                if (!ok) continue;
-                scores(lk, a);
-                if (t + 2 == w.tiles[a]) umma_commit(&qempty[a]);
-              } else {
-                umma_commit(&ofull[a]);
-              }
-            }
-            if (ok) {
-              umma_commit(&empty[sv]);
-              if (t + 1 < w.all) umma_commit(&empty[lk % kStages]);
-            }
-          }
-          at_load += 2 * w.all;
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * ((kKeys * 128) >> 4) + (kk & 3) * 2;
+          umma_bf16(tS, desc(q_lo + off), desc(k_lo + off), idS, kk > 0);
         }
+      };
+      if (a == 1) named_arrive(kBarTurn, 64);  // group 0 begins
+      // An issuer whose wait gave up issues nothing more, but takes and hands on its turns to the last item's end.
+      for (Work w; take(w);) {
+        const int tiles = a ? w.tiles[1] : w.tiles[0];
+        int k = landed(false);
+        if (tiles > 0) ok = ok && wait(&qfull[a], q_n & 1, &s_abort);
+        ok = __all_sync(0xffffffffu, ok);
+        named_bar_sync(kBarTurn + a, 64);
+        tc_fence_after();
+        if (ok && tiles > 0 && lane == 0) {
+          scores(k);
+          umma_commit(&sfull[a]);
+          if (tiles == 1) umma_commit(&qempty[a]);
+        }
+        __syncwarp();
+        named_arrive(kBarTurn + (a ^ 1), 64);
+        if (ok && tiles == 0) arrive(&empty[k]);
+        for (int t = 0; t < w.all; ++t) {
+          const int v = landed(t >= w.edge);
+          const bool more = t + 1 < w.all;
+          if (more) k = landed(false);
+          if (t == 0 && tiles > 0) ok = ok && wait(&ofree[a], (q_n & 1) ^ 1, &s_abort);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) s_abort = 1;
+          if (t < tiles) named_bar_sync(kBarP + a, 160);
+          named_bar_sync(kBarTurn + a, 64);
+          tc_fence_after();
+          if (ok && t < tiles && lane == 0) {
+            const uint32_t v_lo = (kv_lo + v * (C::kTile >> 4)) | v_mn;
+#pragma unroll
+            for (int kk = 0; kk < kKeys / 16; ++kk)
+              umma_bf16_tmem_a(tO, tS + kk * 8, desc(v_lo + kk * (2048 >> 4)), idP, (t > 0 || kk > 0) ? 1u : 0u);
+            if (t + 1 < tiles) scores(k);
+            umma_commit(t + 1 < tiles ? &sfull[a] : &ofull[a]);
+            if (t + 2 == tiles) umma_commit(&qempty[a]);
+          }
+          __syncwarp();
+          named_arrive(kBarTurn + (a ^ 1), 64);
+          if (ok && t >= tiles) arrive(&empty[v]);
+          if (ok && more && t + 1 >= tiles) arrive(&empty[k]);
+        }
+        if (tiles > 0) ++q_n;
+      }
+      if (a == 0) named_bar_sync(kBarTurn, 64);  // (the turn that group 1 hands on at the end)
+      if (lane == 0) {
         if (!ok) {
           s_abort = 1;
           set_status(p.dev_status, SPEC_ERR_TIMEOUT);
         }
-        umma_commit(&drained);
-        mbar_wait_bounded(&drained, 0, nullptr);
+        umma_commit(&drained[a]);
+        mbar_wait_bounded(&drained[a], 0, nullptr);
       }
     } else {
       // ---- guard ----
       uint32_t at_load = 0, phase = 0;
       bool ok = true;
-      for (int u = 0, at; ok && (at = item_index(u, total)) >= 0; ++u) {
-        const Work w = work_at(at);
+      for (Work w; ok && take(w);) {
         for (int t = w.edge; t < w.all; ++t) {
           const int st = (at_load + 2 * t + 1) % kStages;
           ok = __all_sync(0xffffffffu, mbar_wait_bounded(&held[st], (phase >> st) & 1, &s_abort));
@@ -318,19 +427,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           phase ^= 1u << st;
           uint4* v = reinterpret_cast<uint4*>(sKV + st * C::kTile);
           bool found = false;
-#pragma unroll 4
-          for (int i = (warp - 2) * 32 + lane; i < C::kTile / 16; i += 64) {
-            uint4 x = v[i];
-            const bool bad = special_lo(x.x) || special_hi(x.x) || special_lo(x.y) || special_hi(x.y) || special_lo(x.z) ||
-                             special_hi(x.z) || special_lo(x.w) || special_hi(x.w);
+#pragma unroll 1
+          for (int i = lane; i < C::kTile / 16; i += 32 * 8) {
+            uint4 x[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = v[i + 32 * j];
+            uint32_t bad = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) bad |= specials(x[j].x) | specials(x[j].y) | specials(x[j].z) | specials(x[j].w);
             if (bad) {
               found = true;
-              auto clean = [](uint32_t y) {
-                if (special_lo(y)) y &= 0xffff0000u;
-                if (special_hi(y)) y &= 0x0000ffffu;
-                return y;
-              };
-              v[i] = make_uint4(clean(x.x), clean(x.y), clean(x.z), clean(x.w));
+#pragma unroll
+              for (int j = 0; j < 8; ++j) v[i + 32 * j] = make_uint4(clean(x[j].x), clean(x[j].y), clean(x[j].z), clean(x[j].w));
             }
           }
           if (found) *static_cast<volatile int*>(&s_special) = 1;
@@ -347,7 +455,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ---- softmax: group a, one row per thread ----
-    regs_inc<kRegsSoftmax>();
     const int a = (warp - 4) >> 2, q4 = warp & 3;
     const int rl = q4 * 32 + lane;
     const int my_tok = rl / p.G, my_head = rl - my_tok * p.G;
@@ -356,129 +463,140 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tO = tmem + C::kColO + a * D + lane_off;
     const float grow = kRescale / p.scale_log2;
     uint32_t s_n = 0, o_n = 0;
+    int st = 0;  // stage of the item's next load to release
     bool ok = true;
-    for (int u = 0, at; ok && (at = item_index(u, total)) >= 0; ++u) {
-      const Work w = work_at(at);
-      if (w.tiles[a] == 0) continue;
+    Work w, next;
+    for (bool have = take(next); have;) {
+      w = next;
+      // Scores, or O, tell that the group's MMAs before them are done: the stages they read are released for it.
+      auto released = [&]() {
+        if (ok && lane == 0 && q4 == 0) mbar_arrive(&empty[st]);
+        st = st + 1 == kStages ? 0 : st + 1;
+      };
+      if (w.tiles[a] == 0) {
+        st = (st + 2 * w.all) % kStages;
+        have = take(next);
+        continue;
+      }
       const int first = w.tok + a * p.tg;   // the group's first row
       const int row = first + my_tok;
       float m_run = -INFINITY, l_run = 0.f;  // the maximum in the scores' own units
       for (int t = 0; t < w.tiles[a]; ++t) {
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sfull[a], s_n++ & 1, &s_abort));
-        if (!ok) break;
+        // (a warp whose wait gave up goes on to its last tile: the issuer waits for it without a limit)
+        ok = __all_sync(0xffffffffu, ok && mbar_wait_bounded(&sfull[a], s_n++ & 1, &s_abort));
+        if (!ok) s_abort = 1;
+        if (t > 0) released();  // V(t - 1)
+        released();             // K(t)
         tc_fence_after();
-        uint32_t s[4][32];
+        const bool edge = t * kKeys + kKeys - 1 > first;  // some row does not see all of the tile's keys
+        // Weights are taken by the maximum there is, the tile's own beside them (a pass less on the way from S to P); where
+        // it has grown too far, tile_again does the tile once more from the scores.
+        bool again = false;
+        if (ok) {
+          uint32_t s[4][32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld_x32(tS + c * 32, s[c]);
-        tmem_ld_wait();
-        if (t * kKeys + kKeys - 1 > first) {  // keys behind a row's own: out
-          const int lim = row - t * kKeys;
+          for (int c = 0; c < 4; ++c) tmem_ld_x32(tS + c * 32, s[c]);
+          tmem_ld_wait_for(s);
+          if (edge) {
+            const int lim = row - t * kKeys;
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+            for (int c = 0; c < 4; ++c)
+              if (__any_sync(0xffffffffu, lim < c * 32 + 31)) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (c * 32 + j > lim) s[c][j] = 0xff800000u;
-        }
-        float mx[4];
+                for (int j = 0; j < 32; ++j)
+                  if (c * 32 + j > lim) s[c][j] = 0xff800000u;
+              }
+          }
+          if (t == 0) {
+            float first_mx[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          mx[c] = __uint_as_float(s[c][0]);
+            for (int c = 0; c < 4; ++c) {
+              first_mx[c] = -INFINITY;
 #pragma unroll
-          for (int j = 1; j < 32; ++j) mx[c] = fmaxf(mx[c], __uint_as_float(s[c][j]));
-        }
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        const bool need = top > m_run + grow;  // the first finite maximum among them
-        if (__any_sync(0xffffffffu, need)) {
-          const float f = need ? exp2f((m_run - top) * p.scale_log2) : 1.f;
-          if (t > 0) {  // O is complete up to the tile before: the commit behind these scores says so
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld_x32(tO + c * 32, o);
-              tmem_ld_wait();
-#pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-              tmem_st_x32(tO + c * 32, o);
+              for (int j = 0; j < 32; j += 2)
+                first_mx[c] = max3(first_mx[c], __uint_as_float(s[c][j]), __uint_as_float(s[c][j + 1]));
             }
+            m_run = max3(fmaxf(first_mx[0], first_mx[1]), first_mx[2], first_mx[3]);
           }
-          if (need) {
-            l_run *= f;
-            m_run = top;
-          }
-        }
-        const float ref = m_run == -INFINITY ? 0.f : m_run;
-        const float2 sc = make_float2(p.scale_log2, p.scale_log2);
-        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        float shift = ref * p.scale_log2;
-        if (__any_sync(0xffffffffu, fabsf(shift) >= kExact)) {
-          // the rounding of this product would reach into the exponents: such rows take differences ahead of the scale
-          const bool far = fabsf(shift) >= kExact;
-          const float r = far ? ref : 0.f;
-          shift = far ? 0.f : shift;
+          const float shift = (m_run == -INFINITY ? 0.f : m_run) * p.scale_log2;
+          const float2 sc = make_float2(p.scale_log2, p.scale_log2), off = make_float2(-shift, -shift);
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          float mx[2] = {-INFINITY, -INFINITY};
+          uint32_t pk[2][32];
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int j = 0; j < 32; ++j) s[c][j] = __float_as_uint(__uint_as_float(s[c][j]) - r);
-        }
-        const float2 off = make_float2(-shift, -shift);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[c][j]), __uint_as_float(s[c][j + 1])), sc, off);
+          for (int j = 0; j < kKeys; j += 2) {
+            const float s0 = __uint_as_float(s[j / 32][j % 32]), s1 = __uint_as_float(s[j / 32][j % 32 + 1]);
+            const float2 x = __ffma2_rn(make_float2(s0, s1), sc, off);
+            mx[(j >> 1) & 1] = max3(mx[(j >> 1) & 1], s0, s1);
             const float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
             sum[(j >> 1) & 1] = __fadd2_rn(sum[(j >> 1) & 1], make_float2(p0, p1));
-            pk[j / 2] = pack_bf16x2(p0, p1);
+            pk[j / 64][j % 64 / 2] = pack_bf16x2(p0, p1);
           }
-          tmem_st_x16(tS + c * 16, pk);
+          again = __any_sync(0xffffffffu, fmaxf(mx[0], mx[1]) > m_run + grow || fabsf(shift) >= kExact);
+          if (!again) {
+            l_run += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
+            tmem_st_x32(tS, pk[0]);
+            tmem_st_x32(tS + 32, pk[1]);
+            tmem_st_wait();
+          }
         }
-        l_run += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
-        tmem_st_wait();
+        if (ok && again) {
+          const float2 ml = tile_again<D>(tS, tO, edge ? row - t * kKeys : kKeys, t > 0, make_float2(m_run, l_run), p.scale_log2);
+          m_run = ml.x;
+          l_run = ml.y;
+        }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&pfull[a]);
+        named_arrive(kBarP + a, 160);
       }
-      ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(&ofull[a], o_n++ & 1, &s_abort));
-      if (!ok) break;
+      have = take(next);
+      ok = __all_sync(0xffffffffu, ok && mbar_wait_bounded(&ofull[a], o_n++ & 1, &s_abort));
+      if (!ok) s_abort = 1;
+      released();
+      st = (st + 2 * (w.all - w.tiles[a])) % kStages;  // (a group with fewer tiles than the item)
+      if (!ok) continue;
       tc_fence_after();
       const bool valid = rl < p.tg * p.G && row < w.n;
-      const size_t orow = valid ? (size_t)(w.r0 + row) * p.Hq + w.g * p.G + my_head : 0;
+      const size_t out0 = (size_t)(w.r0 + first) * p.Hq + w.g * p.G;   // of [n_rows][Hq]
+      const uint32_t out_row = valid ? (uint32_t)my_tok * p.Hq + my_head : kNoRow;
       const float inv = l_run > 0.f ? 1.f / l_run : (l_run == 0.f ? 0.f : l_run);  // (a NaN sum stays NaN)
-      uint32_t o[D / 32][32];
+      const bool special = *static_cast<volatile int*>(&s_special) != 0;
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        tmem_ld_x32(tO + c * 32, o);
+        tmem_ld_wait();
+        if (c == D / 32 - 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ofree[a]);
+        }
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) tmem_ld_x32(tO + c * 32, o[c]);
-      tmem_ld_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ofree[a]);
-      if (valid) {
-        uint4* dst = reinterpret_cast<uint4*>(p.out + orow * D);
-        const bool special = *static_cast<volatile int*>(&s_special) != 0;
+        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * inv);
+        if (special && valid) {
+          // V's infinities and NaN that the guard has taken out, of the keys this row sees
+          for (int key = w.edge * kKeys; key <= row; ++key) {
+            const uint16_t* v = p.v + (size_t)(w.r0 + key) * p.v_stride + (size_t)w.g * D + c * 32;
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) o[c][j] = __float_as_uint(__uint_as_float(o[c][j]) * inv);
-          if (special) {
-            // V's infinities and NaN that the guard has taken out, of the keys this row sees
-            for (int key = w.edge * kKeys; key <= row; ++key) {
-              const uint16_t* v = p.v + (size_t)(w.r0 + key) * p.v_stride + (size_t)w.g * D + c * 32;
-#pragma unroll
-              for (int j = 0; j < 32; ++j) {
-                const uint32_t x = (uint32_t)v[j] << 16;
-                if (special_hi(x)) o[c][j] = __float_as_uint(__uint_as_float(o[c][j]) + __uint_as_float(x));
-              }
+            for (int j = 0; j < 32; ++j) {
+              const uint32_t x = (uint32_t)v[j] << 16;
+              if (specials(x)) o[j] = __float_as_uint(__uint_as_float(o[j]) + __uint_as_float(x));
             }
           }
-#pragma unroll
-          for (int j = 0; j < 32; j += 8)
-            dst[c * 4 + j / 8] = make_uint4(pack_bf16x2(__uint_as_float(o[c][j]), __uint_as_float(o[c][j + 1])),
-                                            pack_bf16x2(__uint_as_float(o[c][j + 2]), __uint_as_float(o[c][j + 3])),
-                                            pack_bf16x2(__uint_as_float(o[c][j + 4]), __uint_as_float(o[c][j + 5])),
-                                            pack_bf16x2(__uint_as_float(o[c][j + 6]), __uint_as_float(o[c][j + 7])));
         }
-        if (p.lse) p.lse[orow] = m_run * p.scale + logf(l_run);
+        // 64 bytes of a row per thread; four threads swap theirs, so that a store writes 64 bytes of eight rows, not 16 of 32
+        uint32_t y[4][4];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) y[j / 4][j % 4] = pack_bf16x2(__uint_as_float(o[2 * j]), __uint_as_float(o[2 * j + 1]));
+        transpose4(y, lane);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t to = __shfl_sync(0xffffffffu, out_row, (lane & ~3) + j);
+          if (to != kNoRow)
+            reinterpret_cast<uint4*>(p.out + (out0 + to) * D + c * 32)[lane & 3] = make_uint4(y[j][0], y[j][1], y[j][2], y[j][3]);
+        }
       }
+      if (valid && p.lse) p.lse[out0 + out_row] = m_run * p.scale + logf(l_run);
     }
     if (!ok && lane == 0) {
       s_abort = 1;
@@ -493,11 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D>
 static cudaError_t launch_as(const CUtensorMap* tmQ, const CUtensorMap* tmK, const CUtensorMap* tmV,
                              const PromptAttnParams& p, int grid, cudaStream_t stream) {
-  cudaFuncAttributes at;
-  cudaError_t err = cudaFuncGetAttributes(&at, prompt_attn_kernel<D>);
-  if (err != cudaSuccess) return err;
-  if (at.numRegs != kRegsLaunch) return cudaErrorInvalidKernelImage;  // the shares above are of this many
-  err = cudaFuncSetAttribute(prompt_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, PromptCfg<D>::kSmem);
+  cudaError_t err = cudaFuncSetAttribute(prompt_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, PromptCfg<D>::kSmem);
   if (err != cudaSuccess) return err;
   return launch_dependent(prompt_attn_kernel<D>, dim3(grid), dim3(kThreads), PromptCfg<D>::kSmem, stream, *tmQ, *tmK, *tmV, p);
 }
