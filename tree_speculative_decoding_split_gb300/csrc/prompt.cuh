@@ -55,15 +55,50 @@ struct PlanParams {
 inline long long plan_items(long long n_rows, int B, int step) { return n_rows / step + (B < n_rows ? B : n_rows); }
 cudaError_t launch_prompt_plan(const PlanParams& p, cudaStream_t stream);
 
+// What a kernel reads of its plan.  A single request needs no list (items == nullptr): its pieces follow from row_start,
+// those with the most keys first, and 3 us of another kernel ahead are saved.
+struct PlanView {
+  const PromptItem* items;
+  const int32_t* count;
+  const int32_t* row_start;
+  long long n_rows;
+  int step;
+};
+struct PlanReader {
+  const PlanView& v;
+  int count, r0, n;
+  __device__ __forceinline__ PlanReader(const PlanView& view, int32_t* dev_status) : v(view) {
+    r0 = n = 0;
+    if (v.items) {
+      count = v.count[0];
+    } else {
+      r0 = v.row_start[0];
+      n = v.row_start[1] - r0;
+      const bool ok = r0 >= 0 && v.row_start[1] >= r0 && v.row_start[1] <= v.n_rows;
+      if (!ok && blockIdx.x == 0 && threadIdx.x == 0) set_status(dev_status, SPEC_ERR_CAPACITY);
+      count = ok ? (int)(((long long)n + v.step - 1) / v.step) : 0;
+    }
+  }
+  __device__ __forceinline__ PromptItem item(int i) const {
+    if (v.items) return v.items[i];
+    PromptItem it;
+    it.r0 = r0;
+    it.n = n;
+    it.tok = (count - 1 - i) * v.step;
+    it.pad = 0;
+    return it;
+  }
+};
+
 // ---- K11: causal attention over packed prompts --------------------------------------------------
 struct PromptAttnParams {
   int Hq, Hkv, G, tg;       // tg: rows of a request per 128-row group (128 / G)
   float scale, scale_log2;
-  const PromptItem* items;
-  const int32_t* count;
+  PlanView plan;
   const uint16_t* v;        // for keys with infinities
   long long v_stride;
   uint16_t* out;            // [n_rows][Hq][d]
+  bool out32;               // rows of out begin on 32 bytes
   float* lse;               // [n_rows][Hq] or nullptr
   int32_t* dev_status;
 };
@@ -77,8 +112,7 @@ struct KeyWeightsParams {
   int window;
   float scale_log2;
   long long n_rows;
-  const PromptItem* items;
-  const int32_t* count;
+  PlanView plan;
   const float* lse;         // [n_rows][Hq]
   float* weight;            // [Hkv][n_rows]
   int32_t* dev_status;

@@ -137,8 +137,16 @@ bool make_map_heads(CUtensorMap* m, const void* x, int d, int H, long long n_row
 
 float scale_of(float scale, int d) { return scale > 0.f ? scale : 1.f / std::sqrt((float)d); }
 
-spec_status plan(long long n_rows, int B, int step, int by_work, const int32_t* row_start, const PlanLayout& l,
+// Launches the plan where the call needs one (n_rows 0: its checks alone) and says where the kernel finds it.
+spec_status plan(long long n_rows, int B, int step, int by_work, const int32_t* row_start, const PlanLayout& l, PlanView* view,
                  int32_t* dev_status, cudaStream_t stream) {
+  const bool list = B > 1 || n_rows == 0;
+  view->items = list ? l.items : nullptr;
+  view->count = l.count;
+  view->row_start = row_start;
+  view->n_rows = n_rows;
+  view->step = step;
+  if (!list) return SPEC_OK;
   PlanParams p;
   p.B = B; p.step = step; p.by_work = by_work; p.n_rows = n_rows; p.row_start = row_start;
   p.items = l.items; p.count = l.count; p.dev_status = dev_status;
@@ -234,16 +242,16 @@ spec_status spec_prompt_attention(const spec_prompt_attn_args* a, void* workspac
   p.Hq = a->num_q_heads; p.Hkv = a->num_kv_heads; p.G = p.Hq / p.Hkv; p.tg = step / 2;
   p.scale = scale_of(a->scale, a->head_dim);
   p.scale_log2 = p.scale * 1.4426950408889634f;
-  p.items = l.items; p.count = l.count;
   p.v = static_cast<const uint16_t*>(a->v); p.v_stride = a->v_stride;
-  p.out = static_cast<uint16_t*>(a->out); p.lse = a->lse; p.dev_status = dev_status;
+  p.out = static_cast<uint16_t*>(a->out); p.out32 = (reinterpret_cast<uintptr_t>(a->out) & 31u) == 0;
+  p.lse = a->lse; p.dev_status = dev_status;
   CUtensorMap tm[3];
   if (a->n_rows > 0 &&
       (!make_map_heads(&tm[0], a->q, a->head_dim, p.Hq, a->n_rows, a->q_stride, p.G, p.tg) ||
        !make_map_heads(&tm[1], a->k, a->head_dim, p.Hkv, a->n_rows, a->k_stride, 1, 128) ||
        !make_map_heads(&tm[2], a->v, a->head_dim, p.Hkv, a->n_rows, a->v_stride, 1, 128)))
     return SPEC_ERR_CUDA;
-  const spec_status ps = plan(a->n_rows, a->batch, step, 1, a->row_start, l, dev_status, stream);
+  const spec_status ps = plan(a->n_rows, a->batch, step, 1, a->row_start, l, &p.plan, dev_status, stream);
   if (ps != SPEC_OK || a->n_rows == 0) return ps;
   const int grid = grid_for(plan_items(a->n_rows, a->batch, step), p.Hkv);
   return launch_prompt_attention(a->head_dim, &tm[0], &tm[1], &tm[2], p, grid, stream) == cudaSuccess ? SPEC_OK
@@ -266,12 +274,12 @@ spec_status spec_prompt_key_weights(const spec_key_weights_args* a, void* worksp
   KeyWeightsParams p;
   p.Hq = a->num_q_heads; p.Hkv = a->num_kv_heads; p.G = p.Hq / p.Hkv; p.tc = 128 / p.G; p.window = a->window;
   p.scale_log2 = scale_of(a->scale, a->head_dim) * 1.4426950408889634f;
-  p.n_rows = a->n_rows; p.items = l.items; p.count = l.count; p.lse = a->lse; p.weight = a->weight; p.dev_status = dev_status;
+  p.n_rows = a->n_rows; p.lse = a->lse; p.weight = a->weight; p.dev_status = dev_status;
   CUtensorMap tm[2];
   if (a->n_rows > 0 && (!make_map_heads(&tm[0], a->q, a->head_dim, p.Hq, a->n_rows, a->q_stride, p.G, p.tc) ||
                         !make_map_heads(&tm[1], a->k, a->head_dim, p.Hkv, a->n_rows, a->k_stride, 1, 128)))
     return SPEC_ERR_CUDA;
-  const spec_status ps = plan(a->n_rows, a->batch, kWeightKeys, 0, a->row_start, l, dev_status, stream);
+  const spec_status ps = plan(a->n_rows, a->batch, kWeightKeys, 0, a->row_start, l, &p.plan, dev_status, stream);
   if (ps != SPEC_OK || a->n_rows == 0) return ps;
   const int grid = grid_for(plan_items(a->n_rows, a->batch, kWeightKeys), p.Hkv);
   return launch_key_weights(a->head_dim, &tm[0], &tm[1], p, grid, stream) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;

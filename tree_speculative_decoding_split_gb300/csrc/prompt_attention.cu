@@ -14,16 +14,24 @@
 //
 // Roles (12 warps):
 //   warp 0      TMA: Q of each group, then K and V tiles of 128 keys through one ring of 32 KB stages
-//   warp 1      MMA issuer of both groups.  Per tile and group: O += P V, then S of the next tile, one behind
-//               the other: tensor instructions of one thread run in order, so the next S may overwrite the
-//               scores that P lies on, and a commit behind S also tells that P V is done.
-//   warps 2, 3  guard: in tiles that hold keys some row does not see (the causal edge, the end of a request) V's
+//   warps 1, 2  MMA issuers, one for each group, in turns.  A turn is O += P V of a tile and S of the next one, one
+//               behind the other: tensor instructions of one thread run in order, so the next S may overwrite the
+//               scores that P lies on, and the commit behind S also tells that P V is done.  The tensor cores queue
+//               little, so whatever an issuer waits for, it waits for during the other's turn.
+//   warp 3      guard: in tiles that hold keys some row does not see (the causal edge, the end of a request) V's
 //               infinities and NaN are set to 0, since 0 * inf would reach rows that do not see them; the rows that do
 //               see them get them back at the end.  Scores of unseen keys are replaced, so K needs no guard.
-//   warps 4-11  softmax, four warps per group, one row per thread: scores from tensor memory, running
-//               maximum, P as bf16 over the scores' own columns.  O is rescaled only when a maximum has grown by more
-//               than 2^8 (P and the sum use the same stale one); its row leaves through the same thread at the end.
+//   warps 4-11  softmax, four warps per group, one row per thread: scores from tensor memory, P as bf16 over the scores'
+//               own columns.  O is rescaled only where a maximum has grown by more than 2^8 (P and the sum use the same
+//               older one); its row leaves through the same thread at the end.
+// P's completion and the turns go through named barriers, which wait without a limit: the tensor cores' reading slows
+// every access to shared memory, mbarriers included, to some 180 cycles (3250 cycles a tile of both groups against
+// 2900).  So a warp whose other waits gave up does no more work but meets these barriers up to its last item.
 // Tensor memory: 2 x (S 128 + O d) columns.
+//
+// What bounds it: a tile of both groups is 2048 cycles of MMA at d 128 and takes 2750; the rest is the way from S to P and
+// back (1000 cycles of softmax, 600 of hand-offs), which two groups do not hide in full and for more tensor memory is
+// too small.  16384 rows of 64 heads on 8: 2742 us, 1604 TFLOP/s.  At d 64 the MMAs halve and that way does not.
 
 #include "pdl.cuh"
 #include "prompt.cuh"
@@ -38,6 +46,7 @@ constexpr int kRows = 128;        // rows per group
 constexpr int kThreads = 384;
 constexpr int kBarTurn = 1, kBarP = 3;  // named barriers: an issuer's turn, a group's P written
 constexpr float kRescale = 8.f;   // log2
+constexpr float kGrown = 32768.f; // a row's sum over a tile from which its reference is looked over
 constexpr float kExact = 262144.f;  // 2^18: maxima from here on, in log2 units, take differences ahead of the scale
 
 template <int D>
@@ -153,26 +162,19 @@ __device__ __forceinline__ uint32_t clean(uint32_t w) {
   return w & ~((bad & 0x80000000u ? 0xffff0000u : 0u) | (bad & 0x8000u ? 0xffffu : 0u));
 }
 
-// Of four threads, each with four pieces: thread i's piece j becomes thread j's piece i.
-__device__ __forceinline__ void transpose4(uint32_t (&y)[4][4], int lane) {
+// 64 bytes of a row: in whole 32-byte sectors where the rows begin on one.
+__device__ __forceinline__ void store_64(uint16_t* dst, const uint32_t (&y)[16], bool sectors) {
+  if (sectors) {
 #pragma unroll
-  for (int step = 1; step < 4; step <<= 1) {
-    const bool up = lane & step;
+    for (int j = 0; j < 16; j += 8)
+      asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst + 2 * j), "r"(y[j]), "r"(y[j + 1]),
+                   "r"(y[j + 2]), "r"(y[j + 3]), "r"(y[j + 4]), "r"(y[j + 5]), "r"(y[j + 6]), "r"(y[j + 7])
+                   : "memory");
+  } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (i & step) continue;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? y[i][e] : y[i | step][e], step);
-        if (up)
-          y[i][e] = got;
-        else
-          y[i | step][e] = got;
-      }
-    }
+    for (int j = 0; j < 16; j += 4) *reinterpret_cast<uint4*>(dst + 2 * j) = make_uint4(y[j], y[j + 1], y[j + 2], y[j + 3]);
   }
 }
-constexpr uint32_t kNoRow = 0xffffffffu;
 
 // An item as every role sees it.
 struct Work {
@@ -259,15 +261,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   pdl_wait();  // the plan
-  const int total = p.count[0] * p.Hkv;
+  const PlanReader plan(p.plan, p.dev_status);
+  const int total = plan.count * p.Hkv;
   // This CTA's items one by one, the next one's entry fetched while the current one is under way.
   int u = 0, at = item_index(0, total);
-  PromptItem entry = at >= 0 ? p.items[at / p.Hkv] : PromptItem{};
+  PromptItem entry = at >= 0 ? plan.item(at / p.Hkv) : PromptItem{};
   auto take = [&](Work& w) -> bool {
     if (at < 0) return false;
     w = work_of(p, entry, at % p.Hkv);
     at = item_index(++u, total);
-    if (at >= 0) entry = p.items[at / p.Hkv];
+    if (at >= 0) entry = plan.item(at / p.Hkv);
     return true;
   };
 
@@ -461,7 +464,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
     const uint32_t tS = tmem + C::kColS + a * kKeys + lane_off;
     const uint32_t tO = tmem + C::kColO + a * D + lane_off;
-    const float grow = kRescale / p.scale_log2;
     uint32_t s_n = 0, o_n = 0;
     int st = 0;  // stage of the item's next load to release
     bool ok = true;
@@ -489,8 +491,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         released();             // K(t)
         tc_fence_after();
         const bool edge = t * kKeys + kKeys - 1 > first;  // some row does not see all of the tile's keys
-        // Weights are taken by the maximum there is, the tile's own beside them (a pass less on the way from S to P); where
-        // it has grown too far, tile_again does the tile once more from the scores.
+        // Weights are taken by the reference there is, the first tile's maximum at first.  Their sum tells where scores have
+        // outgrown it (128 weights of up to 2^8 stay below 2^15, and what overflows shows as well): tile_again then does the
+        // tile once more, by its maximum.  No other tile needs one, which is a pass less on the way from S to P.
         bool again = false;
         if (ok) {
           uint32_t s[4][32];
@@ -521,20 +524,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float shift = (m_run == -INFINITY ? 0.f : m_run) * p.scale_log2;
           const float2 sc = make_float2(p.scale_log2, p.scale_log2), off = make_float2(-shift, -shift);
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          float mx[2] = {-INFINITY, -INFINITY};
           uint32_t pk[2][32];
 #pragma unroll
           for (int j = 0; j < kKeys; j += 2) {
             const float s0 = __uint_as_float(s[j / 32][j % 32]), s1 = __uint_as_float(s[j / 32][j % 32 + 1]);
             const float2 x = __ffma2_rn(make_float2(s0, s1), sc, off);
-            mx[(j >> 1) & 1] = max3(mx[(j >> 1) & 1], s0, s1);
             const float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
             sum[(j >> 1) & 1] = __fadd2_rn(sum[(j >> 1) & 1], make_float2(p0, p1));
             pk[j / 64][j % 64 / 2] = pack_bf16x2(p0, p1);
           }
-          again = __any_sync(0xffffffffu, fmaxf(mx[0], mx[1]) > m_run + grow || fabsf(shift) >= kExact);
+          const float part = (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
+          again = __any_sync(0xffffffffu, part > kGrown || fabsf(shift) >= kExact);
           if (!again) {
-            l_run += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
+            l_run += part;
             tmem_st_x32(tS, pk[0]);
             tmem_st_x32(tS + 32, pk[1]);
             tmem_st_wait();
@@ -557,8 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) continue;
       tc_fence_after();
       const bool valid = rl < p.tg * p.G && row < w.n;
-      const size_t out0 = (size_t)(w.r0 + first) * p.Hq + w.g * p.G;   // of [n_rows][Hq]
-      const uint32_t out_row = valid ? (uint32_t)my_tok * p.Hq + my_head : kNoRow;
+      const size_t orow = valid ? (size_t)(w.r0 + row) * p.Hq + w.g * p.G + my_head : 0;
       const float inv = l_run > 0.f ? 1.f / l_run : (l_run == 0.f ? 0.f : l_run);  // (a NaN sum stays NaN)
       const bool special = *static_cast<volatile int*>(&s_special) != 0;
 #pragma unroll 1
@@ -584,19 +585,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        // 64 bytes of a row per thread; four threads swap theirs, so that a store writes 64 bytes of eight rows, not 16 of 32
-        uint32_t y[4][4];
+        if (valid) {
+          uint32_t y[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) y[j / 4][j % 4] = pack_bf16x2(__uint_as_float(o[2 * j]), __uint_as_float(o[2 * j + 1]));
-        transpose4(y, lane);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t to = __shfl_sync(0xffffffffu, out_row, (lane & ~3) + j);
-          if (to != kNoRow)
-            reinterpret_cast<uint4*>(p.out + (out0 + to) * D + c * 32)[lane & 3] = make_uint4(y[j][0], y[j][1], y[j][2], y[j][3]);
+          for (int j = 0; j < 16; ++j) y[j] = pack_bf16x2(__uint_as_float(o[2 * j]), __uint_as_float(o[2 * j + 1]));
+          store_64(p.out + orow * D + c * 32, y, p.out32);
         }
       }
-      if (valid && p.lse) p.lse[out0 + out_row] = m_run * p.scale + logf(l_run);
+      if (valid && p.lse) p.lse[orow] = m_run * p.scale + logf(l_run);
     }
     if (!ok && lane == 0) {
       s_abort = 1;

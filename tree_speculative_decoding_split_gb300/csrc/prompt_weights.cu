@@ -40,8 +40,8 @@ struct Work {
   int groups;
 };
 
-__device__ __forceinline__ Work work_of(const KeyWeightsParams& p, int at) {
-  const PromptItem it = p.items[at / p.Hkv];
+__device__ __forceinline__ Work work_of(const KeyWeightsParams& p, const PlanReader& plan, int at) {
+  const PromptItem it = plan.item(at / p.Hkv);
   Work w;
   w.r0 = it.r0;
   w.n = it.n;
@@ -107,7 +107,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   pdl_wait();  // the plan
-  const int total = p.count[0] * p.Hkv;
+  const PlanReader plan(p.plan, p.dev_status);
+  const int total = plan.count * p.Hkv;
 
   if (warp == 0) {
     // ---- TMA producer ----
@@ -115,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t k_n = 0, q_n = 0;
       bool ok = true;
       for (int at = blockIdx.x; ok && at < total; at += gridDim.x) {
-        const Work w = work_of(p, at);
+        const Work w = work_of(p, plan, at);
         const int ks = k_n % kKSlots;
         ok = mbar_wait_bounded(&kempty[ks], ((k_n / kKSlots) & 1) ^ 1, &s_abort);
         if (!ok) break;
@@ -157,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t k_n = 0, q_n = 0, s_n[2] = {0, 0};
       bool ok = true;
       for (int at = blockIdx.x; ok && at < total; at += gridDim.x) {
-        const Work w = work_of(p, at);
+        const Work w = work_of(p, plan, at);
         const int ks = k_n % kKSlots;
         ok = mbar_wait_bounded(&kfull[ks], (k_n / kKSlots) & 1, &s_abort);
         const int chunks[2] = {chunks_of(p, w, 0), chunks_of(p, w, 1)};
@@ -203,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     // A warp whose wait gave up goes on with its group's barriers to the last item: no wait takes long any more.
     for (int at = blockIdx.x; at < total; at += gridDim.x) {
-      const Work w = work_of(p, at);
+      const Work w = work_of(p, plan, at);
       const int chunks = chunks_of(p, w, a);
       if (chunks == 0) continue;
       const int key = w.key + a * kKeys + kl, last_key = w.key + a * kKeys + kKeys - 1;
