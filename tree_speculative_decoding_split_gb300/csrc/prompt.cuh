@@ -106,7 +106,8 @@ cudaError_t launch_prompt_attention(int d, const CUtensorMap* tmQ, const CUtenso
                                     const PromptAttnParams& p, int grid, cudaStream_t stream);
 
 // ---- K12: key weights -----------------------------------------------------------------------------
-constexpr int kWeightKeys = 256;  // keys per item
+// Keys per item.
+int key_weights_step(long long n_rows, int Hkv, int num_sms);
 struct KeyWeightsParams {
   int Hq, Hkv, G, tc;       // tc: rows of the window per chunk (128 / G)
   int window;

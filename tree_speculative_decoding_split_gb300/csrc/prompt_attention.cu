@@ -63,9 +63,6 @@ __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, int* abor
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* abort) {
   return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort);
 }
-// A 128-byte-swizzle K-major operand's descriptor, the address apart: base plus (address >> 4) in the lower word.
-constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
-__device__ __forceinline__ uint64_t desc(uint32_t lo) { return ((uint64_t)kDescHi << 32) | lo; }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -363,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = (kk >> 2) * ((kKeys * 128) >> 4) + (kk & 3) * 2;
-          umma_bf16(tS, desc(q_lo + off), desc(k_lo + off), idS, kk > 0);
+          umma_bf16(tS, desc_sw128(q_lo + off), desc_sw128(k_lo + off), idS, kk > 0);
         }
       };
       if (a == 1) named_arrive(kBarTurn, 64);  // group 0 begins
@@ -397,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t v_lo = (kv_lo + v * (C::kTile >> 4)) | v_mn;
 #pragma unroll
             for (int kk = 0; kk < kKeys / 16; ++kk)
-              umma_bf16_tmem_a(tO, tS + kk * 8, desc(v_lo + kk * (2048 >> 4)), idP, (t > 0 || kk > 0) ? 1u : 0u);
+              umma_bf16_tmem_a(tO, tS + kk * 8, desc_sw128(v_lo + kk * (2048 >> 4)), idP, (t > 0 || kk > 0) ? 1u : 0u);
             if (t + 1 < tiles) scores(k);
             umma_commit(t + 1 < tiles ? &sfull[a] : &ofull[a]);
             if (t + 2 == tiles) umma_commit(&qempty[a]);

@@ -6,13 +6,16 @@
 // over the queries is one thread's walk along its own row of tensor memory: no reduction between threads, no
 // atomics, one order of terms.
 //
-// An item is 256 keys of one request and KV head, as two groups of 128 (the M of an MMA); the window's rows times
-// the G heads come past them in chunks of tc = 128 / G rows (N).  K is read once; Q chunks come from L2.  2 d
-// operations per pair against 2 d bytes per key: a window of 64 rows with 4 heads a group is where HBM and the
-// exponentials take equally long.
+// An item is a stretch of one request's keys for one KV head, in tiles of 128 keys (the M of an MMA).  The window's
+// rows times the G heads are the columns (N), in chunks of tc = 128 / G rows, up to three of which stay in shared
+// memory with their lse while the stretch's keys stream past.  Longer windows take several such passes over a
+// stretch (its keys come from L2 then), the later ones adding to what the earlier ones wrote.  K is read once, 2 d
+// bytes for 2 d operations a column: a window of 64 rows with 4 heads a group is where HBM, MMA and exponentials
+// (512 cycles for 128 x 128 of each) take equally long.
 //
-// Roles (10 warps): warp 0 TMA (two slots of 256 keys, three of a Q chunk), warp 1 MMA issuer, warps 2-9 sums, four per
-// group, each group with two score buffers of 128 columns, so that the products run while sums are taken.
+// Roles (12 warps): warp 0 TMA (a ring of key tiles, three slots of query chunks), warp 3 the chunks' lse, warps 4-11 sums:
+// two groups of four warps take every other key tile, each with two score buffers of 128 columns, so that products run
+// while sums are taken; warps 1 and 2 issue their MMAs.
 
 #include "pdl.cuh"
 #include "prompt.cuh"
@@ -22,22 +25,23 @@ namespace spectree {
 
 namespace {
 
-constexpr int kKeys = 128;   // keys per group
-constexpr int kCols = 128;   // query rows per chunk
-constexpr int kThreads = 320;
-constexpr int kKSlots = 2, kQSlots = 3;
+constexpr int kKeys = 128;   // keys per tile
+constexpr int kCols = 128;   // columns per chunk at most
+constexpr int kThreads = 384;
+constexpr int kKSlots = 4, kQSlots = 3;
 
 template <int D>
 struct WeightCfg {
-  static constexpr int kK = kKeys * D * 2;   // a group's keys
+  static constexpr int kK = kKeys * D * 2;
   static constexpr int kQ = kCols * D * 2;
-  static constexpr int kSmem = 1024 + kKSlots * 2 * kK + kQSlots * kQ;
+  static constexpr int kSmem = 1024 + kKSlots * kK + kQSlots * kQ;
 };
 
 struct Work {
-  int r0, n, key, g;  // first key of the item
-  int q0, chunks;     // the window's first row and its chunks
-  int groups;
+  int r0, n, key, g;   // first key
+  int tiles;
+  int q0, chunks;      // the window's first row and its chunks
+  int passes, per;     // passes over the keys, chunks of a pass
 };
 
 __device__ __forceinline__ Work work_of(const KeyWeightsParams& p, const PlanReader& plan, int at) {
@@ -47,20 +51,30 @@ __device__ __forceinline__ Work work_of(const KeyWeightsParams& p, const PlanRea
   w.n = it.n;
   w.key = it.tok;
   w.g = at % p.Hkv;
+  const int keys = it.n - it.tok < p.plan.step ? it.n - it.tok : p.plan.step;
+  w.tiles = (keys + kKeys - 1) / kKeys;
   w.q0 = it.n > p.window ? it.n - p.window : 0;
   w.chunks = (it.n - w.q0 + p.tc - 1) / p.tc;
-  w.groups = it.n - it.tok > kKeys ? 2 : 1;
+  w.passes = (w.chunks + kQSlots - 1) / kQSlots;
+  w.per = (w.chunks + w.passes - 1) / w.passes;
   return w;
 }
-// Chunks are taken from the window's end; those that no key of a group is visible to are left out, which are the last.
-__device__ __forceinline__ int chunk_row(const KeyWeightsParams& p, const Work& w, int c) {
-  return w.q0 + (w.chunks - 1 - c) * p.tc;
+// The pass's chunks that some key of tile `i` is visible to: [first, end).  Later tiles need fewer of them.
+struct Chunks {
+  int first, end;
+};
+__device__ __forceinline__ Chunks chunks_of(const KeyWeightsParams& p, const Work& w, int pass, int i) {
+  const int key = w.key + i * kKeys;
+  const int first = key > w.q0 ? (key - w.q0) / p.tc : 0;  // the chunk of the first row that sees the tile's first key
+  Chunks c;
+  c.first = first > pass * w.per ? first : pass * w.per;
+  c.end = (pass + 1) * w.per < w.chunks ? (pass + 1) * w.per : w.chunks;
+  return c;
 }
-__device__ __forceinline__ int chunks_of(const KeyWeightsParams& p, const Work& w, int a) {
-  if (a >= w.groups) return 0;
-  const int first = w.key + a * kKeys;             // the group's first key: rows before it see none of them
-  const int skip = first > w.q0 ? (first - w.q0) / p.tc : 0;
-  return w.chunks - skip;                          // (first < n, so one chunk at least is left)
+// Rows of chunk c in the window.
+__device__ __forceinline__ int chunk_rows(const KeyWeightsParams& p, const Work& w, int c) {
+  const int left = w.n - w.q0 - c * p.tc;
+  return left < p.tc ? left : p.tc;
 }
 
 }  // namespace
@@ -71,12 +85,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = WeightCfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sK = base;                          // [slot][group][d / 64][128 keys][128 B]
-  uint8_t* sQ = base + kKSlots * 2 * C::kK;    // [slot][d / 64][128 rows][128 B]
+  uint8_t* sK = base;                      // [slot][d / 64][128 keys][128 B]
+  uint8_t* sQ = base + kKSlots * C::kK;    // [slot][d / 64][128 rows][128 B]
   __shared__ uint64_t kfull[kKSlots], kempty[kKSlots], qfull[kQSlots], qempty[kQSlots];
-  __shared__ uint64_t sfull[4], sfree[4];      // [group][buffer]
-  __shared__ uint64_t drained;
-  __shared__ __align__(16) float s_lse[2][kCols];  // [group]: log2(e) lse of the chunk's columns, +inf behind the window
+  __shared__ uint64_t sfull[4], sfree[4];  // [group][buffer]
+  __shared__ uint64_t lfull, lfree;        // the pass's lse written, read
+  __shared__ uint64_t drained[2];
+  __shared__ __align__(16) float s_lse[kQSlots][kCols];  // log2(e) lse, +inf behind the window
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
 
@@ -88,13 +103,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < kQSlots; ++s) {
       mbar_init(&qfull[s], 1);
-      mbar_init(&qempty[s], 1);
+      mbar_init(&qempty[s], 2);
     }
     for (int s = 0; s < 4; ++s) {
       mbar_init(&sfull[s], 1);
       mbar_init(&sfree[s], 4);
     }
-    mbar_init(&drained, 1);
+    mbar_init(&lfull, 1);
+    mbar_init(&lfree, 8);
+    mbar_init(&drained[0], 1);
+    mbar_init(&drained[1], 1);
     s_abort = 0;
     fence_mbar_init();
   }
@@ -109,33 +127,40 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();  // the plan
   const PlanReader plan(p.plan, p.dev_status);
   const int total = plan.count * p.Hkv;
+  bool ok = true;
 
   if (warp == 0) {
     // ---- TMA producer ----
     if (lane == 0) {
-      uint32_t k_n = 0, q_n = 0;
-      bool ok = true;
+      uint32_t k_n = 0, q_n[kQSlots] = {0, 0, 0};
       for (int at = blockIdx.x; ok && at < total; at += gridDim.x) {
         const Work w = work_of(p, plan, at);
-        const int ks = k_n % kKSlots;
-        ok = mbar_wait_bounded(&kempty[ks], ((k_n / kKSlots) & 1) ^ 1, &s_abort);
-        if (!ok) break;
-        mbar_arrive_expect_tx(&kfull[ks], w.groups * C::kK);
-        for (int a = 0; a < w.groups; ++a)
+        for (int pass = 0; ok && pass < w.passes; ++pass) {
+          for (int i = 0; ok && i < w.tiles; ++i) {
+            const Chunks c = chunks_of(p, w, pass, i);
+            if (c.first >= c.end) break;  // (so do all later tiles)
+            const int ks = k_n % kKSlots;
+            ok = mbar_wait_bounded(&kempty[ks], ((k_n / kKSlots) & 1) ^ 1, &s_abort);
+            if (!ok) break;
+            mbar_arrive_expect_tx(&kfull[ks], C::kK);
 #pragma unroll
-          for (int c = 0; c < D / 64; ++c)
-            tma_load_3d(sK + (ks * 2 + a) * C::kK + c * kKeys * 128, &tmK, &kfull[ks], c * 64, w.g, w.r0 + w.key + a * kKeys);
-        ++k_n;
-        const int chunks = chunks_of(p, w, 0);  // group 0 has the earlier keys, so no fewer than group 1
-        for (int c = 0; ok && c < chunks; ++c) {
-          const int qs = q_n % kQSlots;
-          ok = mbar_wait_bounded(&qempty[qs], ((q_n / kQSlots) & 1) ^ 1, &s_abort);
-          if (!ok) break;
-          mbar_arrive_expect_tx(&qfull[qs], (D / 64) * p.tc * p.G * 128);
+            for (int h = 0; h < D / 64; ++h)
+              tma_load_3d(sK + ks * C::kK + h * kKeys * 128, &tmK, &kfull[ks], h * 64, w.g, w.r0 + w.key + i * kKeys);
+            ++k_n;
+            if (i > 0) continue;
 #pragma unroll
-          for (int h = 0; h < D / 64; ++h)
-            tma_load_3d(sQ + qs * C::kQ + h * kCols * 128, &tmQ, &qfull[qs], h * 64, w.g * p.G, w.r0 + chunk_row(p, w, c));
-          ++q_n;
+            for (int s = 0; s < kQSlots; ++s) {  // the first tile needs every chunk that any tile needs
+              const int ch = pass * w.per + s;
+              if (!ok || ch < c.first || ch >= c.end) continue;
+              ok = mbar_wait_bounded(&qempty[s], (q_n[s] & 1) ^ 1, &s_abort);
+              if (!ok) continue;
+              mbar_arrive_expect_tx(&qfull[s], (D / 64) * p.tc * p.G * 128);
+#pragma unroll
+              for (int h = 0; h < D / 64; ++h)
+                tma_load_3d(sQ + s * C::kQ + h * kCols * 128, &tmQ, &qfull[s], h * 64, w.g * p.G, w.r0 + w.q0 + ch * p.tc);
+              ++q_n[s];
+            }
+          }
         }
       }
       if (!ok) {
@@ -145,136 +170,190 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t n = (k_n + kKSlots - 1 - s) / kKSlots;
           if (n) mbar_wait_bounded(&kfull[s], (n - 1) & 1, nullptr);
         }
-        for (uint32_t s = 0; s < kQSlots; ++s) {
-          const uint32_t n = (q_n + kQSlots - 1 - s) / kQSlots;
-          if (n) mbar_wait_bounded(&qfull[s], (n - 1) & 1, nullptr);
-        }
+#pragma unroll
+        for (int s = 0; s < kQSlots; ++s)
+          if (q_n[s]) mbar_wait_bounded(&qfull[s], (q_n[s] - 1) & 1, nullptr);
       }
     }
-  } else if (warp == 1) {
-    // ---- MMA issuer ----
+  } else if (warp < 3) {
+    // ---- MMA issuer of group a (one for both would wait for one group's buffers while the other runs dry) ----
     if (lane == 0) {
-      constexpr uint32_t idS = idesc_bf16_f32(kKeys, kCols, 0);
-      uint32_t k_n = 0, q_n = 0, s_n[2] = {0, 0};
-      bool ok = true;
+      const int a = warp - 1;
+      const uint32_t k_lo0 = smem_u32(sK) >> 4, q_lo0 = smem_u32(sQ) >> 4;
+      uint32_t k_n = 0, q_n[kQSlots] = {0, 0, 0}, s_n = 0;
       for (int at = blockIdx.x; ok && at < total; at += gridDim.x) {
         const Work w = work_of(p, plan, at);
-        const int ks = k_n % kKSlots;
-        ok = mbar_wait_bounded(&kfull[ks], (k_n / kKSlots) & 1, &s_abort);
-        const int chunks[2] = {chunks_of(p, w, 0), chunks_of(p, w, 1)};
-        for (int c = 0; ok && c < chunks[0]; ++c) {
-          const int qs = q_n % kQSlots;
-          ok = mbar_wait_bounded(&qfull[qs], (q_n / kQSlots) & 1, &s_abort);
+        for (int pass = 0; ok && pass < w.passes; ++pass) {
+          const Chunks all = chunks_of(p, w, pass, 0);
+          if (all.first >= all.end) continue;
 #pragma unroll
-          for (int a = 0; a < 2; ++a) {
-            if (!ok || c >= chunks[a]) continue;
-            const int buf = a * 2 + (s_n[a] & 1);
-            ok = mbar_wait_bounded(&sfree[buf], ((s_n[a] >> 1) & 1) ^ 1, &s_abort);
-            if (!ok) continue;
-            ++s_n[a];
-            tc_fence_after();
-            const uint32_t ka = smem_u32(sK + (ks * 2 + a) * C::kK), qa = smem_u32(sQ + qs * C::kQ);
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              umma_bf16(tmem + buf * kCols, sdesc_sw128(ka + (kk >> 2) * (kKeys * 128) + (kk & 3) * 32, 0, 1024),
-                        sdesc_sw128(qa + (kk >> 2) * (kCols * 128) + (kk & 3) * 32, 0, 1024), idS, kk > 0);
-            umma_commit(&sfull[buf]);
+          for (int s = 0; s < kQSlots; ++s) {
+            const int ch = pass * w.per + s;
+            if (ch >= all.first && ch < all.end) ok = ok && mbar_wait_bounded(&qfull[s], q_n[s]++ & 1, &s_abort);
           }
-          if (!ok) break;
-          umma_commit(&qempty[qs]);
-          ++q_n;
+          for (int i = 0; ok && i < w.tiles; ++i) {
+            const Chunks c = chunks_of(p, w, pass, i);
+            if (c.first >= c.end) break;
+            const int ks = k_n % kKSlots;
+            const uint32_t k_phase = (k_n / kKSlots) & 1;
+            if ((int)(k_n++ & 1) != a) continue;   // (slots alternate as groups do: each sees every phase of its own)
+            ok = mbar_wait_bounded(&kfull[ks], k_phase, &s_abort);
+            const uint32_t k_lo = k_lo0 + ks * (C::kK >> 4);
+            for (int ch = c.first; ch < c.end; ++ch) {
+              const int buf = a * 2 + (s_n & 1);
+              ok = ok && mbar_wait_bounded(&sfree[buf], ((s_n >> 1) & 1) ^ 1, &s_abort);
+              if (!ok) break;
+              ++s_n;
+              tc_fence_after();
+              // as many columns as the chunk has, in steps of 16
+              const uint32_t idS = idesc_bf16_f32(kKeys, (chunk_rows(p, w, ch) * p.G + 15) & ~15, 0);
+              const uint32_t q_lo = q_lo0 + (ch - pass * w.per) * (C::kQ >> 4);
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = (kk >> 2) * ((kKeys * 128) >> 4) + (kk & 3) * 2;
+                umma_bf16(tmem + buf * kCols, desc_sw128(k_lo + off), desc_sw128(q_lo + off), idS, kk > 0);
+              }
+              umma_commit(&sfull[buf]);
+            }
+            if (ok) umma_commit(&kempty[ks]);
+          }
+#pragma unroll
+          for (int s = 0; s < kQSlots; ++s) {
+            const int ch = pass * w.per + s;
+            if (ok && ch >= all.first && ch < all.end) umma_commit(&qempty[s]);
+          }
         }
-        if (ok) umma_commit(&kempty[ks]);
-        ++k_n;
       }
       if (!ok) {
         s_abort = 1;
         set_status(p.dev_status, SPEC_ERR_TIMEOUT);
       }
-      umma_commit(&drained);
-      mbar_wait_bounded(&drained, 0, nullptr);
+      umma_commit(&drained[a]);
+      mbar_wait_bounded(&drained[a], 0, nullptr);
+    }
+  } else if (warp == 3) {
+    // ---- the chunks' lse: four columns per thread and chunk, fetched while the pass before is under way ----
+    uint32_t l_n = 0;
+    for (int at = blockIdx.x; ok && at < total; at += gridDim.x) {
+      const Work w = work_of(p, plan, at);
+      for (int pass = 0; ok && pass < w.passes; ++pass) {
+        float x[kQSlots][4];
+#pragma unroll
+        for (int s = 0; s < kQSlots; ++s)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int ch = pass * w.per + s, col = lane + 32 * e, tok = col / p.G;
+            const bool there = s < w.per && ch < w.chunks && tok < chunk_rows(p, w, ch);
+            x[s][e] = there ? p.lse[(size_t)(w.r0 + w.q0 + ch * p.tc + tok) * p.Hq + w.g * p.G + col - tok * p.G] *
+                                  1.4426950408889634f
+                            : INFINITY;
+          }
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&lfree, (l_n & 1) ^ 1, &s_abort));
+        if (!ok) break;
+#pragma unroll
+        for (int s = 0; s < kQSlots; ++s)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s_lse[s][lane + 32 * e] = x[s][e];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&lfull);
+        ++l_n;
+      }
+    }
+    if (!ok && lane == 0) {
+      s_abort = 1;
+      set_status(p.dev_status, SPEC_ERR_TIMEOUT);
     }
   } else {
     // ---- sums: group a, one key per thread ----
-    const int a = (warp - 2) >> 2, q4 = warp & 3;
+    const int a = (warp - 4) >> 2, q4 = warp & 3;
     const int kl = q4 * 32 + lane;
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
-    const int col_tok = kl / p.G, col_head = kl - col_tok * p.G;  // the column whose lse this thread fetches
-    uint32_t s_n = 0;
-    bool ok = true;
-    // A warp whose wait gave up goes on with its group's barriers to the last item: no wait takes long any more.
-    for (int at = blockIdx.x; at < total; at += gridDim.x) {
+    const float2 sc = make_float2(p.scale_log2, p.scale_log2);
+    uint32_t k_n = 0, s_n = 0, l_n = 0;
+    for (int at = blockIdx.x; ok && at < total; at += gridDim.x) {
       const Work w = work_of(p, plan, at);
-      const int chunks = chunks_of(p, w, a);
-      if (chunks == 0) continue;
-      const int key = w.key + a * kKeys + kl, last_key = w.key + a * kKeys + kKeys - 1;
-      float total_w = 0.f;
-      auto fetch = [&](int c) {  // log2(e) lse of this thread's column
-        const int row = chunk_row(p, w, c) + col_tok;
-        return col_tok < p.tc && row < w.n ? p.lse[(size_t)(w.r0 + row) * p.Hq + w.g * p.G + col_head] * 1.4426950408889634f
-                                           : INFINITY;
-      };
-      float next = fetch(0);
-      for (int c = 0; c < chunks; ++c) {
-        const float* lse = s_lse[a];
-        named_bar_sync(1 + a, 128);  // the chunk before has been read
-        s_lse[a][kl] = next;
-        named_bar_sync(1 + a, 128);
-        if (c + 1 < chunks) next = fetch(c + 1);
-        const int buf = a * 2 + (s_n & 1);
-        ok = __all_sync(0xffffffffu, ok && mbar_wait_bounded(&sfull[buf], (s_n >> 1) & 1, &s_abort));
-        if (!ok) s_abort = 1;
-        const int row0 = chunk_row(p, w, c);
-        // columns [lo, hi) count: rows from this key on, inside the window
-        const bool edge = row0 < last_key || row0 + p.tc > w.n || p.tc * p.G < kCols;
-        const int lo = key > row0 ? (key - row0) * p.G : 0;
-        const int hi = (w.n - row0 < p.tc ? w.n - row0 : p.tc) * p.G;
-        tc_fence_after();
-        const float2 sc = make_float2(p.scale_log2, p.scale_log2);
-        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll 2
-        for (int q = 0; q < kCols; q += 32) {
-          uint32_t s[32];
-          if (ok) {
-            tmem_ld_x32(tmem + buf * kCols + q + lane_off, s);
-            tmem_ld_wait();
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) s[j] = 0u;
+      float* weight = p.weight + (size_t)w.g * p.n_rows + w.r0;
+      for (int pass = 0; ok && pass < w.passes; ++pass) {
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&lfull, l_n++ & 1, &s_abort));
+        for (int i = 0; ok && i < w.tiles; ++i) {
+          const Chunks c = chunks_of(p, w, pass, i);
+          const int key0 = w.key + i * kKeys, key = key0 + kl;
+          if (c.first >= c.end) {  // nothing of this pass: group 0 writes what pass 0 has to
+            if (pass == 0 && a == 0 && key < w.n) weight[key] = 0.f;
+            continue;
           }
-          if (edge) {
+          if ((int)(k_n++ & 1) != a) continue;
+          float sum_w = pass > 0 && key < w.n ? weight[key] : 0.f;
+          for (int ch = c.first; ch < c.end; ++ch) {
+            const int buf = a * 2 + (s_n & 1);
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sfull[buf], (s_n >> 1) & 1, &s_abort));
+            if (!ok) break;
+            ++s_n;
+            const float* lse = s_lse[ch - pass * w.per];
+            const int row0 = w.q0 + ch * p.tc;
+            // columns [lo, cols) count: rows from this key on, inside the window
+            const int cols = chunk_rows(p, w, ch) * p.G;
+            const int lo = key > row0 ? (key - row0) * p.G : 0;
+            const bool edge = row0 < key0 + kKeys - 1;
+            tc_fence_after();
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            const uint32_t tS = tmem + buf * kCols + lane_off;
+#pragma unroll 1
+            for (int q = 0; q < cols; q += 64) {
+              uint32_t s[2][32];
+              tmem_ld_x32(tS + q, s[0]);
+              if (q + 32 < cols) tmem_ld_x32(tS + q + 32, s[1]);
+              tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (q + j < lo || q + j >= hi) s[j] = 0xff800000u;
-          }
+              for (int b = 0; b < 2; ++b) {
+                const int q1 = q + b * 32;
+                if (q1 >= cols) break;
+                if (edge || q1 + 32 > cols) {
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            const float4 l4 = *reinterpret_cast<const float4*>(lse + q + j);
-            const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), sc, make_float2(-l4.x, -l4.y));
-            const float2 y = __ffma2_rn(make_float2(__uint_as_float(s[j + 2]), __uint_as_float(s[j + 3])), sc, make_float2(-l4.z, -l4.w));
-            sum[0] = __fadd2_rn(sum[0], make_float2(ex2_approx(x.x), ex2_approx(x.y)));
-            sum[1] = __fadd2_rn(sum[1], make_float2(ex2_approx(y.x), ex2_approx(y.y)));
+                  for (int j = 0; j < 32; ++j)
+                    if (q1 + j < lo || q1 + j >= cols) s[b][j] = 0xff800000u;
+                }
+#pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+                  const float4 l4 = *reinterpret_cast<const float4*>(lse + q1 + j);
+                  const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[b][j]), __uint_as_float(s[b][j + 1])), sc,
+                                              make_float2(-l4.x, -l4.y));
+                  const float2 y = __ffma2_rn(make_float2(__uint_as_float(s[b][j + 2]), __uint_as_float(s[b][j + 3])), sc,
+                                              make_float2(-l4.z, -l4.w));
+                  sum[0] = __fadd2_rn(sum[0], make_float2(ex2_approx(x.x), ex2_approx(x.y)));
+                  sum[1] = __fadd2_rn(sum[1], make_float2(ex2_approx(y.x), ex2_approx(y.y)));
+                }
+              }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sfree[buf]);
+            sum_w += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
           }
+          if (ok && key < w.n) weight[key] = sum_w;
         }
-        tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sfree[buf]);
-        ++s_n;
-        total_w += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
+        if (lane == 0) mbar_arrive(&lfree);
       }
-      if (!ok) {
-        if (lane == 0) {
-          s_abort = 1;
-          set_status(p.dev_status, SPEC_ERR_TIMEOUT);
-        }
-      } else if (key < w.n) {
-        p.weight[(size_t)w.g * p.n_rows + w.r0 + key] = total_w;
-      }
+    }
+    if (!ok && lane == 0) {
+      s_abort = 1;
+      set_status(p.dev_status, SPEC_ERR_TIMEOUT);
     }
   }
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+int key_weights_step(long long n_rows, int Hkv, int num_sms) {
+  // Tiles of an item: up to 16 a CTA, all of them at once (the queries are loaded once); beyond that a quarter of its
+  // share, so that requests of uneven lengths spread over the CTAs.
+  const long long share = ((n_rows + kKeys - 1) / kKeys * Hkv + num_sms - 1) / num_sms;
+  long long tiles = share <= 16 ? share : (share + 3) / 4;
+  if (tiles > 32) tiles = 32;
+  if (tiles < 1) tiles = 1;
+  return (int)tiles * kKeys;
 }
 
 template <int D>

@@ -100,6 +100,12 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo, ui
   return d;
 }
 
+// sdesc_sw128 of densely packed 8-row groups (sbo 1024) from its lower word, (address >> 4) and lbo: for issuers that count
+// addresses on.
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t lo) {
+  return ((uint64_t)((1024u >> 4) | (1u << 14) | (2u << 29)) << 32) | lo;
+}
+
 // Instruction descriptor, kind::f16: D fp32, A and B bf16, shape M x N; b_mn_major selects an
 // MN-major B operand (A is K-major).
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, int b_mn_major) {
