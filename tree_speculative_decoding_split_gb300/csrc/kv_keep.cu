@@ -1,6 +1,6 @@
 // K13: the rows of each prompt that a budget leaves in the cache.
 //
-// Three kernels: the counts and their sums (one CTA), the choice, and the copying of the chosen rows.
+// Two kernels, the choice and the copying of the chosen rows (ahead of them, for large batches, the counts).
 //
 // The choice is a radix selection.  Weights become 32-bit keys in their order; three passes of 11, 11 and 10 bits
 // count the keys that share what is known of the threshold, and the bin in which the budget runs out is the
@@ -26,44 +26,80 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kHeld = 40960;        // keys a CTA holds
 constexpr int kCopyThreads = 256;
 constexpr int kCopies = 4;          // (row, head)s per thread
+constexpr int kBatch = 8;           // keys of a thread on their way at once
+constexpr int kCountedBatch = 1024; // requests from which the counts have a kernel of their own
 
-__global__ void __launch_bounds__(kThreads) keep_counts_kernel(const KeepParams p) {
-  __shared__ long long s_warp[kWarps];
+// Rows kept before request `upto` and in all (-1 where they are refused), by all threads of the block.
+struct Kept {
+  long long before, total;
+};
+__device__ __forceinline__ int rows_kept(const KeepParams& p, int b) {
+  const int n = p.row_start[b + 1] - p.row_start[b];
+  return n < p.budget ? n : p.budget;
+}
+__device__ __forceinline__ Kept count_kept(const KeepParams& p, int upto, long long (*s_sum)[2]) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  bool ok = row_start_ok(p.row_start, p.B, p.n_rows);
+  long long before = 0, total = 0;
+  if (ok)
+    for (int b = tid; b < p.B; b += kThreads) {
+      const int n = rows_kept(p, b);
+      total += n;
+      if (b < upto) before += n;
+    }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+    total += __shfl_xor_sync(0xffffffffu, total, o);
+  }
+  if (lane == 0) {
+    s_sum[warp][0] = before;
+    s_sum[warp][1] = total;
+  }
+  __syncthreads();
+  Kept k = {0, 0};
+  for (int w = 0; w < kWarps; ++w) {
+    k.before += s_sum[w][0];
+    k.total += s_sum[w][1];
+  }
+  if (!ok || k.total > p.rows_out) k.before = k.total = -1;
+  return k;
+}
+
+// The counts of a large batch, once for all (a small one's are worked out by every CTA of the choice).
+__global__ void __launch_bounds__(kThreads) keep_counts_kernel(const KeepParams p) {
+  __shared__ long long s_sum[kWarps][2];
+  const int tid = threadIdx.x;
   pdl_wait();
   pdl_launch_dependents();
-  bool ok = row_start_ok(p.row_start, p.B, p.n_rows);
+  // thread t takes requests [t * per, (t + 1) * per): their sums, then a scan over the threads
+  const Kept k = count_kept(p, 0, s_sum);
+  const bool ok = k.total >= 0;
+  if (!ok && tid == 0) set_status(p.dev_status, SPEC_ERR_CAPACITY);
   const int per = (p.B + kThreads - 1) / kThreads;
   const int b0 = tid * per, b1 = b0 + per < p.B ? b0 + per : p.B;
-  auto kept = [&](int b) {
-    const int n = p.row_start[b + 1] - p.row_start[b];
-    return n < p.budget ? n : p.budget;
-  };
   long long mine = 0;
   if (ok)
-    for (int b = b0; b < b1; ++b) mine += kept(b);
+    for (int b = b0; b < b1; ++b) mine += rows_kept(p, b);
+  const int lane = tid & 31, warp = tid >> 5;
   long long v = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const long long y = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += y;
   }
-  if (lane == 31) s_warp[warp] = v;
   __syncthreads();
-  long long before = v - mine, total = 0;
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += s_warp[w];
-    total += s_warp[w];
-  }
-  ok = ok && total <= p.rows_out;
-  if (!ok && tid == 0) set_status(p.dev_status, SPEC_ERR_CAPACITY);
+  if (lane == 31) s_sum[warp][0] = v;
+  __syncthreads();
+  long long before = v - mine;
+  for (int w = 0; w < warp; ++w) before += s_sum[w][0];
   for (int b = b0; b < b1; ++b) {
-    const int n = ok ? kept(b) : 0;
+    const int n = ok ? rows_kept(p, b) : 0;
     p.n_keep[b] = n;
     p.keep_start[b] = ok ? (int)before : 0;
     before += n;
   }
-  if (tid == 0) p.keep_start[p.B] = ok ? (int)total : 0;
+  if (tid == 0) p.keep_start[p.B] = ok ? (int)k.total : 0;
 }
 
 __device__ __forceinline__ int cluster_ld(const int* at, uint32_t rank) {
@@ -79,9 +115,10 @@ struct SelectShared {
   int totals[2];        // keys above and at the threshold
   int warp_n[kWarps][2];
   int bin, left;
+  long long sum[kWarps][2];
 };
 
-__global__ void __launch_bounds__(kThreads, 1) keep_select_kernel(const KeepParams p, int32_t* source, int cluster) {
+__global__ void __launch_bounds__(kThreads, 1) keep_select_kernel(const KeepParams p, int32_t* source, int cluster, int counted) {
   extern __shared__ __align__(16) uint8_t s_raw[];
   SelectShared& s = *reinterpret_cast<SelectShared*>(s_raw);
   uint32_t* s_key = reinterpret_cast<uint32_t*>(s_raw + sizeof(SelectShared));  // [kHeld]
@@ -91,10 +128,26 @@ __global__ void __launch_bounds__(kThreads, 1) keep_select_kernel(const KeepPara
   const int b = seg / p.Hkv, g = seg % p.Hkv;
   pdl_wait();
   pdl_launch_dependents();
-  const int keep = p.n_keep[b];
+  int keep;
+  long long out0;
+  if (counted) {
+    keep = p.n_keep[b];
+    out0 = p.keep_start[b];
+  } else {
+    const Kept k = count_kept(p, b, s.sum);
+    keep = k.total < 0 ? 0 : rows_kept(p, b);
+    out0 = k.total < 0 ? 0 : k.before;
+    if (rank == 0 && g == 0 && tid == 0) {
+      p.n_keep[b] = keep;
+      p.keep_start[b] = (int)out0;
+      if (b == 0) {
+        p.keep_start[p.B] = k.total < 0 ? 0 : (int)k.total;
+        if (k.total < 0) set_status(p.dev_status, SPEC_ERR_CAPACITY);
+      }
+    }
+  }
   if (keep == 0) return;  // (the whole cluster)
   const int r0 = p.row_start[b], n = p.row_start[b + 1] - r0;
-  const long long out0 = p.keep_start[b];
   auto put = [&](int place, int j) {
     const long long at = (out0 + place) * p.Hkv + g;
     p.index[at] = j;
@@ -125,15 +178,23 @@ __global__ void __launch_bounds__(kThreads, 1) keep_select_kernel(const KeepPara
     for (int i = tid; i < 4 * 2048; i += kThreads) (&s.part[0][0])[i] = 0;
     __syncthreads();
     int* part = s.part[warp & 3];
-    for (int i = tid; i < mine; i += kThreads) {
-      uint32_t key;
-      if (pass == 0) {
-        key = order_u(weight[i]);
-        if (i < kHeld) s_key[i] = key;
-      } else {
-        key = key_at(i);
+    for (int i0 = tid; i0 < mine; i0 += kThreads * kBatch) {
+      uint32_t key[kBatch];  // (all reads first)
+#pragma unroll
+      for (int e = 0; e < kBatch; ++e) {
+        const int i = i0 + e * kThreads;
+        key[e] = i < mine ? (pass == 0 ? __float_as_uint(weight[i]) : key_at(i)) : 0u;
       }
-      if (pass == 0 || (key >> (shift + bits)) == known) atomicAdd(&part[(key >> shift) & ((1u << bits) - 1)], 1);
+#pragma unroll
+      for (int e = 0; e < kBatch; ++e) {
+        const int i = i0 + e * kThreads;
+        if (i >= mine) break;
+        if (pass == 0) {
+          key[e] = order_u(__uint_as_float(key[e]));
+          if (i < kHeld) s_key[i] = key[e];
+        }
+        if (pass == 0 || (key[e] >> (shift + bits)) == known) atomicAdd(&part[(key[e] >> shift) & ((1u << bits) - 1)], 1);
+      }
     }
     __syncthreads();
     for (int i = tid; i < 2048; i += kThreads) s.bins[pass][i] = s.part[0][i] + s.part[1][i] + s.part[2][i] + s.part[3][i];
@@ -255,9 +316,12 @@ __global__ void __launch_bounds__(kCopyThreads) keep_copy_kernel(const KeepParam
 }  // namespace
 
 cudaError_t launch_kv_keep(const KeepParams& p, int32_t* source, int num_sms, cudaStream_t stream) {
-  cudaError_t err = launch_dependent(keep_counts_kernel, dim3(1), dim3(kThreads), 0, stream, p);
-  if (err != cudaSuccess) return err;
-  if (p.n_rows == 0 || p.rows_out == 0) return cudaSuccess;
+  // Each CTA of the choice reads the whole of row_start: 1 us up to a request per thread, against 4 us for a kernel ahead.
+  const bool copies = p.n_rows > 0 && p.rows_out > 0;
+  const int counted = p.B > kCountedBatch || !copies;
+  cudaError_t err = cudaSuccess;
+  if (counted) err = launch_dependent(keep_counts_kernel, dim3(1), dim3(kThreads), 0, stream, p);
+  if (err != cudaSuccess || !copies) return err;
   // CTAs per request and head: as many as there are SMs for, and 2048 rows for each.
   const long long segs = (long long)p.B * p.Hkv;
   int cluster = 1;
@@ -279,7 +343,7 @@ cudaError_t launch_kv_keep(const KeepParams& p, int32_t* source, int num_sms, cu
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  err = cudaLaunchKernelEx(&cfg, keep_select_kernel, p, source, cluster);
+  err = cudaLaunchKernelEx(&cfg, keep_select_kernel, p, source, cluster, counted);
   if (err != cudaSuccess) return err;
   const int vecs = p.row_bytes / 16;
   const long long per_block = (long long)(kCopyThreads / vecs) * kCopies;
