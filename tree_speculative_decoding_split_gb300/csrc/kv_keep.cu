@@ -58,7 +58,8 @@ __device__ __forceinline__ Kept count_kept(const KeepParams& p, int upto, long l
   }
   __syncthreads();
   Kept k = {0, 0};
-  for (int w = 0; w < kWarps; ++w) {
+  const int warps = p.B < kThreads ? (p.B + 31) / 32 : kWarps;  // those with a request
+  for (int w = 0; w < warps; ++w) {
     k.before += s_sum[w][0];
     k.total += s_sum[w][1];
   }
@@ -108,15 +109,22 @@ __device__ __forceinline__ int cluster_ld(const int* at, uint32_t rank) {
   return v;
 }
 
+__device__ __forceinline__ void cluster_st(int* at, uint32_t rank, int v) {
+  asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(cluster_addr(at, rank)), "r"(v) : "memory");
+}
+
 struct SelectShared {
   int part[4][2048];    // a pass's counts, by warp & 3
   int bins[3][2048];    // their sums, one set per pass (other CTAs read them)
   int warp_sum[kWarps];
   int totals[2];        // keys above and at the threshold
   int warp_n[kWarps][2];
-  int bin, left;
+  int bin, left;        // written by the CTA that finds them, in every CTA of the cluster
+  int slice[8];         // keys in each CTA's slice of the bins
   long long sum[kWarps][2];
 };
+
+static_assert(sizeof(SelectShared) % 16 == 0, "the keys behind it are read four at a time");
 
 __global__ void __launch_bounds__(kThreads, 1) keep_select_kernel(const KeepParams p, int32_t* source, int cluster, int counted) {
   extern __shared__ __align__(16) uint8_t s_raw[];
@@ -202,16 +210,20 @@ __global__ void __launch_bounds__(kThreads, 1) keep_select_kernel(const KeepPara
       cluster_sync_all();
     else
       __syncthreads();
-    // the bin, from above, in which the rows to choose run out; thread t looks at bins 2047 - 2 t and 2046 - 2 t
-    int x[2];
+    // The bin, from above, in which the rows to choose run out.  Each CTA sums a slice of the bins over the cluster (all of
+    // them in every CTA took 8000 cycles a pass), rank 0 the uppermost; a thread looks at two neighbouring bins of it.
+    const int slice = 2048 / cluster, top_bin = 2047 - rank * slice - 2 * tid;
+    const bool mine_bins = 2 * tid < slice;
+    int x[2] = {0, 0};
+    if (mine_bins) {
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int bin = 2047 - 2 * tid - e;
-      x[e] = 0;
-      if (cluster > 1) {
-        for (int r = 0; r < cluster; ++r) x[e] += cluster_ld(&s.bins[pass][bin], (uint32_t)r);
-      } else {
-        x[e] = s.bins[pass][bin];
+      for (int e = 0; e < 2; ++e) {
+        if (cluster > 1) {
+#pragma unroll 8
+          for (int r = 0; r < cluster; ++r) x[e] += cluster_ld(&s.bins[pass][top_bin - e], (uint32_t)r);
+        } else {
+          x[e] = s.bins[pass][top_bin - e];
+        }
       }
     }
     int v = x[0] + x[1];
@@ -223,40 +235,99 @@ __global__ void __launch_bounds__(kThreads, 1) keep_select_kernel(const KeepPara
     if (lane == 31) s.warp_sum[warp] = v;
     __syncthreads();
     int above = v - x[0] - x[1];
-    for (int w = 0; w < warp; ++w) above += s.warp_sum[w];
+    {  // every warp scans the warps' sums for itself
+      int y = s.warp_sum[lane];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int z = __shfl_up_sync(0xffffffffu, y, o);
+        if (lane >= o) y += z;
+      }
+      const int before = __shfl_sync(0xffffffffu, y, (warp + 31) & 31), all = __shfl_sync(0xffffffffu, y, 31);
+      if (warp > 0) above += before;
+      if (cluster > 1) {
+        if (tid < cluster) cluster_st(&s.slice[rank], (uint32_t)tid, all);
+        cluster_sync_all();
+        for (int r = 0; r < rank; ++r) above += s.slice[r];
+      }
+    }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      if (above < left && above + x[e] >= left) {
-        s.bin = 2047 - 2 * tid - e;
-        s.left = left - above;
+      if (mine_bins && above < left && above + x[e] >= left) {
+        for (int r = 0; r < cluster; ++r) {
+          if (cluster > 1) {
+            cluster_st(&s.bin, (uint32_t)r, top_bin - e);
+            cluster_st(&s.left, (uint32_t)r, left - above);
+          } else {
+            s.bin = top_bin - e;
+            s.left = left - above;
+          }
+        }
       }
       above += x[e];
     }
-    __syncthreads();
+    if (cluster > 1)
+      cluster_sync_all();
+    else
+      __syncthreads();
     known = (known << bits) | (uint32_t)s.bin;
     left = s.left;
     __syncthreads();
   }
-  // `known` is the threshold, `left` the number of keys equal to it that stay.  Warps walk stretches of 32 w keys.
-  const int stretch = ((mine + kWarps - 1) / kWarps + 31) & ~31;
+  // `known` is the threshold, `left` the number of keys equal to it that stay.  Warps walk stretches, four neighbouring keys
+  // per lane; keys above and at the threshold are counted in the halves of a word (128 a step) and summed apart.
+  const int stretch = ((mine + kWarps - 1) / kWarps + 127) & ~127;
   const int w0 = warp * stretch < mine ? warp * stretch : mine, w1 = w0 + stretch < mine ? w0 + stretch : mine;
+  auto four = [&](int i, uint32_t (&key)[4]) {
+    if (i + 4 <= w1 && i + 4 <= kHeld) {
+      const uint4 k = *reinterpret_cast<const uint4*>(s_key + i);
+      key[0] = k.x, key[1] = k.y, key[2] = k.z, key[3] = k.w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) key[e] = i + e < w1 ? key_at(i + e) : 0u;
+    }
+  };
+  // (known == 0: NaN alone are at the threshold, and places behind the stretch are not keys)
+  auto count = [&](int i, const uint32_t (&key)[4]) {
+    uint32_t n = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (i + e < w1) n += key[e] > known ? 1u : (key[e] == known ? 0x10000u : 0u);
+    return n;
+  };
   int above = 0, equal = 0;
-  for (int i = w0; i < w1; i += 32) {
-    const uint32_t key = i + lane < w1 ? key_at(i + lane) : 0u;
-    above += __popc(__ballot_sync(0xffffffffu, i + lane < w1 && key > known));
-    equal += __popc(__ballot_sync(0xffffffffu, i + lane < w1 && key == known));
+  for (int i = w0 + lane * 4; i < w1; i += 128) {
+    uint32_t key[4];
+    four(i, key);
+    const uint32_t n = count(i, key);
+    above += n & 0xffffu;
+    equal += n >> 16;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    above += __shfl_xor_sync(0xffffffffu, above, o);
+    equal += __shfl_xor_sync(0xffffffffu, equal, o);
   }
   if (lane == 0) {
     s.warp_n[warp][0] = above;
     s.warp_n[warp][1] = equal;
   }
   __syncthreads();
-  if (tid < 2) {
-    int sum = 0;
-    for (int w = 0; w < kWarps; ++w) sum += s.warp_n[w][tid];
-    s.totals[tid] = sum;
+  {  // sums over the warps before this one, and over the CTAs before
+    int n[2] = {s.warp_n[lane][0], s.warp_n[lane][1]};
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      int y = n[e];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int z = __shfl_up_sync(0xffffffffu, y, o);
+        if (lane >= o) y += z;
+      }
+      const int all = __shfl_sync(0xffffffffu, y, 31);
+      if (tid == 0) s.totals[e] = all;
+      const int before = __shfl_sync(0xffffffffu, y - n[e], warp);
+      (e ? equal : above) = before;
+    }
   }
-  above = equal = 0;
   if (cluster > 1) {
     cluster_sync_all();
     for (int r = 0; r < rank; ++r) {
@@ -264,23 +335,31 @@ __global__ void __launch_bounds__(kThreads, 1) keep_select_kernel(const KeepPara
       equal += cluster_ld(&s.totals[1], (uint32_t)r);
     }
   }
-  for (int w = 0; w < warp; ++w) {
-    above += s.warp_n[w][0];
-    equal += s.warp_n[w][1];
-  }
-  const uint32_t below = (1u << lane) - 1u;
-  for (int i = w0; i < w1; i += 32) {
-    const uint32_t key = i + lane < w1 ? key_at(i + lane) : 0u;
-    const uint32_t up = __ballot_sync(0xffffffffu, i + lane < w1 && key > known);
-    const uint32_t eq = __ballot_sync(0xffffffffu, i + lane < w1 && key == known);
-    const int eq_before = equal + __popc(eq & below);
-    const bool is_eq = (eq >> lane) & 1u;
-    if (((up >> lane) & 1u) || (is_eq && eq_before < left)) {
-      const int place = above + __popc(up & below) + (eq_before < left ? eq_before : left);
-      put(p.first + place, p.first + (int)lo + i + lane);
+  for (int i0 = w0; i0 < w1; i0 += 128) {
+    const int i = i0 + lane * 4;
+    uint32_t key[4];
+    four(i, key);
+    const uint32_t n = count(i, key);
+    uint32_t sum = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t z = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += z;
     }
-    above += __popc(up);
-    equal += __popc(eq);
+    const uint32_t all = __shfl_sync(0xffffffffu, sum, 31);
+    int up = above + (int)((sum - n) & 0xffffu), eq = equal + (int)((sum - n) >> 16);
+    if (n) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (i + e >= w1) break;
+        const bool is_up = key[e] > known, is_eq = key[e] == known;
+        if (is_up || (is_eq && eq < left)) put(p.first + up + (eq < left ? eq : left), p.first + (int)lo + i + e);
+        up += is_up;
+        eq += is_eq;
+      }
+    }
+    above += all & 0xffffu;
+    equal += all >> 16;
   }
   if (cluster > 1) cluster_sync_all();  // no CTA leaves while another may still read its counts
 }

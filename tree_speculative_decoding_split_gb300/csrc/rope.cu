@@ -132,7 +132,7 @@ template <bool BF16, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p, int rows_block, int units, int rot_units) {
   using V = Vec<BF16>;
   constexpr int kN = V::kN;      // elements of a 16-byte vector = pairs of a unit
-  constexpr int kFlight = 4;     // (row, head)s of a thread whose loads are under way at once
+  constexpr int kFlight = BF16 ? 2 : 4;     // (row, head)s of a thread whose loads are under way at once
   extern __shared__ float2 s_cs[];  // [rows_block][rot / 2] cos, sin times the amplitude
   __shared__ int s_pos[64];
   const int tid = threadIdx.x;
