@@ -56,13 +56,13 @@ inline long long plan_items(long long n_rows, int B, int step) { return n_rows /
 cudaError_t launch_prompt_plan(const PlanParams& p, cudaStream_t stream);
 
 // What a kernel reads of its plan.  A single request needs no list (items == nullptr): its pieces follow from row_start,
-// those with the most keys first, and 3 us of another kernel ahead are saved.
+// in order or (by_work) the last first, and 3 us of another kernel ahead are saved.
 struct PlanView {
   const PromptItem* items;
   const int32_t* count;
   const int32_t* row_start;
   long long n_rows;
-  int step;
+  int step, by_work;
 };
 struct PlanReader {
   const PlanView& v;
@@ -84,7 +84,7 @@ struct PlanReader {
     PromptItem it;
     it.r0 = r0;
     it.n = n;
-    it.tok = (count - 1 - i) * v.step;
+    it.tok = (v.by_work ? count - 1 - i : i) * v.step;
     it.pad = 0;
     return it;
   }
@@ -106,8 +106,7 @@ cudaError_t launch_prompt_attention(int d, const CUtensorMap* tmQ, const CUtenso
                                     const PromptAttnParams& p, int grid, cudaStream_t stream);
 
 // ---- K12: key weights -----------------------------------------------------------------------------
-// Keys per item.
-int key_weights_step(long long n_rows, int Hkv, int num_sms);
+constexpr int kWeightKeys = 128;  // keys per tile
 struct KeyWeightsParams {
   int Hq, Hkv, G, tc;       // tc: rows of the window per chunk (128 / G)
   int window;

@@ -146,6 +146,7 @@ spec_status plan(long long n_rows, int B, int step, int by_work, const int32_t* 
   view->row_start = row_start;
   view->n_rows = n_rows;
   view->step = step;
+  view->by_work = by_work;
   if (!list) return SPEC_OK;
   PlanParams p;
   p.B = B; p.step = step; p.by_work = by_work; p.n_rows = n_rows; p.row_start = row_start;
@@ -260,7 +261,7 @@ spec_status spec_prompt_attention(const spec_prompt_attn_args* a, void* workspac
 
 size_t spec_prompt_key_weights_workspace(const spec_key_weights_args* a) {
   if (check_key_weights(a) != SPEC_OK) return 0;
-  return layout_plan(a->n_rows, a->batch, key_weights_step(a->n_rows, a->num_kv_heads, num_sms_current()), nullptr).bytes;
+  return layout_plan(a->n_rows, a->batch, kWeightKeys, nullptr).bytes;
 }
 
 spec_status spec_prompt_key_weights(const spec_key_weights_args* a, void* workspace, size_t workspace_bytes,
@@ -268,8 +269,7 @@ spec_status spec_prompt_key_weights(const spec_key_weights_args* a, void* worksp
   const spec_status st = check_key_weights(a);
   if (st != SPEC_OK) return st;
   if (!workspace || !aligned16(workspace)) return SPEC_ERR_INVALID_ARGUMENT;
-  const int step = key_weights_step(a->n_rows, a->num_kv_heads, num_sms_current());
-  const PlanLayout l = layout_plan(a->n_rows, a->batch, step, workspace);
+  const PlanLayout l = layout_plan(a->n_rows, a->batch, kWeightKeys, workspace);
   if (workspace_bytes < l.bytes) return SPEC_ERR_WORKSPACE_TOO_SMALL;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
   KeyWeightsParams p;
@@ -280,9 +280,9 @@ spec_status spec_prompt_key_weights(const spec_key_weights_args* a, void* worksp
   if (a->n_rows > 0 && (!make_map_heads(&tm[0], a->q, a->head_dim, p.Hq, a->n_rows, a->q_stride, p.G, p.tc) ||
                         !make_map_heads(&tm[1], a->k, a->head_dim, p.Hkv, a->n_rows, a->k_stride, 1, 128)))
     return SPEC_ERR_CUDA;
-  const spec_status ps = plan(a->n_rows, a->batch, step, 0, a->row_start, l, &p.plan, dev_status, stream);
+  const spec_status ps = plan(a->n_rows, a->batch, kWeightKeys, 0, a->row_start, l, &p.plan, dev_status, stream);
   if (ps != SPEC_OK || a->n_rows == 0) return ps;
-  const int grid = grid_for(plan_items(a->n_rows, a->batch, step), p.Hkv);
+  const int grid = grid_for(plan_items(a->n_rows, a->batch, kWeightKeys), p.Hkv);
   return launch_key_weights(a->head_dim, &tm[0], &tm[1], p, grid, stream) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 

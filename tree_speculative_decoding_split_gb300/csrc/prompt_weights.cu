@@ -6,9 +6,9 @@
 // over the queries is one thread's walk along its own row of tensor memory: no reduction between threads, no
 // atomics, one order of terms.
 //
-// An item is a stretch of one request's keys for one KV head, in tiles of 128 keys (the M of an MMA).  The window's
-// rows times the G heads are the columns (N), in chunks of tc = 128 / G rows, up to three of which stay in shared
-// memory with their lse while the stretch's keys stream past.  Longer windows take several such passes over a
+// Keys come in tiles of 128 (the M of an MMA); every CTA has an even share of all tiles, in stretches of one request and KV
+// head.  The window's rows times the G heads are the columns (N), in chunks of tc = 128 / G rows, up to three of which
+// stay in shared memory with their lse while the stretch's keys stream past.  Longer windows take several such passes over a
 // stretch (its keys come from L2 then), the later ones adding to what the earlier ones wrote.  K is read once, 2 d
 // bytes for 2 d operations a column: a window of 64 rows with 4 heads a group is where HBM, MMA and exponentials
 // (512 cycles for 128 x 128 of each) take equally long.
@@ -50,15 +50,17 @@ struct Work {
   int passes, per;     // passes over the keys, chunks of a pass
 };
 
-__device__ __forceinline__ Work work_of(const KeyWeightsParams& p, const PlanReader& plan, int at) {
-  const PromptItem it = plan.item(at / p.Hkv);
+// The CTA's tiles are an even share [at, end) of all: the plan's pieces of 128 keys, head after head.  A stretch is what
+// one request and head have of it.
+__device__ __forceinline__ Work work_of(const KeyWeightsParams& p, const PlanReader& plan, long long at, long long end) {
   Work w;
+  w.g = (int)(at / plan.count);
+  const PromptItem it = plan.item((int)(at - (long long)w.g * plan.count));
   w.r0 = it.r0;
   w.n = it.n;
   w.key = it.tok;
-  w.g = at % p.Hkv;
-  const int keys = it.n - it.tok < p.plan.step ? it.n - it.tok : p.plan.step;
-  w.tiles = (keys + kKeys - 1) / kKeys;
+  const int tiles = (it.n - it.tok + kKeys - 1) / kKeys;
+  w.tiles = tiles < end - at ? tiles : (int)(end - at);
   w.q0 = it.n > p.window ? it.n - p.window : 0;
   w.chunks = (it.n - w.q0 + p.tc - 1) / p.tc;
   w.passes = (w.chunks + kQSlots - 1) / kQSlots;
@@ -132,15 +134,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = s_tmem;
   pdl_wait();  // the plan
   const PlanReader plan(p.plan, p.dev_status);
-  const int total = plan.count * p.Hkv;
+  const long long total = (long long)plan.count * p.Hkv;
+  const long long begin = total * blockIdx.x / gridDim.x, end = total * (blockIdx.x + 1) / gridDim.x;
   bool ok = true;
 
   if (warp == 0) {
     // ---- TMA producer ----
     if (lane == 0) {
       uint32_t k_n = 0, q_n[kQSlots] = {0, 0, 0};
-      for (int at = blockIdx.x; ok && at < total; at += gridDim.x) {
-        const Work w = work_of(p, plan, at);
+      Work w;
+      for (long long at = begin; ok && at < end; at += w.tiles) {
+        w = work_of(p, plan, at, end);
         for (int pass = 0; ok && pass < w.passes; ++pass) {
           for (int i = 0; ok && i < w.tiles; ++i) {
             const Chunks c = chunks_of(p, w, pass, i);
@@ -187,8 +191,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int a = warp - 1;
       const uint32_t k_lo0 = smem_u32(sK) >> 4, q_lo0 = smem_u32(sQ) >> 4;
       uint32_t k_n = 0, q_n[kQSlots] = {0, 0, 0}, s_n = 0;
-      for (int at = blockIdx.x; ok && at < total; at += gridDim.x) {
-        const Work w = work_of(p, plan, at);
+      Work w;
+      for (long long at = begin; ok && at < end; at += w.tiles) {
+        w = work_of(p, plan, at, end);
         for (int pass = 0; ok && pass < w.passes; ++pass) {
           const Chunks all = chunks_of(p, w, pass, 0);
           if (all.first >= all.end) continue;
@@ -240,8 +245,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 3) {
     // ---- the chunks' lse: four columns per thread and chunk, fetched while the pass before is under way ----
     uint32_t l_n = 0;
-    for (int at = blockIdx.x; ok && at < total; at += gridDim.x) {
-      const Work w = work_of(p, plan, at);
+    Work w;
+    for (long long at = begin; ok && at < end; at += w.tiles) {
+      w = work_of(p, plan, at, end);
       for (int pass = 0; ok && pass < w.passes; ++pass) {
         float x[kQSlots][4];
 #pragma unroll
@@ -276,8 +282,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
     const float2 sc = make_float2(p.scale_log2, p.scale_log2);
     uint32_t k_n = 0, s_n = 0, l_n = 0;
-    for (int at = blockIdx.x; ok && at < total; at += gridDim.x) {
-      const Work w = work_of(p, plan, at);
+    Work w;
+    for (long long at = begin; ok && at < end; at += w.tiles) {
+      w = work_of(p, plan, at, end);
       float* weight = p.weight + (size_t)w.g * p.n_rows + w.r0;
       for (int pass = 0; ok && pass < w.passes; ++pass) {
         ok = __all_sync(0xffffffffu, mbar_wait_bounded(&lfull, l_n++ & 1, &s_abort));
@@ -374,16 +381,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, 512);
-}
-
-int key_weights_step(long long n_rows, int Hkv, int num_sms) {
-  // Tiles of an item: up to 16 a CTA, all of them at once (the queries are loaded once); beyond that a quarter of its
-  // share, so that requests of uneven lengths spread over the CTAs.
-  const long long share = ((n_rows + kKeys - 1) / kKeys * Hkv + num_sms - 1) / num_sms;
-  long long tiles = share <= 16 ? share : (share + 3) / 4;
-  if (tiles > 32) tiles = 32;
-  if (tiles < 1) tiles = 1;
-  return (int)tiles * kKeys;
 }
 
 template <int D>
