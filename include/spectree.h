@@ -696,7 +696,8 @@ spec_status spec_rope(const spec_rope_args* args, void* stream);
  * by 2^-8 of themselves at most, as the output's own rounding), their sum as float32.  Keys that a row does not see
  * have no influence on it, NaN and infinities included.
  * Host errors: SPEC_ERR_INVALID_ARGUMENT, SPEC_ERR_UNSUPPORTED (dtype other than bf16, head_dim other
- * than 64 or 128, Hq / Hkv > 128, n_rows >= 2^31 - 256, B > SPEC_MAX_RESERVE_BATCH, strides of 2^38 elements or more),
+ * than 64 or 128, Hq / Hkv > 128, n_rows >= 2^31 - 256, B > SPEC_MAX_RESERVE_BATCH, strides of 2^38 elements or more,
+ * (n_rows / s + B) * Hkv >= 2^31 for pieces of s = 2 * floor(128 / (Hq / Hkv)) rows),
  * SPEC_ERR_WORKSPACE_TOO_SMALL. */
 typedef struct spec_prompt_attn_args {
   int32_t dtype;            /* SPEC_DTYPE_BF16 */
@@ -729,7 +730,7 @@ spec_status spec_prompt_attention(const spec_prompt_attn_args* args, void* works
  * in float32, the terms added in an order of their own that does not change from call to call; rows
  * outside of the requests keep what they hold.  lse is spec_prompt_attention's; only the window's rows
  * of q and lse are read.
- * Host errors and workspace as for spec_prompt_attention, and window < 1. */
+ * Host errors and workspace as for spec_prompt_attention (pieces of 128 rows), and window < 1. */
 typedef struct spec_key_weights_args {
   int32_t dtype;            /* SPEC_DTYPE_BF16 */
   int32_t batch;            /* B */

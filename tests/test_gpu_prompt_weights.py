@@ -131,3 +131,16 @@ def test_repeated_and_captured_calls():
     weight.zero_()
     graph.replay()
     assert torch.equal(weight, want)
+
+
+@pytest.mark.parametrize("hq,hkv", [(8, 1), (64, 1)])
+def test_long_windows_take_several_passes(hq, hkv):
+    """Windows of many chunks, stretches of odd numbers of tiles, and the same answer call after call."""
+    lens = [130, 2500, 1, 129, 700, 385]
+    start = starts(lens)
+    q, k, _ = fused(_gen(7), int(start[-1]), hq, hkv, 64)
+    lse = attention(q, k, k, start)[1].float()
+    for window in (100, 333):
+        weight = st.prompt_key_weights(q, k, lse, start, window)
+        _check(weight, q, k, lse, start, window)
+        assert all(torch.equal(st.prompt_key_weights(q, k, lse, start, window), weight) for _ in range(5))

@@ -110,6 +110,7 @@ constexpr int kWeightKeys = 128;  // keys per tile
 struct KeyWeightsParams {
   int Hq, Hkv, G, tc;       // tc: rows of the window per chunk (128 / G)
   int window;
+  int per_head;             // CTAs of each head, 0 where shares run over heads
   float scale_log2;
   long long n_rows;
   PlanView plan;
