@@ -89,22 +89,27 @@ def test_rows_of_no_request_and_behind_the_kept_ones_stay():
     assert all((x[50:] == (-7 if x.dtype == torch.int32 else 7)).all() for x in outputs[:3])
 
 
-def test_refusals_on_the_device():
+@pytest.mark.parametrize("empty", [0, 2000])
+def test_refusals_on_the_device(empty):
+    """Among few requests and (with empty ones behind) among many."""
     k = rows(_gen(13), 100, 2, 64)
     w = _weights(_gen(14), 2, 100)
     for start, rows_out in (([0, 60, 50, 100], 100), ([-1, 50, 60, 100], 100), ([0, 50, 60, 101], 100), ([0, 50, 60, 100], 49)):
         status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        start = start + [start[-1]] * empty
         outputs = (torch.full((rows_out, 2, 64), 7.0, dtype=torch.bfloat16, device="cuda"),
                    torch.full((rows_out, 2, 64), 7.0, dtype=torch.bfloat16, device="cuda"),
-                   torch.full((rows_out, 2), -7, dtype=torch.int32, device="cuda"), torch.full((4,), -7, dtype=torch.int32, device="cuda"),
-                   torch.full((3,), -7, dtype=torch.int32, device="cuda"))
+                   torch.full((rows_out, 2), -7, dtype=torch.int32, device="cuda"),
+                   torch.full((len(start),), -7, dtype=torch.int32, device="cuda"),
+                   torch.full((len(start) - 1,), -7, dtype=torch.int32, device="cuda"))
         st.kv_keep(k, k, w, torch.tensor(start, dtype=torch.int32, device="cuda"), 20, outputs=outputs, dev_status=status)
         assert int(status) == 7 and (outputs[0] == 7).all() and (outputs[1] == 7).all() and (outputs[2] == -7).all()
-        assert outputs[3].tolist() == [0] * 4 and outputs[4].tolist() == [0] * 3
+        assert not outputs[3].any() and not outputs[4].any()
 
 
-def test_many_requests():
-    lens = [(31 * b) % 97 for b in range(700)]
+@pytest.mark.parametrize("batch", [700, 1024, 1025, 3000])
+def test_many_requests(batch):
+    lens = [(31 * b) % 97 for b in range(batch)]
     start = starts(lens)
     n = int(start[-1])
     gen = _gen(15)

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import tree_speculative_decoding_split_gb300 as st
-from prompt_helpers import check_attention, fused, rows, starts
+from prompt_helpers import attention, check_attention, fused, rows, starts
 
 pytestmark = pytest.mark.gpu
 
@@ -193,3 +193,28 @@ def test_captured_calls_follow_lengths_on_the_device():
         start.copy_(starts(lens))
         graph.replay()
         check_attention((out, lse), q, k, v, start)
+
+
+def test_a_first_tile_of_infinities():
+    """Rows whose first 128 scores are all -inf (K rows of -inf) take their weights from what follows, however small."""
+    n, d = 300, 64
+    start = starts([n])
+    q = torch.ones((n, 2, d), device="cuda").bfloat16()
+    k = torch.full((n, 1, d), -4.0, device="cuda")
+    k[:128, 0, 0] = -math.inf
+    k[128:, 0, 1] = torch.arange(n - 128, device="cuda") % 8 * 0.5
+    v = rows(_gen(14), n, 1, d)
+    out, lse = st.prompt_attention(q, k.bfloat16(), v, start, scale=1.0)
+    want, want_lse, mag, _ = attention(q[128:], k[128:].bfloat16(), v[128:], starts([n - 128]), 1.0)
+    assert ((out[128:].double() - want).abs() <= 2.1 * 2.0 ** -8 * mag + 1e-30).all()
+    assert ((lse[128:].double() - want_lse).abs() <= 2.0 ** -20 * want_lse.abs()).all()
+
+
+def test_many_heads_and_unaligned_rows():
+    """More heads than SMs, and outputs that begin 16 bytes off a 32-byte sector."""
+    start = starts([70, 200])
+    q, k, v = fused(_gen(15), 270, 200, 200, 64)
+    out = torch.zeros(270 * 200 * 64 + 8, dtype=torch.bfloat16, device="cuda")[8:].view(270, 200, 64)
+    assert out.data_ptr() % 32 == 16
+    got = st.prompt_attention(q, k, v, start, out=out)
+    check_attention(got, q, k, v, start)

@@ -144,3 +144,10 @@ def test_long_windows_take_several_passes(hq, hkv):
         weight = st.prompt_key_weights(q, k, lse, start, window)
         _check(weight, q, k, lse, start, window)
         assert all(torch.equal(st.prompt_key_weights(q, k, lse, start, window), weight) for _ in range(5))
+
+
+def test_more_heads_than_shares():
+    start = starts([300, 40, 129])
+    q, k, _ = fused(_gen(8), 469, 100, 100, 64)
+    lse = attention(q, k, k, start)[1].float()
+    _check(st.prompt_key_weights(q, k, lse, start, 30), q, k, lse, start, 30)

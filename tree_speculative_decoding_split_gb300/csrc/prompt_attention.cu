@@ -490,7 +490,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool edge = t * kKeys + kKeys - 1 > first;  // some row does not see all of the tile's keys
         // Weights are taken by the reference there is, the first tile's maximum at first.  Their sum tells where scores have
         // outgrown it (128 weights of up to 2^8 stay below 2^15, and what overflows shows as well): tile_again then does the
-        // tile once more, by its maximum.  No other tile needs one, which is a pass less on the way from S to P.
+        // tile once more, by its maximum.  (So does a row that has seen nothing but -inf, whose reference is none yet.)  No
+        // other tile needs one, which is a pass less on the way from S to P.
         bool again = false;
         if (ok) {
           uint32_t s[4][32];
@@ -516,9 +517,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int j = 0; j < 32; j += 2)
                 first_mx[c] = max3(first_mx[c], __uint_as_float(s[c][j]), __uint_as_float(s[c][j + 1]));
             }
-            m_run = max3(fmaxf(first_mx[0], first_mx[1]), first_mx[2], first_mx[3]);
+            // (128 is no multiple of every G: rows behind the last head have a reference all the same)
+            m_run = rl < p.tg * p.G ? max3(fmaxf(first_mx[0], first_mx[1]), first_mx[2], first_mx[3]) : 0.f;
           }
-          const float shift = (m_run == -INFINITY ? 0.f : m_run) * p.scale_log2;
+          // (without a reference: weights that do not count, and tile_again)
+          const float shift = (m_run == -INFINITY ? INFINITY : m_run) * p.scale_log2;
           const float2 sc = make_float2(p.scale_log2, p.scale_log2), off = make_float2(-shift, -shift);
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
           uint32_t pk[2][32];
@@ -546,7 +549,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        named_arrive(kBarP + a, 160);
+        // (not an arrival alone: a warp whose next wait gives up must not come to the next tile's before the issuer has left
+        // this one's)
+        named_bar_sync(kBarP + a, 160);
       }
       have = take(next);
       ok = __all_sync(0xffffffffu, ok && mbar_wait_bounded(&ofull[a], o_n++ & 1, &s_abort));
