@@ -139,3 +139,17 @@ def test_no_rows():
     w = torch.empty((2, 0), device="cuda")
     _, _, index, keep_start, n_keep = st.kv_keep(k, k, w, starts([0, 0]), 5)
     assert index.shape == (0, 2) and keep_start.tolist() == [0, 0, 0] and n_keep.tolist() == [0, 0]
+
+
+def test_budgets_past_32_bits_and_refusals():
+    k = rows(_gen(17), 30, 2, 64)
+    w, start = _weights(_gen(18), 2, 30), starts([10, 20])
+    _run(k, k, w, start, 2 ** 32 + 3)
+    for args in ((k, k.float(), w, start, 4), (k, k[:29], w, start, 4), (k, k, w[:, :29], start, 4), (k, k, w.double(), start, 4),
+                 (k, k, w, start.long(), 4)):
+        with pytest.raises((TypeError, ValueError)):
+            st.kv_keep(*args)
+    for more in (dict(budget=0), dict(budget=-2 ** 33), dict(budget=4, first=3, last=2), dict(budget=4, first=-1), dict(budget=4, last=2 ** 33)):
+        with pytest.raises(st.SpecError) as e:
+            st.kv_keep(k, k, w, start, **more)
+        assert e.value.code == 1

@@ -146,7 +146,7 @@ def test_strides_scale_and_workspace():
         st.prompt_attention(q, k, v, start, workspace=ws[:16])
 
 
-@pytest.mark.parametrize("bad", [[0, 60, 50, 100], [-1, 50, 60, 100], [0, 50, 60, 101]])
+@pytest.mark.parametrize("bad", [[0, 60, 50, 100], [-1, 50, 60, 100], [0, 50, 60, 101], [5, 3], [-1, 50], [0, 101]])
 def test_bad_row_start_writes_nothing(bad):
     q, k, v = fused(_gen(11), 100, 4, 2, 128)
     out, lse = torch.full((100, 4, 128), 7.0, dtype=torch.bfloat16, device="cuda"), torch.full((100, 4), 7.0, device="cuda")
@@ -178,10 +178,11 @@ def test_calls_repeat_and_streams_do_not_meet():
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
 
 
-def test_captured_calls_follow_lengths_on_the_device():
+@pytest.mark.parametrize("all_lens", [([100, 500], [599, 1], [0, 600], [300, 300]), ([600], [1], [0], [300])])
+def test_captured_calls_follow_lengths_on_the_device(all_lens):
     n = 600
     q, k, v = fused(_gen(13), n, 8, 2, 64)
-    start = starts([100, 500])
+    start = starts(all_lens[0])
     out, lse = torch.empty((n, 8, 64), dtype=torch.bfloat16, device="cuda"), torch.empty((n, 8), device="cuda")
     ws = torch.empty(1 << 16, dtype=torch.uint8, device="cuda")
     st.prompt_attention(q, k, v, start, out=out, lse=lse, workspace=ws)
@@ -189,7 +190,7 @@ def test_captured_calls_follow_lengths_on_the_device():
     with torch.cuda.graph(graph):
         st.prompt_attention(q, k, v, start, out=out, lse=lse, workspace=ws)
         st.prompt_attention(q, k, v, start, out=out, lse=lse, workspace=ws)
-    for lens in ([100, 500], [599, 1], [0, 600], [300, 300]):
+    for lens in all_lens:
         start.copy_(starts(lens))
         graph.replay()
         check_attention((out, lse), q, k, v, start)
@@ -218,3 +219,25 @@ def test_many_heads_and_unaligned_rows():
     assert out.data_ptr() % 32 == 16
     got = st.prompt_attention(q, k, v, start, out=out)
     check_attention(got, q, k, v, start)
+
+
+def test_refusals():
+    start = starts([10, 20])
+    q, k, v = fused(_gen(16), 30, 4, 2, 64)
+    for args in ((q.float(), k, v, start), (q, k.half(), v, start), (q, k, v, start.long()), (q, k, v, start.cpu()), (q.cpu(), k, v, start),
+                 (q, k[:29], v, start), (q, k, v[:, :1], start), (q, k, v[..., :32], start), (q[None], k, v, start),
+                 (q.transpose(0, 1), k, v, start), (q[..., ::2], k[..., ::2], v[..., ::2], start), (q, k, v[::2], start)):
+        with pytest.raises((TypeError, ValueError)):
+            st.prompt_attention(*args)
+    for args, code in (((q.float(), k.float(), v.float(), start), 2), ((q[:, :3], k, v, start), 1),
+                       ((q[..., :32], k[..., :32], v[..., :32], start), 2), ((q.reshape(-1)[4:4 + 29 * 256].view(29, 4, 64), k[:29], v[:29], start), 1)):
+        q2 = args[0]
+        if q2.shape[2] == 32:
+            args = tuple(x.contiguous() for x in args[:3]) + args[3:]
+        with pytest.raises(st.SpecError) as e:
+            st.prompt_attention(*args)
+        assert e.value.code == code
+    out = torch.empty((30, 4, 64), dtype=torch.bfloat16, device="cuda")
+    for more in (dict(out=out[:29]), dict(out=out.float()), dict(lse=torch.empty((30, 2), device="cuda")), dict(dev_status=start.long())):
+        with pytest.raises((TypeError, ValueError)):
+            st.prompt_attention(q, k, v, start, **more)

@@ -107,7 +107,7 @@ def test_keys_with_infinities():
     assert torch.isfinite(weight).all()
 
 
-@pytest.mark.parametrize("bad", [[0, 60, 50, 100], [-1, 50, 60, 100], [0, 50, 60, 101]])
+@pytest.mark.parametrize("bad", [[0, 60, 50, 100], [-1, 50, 60, 100], [0, 50, 60, 101], [5, 3], [-1, 50], [0, 101]])
 def test_bad_row_start_writes_nothing(bad):
     q, k, _ = fused(_gen(5), 100, 4, 2, 128)
     weight = torch.full((2, 100), 7.0, device="cuda")
@@ -151,3 +151,17 @@ def test_more_heads_than_shares():
     q, k, _ = fused(_gen(8), 469, 100, 100, 64)
     lse = attention(q, k, k, start)[1].float()
     _check(st.prompt_key_weights(q, k, lse, start, 30), q, k, lse, start, 30)
+
+
+def test_windows_past_32_bits_and_refusals():
+    start = starts([10, 20])
+    q, k, _ = fused(_gen(9), 30, 4, 2, 64)
+    lse = torch.zeros((30, 4), device="cuda")
+    assert torch.equal(st.prompt_key_weights(q, k, lse, start, 2 ** 32 + 1), st.prompt_key_weights(q, k, lse, start, 20))
+    for args in ((q, k, lse.double(), start, 4), (q, k, lse[:29], start, 4), (q, k[..., :32], lse, start, 4), (q, k, lse, start.cpu(), 4)):
+        with pytest.raises((TypeError, ValueError)):
+            st.prompt_key_weights(*args)
+    for window in (0, -1, -2 ** 40):
+        with pytest.raises(st.SpecError) as e:
+            st.prompt_key_weights(q, k, lse, start, window)
+        assert e.value.code == 1

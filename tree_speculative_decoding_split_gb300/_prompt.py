@@ -99,6 +99,11 @@ def _rows(t, name, dtype, dev):
     return t.data_ptr(), rows, H, d, H * d if step is None else step
 
 
+def _clip(x):
+    """x for a 32-bit field: what lies outside is as good as its nearer end (and would be cut to its lower bits)."""
+    return max(-2 ** 31, min(int(x), 2 ** 31 - 1))
+
+
 def _on(dev, fn, *args):
     """fn(*args) with dev current (sizes go by the current device)."""
     torch = _torch()
@@ -270,7 +275,7 @@ def key_weights_args(q, k, lse, row_start, window, weight=None, scale=0.0):
     ptr = _fast(weight, "weight", torch.float32, dev, dev.index)
     if lse.shape != (rows, Hq) or weight.shape != (Hkv, rows):
         raise ValueError("lse must be [n_rows][Hq], weight [Hkv][n_rows]")
-    a = KeyWeightsArgs(code, B, Hq, Hkv, d, float(scale), int(window), 0, rows, q_step, k_step, q_ptr, k_ptr, lse_ptr, start, ptr)
+    a = KeyWeightsArgs(code, B, Hq, Hkv, d, float(scale), _clip(window), 0, rows, q_step, k_step, q_ptr, k_ptr, lse_ptr, start, ptr)
     return a, weight
 
 
@@ -307,7 +312,7 @@ def kv_keep_args(k, v, weight, row_start, budget, first=0, last=0, rows_out=None
         raise ValueError("weight must be [Hkv][n_rows]")
     B = row_start.numel() - 1
     if outputs is None:
-        n_out = min(rows, B * int(budget)) if rows_out is None else int(rows_out)
+        n_out = max(0, min(rows, B * _clip(budget))) if rows_out is None else int(rows_out)
         outputs = (torch.empty((n_out, Hkv, d), dtype=dtype, device=dev), torch.empty((n_out, Hkv, d), dtype=dtype, device=dev),
                    torch.empty((n_out, Hkv), dtype=i32, device=dev), torch.empty(B + 1, dtype=i32, device=dev),
                    torch.empty(B, dtype=i32, device=dev))
@@ -318,7 +323,7 @@ def kv_keep_args(k, v, weight, row_start, budget, first=0, last=0, rows_out=None
     if k_out.shape != (n_out, Hkv, d) or v_out.shape != k_out.shape or index.shape != (n_out, Hkv) or \
             keep_start.numel() != B + 1 or n_keep.numel() != B:
         raise ValueError("k_out and v_out must be [rows_out][Hkv][d], index [rows_out][Hkv], keep_start [B + 1], n_keep [B]")
-    a = KvKeepArgs(code, B, Hkv, d, int(budget), int(first), int(last), 0, rows, n_out, k_step, v_step, k_ptr, v_ptr, w_ptr,
+    a = KvKeepArgs(code, B, Hkv, d, _clip(budget), _clip(first), _clip(last), 0, rows, n_out, k_step, v_step, k_ptr, v_ptr, w_ptr,
                    start, *ptr)
     return a, outputs
 
