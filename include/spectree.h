@@ -20,6 +20,9 @@
  *       "ツリー構造の候補構築").
  *   spec_eagle_expand / spec_eagle_tree  Build a dynamic draft tree layer by layer from the
  *       draft model's log-probabilities, EAGLE-2 style (tech-tldr, section "ツリー検証").
+ *   spec_kv_reserve / spec_kv8_append / spec_tree_attention_kv8  The paged cache in 8 bits.
+ *   spec_rope_positions / spec_rope / spec_prompt_attention / spec_prompt_key_weights / spec_kv_keep
+ *       Prompts on their way into it.
  *
  * Conventions shared by every call
  *   - Node 0 of a tree is its root (the last accepted token); parent[0] = -1 and

@@ -23,7 +23,7 @@ def _ints(x):
 # ---- positions -----------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("lens,front,behind", [([1], 0, 0), ([5, 0, 0, 3], 0, 0), ([0, 7, 0], 3, 5), ([1024, 1, 2047], 0, 1),
-                                               ([3] * 2000, 2, 7), ([0, 0], 4, 9)])
+                                               ([3] * 2000, 2, 7), ([1] * 2048, 0, 1), ([2, 0, 1] * 700, 1, 3), ([0, 0], 4, 9)])
 def test_positions_of_rows(lens, front, behind):
     start = starts(lens, front=front)
     n_rows = int(start[-1]) + behind

@@ -5,12 +5,18 @@
 // The choice is a radix selection.  Weights become 32-bit keys in their order; three passes of 11, 11 and 10 bits
 // count the keys that share what is known of the threshold, and the bin in which the budget runs out is the
 // threshold's next piece.  Then a row stays if its key is above the threshold, or equal to it and among the first of
-// the equal ones; warps walk disjoint stretches in order, so a row's place is the number of rows that stay before
-// it, counted by ballots.  One cluster works on a request and KV head: its CTAs hold the keys in shared memory (one
-// read of the weights; stretches past 40960 keys per CTA are read again in each pass) and add their
-// counts through distributed shared memory.  All counts are integers: no order of additions changes the result.
+// the equal ones; warps walk disjoint stretches in order, four neighbouring keys to a lane, so a row's place is the
+// number of rows that stay before it: sums over the lanes, the warps and the CTAs before.  One cluster works on a
+// request and KV head: its CTAs hold the keys in shared memory (one read of the weights; stretches past 40960 keys per
+// CTA are read again in each pass), and each adds up a slice of all CTAs' counts through distributed shared memory.  All
+// counts are integers: no order of additions changes the result.
 //
 // The copy reads and writes every kept row once, with 16-byte accesses, four rows of K and V in flight per thread.
+//
+// What bounds it: the choice by its chain of passes and meetings of the cluster (three of each a pass, some 500 cycles
+// apiece), 14 to 19 us whatever the bytes; the copy by memory, at 0.88 of a plain copy's rate.  16 prompts of up to 8192
+// rows at a budget of 1024: 37.8 us; one of 131072 rows on 8 heads, a cluster of 8 each: 29.0 us (36.1 with every CTA adding
+// up all the bins).
 
 #include "pdl.cuh"
 #include "prompt.cuh"
