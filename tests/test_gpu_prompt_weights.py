@@ -95,6 +95,21 @@ def test_window_rows_with_nan_reach_the_keys_they_see():
     assert weight[0, :291].isnan().all() and torch.isfinite(weight[0, 291:]).all()
 
 
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("row", [290, 140])
+def test_window_rows_with_any_lse_reach_no_other_keys(bad, row):
+    """A row whose lse is no number (its query, or a key that it sees, was none) leaves the keys behind it as they are."""
+    start = starts([300])
+    q, k, _ = fused(_gen(11), 300, 4, 1, 64)
+    lse = attention(q, k, k, start)[1].float()
+    want = st.prompt_key_weights(q, k, lse, start, 200)
+    lse[row] = bad
+    got = st.prompt_key_weights(q, k, lse, start, 200)
+    assert torch.equal(got[0, row + 1:], want[0, row + 1:])
+    seen = got[0, :row + 1]
+    assert {math.inf: (seen <= want[0, :row + 1]).all(), -math.inf: (seen == math.inf).all()}.get(bad, seen.isnan().all())
+
+
 def test_keys_with_infinities():
     start = starts([200])
     q, k, _ = fused(_gen(4), 200, 5, 1, 128)

@@ -356,10 +356,23 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int b = 0; b < 2; ++b) {
                 const int q1 = q + b * 32;
                 if (q1 >= cols) break;
-                if (edge || q1 + 32 > cols) {
+                if (edge) {  // (masked behind the lse, which may be infinite or NaN where a row does not count)
+#pragma unroll
+                  for (int j = 0; j < 32; ++j) {
+                    const float x = fmaf(__uint_as_float(s[b][j]), p.scale_log2, -lse[q1 + j]);
+                    s[b][j] = __float_as_uint(q1 + j < lo || q1 + j >= cols ? -INFINITY : x);
+                  }
+#pragma unroll
+                  for (int j = 0; j < 32; j += 4) {
+                    sum[0] = __fadd2_rn(sum[0], make_float2(ex2_approx(__uint_as_float(s[b][j])), ex2_approx(__uint_as_float(s[b][j + 1]))));
+                    sum[1] = __fadd2_rn(sum[1], make_float2(ex2_approx(__uint_as_float(s[b][j + 2])), ex2_approx(__uint_as_float(s[b][j + 3]))));
+                  }
+                  continue;
+                }
+                if (q1 + 32 > cols) {
 #pragma unroll
                   for (int j = 0; j < 32; ++j)
-                    if (q1 + j < lo || q1 + j >= cols) s[b][j] = 0xff800000u;
+                    if (q1 + j >= cols) s[b][j] = 0xff800000u;  // (whose lse is +inf)
                 }
 #pragma unroll
                 for (int j = 0; j < 32; j += 4) {
