@@ -203,7 +203,7 @@ def test_refused_key_weights(L, kw, code):
 @pytest.mark.parametrize("kw,code", [
     (dict(dtype=3), 2), (dict(head_dim=32), 2), (dict(batch=0), 1), (dict(batch=8193), 2), (dict(num_kv_heads=0), 1),
     (dict(budget=0), 1), (dict(first=-1), 1), (dict(last=-1), 1), (dict(first=3, last=3), 1), (dict(n_rows=-1), 1),
-    (dict(rows_out=-1), 1), (dict(n_rows=1 << 31), 2), (dict(rows_out=1 << 31), 2), (dict(k_stride=120), 1), (dict(v_stride=132), 1),
+    (dict(rows_out=-1), 1), (dict(n_rows=1 << 31), 2), (dict(n_rows=(1 << 31) - 16384), 2), (dict(rows_out=1 << 31), 2), (dict(k_stride=120), 1), (dict(v_stride=132), 1),
     (dict(k=None), 1), (dict(v=ODD), 1), (dict(weight=None), 1), (dict(row_start=None), 1), (dict(index=None), 1),
     (dict(keep_start=None), 1), (dict(n_keep=None), 1), (dict(reserved0=1), 1),
     (dict(batch=8192, num_kv_heads=1 << 15, k_stride=1 << 21, v_stride=1 << 21), 2)])

@@ -14,6 +14,8 @@ namespace {
 
 constexpr long long kMaxRows = 0x7fffffffLL - 256;  // tiles may reach 255 rows past the last one
 
+constexpr long long kMaxKeepRows = 0x7fffffffLL - 16384;  // the choice counts up to two batches of a block past the last one
+
 // Rows of `heads` heads of d elements, `stride` elements apart: long enough, and multiples of 16 bytes.
 bool row_stride_ok(long long stride, long long heads, int d, int size) {
   return stride >= heads * d && (stride * size) % 16 == 0 && stride < (1LL << 38);
@@ -104,7 +106,7 @@ spec_status check_keep(const spec_kv_keep_args* a) {
   if (a->batch < 1 || a->num_kv_heads < 1 || a->n_rows < 0 || a->rows_out < 0 || a->budget < 1 || a->first < 0 || a->last < 0 ||
       (long long)a->first + a->last > a->budget || a->reserved0 != 0)
     return SPEC_ERR_INVALID_ARGUMENT;
-  if (a->n_rows > 0x7fffffffLL || a->rows_out > 0x7fffffffLL || a->batch > SPEC_MAX_RESERVE_BATCH ||
+  if (a->n_rows > kMaxKeepRows || a->rows_out > 0x7fffffffLL || a->batch > SPEC_MAX_RESERVE_BATCH ||
       (long long)a->batch * a->num_kv_heads >= (1LL << 27))
     return SPEC_ERR_UNSUPPORTED;
   if (a->rows_out * a->num_kv_heads >= (1LL << 35)) return SPEC_ERR_UNSUPPORTED;  // the copy's grid

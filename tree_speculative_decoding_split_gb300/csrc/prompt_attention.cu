@@ -257,6 +257,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(&s_tmem, 512);
     tmem_relinquish();
   }
+  // Rows behind the last head, where G does not divide 128, are never loaded: zeros, not what shared memory holds, whose
+  // scores could outgrow their reference time and again.
+  const int behind = (kRows - p.tg * p.G) * 8;  // 16-byte pieces in each of the 2 D / 64 slabs
+  for (int i = tid; i < 2 * (D / 64) * behind; i += kThreads) {
+    const int slab = i / behind, at = i - slab * behind;
+    *reinterpret_cast<uint4*>(sQ + slab * kRows * 128 + p.tg * p.G * 128 + at * 16) = make_uint4(0, 0, 0, 0);
+  }
+  if (behind) fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
