@@ -60,6 +60,31 @@ def test_long_prompts(heads):
     _run(k, k, _weights(gen, heads, n), start, 777, 3, 5)
 
 
+def test_more_rows_than_a_single_cta_holds():
+    """So many heads that no CTA has another beside it, and more rows than shared memory keeps."""
+    heads, n = 80, 42000
+    gen = _gen(5)
+    k = torch.arange(n, device="cuda").float()[:, None, None].expand(n, heads, 64).contiguous().bfloat16()
+    _run(k, k, _weights(gen, heads, n), starts([n]), 600, 1, 2)
+    w = torch.zeros((heads, n), device="cuda")
+    w[::2, 41000:41500] = 1  # what stays lies behind what is held; elsewhere all is equal
+    _run(k, k, w, starts([n]), 600)
+
+
+@pytest.mark.parametrize("batch", [31, 32, 33, 70])
+def test_batches_counted_by_warps_and_by_blocks(batch):
+    gen = _gen(batch)
+    lens = [(37 * i) % 90 for i in range(batch)]
+    start = starts(lens)
+    n = int(start[-1])
+    x = rows(gen, n, 2, 64)
+    _run(x, x, _weights(gen, 2, n), start, 40, 2, 3)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kept_rows = sum(min(c, 40) for c in lens)
+    out = st.kv_keep(x, x, _weights(gen, 2, n), start, 40, rows_out=kept_rows - 1, dev_status=status)
+    assert int(status) == 7 and not out[3].any() and not out[4].any()
+
+
 @pytest.mark.parametrize("kind", ["equal", "zeros", "two", "negative", "special", "steps"])
 def test_ties_and_order(kind):
     n, gen = 5000, _gen(11)

@@ -5,18 +5,18 @@
 // The choice is a radix selection.  Weights become 32-bit keys in their order; three passes of 11, 11 and 10 bits
 // count the keys that share what is known of the threshold, and the bin in which the budget runs out is the
 // threshold's next piece.  Then a row stays if its key is above the threshold, or equal to it and among the first of
-// the equal ones; warps walk disjoint stretches in order, four neighbouring keys to a lane, so a row's place is the
-// number of rows that stay before it: sums over the lanes, the warps and the CTAs before.  One cluster works on a
-// request and KV head: its CTAs hold the keys in shared memory (one read of the weights; stretches past 40960 keys per
-// CTA are read again in each pass), and each adds up a slice of all CTAs' counts through distributed shared memory.  All
-// counts are integers: no order of additions changes the result.
+// the equal ones; threads have neighbouring keys, so a row's place is the number of rows that stay before it: sums
+// over the threads, the warps and the CTAs before.  One cluster works on a request and KV head: its CTAs hold the keys in
+// shared memory (one read of the weights; stretches past 40960 keys per CTA are read again in each pass), tell one another
+// how many counts lie in each slice of the bins, and the one whose slice has the threshold adds it up through
+// distributed shared memory.  All counts are integers: no order of additions changes the result.
 //
 // The copy reads and writes every kept row once, with 16-byte accesses, four rows of K and V in flight per thread.
 //
-// What bounds it: the choice by its chain of passes and meetings of the cluster (three of each a pass, some 500 cycles
-// apiece), 14 to 19 us whatever the bytes; the copy by memory, at 0.88 of a plain copy's rate.  16 prompts of up to 8192
-// rows at a budget of 1024: 37.8 us; one of 131072 rows on 8 heads, a cluster of 8 each: 29.0 us (36.1 with every CTA adding
-// up all the bins).
+// What bounds it: the choice by its chain of passes and meetings of the cluster (two a pass), 11 to 15 us whatever the
+// bytes; the copy by memory, at 0.88 of a plain copy's rate.  16 prompts of up to 8192 rows at a budget of 1024: 35.1 us; one
+// of 131072 rows on 8 heads, a cluster of 8 each: 24.9 us (36.1 with every CTA adding up all the bins, 29.0 with every CTA
+// adding up a slice, a third meeting and the last walk in steps of 128 keys a warp).
 
 #include "pdl.cuh"
 #include "prompt.cuh"
@@ -73,6 +73,31 @@ __device__ __forceinline__ Kept count_kept(const KeepParams& p, int upto, long l
   return k;
 }
 
+// Request b as a CTA of the choice needs it: rows kept of it, before it and in all (-1 where they are refused).
+struct Request {
+  int keep, before, total, r0, n;
+};
+// Up to 32 requests, by every warp for itself, with one read and no meeting of the block (1 us less than count_kept).  Rows
+// kept are rows there are: sums stay below 2^31.
+__device__ __forceinline__ Request request_in_warp(const KeepParams& p, int b) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = 0;
+  if (lane < p.B) {
+    lo = p.row_start[lane];
+    hi = p.row_start[lane + 1];
+  }
+  const bool ok = !__any_sync(0xffffffffu, lo < 0 || hi < lo || hi > p.n_rows);
+  const int kept = !ok ? 0 : (hi - lo < p.budget ? hi - lo : p.budget);
+  Request r;
+  r.total = __reduce_add_sync(0xffffffffu, kept);
+  r.before = __reduce_add_sync(0xffffffffu, lane < b ? kept : 0);
+  r.keep = __shfl_sync(0xffffffffu, kept, b);
+  r.r0 = __shfl_sync(0xffffffffu, lo, b);
+  r.n = __shfl_sync(0xffffffffu, hi, b) - r.r0;
+  if (!ok || r.total > p.rows_out) r.total = -1;
+  return r;
+}
+
 // The counts of a large batch, once for all (a small one's are worked out by every CTA of the choice).
 __global__ void __launch_bounds__(kThreads) keep_counts_kernel(const KeepParams p) {
   __shared__ long long s_sum[kWarps][2];
@@ -119,18 +144,16 @@ __device__ __forceinline__ void cluster_st(int* at, uint32_t rank, int v) {
   asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(cluster_addr(at, rank)), "r"(v) : "memory");
 }
 
-struct SelectShared {
-  int part[4][2048];    // a pass's counts, by warp & 3
-  int bins[3][2048];    // their sums, one set per pass (other CTAs read them)
+struct alignas(16) SelectShared {
+  int part[4][2048];    // the first pass's counts, by warp & 3
+  int bins[3][2048];    // each pass's counts (other CTAs read them)
   int warp_sum[kWarps];
-  int totals[2];        // keys above and at the threshold
   int warp_n[kWarps][2];
   int bin, left;        // written by the CTA that finds them, in every CTA of the cluster
-  int slice[8];         // keys in each CTA's slice of the bins
+  int slice[8][8];      // [CTA][slice of the bins] its counts there, in every CTA
+  int totals[8][2];     // [CTA] its keys above and at the threshold, in every CTA
   long long sum[kWarps][2];
 };
-
-static_assert(sizeof(SelectShared) % 16 == 0, "the keys behind it are read four at a time");
 
 __global__ void __launch_bounds__(kThreads, 1) keep_select_kernel(const KeepParams p, int32_t* source, int cluster, int counted) {
   extern __shared__ __align__(16) uint8_t s_raw[];
@@ -142,26 +165,36 @@ __global__ void __launch_bounds__(kThreads, 1) keep_select_kernel(const KeepPara
   const int b = seg / p.Hkv, g = seg % p.Hkv;
   pdl_wait();
   pdl_launch_dependents();
-  int keep;
-  long long out0;
+  Request r;
   if (counted) {
-    keep = p.n_keep[b];
-    out0 = p.keep_start[b];
+    r.keep = p.n_keep[b];
+    r.before = p.keep_start[b];
   } else {
-    const Kept k = count_kept(p, b, s.sum);
-    keep = k.total < 0 ? 0 : rows_kept(p, b);
-    out0 = k.total < 0 ? 0 : k.before;
+    if (p.B <= 32) {
+      r = request_in_warp(p, b);
+    } else {
+      const Kept k = count_kept(p, b, s.sum);
+      r.total = (int)k.total;
+      r.before = (int)k.before;
+      r.keep = r.total < 0 ? 0 : rows_kept(p, b);
+    }
+    if (r.total < 0) r.keep = r.before = 0;
     if (rank == 0 && g == 0 && tid == 0) {
-      p.n_keep[b] = keep;
-      p.keep_start[b] = (int)out0;
+      p.n_keep[b] = r.keep;
+      p.keep_start[b] = r.before;
       if (b == 0) {
-        p.keep_start[p.B] = k.total < 0 ? 0 : (int)k.total;
-        if (k.total < 0) set_status(p.dev_status, SPEC_ERR_CAPACITY);
+        p.keep_start[p.B] = r.total < 0 ? 0 : r.total;
+        if (r.total < 0) set_status(p.dev_status, SPEC_ERR_CAPACITY);
       }
     }
   }
-  if (keep == 0) return;  // (the whole cluster)
-  const int r0 = p.row_start[b], n = p.row_start[b + 1] - r0;
+  if (r.keep == 0) return;  // (the whole cluster)
+  if (counted || p.B > 32) {
+    r.r0 = p.row_start[b];
+    r.n = p.row_start[b + 1] - r.r0;
+  }
+  const int r0 = r.r0, n = r.n;
+  const long long out0 = r.before;
   auto put = [&](int place, int j) {
     const long long at = (out0 + place) * p.Hkv + g;
     p.index[at] = j;
@@ -177,99 +210,135 @@ __global__ void __launch_bounds__(kThreads, 1) keep_select_kernel(const KeepPara
   }
   int left = p.budget - p.first - p.last;  // rows to choose
   if (left == 0) return;
+  __syncwarp();
+  if (cluster > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // (it runs: others may write to it)
   // candidates [first, n - last); this CTA's are [c0, c1)
   const int cands = n - p.first - p.last;
   const int per = (int)(((long long)cands + cluster - 1) / cluster);
   const long long lo = (long long)rank * per, hi = lo + per < cands ? lo + per : cands;
   const int mine = hi > lo ? (int)(hi - lo) : 0;
   const float* weight = p.weight + (size_t)g * p.n_rows + r0 + p.first + (mine ? lo : 0);
-  auto key_at = [&](int i) { return i < kHeld ? s_key[i] : order_u(weight[i]); };
+  const int held = mine < kHeld ? mine : kHeld;
+  for (int i = tid; i < 4 * 2048; i += kThreads) (&s.part[0][0])[i] = 0;
+  for (int i = tid; i < 2 * 2048; i += kThreads) s.bins[1][i] = 0;  // (and the last)
   uint32_t known = 0;  // the threshold's upper bits
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
     const int bits = pass == 2 ? 10 : 11;
-    for (int i = tid; i < 4 * 2048; i += kThreads) (&s.part[0][0])[i] = 0;
-    __syncthreads();
-    int* part = s.part[warp & 3];
-    for (int i0 = tid; i0 < mine; i0 += kThreads * kBatch) {
-      uint32_t key[kBatch];  // (all reads first)
-#pragma unroll
-      for (int e = 0; e < kBatch; ++e) {
-        const int i = i0 + e * kThreads;
-        key[e] = i < mine ? (pass == 0 ? __float_as_uint(weight[i]) : key_at(i)) : 0u;
-      }
-#pragma unroll
-      for (int e = 0; e < kBatch; ++e) {
-        const int i = i0 + e * kThreads;
-        if (i >= mine) break;
-        if (pass == 0) {
-          key[e] = order_u(__uint_as_float(key[e]));
-          if (i < kHeld) s_key[i] = key[e];
-        }
-        if (pass == 0 || (key[e] >> (shift + bits)) == known) atomicAdd(&part[(key[e] >> shift) & ((1u << bits) - 1)], 1);
-      }
-    }
-    __syncthreads();
-    for (int i = tid; i < 2048; i += kThreads) s.bins[pass][i] = s.part[0][i] + s.part[1][i] + s.part[2][i] + s.part[3][i];
-    if (cluster > 1)
-      cluster_sync_all();
-    else
+    const uint32_t mask = (1u << bits) - 1;
+    if (pass == 0) {
       __syncthreads();
-    // The bin, from above, in which the rows to choose run out.  Each CTA sums a slice of the bins over the cluster (all of
-    // them in every CTA took 8000 cycles a pass), rank 0 the uppermost; a thread looks at two neighbouring bins of it.
-    const int slice = 2048 / cluster, top_bin = 2047 - rank * slice - 2 * tid;
-    const bool mine_bins = 2 * tid < slice;
-    int x[2] = {0, 0};
-    if (mine_bins) {
+      int* part = s.part[warp & 3];
+      for (int i0 = tid; i0 < mine; i0 += kThreads * kBatch) {
+        float w[kBatch];  // (all reads first)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        if (cluster > 1) {
-#pragma unroll 8
-          for (int r = 0; r < cluster; ++r) x[e] += cluster_ld(&s.bins[pass][top_bin - e], (uint32_t)r);
-        } else {
-          x[e] = s.bins[pass][top_bin - e];
+        for (int e = 0; e < kBatch; ++e) {
+          const int i = i0 + e * kThreads;
+          w[e] = i < mine ? weight[i] : 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) {
+          const int i = i0 + e * kThreads;
+          if (i >= mine) break;
+          const uint32_t key = order_u(w[e]);
+          if (i < kHeld) s_key[i] = key;
+          atomicAdd(&part[key >> 21], 1);
         }
       }
-    }
-    int v = x[0] + x[1];
+    } else {
+      // few keys share what is known: one set of counts, keys read four at a time
+      int* bins = s.bins[pass];
+      auto add = [&](uint32_t key) {
+        if (key >> (shift + bits) == known) atomicAdd(&bins[(key >> shift) & mask], 1);
+      };
+      for (int i = tid * 4; i < held; i += kThreads * 4) {
+        if (i + 4 <= held) {
+          const uint4 k = *reinterpret_cast<const uint4*>(s_key + i);
+          add(k.x), add(k.y), add(k.z), add(k.w);
+        } else {
+          for (int e = i; e < held; ++e) add(s_key[e]);
+        }
+      }
+      for (int i0 = kHeld + tid; i0 < mine; i0 += kThreads * kBatch) {
+        float w[kBatch];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += y;
+        for (int e = 0; e < kBatch; ++e) w[e] = i0 + e * kThreads < mine ? weight[i0 + e * kThreads] : 0.f;
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e)
+          if (i0 + e * kThreads < mine) add(order_u(w[e]));
+      }
     }
-    if (lane == 31) s.warp_sum[warp] = v;
     __syncthreads();
-    int above = v - x[0] - x[1];
-    {  // every warp scans the warps' sums for itself
-      int y = s.warp_sum[lane];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int z = __shfl_up_sync(0xffffffffu, y, o);
-        if (lane >= o) y += z;
-      }
-      const int before = __shfl_sync(0xffffffffu, y, (warp + 31) & 31), all = __shfl_sync(0xffffffffu, y, 31);
-      if (warp > 0) above += before;
-      if (cluster > 1) {
-        if (tid < cluster) cluster_st(&s.slice[rank], (uint32_t)tid, all);
-        cluster_sync_all();
-        for (int r = 0; r < rank; ++r) above += s.slice[r];
-      }
-    }
+    // The bin, from above, in which the rows to choose run out.  A thread has two neighbouring bins, in falling order.
+    int top_bin = 2047 - 2 * tid, above = 0;
+    int x[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      if (mine_bins && above < left && above + x[e] >= left) {
-        for (int r = 0; r < cluster; ++r) {
-          if (cluster > 1) {
-            cluster_st(&s.bin, (uint32_t)r, top_bin - e);
-            cluster_st(&s.left, (uint32_t)r, left - above);
-          } else {
-            s.bin = top_bin - e;
-            s.left = left - above;
+      const int i = top_bin - e;
+      if (pass == 0) s.bins[0][i] = s.part[0][i] + s.part[1][i] + s.part[2][i] + s.part[3][i];
+      x[e] = s.bins[pass][i];
+    }
+    bool finds = true;
+    if (cluster > 1) {
+      // Every CTA tells all others what it has in each of `cluster` slices of the bins.  So each knows of its own slice (rank
+      // 0 has the uppermost) whether the rows run out there, and that one alone adds up the bins of it over the cluster (all
+      // bins in every CTA took 8000 cycles a pass, a slice in every CTA and a third meeting 5200 where this takes 3500).
+      const int sum = __reduce_add_sync(0xffffffffu, x[0] + x[1]);
+      if (lane == 0) s.warp_sum[warp] = sum;
+      __syncthreads();
+      if (pass == 0) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+      if (tid < cluster * cluster) {
+        const int to = tid / cluster, slice = tid % cluster, warps = kWarps / cluster;
+        int n_slice = 0;
+        for (int w = 0; w < warps; ++w) n_slice += s.warp_sum[slice * warps + w];
+        cluster_st(&s.slice[rank][slice], (uint32_t)to, n_slice);
+      }
+      cluster_sync_all();
+      int before = 0, inside = 0;
+      for (int i = lane; i < cluster * cluster; i += 32) {
+        const int v = s.slice[i / cluster][i % cluster];
+        if (i % cluster < rank) before += v;
+        if (i % cluster == rank) inside += v;
+      }
+      above = __reduce_add_sync(0xffffffffu, before);
+      inside = __reduce_add_sync(0xffffffffu, inside);
+      finds = above < left && above + inside >= left;
+      const int slice = 2048 / cluster;
+      top_bin -= rank * slice;
+      x[0] = x[1] = 0;
+      if (finds && 2 * tid < slice) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll 8
+          for (int c = 0; c < cluster; ++c) x[e] += cluster_ld(&s.bins[pass][top_bin - e], (uint32_t)c);
+      }
+    }
+    if (finds) {  // (the whole block)
+      int v = x[0] + x[1];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += y;
+      }
+      if (lane == 31) s.warp_sum[warp] = v;
+      __syncthreads();
+      above += v - x[0] - x[1] + __reduce_add_sync(0xffffffffu, lane < warp ? s.warp_sum[lane] : 0);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if (above < left && above + x[e] >= left) {
+          for (int c = 0; c < cluster; ++c) {
+            if (cluster > 1) {
+              cluster_st(&s.bin, (uint32_t)c, top_bin - e);
+              cluster_st(&s.left, (uint32_t)c, left - above);
+            } else {
+              s.bin = top_bin - e;
+              s.left = left - above;
+            }
           }
         }
+        above += x[e];
       }
-      above += x[e];
     }
     if (cluster > 1)
       cluster_sync_all();
@@ -277,97 +346,90 @@ __global__ void __launch_bounds__(kThreads, 1) keep_select_kernel(const KeepPara
       __syncthreads();
     known = (known << bits) | (uint32_t)s.bin;
     left = s.left;
-    __syncthreads();
   }
-  // `known` is the threshold, `left` the number of keys equal to it that stay.  Warps walk stretches, four neighbouring keys
-  // per lane; keys above and at the threshold are counted in the halves of a word (128 a step) and summed apart.
-  const int stretch = ((mine + kWarps - 1) / kWarps + 127) & ~127;
-  const int w0 = warp * stretch < mine ? warp * stretch : mine, w1 = w0 + stretch < mine ? w0 + stretch : mine;
-  auto four = [&](int i, uint32_t (&key)[4]) {
-    if (i + 4 <= w1 && i + 4 <= kHeld) {
+  // `known` is the threshold, `left` the number of keys equal to it that stay.  Every thread has neighbouring keys, as many
+  // as make 16 bytes times an odd number (so that a warp's reads spread over the banks); keys above and at the threshold
+  // are counted in the halves of a word (40960 of each at most).  Keys that are not held are walked by warps behind them.
+  const int fours = (held + 4 * kThreads - 1) / (4 * kThreads) | 1;
+  const int t0 = tid * fours * 4 < held ? tid * fours * 4 : held, t1 = t0 + fours * 4 < held ? t0 + fours * 4 : held;
+  auto of = [&](uint32_t key) { return key > known ? 1u : (key == known ? 0x10000u : 0u); };
+  uint32_t n_mine = 0;
+  for (int i = t0; i < t1; i += 4) {
+    if (i + 4 <= t1) {
       const uint4 k = *reinterpret_cast<const uint4*>(s_key + i);
-      key[0] = k.x, key[1] = k.y, key[2] = k.z, key[3] = k.w;
+      n_mine += of(k.x) + of(k.y) + of(k.z) + of(k.w);
     } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) key[e] = i + e < w1 ? key_at(i + e) : 0u;
+      for (int e = i; e < t1; ++e) n_mine += of(s_key[e]);
     }
-  };
-  // (known == 0: NaN alone are at the threshold, and places behind the stretch are not keys)
-  auto count = [&](int i, const uint32_t (&key)[4]) {
-    uint32_t n = 0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (i + e < w1) n += key[e] > known ? 1u : (key[e] == known ? 0x10000u : 0u);
-    return n;
-  };
-  int above = 0, equal = 0;
-  for (int i = w0 + lane * 4; i < w1; i += 128) {
-    uint32_t key[4];
-    four(i, key);
-    const uint32_t n = count(i, key);
-    above += n & 0xffffu;
-    equal += n >> 16;
   }
+  uint32_t n_sum = n_mine;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    above += __shfl_xor_sync(0xffffffffu, above, o);
-    equal += __shfl_xor_sync(0xffffffffu, equal, o);
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, n_sum, o);
+    if (lane >= o) n_sum += y;
   }
-  if (lane == 0) {
-    s.warp_n[warp][0] = above;
-    s.warp_n[warp][1] = equal;
+  if (lane == 31) s.warp_sum[warp] = (int)n_sum;
+  const int rest = mine - held, stretch = ((rest + kWarps - 1) / kWarps + 31) & ~31;
+  const int w0 = held + (warp * stretch < rest ? warp * stretch : rest), w1 = mine - w0 > stretch ? w0 + stretch : mine;
+  if (rest > 0) {
+    int up = 0, eq = 0;
+    for (int i = w0 + lane; i < w1; i += 32) {
+      const uint32_t key = order_u(weight[i]);
+      up += key > known;
+      eq += key == known;
+    }
+    up = __reduce_add_sync(0xffffffffu, up);
+    eq = __reduce_add_sync(0xffffffffu, eq);
+    if (lane == 0) s.warp_n[warp][0] = up, s.warp_n[warp][1] = eq;
   }
   __syncthreads();
-  {  // sums over the warps before this one, and over the CTAs before
-    int n[2] = {s.warp_n[lane][0], s.warp_n[lane][1]};
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      int y = n[e];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int z = __shfl_up_sync(0xffffffffu, y, o);
-        if (lane >= o) y += z;
-      }
-      const int all = __shfl_sync(0xffffffffu, y, 31);
-      if (tid == 0) s.totals[e] = all;
-      const int before = __shfl_sync(0xffffffffu, y - n[e], warp);
-      (e ? equal : above) = before;
-    }
+  const uint32_t warp_sum = (uint32_t)s.warp_sum[lane];
+  const uint32_t all = __reduce_add_sync(0xffffffffu, warp_sum);
+  const uint32_t n_before = __reduce_add_sync(0xffffffffu, lane < warp ? warp_sum : 0u) + n_sum - n_mine;
+  int above = 0, equal = 0;  // in the CTAs before this one
+  int rest_up = (int)(all & 0xffffu), rest_eq = (int)(all >> 16), up_all = rest_up, eq_all = rest_eq;
+  if (rest > 0) {
+    const int up = s.warp_n[lane][0], eq = s.warp_n[lane][1];
+    up_all += __reduce_add_sync(0xffffffffu, up);
+    eq_all += __reduce_add_sync(0xffffffffu, eq);
+    rest_up += __reduce_add_sync(0xffffffffu, lane < warp ? up : 0);
+    rest_eq += __reduce_add_sync(0xffffffffu, lane < warp ? eq : 0);
   }
   if (cluster > 1) {
-    cluster_sync_all();
-    for (int r = 0; r < rank; ++r) {
-      above += cluster_ld(&s.totals[0], (uint32_t)r);
-      equal += cluster_ld(&s.totals[1], (uint32_t)r);
+    if (tid < cluster) {
+      cluster_st(&s.totals[rank][0], (uint32_t)tid, up_all);
+      cluster_st(&s.totals[rank][1], (uint32_t)tid, eq_all);
+    }
+    cluster_sync_all();  // (the last: no CTA touches another's memory from here on)
+    for (int c = 0; c < rank; ++c) {
+      above += s.totals[c][0];
+      equal += s.totals[c][1];
     }
   }
-  for (int i0 = w0; i0 < w1; i0 += 128) {
-    const int i = i0 + lane * 4;
-    uint32_t key[4];
-    four(i, key);
-    const uint32_t n = count(i, key);
-    uint32_t sum = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t z = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += z;
+  if (n_mine) {
+    int up = above + (int)(n_before & 0xffffu), eq = equal + (int)(n_before >> 16);
+    for (int i = t0; i < t1; ++i) {
+      const uint32_t key = s_key[i];
+      const bool is_up = key > known, is_eq = key == known;
+      if (is_up || (is_eq && eq < left)) put(p.first + up + (eq < left ? eq : left), p.first + (int)lo + i);
+      up += is_up;
+      eq += is_eq;
     }
-    const uint32_t all = __shfl_sync(0xffffffffu, sum, 31);
-    int up = above + (int)((sum - n) & 0xffffu), eq = equal + (int)((sum - n) >> 16);
-    if (n) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (i + e >= w1) break;
-        const bool is_up = key[e] > known, is_eq = key[e] == known;
-        if (is_up || (is_eq && eq < left)) put(p.first + up + (eq < left ? eq : left), p.first + (int)lo + i + e);
-        up += is_up;
-        eq += is_eq;
-      }
-    }
-    above += all & 0xffffu;
-    equal += all >> 16;
   }
-  if (cluster > 1) cluster_sync_all();  // no CTA leaves while another may still read its counts
+  if (rest > 0) {
+    above += rest_up;
+    equal += rest_eq;
+    for (int i0 = w0; i0 < w1; i0 += 32) {
+      const int i = i0 + lane;
+      const uint32_t key = i < w1 ? order_u(weight[i]) : 0u;
+      const bool is_up = i < w1 && key > known, is_eq = i < w1 && key == known;
+      const uint32_t ups = __ballot_sync(0xffffffffu, is_up), eqs = __ballot_sync(0xffffffffu, is_eq), low = (1u << lane) - 1;
+      const int up = above + __popc(ups & low), eq = equal + __popc(eqs & low);
+      if (is_up || (is_eq && eq < left)) put(p.first + up + (eq < left ? eq : left), p.first + (int)lo + i);
+      above += __popc(ups);
+      equal += __popc(eqs);
+    }
+  }
 }
 
 // Copies K and V of every kept (row, head): `vecs` lanes of 16 bytes per row.
