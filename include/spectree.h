@@ -772,7 +772,7 @@ spec_status spec_prompt_key_weights(const spec_key_weights_args* args, void* wor
  * keep_start are then 0 and no row is written.
  * Host errors: SPEC_ERR_INVALID_ARGUMENT (sizes < 1, first or last < 0, first + last > budget, NULL
  * pointers, strides or addresses that are no multiple of 16 bytes or too short), SPEC_ERR_UNSUPPORTED (dtype,
- * head_dim, n_rows >= 2^31 - 16384, rows_out >= 2^31, B > SPEC_MAX_RESERVE_BATCH, B * Hkv >= 2^27), SPEC_ERR_WORKSPACE_TOO_SMALL. */
+ * head_dim, n_rows >= 2^31 - 16384, rows_out >= 2^31, rows_out * Hkv >= 2^33, B > SPEC_MAX_RESERVE_BATCH, B * Hkv >= 2^27), SPEC_ERR_WORKSPACE_TOO_SMALL. */
 typedef struct spec_kv_keep_args {
   int32_t dtype;            /* of k, v: SPEC_DTYPE_BF16 or SPEC_DTYPE_F32 */
   int32_t batch;            /* B */

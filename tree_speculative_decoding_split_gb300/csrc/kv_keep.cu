@@ -11,12 +11,13 @@
 // how many counts lie in each slice of the bins, and the one whose slice has the threshold adds it up through
 // distributed shared memory.  All counts are integers: no order of additions changes the result.
 //
-// The copy reads and writes every kept row once, with 16-byte accesses, four rows of K and V in flight per thread.
+// The copy reads and writes every kept row once, 16 bytes of K and of V per thread; what it reads makes way in the L2 for
+// what it writes, which the cache's append reads next (16 prompts 32.2 us without; two rows a thread 32.8, four 34.8).
 //
-// What bounds it: the choice by its chain of passes and meetings of the cluster (two a pass), 11 to 15 us whatever the
-// bytes; the copy by memory, at 0.88 of a plain copy's rate.  16 prompts of up to 8192 rows at a budget of 1024: 35.1 us; one
-// of 131072 rows on 8 heads, a cluster of 8 each: 24.9 us (36.1 with every CTA adding up all the bins, 29.0 with every CTA
-// adding up a slice, a third meeting and the last walk in steps of 128 keys a warp).
+// What bounds it: the choice by its chain of passes and meetings of the cluster (two a pass), 10 to 14 us whatever the
+// bytes; the copy by memory.  16 prompts of up to 8192 rows at a budget of 1024: 29.1 us; one of 131072 rows on 8 heads, a
+// cluster of 8 each: 22.3 us (before its last copy, 36.1 with every CTA adding up all the bins, 29.0 with every CTA adding up a
+// slice, a third meeting and the last walk in steps of 128 keys a warp, 22.9 as it is).
 
 #include "pdl.cuh"
 #include "prompt.cuh"
@@ -31,7 +32,6 @@ constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kHeld = 40960;        // keys a CTA holds
 constexpr int kCopyThreads = 256;
-constexpr int kCopies = 4;          // (row, head)s per thread
 constexpr int kBatch = 8;           // keys of a thread on their way at once
 constexpr int kCountedBatch = 1024; // requests from which the counts have a kernel of their own
 
@@ -155,13 +155,13 @@ struct alignas(16) SelectShared {
   long long sum[kWarps][2];
 };
 
-__global__ void __launch_bounds__(kThreads, 1) keep_select_kernel(const KeepParams p, int32_t* source, int cluster, int counted) {
+__global__ void __launch_bounds__(kThreads, 1) keep_select_kernel(const KeepParams p, int32_t* source, int log_cluster, int counted) {
   extern __shared__ __align__(16) uint8_t s_raw[];
   SelectShared& s = *reinterpret_cast<SelectShared*>(s_raw);
   uint32_t* s_key = reinterpret_cast<uint32_t*>(s_raw + sizeof(SelectShared));  // [kHeld]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rank = cluster > 1 ? (int)cluster_rank() : 0;
-  const int seg = blockIdx.x / cluster;
+  const int cluster = 1 << log_cluster, rank = cluster > 1 ? (int)cluster_rank() : 0;
+  const int seg = (int)(blockIdx.x >> log_cluster);
   const int b = seg / p.Hkv, g = seg % p.Hkv;
   pdl_wait();
   pdl_launch_dependents();
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1) keep_select_kernel(const KeepPara
   if (cluster > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // (it runs: others may write to it)
   // candidates [first, n - last); this CTA's are [c0, c1)
   const int cands = n - p.first - p.last;
-  const int per = (int)(((long long)cands + cluster - 1) / cluster);
+  const int per = (int)(((long long)cands + cluster - 1) >> log_cluster);
   const long long lo = (long long)rank * per, hi = lo + per < cands ? lo + per : cands;
   const int mine = hi > lo ? (int)(hi - lo) : 0;
   const float* weight = p.weight + (size_t)g * p.n_rows + r0 + p.first + (mine ? lo : 0);
@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1) keep_select_kernel(const KeepPara
       __syncthreads();
       if (pass == 0) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
       if (tid < cluster * cluster) {
-        const int to = tid / cluster, slice = tid % cluster, warps = kWarps / cluster;
+        const int to = tid >> log_cluster, slice = tid & (cluster - 1), warps = kWarps >> log_cluster;
         int n_slice = 0;
         for (int w = 0; w < warps; ++w) n_slice += s.warp_sum[slice * warps + w];
         cluster_st(&s.slice[rank][slice], (uint32_t)to, n_slice);
@@ -297,14 +297,14 @@ __global__ void __launch_bounds__(kThreads, 1) keep_select_kernel(const KeepPara
       cluster_sync_all();
       int before = 0, inside = 0;
       for (int i = lane; i < cluster * cluster; i += 32) {
-        const int v = s.slice[i / cluster][i % cluster];
-        if (i % cluster < rank) before += v;
-        if (i % cluster == rank) inside += v;
+        const int slice = i & (cluster - 1), v = s.slice[i >> log_cluster][slice];
+        if (slice < rank) before += v;
+        if (slice == rank) inside += v;
       }
       above = __reduce_add_sync(0xffffffffu, before);
       inside = __reduce_add_sync(0xffffffffu, inside);
       finds = above < left && above + inside >= left;
-      const int slice = 2048 / cluster;
+      const int slice = 2048 >> log_cluster;
       top_bin -= rank * slice;
       x[0] = x[1] = 0;
       if (finds && 2 * tid < slice) {
@@ -353,14 +353,17 @@ __global__ void __launch_bounds__(kThreads, 1) keep_select_kernel(const KeepPara
   const int fours = (held + 4 * kThreads - 1) / (4 * kThreads) | 1;
   const int t0 = tid * fours * 4 < held ? tid * fours * 4 : held, t1 = t0 + fours * 4 < held ? t0 + fours * 4 : held;
   auto of = [&](uint32_t key) { return key > known ? 1u : (key == known ? 0x10000u : 0u); };
-  uint32_t n_mine = 0;
-  for (int i = t0; i < t1; i += 4) {
+  uint32_t n_mine = 0, there = 0;  // there: a bit for each four keys with one that may stay
+  for (int i = t0, bit = 1; i < t1; i += 4, bit <<= 1) {
+    uint32_t n_four = 0;
     if (i + 4 <= t1) {
       const uint4 k = *reinterpret_cast<const uint4*>(s_key + i);
-      n_mine += of(k.x) + of(k.y) + of(k.z) + of(k.w);
+      n_four = of(k.x) + of(k.y) + of(k.z) + of(k.w);
     } else {
-      for (int e = i; e < t1; ++e) n_mine += of(s_key[e]);
+      for (int e = i; e < t1; ++e) n_four += of(s_key[e]);
     }
+    n_mine += n_four;
+    if (n_four) there |= bit;
   }
   uint32_t n_sum = n_mine;
 #pragma unroll
@@ -406,9 +409,10 @@ __global__ void __launch_bounds__(kThreads, 1) keep_select_kernel(const KeepPara
       equal += s.totals[c][1];
     }
   }
-  if (n_mine) {
-    int up = above + (int)(n_before & 0xffffu), eq = equal + (int)(n_before >> 16);
-    for (int i = t0; i < t1; ++i) {
+  int up = above + (int)(n_before & 0xffffu), eq = equal + (int)(n_before >> 16);
+  for (; there; there &= there - 1) {
+    const int i0 = t0 + 4 * (__ffs(there) - 1), i1 = i0 + 4 < t1 ? i0 + 4 : t1;
+    for (int i = i0; i < i1; ++i) {
       const uint32_t key = s_key[i];
       const bool is_up = key > known, is_eq = key == known;
       if (is_up || (is_eq && eq < left)) put(p.first + up + (eq < left ? eq : left), p.first + (int)lo + i);
@@ -432,32 +436,21 @@ __global__ void __launch_bounds__(kThreads, 1) keep_select_kernel(const KeepPara
   }
 }
 
-// Copies K and V of every kept (row, head): `vecs` lanes of 16 bytes per row.
-__global__ void __launch_bounds__(kCopyThreads) keep_copy_kernel(const KeepParams p, const int32_t* source, int vecs) {
+// Copies K and V of every kept (row, head), 2^log_vecs lanes of 16 bytes per row.
+__global__ void __launch_bounds__(kCopyThreads) keep_copy_kernel(const KeepParams p, const int32_t* source, int log_vecs) {
   pdl_wait();
   const long long units = (long long)p.keep_start[p.B] * p.Hkv;
-  const int per_block = kCopyThreads / vecs;  // units side by side
-  const int lane = threadIdx.x % vecs, at = threadIdx.x / vecs;
-  const long long u0 = (long long)blockIdx.x * per_block * kCopies + at;
-  uint4 kv[kCopies][2];
-#pragma unroll
-  for (int f = 0; f < kCopies; ++f) {
-    const long long u = u0 + (long long)f * per_block;
-    if (u < units) {
-      const long long row = source[u];
-      const int g = (int)(u % p.Hkv);
-      kv[f][0] = *reinterpret_cast<const uint4*>(p.k + row * p.k_stride + (size_t)g * p.row_bytes + lane * 16);
-      kv[f][1] = *reinterpret_cast<const uint4*>(p.v + row * p.v_stride + (size_t)g * p.row_bytes + lane * 16);
-    }
-  }
-#pragma unroll
-  for (int f = 0; f < kCopies; ++f) {
-    const long long u = u0 + (long long)f * per_block;
-    if (u < units) {
-      *reinterpret_cast<uint4*>(p.k_out + (size_t)u * p.row_bytes + lane * 16) = kv[f][0];
-      *reinterpret_cast<uint4*>(p.v_out + (size_t)u * p.row_bytes + lane * 16) = kv[f][1];
-    }
-  }
+  const int vecs = 1 << log_vecs;
+  const int lane = threadIdx.x & (vecs - 1);
+  const long long u = ((long long)blockIdx.x * kCopyThreads + threadIdx.x) >> log_vecs;
+  if (u >= units) return;
+  const int row = source[u];
+  const int g = u <= 0xffffffffLL ? (int)((unsigned)u % (unsigned)p.Hkv) : (int)(u % p.Hkv);
+  const size_t in = (size_t)g * p.row_bytes + lane * 16, out = (size_t)u * p.row_bytes + lane * 16;
+  const uint4 k = __ldcs(reinterpret_cast<const uint4*>(p.k + row * p.k_stride + in));
+  const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p.v + row * p.v_stride + in));
+  *reinterpret_cast<uint4*>(p.k_out + out) = k;
+  *reinterpret_cast<uint4*>(p.v_out + out) = v;
 }
 
 }  // namespace
@@ -471,8 +464,9 @@ cudaError_t launch_kv_keep(const KeepParams& p, int32_t* source, int num_sms, cu
   if (err != cudaSuccess || !copies) return err;
   // CTAs per request and head: as many as there are SMs for, and 2048 rows for each.
   const long long segs = (long long)p.B * p.Hkv;
-  int cluster = 1;
-  while (cluster < 8 && segs * cluster * 2 <= num_sms && (long long)cluster * 2 * 2048 <= p.n_rows) cluster *= 2;
+  int log_cluster = 0;
+  while (log_cluster < 3 && (segs << (log_cluster + 1)) <= num_sms && (2LL * 2048 << log_cluster) <= p.n_rows) ++log_cluster;
+  const int cluster = 1 << log_cluster;
   err = cudaFuncSetAttribute(keep_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)sizeof(SelectShared) + kHeld * 4);
   if (err != cudaSuccess) return err;
@@ -490,13 +484,13 @@ cudaError_t launch_kv_keep(const KeepParams& p, int32_t* source, int num_sms, cu
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  err = cudaLaunchKernelEx(&cfg, keep_select_kernel, p, source, cluster, counted);
+  err = cudaLaunchKernelEx(&cfg, keep_select_kernel, p, source, log_cluster, counted);
   if (err != cudaSuccess) return err;
-  const int vecs = p.row_bytes / 16;
-  const long long per_block = (long long)(kCopyThreads / vecs) * kCopies;
+  const int log_vecs = p.row_bytes == 128 ? 3 : (p.row_bytes == 256 ? 4 : 5), vecs = 1 << log_vecs;
+  const long long per_block = kCopyThreads / vecs;
   const long long most = p.rows_out < p.n_rows ? p.rows_out : p.n_rows;  // a request keeps no more rows than it has
   const long long blocks = (most * p.Hkv + per_block - 1) / per_block;
-  return launch_dependent(keep_copy_kernel, dim3((unsigned)blocks), dim3(kCopyThreads), 0, stream, p, source, vecs);
+  return launch_dependent(keep_copy_kernel, dim3((unsigned)blocks), dim3(kCopyThreads), 0, stream, p, source, log_vecs);
 }
 
 }  // namespace spectree

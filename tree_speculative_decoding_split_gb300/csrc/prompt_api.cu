@@ -109,7 +109,7 @@ spec_status check_keep(const spec_kv_keep_args* a) {
   if (a->n_rows > kMaxKeepRows || a->rows_out > 0x7fffffffLL || a->batch > SPEC_MAX_RESERVE_BATCH ||
       (long long)a->batch * a->num_kv_heads >= (1LL << 27))
     return SPEC_ERR_UNSUPPORTED;
-  if (a->rows_out * a->num_kv_heads >= (1LL << 35)) return SPEC_ERR_UNSUPPORTED;  // the copy's grid
+  if (a->rows_out * a->num_kv_heads >= (1LL << 33)) return SPEC_ERR_UNSUPPORTED;  // the copy's grid
   const int size = a->dtype == SPEC_DTYPE_BF16 ? 2 : 4;
   if (!row_stride_ok(a->k_stride, a->num_kv_heads, a->head_dim, size) ||
       !row_stride_ok(a->v_stride, a->num_kv_heads, a->head_dim, size))
