@@ -155,6 +155,24 @@ def test_bad_row_start_writes_nothing(bad):
     assert int(status) == 7 and (out == 7).all() and (lse == 7).all()
 
 
+@pytest.mark.parametrize("batch", [31, 32, 33, 64])
+@pytest.mark.parametrize("heads", [1, 40])
+def test_batches_with_and_without_a_list(batch, heads):
+    """Pieces found in row_start by the kernel or listed ahead of it, in order or by work; requests without rows at the ends."""
+    lens = [0 if i in (0, 7, 8, batch - 1) else 1 + (53 * i) % 140 for i in range(batch)]
+    start = starts(lens)
+    n = int(start[-1])
+    q, k, v = fused(_gen(batch), n, heads, heads, 64)
+    status = _status()
+    out, lse = st.prompt_attention(q, k, v, start, dev_status=status)
+    check_attention((out, lse), q, k, v, start)
+    bad = start.clone()
+    bad[batch // 2] = n + 1
+    out.fill_(7)
+    st.prompt_attention(q, k, v, bad, out=out, lse=lse, dev_status=status)
+    assert int(status) == 7 and (out == 7).all()
+
+
 def test_no_rows():
     start = starts([0, 0])
     q = torch.empty((0, 4, 128), dtype=torch.bfloat16, device="cuda")

@@ -132,6 +132,23 @@ def test_bad_row_start_writes_nothing(bad):
     assert int(status) == 7 and (weight == 7).all()
 
 
+@pytest.mark.parametrize("batch", [31, 32, 33, 64])
+def test_batches_with_and_without_a_list(batch):
+    lens = [0 if i in (0, 7, 8, batch - 1) else 1 + (53 * i) % 400 for i in range(batch)]
+    start = starts(lens)
+    n = int(start[-1])
+    q, k, _ = fused(_gen(batch), n, 4, 2, 64)
+    lse = attention(q, k, k, start)[1].float()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    weight = st.prompt_key_weights(q, k, lse, start, 40, dev_status=status)
+    _check(weight, q, k, lse, start, 40)
+    bad = start.clone()
+    bad[batch // 2] = -1
+    weight.fill_(7)
+    st.prompt_key_weights(q, k, lse, bad, 40, weight=weight, dev_status=status)
+    assert int(status) == 7 and (weight == 7).all()
+
+
 def test_repeated_and_captured_calls():
     n = 900
     q, k, _ = fused(_gen(6), n, 8, 2, 128)

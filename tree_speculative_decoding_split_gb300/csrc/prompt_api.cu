@@ -149,11 +149,12 @@ float scale_of(float scale, int d) { return scale > 0.f ? scale : 1.f / std::sqr
 // Launches the plan where the call needs one (n_rows 0: its checks alone) and says where the kernel finds it.
 spec_status plan(long long n_rows, int B, int step, int by_work, const int32_t* row_start, const PlanLayout& l, PlanView* view,
                  int32_t* dev_status, cudaStream_t stream) {
-  const bool list = B > 1 || n_rows == 0;
+  const bool list = B > (by_work ? 1 : kPlanInKernel) || n_rows == 0;
   view->items = list ? l.items : nullptr;
   view->count = l.count;
   view->row_start = row_start;
   view->n_rows = n_rows;
+  view->B = B;
   view->step = step;
   view->by_work = by_work;
   if (!list) return SPEC_OK;

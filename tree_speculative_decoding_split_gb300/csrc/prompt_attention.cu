@@ -232,6 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint64_t drained[2];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort, s_special;
+  __shared__ PlanShared s_plan;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -270,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   pdl_wait();  // the plan
-  const PlanReader plan(p.plan, p.dev_status);
+  const PlanReader<false> plan(p.plan, s_plan, p.dev_status);
   const int total = plan.count * p.Hkv;
   // This CTA's items one by one, the next one's entry fetched while the current one is under way.
   int u = 0, at = item_index(0, total);

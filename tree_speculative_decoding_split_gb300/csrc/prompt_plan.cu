@@ -6,7 +6,7 @@
 // attention pieces are listed by falling work (a counting sort over the number of key tiles before a piece's
 // end): CTAs take them from the front, so the longest never start last.  (Which of two pieces of equal work
 // comes first is left to the atomics; no result depends on it.)  It takes 3 to 4 us, most of it a launch and three
-// reads of row_start behind one another; a call of one request does without it, its pieces being known on the host.
+// reads of row_start behind one another; calls of a single request, and key weights of few, do without (PlanReader).
 
 #include "pdl.cuh"
 #include "prompt.cuh"

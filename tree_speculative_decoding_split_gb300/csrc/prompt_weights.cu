@@ -16,6 +16,11 @@
 // Roles (12 warps): warp 0 TMA (a ring of key tiles, three slots of query chunks), warp 3 the chunks' lse, warps 4-11 sums:
 // two groups of four warps take every other key tile, each with two score buffers of 128 columns, so that products run
 // while sums are taken; warps 1 and 2 issue their MMAs.
+//
+// What bounds it: 8 prompts of 512 to 32768 rows, 64 heads on 8, window 37: 90.8 us where the bytes take 41.5; loads and
+// hand-offs alone 59, with the MMAs 77, and exponentials fill in only as far as two groups overlap (three groups 148 us, four
+// with one buffer each 122: less room for keys and queries).  One prompt of 16384 rows, 32 heads on 8, window 64: 13.2 us, of
+// which a launch, a start and seven tiles one behind the other.
 
 #include "pdl.cuh"
 #include "prompt.cuh"
@@ -52,7 +57,8 @@ struct Work {
 
 // The CTA's tiles are an even share [at, end) of all: the plan's pieces of 128 keys, head after head.  A stretch is what
 // one request and head have of it.
-__device__ __forceinline__ Work work_of(const KeyWeightsParams& p, const PlanReader& plan, int at, int end) {
+template <bool FEW>
+__device__ __forceinline__ Work work_of(const KeyWeightsParams& p, const PlanReader<FEW>& plan, int at, int end) {
   Work w;
   w.g = at / plan.count;
   const PromptItem it = plan.item(at - w.g * plan.count);
@@ -87,7 +93,7 @@ __device__ __forceinline__ int chunk_rows(const KeyWeightsParams& p, const Work&
 
 }  // namespace
 
-template <int D>
+template <int D, bool FEW>
 __global__ void __launch_bounds__(kThreads, 1)
     key_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK, const KeyWeightsParams p) {
   using C = WeightCfg<D>;
@@ -102,6 +108,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ __align__(16) float s_lse[kQSlots][kCols];  // log2(e) lse, +inf behind the window
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
+  __shared__ PlanShared s_plan;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -133,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   pdl_wait();  // the plan
-  const PlanReader plan(p.plan, p.dev_status);
+  const PlanReader<FEW> plan(p.plan, s_plan, p.dev_status);
   int begin, end;
   if (p.per_head) {  // neighbouring CTAs take the same keys of neighbouring heads, which lie together in memory
     const int head = blockIdx.x % p.Hkv;
@@ -408,18 +415,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-template <int D>
+template <int D, bool FEW>
 static cudaError_t launch_as(const CUtensorMap* tmQ, const CUtensorMap* tmK, const KeyWeightsParams& p, int grid,
                              cudaStream_t stream) {
   const cudaError_t err =
-      cudaFuncSetAttribute(key_weights_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, WeightCfg<D>::kSmem);
+      cudaFuncSetAttribute(key_weights_kernel<D, FEW>, cudaFuncAttributeMaxDynamicSharedMemorySize, WeightCfg<D>::kSmem);
   if (err != cudaSuccess) return err;
-  return launch_dependent(key_weights_kernel<D>, dim3(grid), dim3(kThreads), WeightCfg<D>::kSmem, stream, *tmQ, *tmK, p);
+  return launch_dependent(key_weights_kernel<D, FEW>, dim3(grid), dim3(kThreads), WeightCfg<D>::kSmem, stream, *tmQ, *tmK, p);
 }
 
 cudaError_t launch_key_weights(int d, const CUtensorMap* tmQ, const CUtensorMap* tmK, const KeyWeightsParams& p, int grid,
                                cudaStream_t stream) {
-  return d == 128 ? launch_as<128>(tmQ, tmK, p, grid, stream) : launch_as<64>(tmQ, tmK, p, grid, stream);
+  if (!p.plan.items && p.plan.B > 1)
+    return d == 128 ? launch_as<128, true>(tmQ, tmK, p, grid, stream) : launch_as<64, true>(tmQ, tmK, p, grid, stream);
+  return d == 128 ? launch_as<128, false>(tmQ, tmK, p, grid, stream) : launch_as<64, false>(tmQ, tmK, p, grid, stream);
 }
 
 }  // namespace spectree
