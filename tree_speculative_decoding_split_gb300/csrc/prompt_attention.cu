@@ -31,9 +31,9 @@
 //
 // What bounds it: a tile of both groups is 2048 cycles of MMA at d 128 and takes 2750; the rest is the way from S to P and
 // back (1000 cycles of softmax, 600 of hand-offs), which two groups do not hide in full and for more tensor memory is
-// too small.  16384 rows of 64 heads on 8: 2710 us, 1623 TFLOP/s.  At d 64 the MMAs of S halve in number, those of P V (64
+// too small.  16384 rows of 64 heads on 8: 2720 us, 1617 TFLOP/s.  At d 64 the MMAs of S halve in number, those of P V (64
 // columns of output) take as long as with 128, and that way does not change: 2620 cycles a tile, and 3600 to go from one item to
-// the next, which weighs where prompts are short.  48 prompts of up to 1800 rows, 16 heads on 8: 187 us.
+// the next, which weighs where prompts are short.  48 prompts of up to 1800 rows, 16 heads on 8: 190 us.
 // Weights go into P as bf16, off by 2^-8 of each at most: the tensor cores take 16-bit operands at twice the rate of wider
 // ones.  The sum, the maximum and O stay in fp32, and the sum adds the weights before that rounding.
 

@@ -17,7 +17,7 @@
 // two groups of four warps take every other key tile, each with two score buffers of 128 columns, so that products run
 // while sums are taken; warps 1 and 2 issue their MMAs.
 //
-// What bounds it: 8 prompts of 512 to 32768 rows, 64 heads on 8, window 37: 90.8 us where the bytes take 41.5; loads and
+// What bounds it: 8 prompts of 512 to 32768 rows, 64 heads on 8, window 37: 89.0 us where the bytes take 41.5; loads and
 // hand-offs alone 59, with the MMAs 77, and exponentials fill in only as far as two groups overlap (three groups 148 us, four
 // with one buffer each 122: less room for keys and queries).  One prompt of 16384 rows, 32 heads on 8, window 64: 13.2 us, of
 // which a launch, a start and seven tiles one behind the other.
@@ -85,6 +85,9 @@ __device__ __forceinline__ Chunks chunks_of(const KeyWeightsParams& p, const Wor
   c.end = (pass + 1) * w.per < w.chunks ? (pass + 1) * w.per : w.chunks;
   return c;
 }
+// The chunk that group a takes as its u.  The second group goes backwards: a short last chunk of one beside a whole one of the
+// other, as two groups in step would want the exponentials' unit at the same time (8 prompts 91.2 us in step, 89.0 so).
+__device__ __forceinline__ int turned(const Chunks& c, int u, int a) { return a ? c.first + c.end - 1 - u : u; }
 // Rows of chunk c in the window.
 __device__ __forceinline__ int chunk_rows(const KeyWeightsParams& p, const Work& w, int c) {
   const int left = w.n - w.q0 - c * p.tc;
@@ -229,7 +232,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if ((int)(k_n++ & 1) != a) continue;   // (slots alternate as groups do: each sees every phase of its own)
             ok = mbar_wait_bounded(&kfull[ks], k_phase, &s_abort);
             const uint32_t k_lo = k_lo0 + ks * (C::kK >> 4);
-            for (int ch = c.first; ch < c.end; ++ch) {
+            for (int u = c.first; u < c.end; ++u) {
+              const int ch = turned(c, u, a);
               const int buf = a * 2 + (s_n & 1);
               ok = ok && mbar_wait_bounded(&sfree[buf], ((s_n >> 1) & 1) ^ 1, &s_abort);
               if (!ok) break;
@@ -316,7 +320,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if ((int)(k_n++ & 1) != a) continue;
           float sum_w = pass > 0 && key < w.n ? weight[key] : 0.f;
-          for (int ch = c.first; ch < c.end; ++ch) {
+          for (int u = c.first; u < c.end; ++u) {
+            const int ch = turned(c, u, a);
             const int buf = a * 2 + (s_n & 1);
             ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sfull[buf], (s_n >> 1) & 1, &s_abort));
             if (!ok) break;
