@@ -155,7 +155,8 @@ struct alignas(16) SelectShared {
   long long sum[kWarps][2];
 };
 
-__global__ void __launch_bounds__(kThreads, 1) keep_select_kernel(const KeepParams p, int32_t* source, int log_cluster, int counted) {
+__global__ void __launch_bounds__(kThreads, 1)
+    keep_select_kernel(const KeepParams p, int32_t* source, int log_cluster, int counted) {
   extern __shared__ __align__(16) uint8_t s_raw[];
   SelectShared& s = *reinterpret_cast<SelectShared*>(s_raw);
   uint32_t* s_key = reinterpret_cast<uint32_t*>(s_raw + sizeof(SelectShared));  // [kHeld]

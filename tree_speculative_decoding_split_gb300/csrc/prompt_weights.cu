@@ -376,8 +376,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                   }
 #pragma unroll
                   for (int j = 0; j < 32; j += 4) {
-                    sum[0] = __fadd2_rn(sum[0], make_float2(ex2_approx(__uint_as_float(s[b][j])), ex2_approx(__uint_as_float(s[b][j + 1]))));
-                    sum[1] = __fadd2_rn(sum[1], make_float2(ex2_approx(__uint_as_float(s[b][j + 2])), ex2_approx(__uint_as_float(s[b][j + 3]))));
+                    const float x0 = __uint_as_float(s[b][j]), x1 = __uint_as_float(s[b][j + 1]);
+                    const float x2 = __uint_as_float(s[b][j + 2]), x3 = __uint_as_float(s[b][j + 3]);
+                    sum[0] = __fadd2_rn(sum[0], make_float2(ex2_approx(x0), ex2_approx(x1)));
+                    sum[1] = __fadd2_rn(sum[1], make_float2(ex2_approx(x2), ex2_approx(x3)));
                   }
                   continue;
                 }
