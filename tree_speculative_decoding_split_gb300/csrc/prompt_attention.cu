@@ -98,11 +98,12 @@ __device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&a)[4][32]) {
 // A tile's weights in two passes over its scores, of which a row sees those up to key `lim`: the maximum, with what is
 // there brought to it where it has grown by more than 2^8 (with_o: O holds something; the commit behind the scores says
 // that it is complete), then P over the scores that have been read.  Where the maximum is so large that its product
-// with the scale would be rounded by whole units, differences are taken ahead of the scale.  Returns the row's maximum
-// (in the scores' units) and sum.  Out of line and in loops: it runs once or twice an item, and cold code costs more
-// than its instructions.
+// with the scale would be rounded by whole units, differences are taken ahead of the scale.  The whole warp comes here
+// where one of its rows has to (`mine`); the others take the steps, and the order of additions, of the ordinary way, so that
+// a row's bits do not tell what lies beside it.  Returns the row's maximum (in the scores' units) and sum.  Out of line
+// and in loops: it runs once or twice an item, and cold code costs more than its instructions.
 template <int D>
-__device__ __noinline__ float2 tile_again(uint32_t tS, uint32_t tO, int lim, bool with_o, float2 ml, float scale_log2) {
+__device__ __noinline__ float2 tile_again(uint32_t tS, uint32_t tO, int lim, bool mine, bool with_o, float2 ml, float scale_log2) {
   float top = -INFINITY;
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
@@ -113,7 +114,7 @@ __device__ __noinline__ float2 tile_again(uint32_t tS, uint32_t tO, int lim, boo
     for (int j = 0; j < 32; ++j)
       if (c * 32 + j <= lim) top = fmaxf(top, __uint_as_float(s[j]));
   }
-  const bool need = (top - ml.x) * scale_log2 > kRescale;  // the first finite maximum among them
+  const bool need = mine && (top - ml.x) * scale_log2 > kRescale;  // the first finite maximum among them
   if (__any_sync(0xffffffffu, need)) {
     const float f = need ? exp2f((ml.x - top) * scale_log2) : 1.f;
     if (with_o) {
@@ -132,12 +133,12 @@ __device__ __noinline__ float2 tile_again(uint32_t tS, uint32_t tO, int lim, boo
   const float ref = ml.x == -INFINITY ? 0.f : ml.x;
   const bool far = fabsf(ref * scale_log2) >= kExact;
   const float shift = far ? 0.f : ref * scale_log2, before = far ? ref : 0.f;
+  float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
     uint32_t s[32], pk[16];
     tmem_ld_x32(tS + c * 32, s);
     tmem_ld_wait();
-    float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
     for (int j = 0; j < 32; j += 2) {
       float w[2];
@@ -146,12 +147,12 @@ __device__ __noinline__ float2 tile_again(uint32_t tS, uint32_t tO, int lim, boo
         w[e] = ex2_approx(fmaf(__uint_as_float(s[j + e]) - before, scale_log2, -shift));
         if (c * 32 + j + e > lim) w[e] = 0.f;
       }
-      sum = __fadd2_rn(sum, make_float2(w[0], w[1]));
+      sum[(j >> 1) & 1] = __fadd2_rn(sum[(j >> 1) & 1], make_float2(w[0], w[1]));
       pk[j / 2] = pack_bf16x2(w[0], w[1]);
     }
-    ml.y += sum.x + sum.y;
     tmem_st_x16(tS + c * 16, pk);
   }
+  ml.y += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
   tmem_st_wait();
   return ml;
 }
@@ -492,6 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int first = w.tok + a * p.tg;   // the group's first row
       const int row = first + my_tok;
+      const bool valid = rl < p.tg * p.G && row < w.n;  // (rows behind the last head, or of the next request, count for nothing)
       float m_run = -INFINITY, l_run = 0.f;  // the maximum in the scores' own units
       for (int t = 0; t < w.tiles[a]; ++t) {
         // (a warp whose wait gave up goes on to its last tile: the issuer waits for it without a limit)
@@ -505,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // outgrown it (128 weights of up to 2^8 stay below 2^15, and what overflows shows as well): tile_again then does the
         // tile once more, by its maximum.  (So does a row that has seen nothing but -inf, whose reference is none yet.)  No
         // other tile needs one, which is a pass less on the way from S to P.
-        bool again = false;
+        bool mine = false, again = false;
         if (ok) {
           uint32_t s[4][32];
 #pragma unroll
@@ -547,7 +549,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             pk[j / 64][j % 64 / 2] = pack_bf16x2(p0, p1);
           }
           const float part = (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
-          again = __any_sync(0xffffffffu, part > kGrown || fabsf(shift) >= kExact);
+          mine = valid && (part > kGrown || fabsf(shift) >= kExact);
+          again = __any_sync(0xffffffffu, mine);
           if (!again) {
             l_run += part;
             tmem_st_x32(tS, pk[0]);
@@ -556,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (ok && again) {
-          const float2 ml = tile_again<D>(tS, tO, edge ? row - t * kKeys : kKeys, t > 0, make_float2(m_run, l_run), p.scale_log2);
+          const float2 ml = tile_again<D>(tS, tO, edge ? row - t * kKeys : kKeys, mine, t > 0, make_float2(m_run, l_run), p.scale_log2);
           m_run = ml.x;
           l_run = ml.y;
         }
@@ -573,7 +576,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       st = (st + 2 * (w.all - w.tiles[a])) % kStages;  // (a group with fewer tiles than the item)
       if (!ok) continue;
       tc_fence_after();
-      const bool valid = rl < p.tg * p.G && row < w.n;
       const size_t orow = valid ? (size_t)(w.r0 + row) * p.Hq + w.g * p.G + my_head : 0;
       const float inv = l_run > 0.f ? 1.f / l_run : (l_run == 0.f ? 0.f : l_run);  // (a NaN sum stays NaN)
       const bool special = *static_cast<volatile int*>(&s_special) != 0;
