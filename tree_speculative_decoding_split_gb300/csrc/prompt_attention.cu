@@ -22,8 +22,8 @@
 //               infinities and NaN are set to 0, since 0 * inf would reach rows that do not see them; the rows that do
 //               see them get them back at the end.  Scores of unseen keys are replaced, so K needs no guard.
 //   warps 4-11  softmax, four warps per group, one row per thread: scores from tensor memory, P as bf16 over the scores'
-//               own columns.  O is rescaled only where a maximum has grown by more than 2^8 (P and the sum use the same
-//               older one); its row leaves through the same thread at the end.
+//               own columns.  O is rescaled only where a row's weights of a tile sum up to more than 2^8 (until then P and
+//               the sum use an older maximum); its row leaves through the same thread at the end.
 // P's completion and the turns go through named barriers, which wait without a limit: the tensor cores' reading slows
 // every access to shared memory, mbarriers included, to some 180 cycles (3250 cycles a tile of both groups against
 // 2900).  So a warp whose other waits gave up does no more work but meets these barriers up to its last item.
@@ -49,8 +49,7 @@ constexpr int kKeys = 128;        // keys per tile
 constexpr int kRows = 128;        // rows per group
 constexpr int kThreads = 384;
 constexpr int kBarTurn = 1, kBarP = 3;  // named barriers: an issuer's turn, a group's P written
-constexpr float kRescale = 8.f;   // log2
-constexpr float kGrown = 32768.f; // a row's sum over a tile from which its reference is looked over
+constexpr float kGrown = 256.f;   // a row's sum over a tile from which on it takes the tile's maximum as its reference
 constexpr float kExact = 262144.f;  // 2^18: maxima from here on, in log2 units, take differences ahead of the scale
 
 template <int D>
@@ -96,7 +95,7 @@ __device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&a)[4][32]) {
 }
 
 // A tile's weights in two passes over its scores, of which a row sees those up to key `lim`: the maximum, with what is
-// there brought to it where it has grown by more than 2^8 (with_o: O holds something; the commit behind the scores says
+// there brought to it where it has grown (with_o: O holds something; the commit behind the scores says
 // that it is complete), then P over the scores that have been read.  Where the maximum is so large that its product
 // with the scale would be rounded by whole units, differences are taken ahead of the scale.  The whole warp comes here
 // where one of its rows has to (`mine`); the others take the steps, and the order of additions, of the ordinary way, so that
@@ -114,7 +113,7 @@ __device__ __noinline__ float2 tile_again(uint32_t tS, uint32_t tO, int lim, boo
     for (int j = 0; j < 32; ++j)
       if (c * 32 + j <= lim) top = fmaxf(top, __uint_as_float(s[j]));
   }
-  const bool need = mine && (top - ml.x) * scale_log2 > kRescale;  // the first finite maximum among them
+  const bool need = mine && top > ml.x;  // (the first finite maximum among them)
   if (__any_sync(0xffffffffu, need)) {
     const float f = need ? exp2f((ml.x - top) * scale_log2) : 1.f;
     if (with_o) {
@@ -504,8 +503,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const bool edge = t * kKeys + kKeys - 1 > first;  // some row does not see all of the tile's keys
         // Weights are taken by the reference there is, the first tile's maximum at first.  Their sum tells where scores have
-        // outgrown it (128 weights of up to 2^8 stay below 2^15, and what overflows shows as well): tile_again then does the
-        // tile once more, by its maximum.  (So does a row that has seen nothing but -inf, whose reference is none yet.)  No
+        // outgrown it (no weight is larger than the sum, so V of up to 2^-8 of float32's range stays within it; what overflows
+        // shows as well): tile_again then does the tile once more, by its maximum, after which 128 weights sum up to 2^7.  (So does a row that has seen nothing but -inf, whose reference is none yet.)  No
         // other tile needs one, which is a pass less on the way from S to P.
         bool mine = false, again = false;
         if (ok) {
