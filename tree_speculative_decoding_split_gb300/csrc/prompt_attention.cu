@@ -14,20 +14,22 @@
 //
 // Roles (12 warps):
 //   warp 0      TMA: Q of each group, then K and V tiles of 128 keys through one ring of 32 KB stages
-//   warps 1, 2  MMA issuers, one for each group, in turns.  A turn is O += P V of a tile and S of the next one, one
-//               behind the other: tensor instructions of one thread run in order, so the next S may overwrite the
-//               scores that P lies on, and the commit behind S also tells that P V is done.  The tensor cores queue
-//               little, so whatever an issuer waits for, it waits for during the other's turn.
+//   warps 1, 2  MMA issuers, one for each group, in turns.  A turn is O += P V of a tile and S of the next one; the
+//               commit behind S also tells that P V is done.  Tensor instructions keep their order for sure only where
+//               they have one accumulator and one shape, so S may not overwrite a P that P V has yet to read: at d 64
+//               P has columns of its own, at d 128, where tensor memory is full and P lies over its own scores, S is
+//               issued when P V is done (2770 us without that wait, 2830 with it, at the 16384 rows below).  The tensor cores
+//               queue little, so whatever else an issuer waits for, it waits for during the other's turn.
 //   warp 3      guard: in tiles that hold keys some row does not see (the causal edge, the end of a request) V's
 //               infinities and NaN are set to 0, since 0 * inf would reach rows that do not see them; the rows that do
 //               see them get them back at the end.  Scores of unseen keys are replaced, so K needs no guard.
-//   warps 4-11  softmax, four warps per group, one row per thread: scores from tensor memory, P as bf16 over the scores'
-//               own columns.  O is rescaled only where a row's weights of a tile sum up to more than 2^8 (until then P and
+//   warps 4-11  softmax, four warps per group, one row per thread: scores from tensor memory, P as bf16 back
+//               to it.  O is rescaled only where a row's weights of a tile sum up to more than 2^8 (until then P and
 //               the sum use an older maximum); its row leaves through the same thread at the end.
 // P's completion and the turns go through named barriers, which wait without a limit: the tensor cores' reading slows
 // every access to shared memory, mbarriers included, to some 180 cycles (3250 cycles a tile of both groups against
 // 2900).  So a warp whose other waits gave up does no more work but meets these barriers up to its last item.
-// Tensor memory: 2 x (S 128 + O d) columns.
+// Tensor memory: 2 x (S 128 + O d) columns, and 2 x 64 for P at d 64.
 //
 // What bounds it: a tile of both groups is 2048 cycles of MMA at d 128 and takes 2750; the rest is the way from S to P and
 // back (1000 cycles of softmax, 600 of hand-offs), which two groups do not hide in full and for more tensor memory is
@@ -59,6 +61,8 @@ struct PromptCfg {
   static constexpr int kQ = kRows * D * 2;      // a group's Q
   static constexpr int kSmem = 1024 + 2 * kQ + kStages * kTile;
   static constexpr int kColS = 0, kColO = 256;
+  static constexpr bool kOver = D == 128;       // P lies over its own scores
+  static constexpr int kColP = kOver ? kColS : 384, kWideP = kOver ? kKeys : kKeys / 2;
 };
 
 // mbar_wait_bounded with all but the first try out of line: a wait that is over costs the issuing threads a few instructions.
@@ -102,7 +106,8 @@ __device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&a)[4][32]) {
 // a row's bits do not tell what lies beside it.  Returns the row's maximum (in the scores' units) and sum.  Out of line
 // and in loops: it runs once or twice an item, and cold code costs more than its instructions.
 template <int D>
-__device__ __noinline__ float2 tile_again(uint32_t tS, uint32_t tO, int lim, bool mine, bool with_o, float2 ml, float scale_log2) {
+__device__ __noinline__ float2 tile_again(uint32_t tS, uint32_t tP, uint32_t tO, int lim, bool mine, bool with_o, float2 ml,
+                                          float scale_log2) {
   float top = -INFINITY;
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
@@ -149,7 +154,7 @@ __device__ __noinline__ float2 tile_again(uint32_t tS, uint32_t tO, int lim, boo
       sum[(j >> 1) & 1] = __fadd2_rn(sum[(j >> 1) & 1], make_float2(w[0], w[1]));
       pk[j / 2] = pack_bf16x2(w[0], w[1]);
     }
-    tmem_st_x16(tS + c * 16, pk);
+    tmem_st_x16(tP + c * 16, pk);
   }
   ml.y += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
   tmem_st_wait();
@@ -227,6 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint64_t empty[kStages];    // tile read by every MMA
   __shared__ uint64_t qfull[2], qempty[2];
   __shared__ uint64_t sfull[2];        // S computed (and everything issued before it)
+  __shared__ uint64_t pread[2];        // P read (where the next scores go over it)
   __shared__ uint64_t ofull[2];        // O complete
   __shared__ uint64_t ofree[2];        // O read
   __shared__ uint64_t drained[2];
@@ -246,6 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&qfull[a], 1);
       mbar_init(&qempty[a], 1);
       mbar_init(&sfull[a], 1);
+      mbar_init(&pread[a], 1);
       mbar_init(&ofull[a], 1);
       mbar_init(&drained[a], 1);
       mbar_init(&ofree[a], 4);
@@ -351,10 +358,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t idP = idesc_bf16_f32(kRows, D, 1);
       const uint32_t q_lo = (smem_u32(sQ + a * C::kQ) >> 4), kv_lo = (smem_u32(sKV) >> 4);
       const uint32_t v_mn = ((kKeys * 128) >> 4) << 16;  // V (MN-major): the distance of its two halves of d
-      const uint32_t tS = tmem + C::kColS + a * kKeys, tO = tmem + C::kColO + a * D;
+      const uint32_t tS = tmem + C::kColS + a * kKeys, tO = tmem + C::kColO + a * D, tP = tmem + C::kColP + a * C::kWideP;
       int st = 0;                          // stage of the next load
       uint32_t f_phase = 0, g_phase = 0;   // per stage: parity of the next phase of full and guarded
-      uint32_t q_n = 0;
+      uint32_t q_n = 0, p_n = 0;
       bool ok = true;
       // The next load has landed (and been looked over); its stage.
       auto landed = [&](bool guard) -> int {
@@ -381,7 +388,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (Work w; take(w);) {
         const int tiles = a ? w.tiles[1] : w.tiles[0];
         int k = landed(false);
-        if (tiles > 0) ok = ok && wait(&qfull[a], q_n & 1, &s_abort);
+        if (tiles > 0) {
+          ok = ok && wait(&qfull[a], q_n & 1, &s_abort);
+          if (C::kOver && q_n > 0) ok = ok && wait(&ofull[a], (q_n - 1) & 1, &s_abort);  // the last item's P read
+        }
         ok = __all_sync(0xffffffffu, ok);
         named_bar_sync(kBarTurn + a, 64);
         tc_fence_after();
@@ -407,10 +417,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t v_lo = (kv_lo + v * (C::kTile >> 4)) | v_mn;
 #pragma unroll
             for (int kk = 0; kk < kKeys / 16; ++kk)
-              umma_bf16_tmem_a(tO, tS + kk * 8, desc_sw128(v_lo + kk * (2048 >> 4)), idP, (t > 0 || kk > 0) ? 1u : 0u);
-            if (t + 1 < tiles) scores(k);
-            umma_commit(t + 1 < tiles ? &sfull[a] : &ofull[a]);
-            if (t + 2 == tiles) umma_commit(&qempty[a]);
+              umma_bf16_tmem_a(tO, tP + kk * 8, desc_sw128(v_lo + kk * (2048 >> 4)), idP, (t > 0 || kk > 0) ? 1u : 0u);
+            if (t + 1 < tiles) {
+              if (C::kOver) {
+                umma_commit(&pread[a]);
+                ok = wait(&pread[a], p_n++ & 1, &s_abort);
+              }
+              if (ok) {
+                scores(k);
+                umma_commit(&sfull[a]);
+                if (t + 2 == tiles) umma_commit(&qempty[a]);
+              }
+            } else {
+              umma_commit(&ofull[a]);
+            }
           }
           __syncwarp();
           named_arrive(kBarTurn + (a ^ 1), 64);
@@ -474,6 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
     const uint32_t tS = tmem + C::kColS + a * kKeys + lane_off;
     const uint32_t tO = tmem + C::kColO + a * D + lane_off;
+    const uint32_t tP = tmem + C::kColP + a * C::kWideP + lane_off;
     uint32_t s_n = 0, o_n = 0;
     int st = 0;  // stage of the item's next load to release
     bool ok = true;
@@ -552,13 +573,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           again = __any_sync(0xffffffffu, mine);
           if (!again) {
             l_run += part;
-            tmem_st_x32(tS, pk[0]);
-            tmem_st_x32(tS + 32, pk[1]);
+            tmem_st_x32(tP, pk[0]);
+            tmem_st_x32(tP + 32, pk[1]);
             tmem_st_wait();
           }
         }
         if (ok && again) {
-          const float2 ml = tile_again<D>(tS, tO, edge ? row - t * kKeys : kKeys, mine, t > 0, make_float2(m_run, l_run), p.scale_log2);
+          const float2 ml = tile_again<D>(tS, tP, tO, edge ? row - t * kKeys : kKeys, mine, t > 0, make_float2(m_run, l_run),
+                                          p.scale_log2);
           m_run = ml.x;
           l_run = ml.y;
         }
