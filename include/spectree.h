@@ -636,9 +636,12 @@ spec_status spec_rope_table(int32_t rot_dim, double base, int32_t kind, double f
 
 /* Positions of rows.  Packed rows (row_start != NULL): positions[row_start[b] + j] = pos0[b] + j.
  * Trees (parent != NULL): positions[b][i] = pos0[b] + depth of node i, -1 for padded nodes.
+ * Rows of no request, and with a bad row_start all rows, keep what they hold, or are set to -1 (`fill`), which
+ * spec_rope passes over: an array of new memory has to be filled.
  * Data errors: pos0[b] < 0 or a position past 2^31 - 1 (SPEC_ERR_CAPACITY), a bad tree
  * (SPEC_ERR_BAD_TREE): the request's positions are then -1.
- * Host errors: SPEC_ERR_INVALID_ARGUMENT (sizes < 1, NULL pointers, both forms or none),
+ * Host errors: SPEC_ERR_INVALID_ARGUMENT (sizes < 1, NULL pointers, both forms or none, fill neither 0 nor 1 or
+ * with trees),
  * SPEC_ERR_UNSUPPORTED (n_max > SPEC_MAX_NODES, n_rows >= 2^31, B > SPEC_MAX_RESERVE_BATCH for rows). */
 typedef struct spec_rope_positions_args {
   int32_t batch;            /* B */
@@ -649,6 +652,8 @@ typedef struct spec_rope_positions_args {
   const int32_t* parent;    /* [B][N] or NULL */
   const int32_t* n_nodes;   /* [B], with parent */
   int32_t* positions;       /* out [n_rows] or [B][N] */
+  int32_t fill;             /* packed rows: 1 gives rows of no request position -1; else 0 */
+  int32_t reserved0;        /* must be 0 */
 } spec_rope_positions_args;
 
 spec_status spec_rope_positions(const spec_rope_positions_args* args, int32_t* dev_status, void* stream);

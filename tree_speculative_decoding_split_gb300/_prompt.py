@@ -23,7 +23,7 @@ _i32, _i64, _f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_float
 
 class RopePositionsArgs(ctypes.Structure):
     _fields_ = [("batch", _i32), ("n_max", _i32), ("n_rows", _i64), ("pos0", _vp), ("row_start", _vp), ("parent", _vp),
-                ("n_nodes", _vp), ("positions", _vp)]
+                ("n_nodes", _vp), ("positions", _vp), ("fill", _i32), ("reserved0", _i32)]
 
 
 class RopeArgs(ctypes.Structure):
@@ -146,18 +146,20 @@ def rope_positions_args(pos0, row_start=None, n_rows=None, parent=None, n_nodes=
             raise ValueError("row_start must be [B + 1], pos0 [B]")
         rows = positions.numel() if n_rows is None else int(n_rows)
         shape, N = (rows,), 0
+    fill = int(positions is None and parent is None)
     if positions is None:
         positions = torch.empty(shape, dtype=i32, device=dev)
     elif tuple(positions.shape) != shape:
         raise ValueError("positions must be [n_rows], or [B][N] for trees")
-    a = RopePositionsArgs(B, N, rows, pos0.data_ptr(), *source, _fast(positions, "positions", i32, dev, ix))
+    a = RopePositionsArgs(B, N, rows, pos0.data_ptr(), *source, _fast(positions, "positions", i32, dev, ix), fill, 0)
     return a, positions
 
 
 def rope_positions(pos0, row_start=None, n_rows=None, parent=None, n_nodes=None, positions=None, dev_status=None,
                    stream=None):
     """Positions of packed prompt rows (``row_start`` [B + 1], ``n_rows``) or of tree nodes (``parent`` [B][N],
-    ``n_nodes``), int32 (see spec_rope_positions)."""
+    ``n_nodes``), int32 (see spec_rope_positions).  Rows of no request, all of them where row_start is refused, have
+    position -1; in ``positions`` of the caller's own they keep what it holds."""
     if stream is None:
         r = _native().positions(pos0, row_start, n_rows, parent, n_nodes, positions, dev_status)
         if r is not None:

@@ -419,6 +419,7 @@ PyObject* positions(PyObject*, PyObject* const* o, Py_ssize_t n) {
       a.row_start = ptr<int32_t>(start);
       out = o[5] == Py_None ? nullptr : c.shaped(o[5], at::kInt, {a.n_rows});
       if (c.ok && !out) out = &(made = c.make({a.n_rows}, at::kInt));
+      a.fill = made.defined();
     }
     int32_t* status = c.status(o[6]);
     if (!c.ok || !fits({B})) return nullptr;

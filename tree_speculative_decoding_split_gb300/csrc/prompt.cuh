@@ -15,6 +15,7 @@ struct PositionsParams {
   const int32_t* parent;     // [B][N] (trees) or nullptr
   const int32_t* n_nodes;
   int32_t* positions;        // [n_rows] or [B][N]
+  int fill;                  // packed rows: -1 for rows of no request
   int32_t* dev_status;
 };
 cudaError_t launch_rope_positions(const PositionsParams& p, cudaStream_t stream);

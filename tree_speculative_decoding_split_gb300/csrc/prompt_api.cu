@@ -24,6 +24,7 @@ bool row_stride_ok(long long stride, long long heads, int d, int size) {
 spec_status check_positions(const spec_rope_positions_args* a) {
   if (!a || a->batch < 1 || !a->pos0) return SPEC_ERR_INVALID_ARGUMENT;
   if ((a->row_start != nullptr) == (a->parent != nullptr)) return SPEC_ERR_INVALID_ARGUMENT;
+  if (a->fill < 0 || a->fill > 1 || (a->fill && a->parent) || a->reserved0 != 0) return SPEC_ERR_INVALID_ARGUMENT;
   if (a->parent) {
     if (!a->n_nodes || a->n_rows != 0 || a->n_max < 1 || !a->positions) return SPEC_ERR_INVALID_ARGUMENT;
     if (a->n_max > SPEC_MAX_NODES) return SPEC_ERR_UNSUPPORTED;
@@ -218,7 +219,7 @@ spec_status spec_rope_positions(const spec_rope_positions_args* a, int32_t* dev_
   if (st != SPEC_OK) return st;
   PositionsParams p;
   p.B = a->batch; p.N = a->n_max; p.n_rows = a->n_rows; p.pos0 = a->pos0; p.row_start = a->row_start;
-  p.parent = a->parent; p.n_nodes = a->n_nodes; p.positions = a->positions; p.dev_status = dev_status;
+  p.parent = a->parent; p.n_nodes = a->n_nodes; p.positions = a->positions; p.fill = a->fill; p.dev_status = dev_status;
   return launch_rope_positions(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 

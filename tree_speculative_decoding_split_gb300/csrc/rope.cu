@@ -33,11 +33,15 @@ constexpr int kRopeThreads = 256;
 __global__ void __launch_bounds__(kPosThreads) positions_rows_kernel(const PositionsParams p) {
   pdl_wait();
   const int tid = threadIdx.x;
+  const long long first = (long long)blockIdx.x * kPosRows;
+  auto none = [&](long long r) {
+    if (p.fill && r < p.n_rows) p.positions[r] = -1;
+  };
   if (!row_start_ok(p.row_start, p.B, p.n_rows)) {
     if (blockIdx.x == 0 && tid == 0) set_status(p.dev_status, SPEC_ERR_CAPACITY);
+    for (int u = 0; u < kPosRows / kPosThreads; ++u) none(first + u * kPosThreads + tid);
     return;
   }
-  const long long first = (long long)blockIdx.x * kPosRows;
   const long long behind = p.row_start[p.B], front = p.row_start[0];
   __shared__ int s_lo, s_hi;
   if (tid < 2) {  // the block's first and last request; each thread then searches between them
@@ -53,7 +57,10 @@ __global__ void __launch_bounds__(kPosThreads) positions_rows_kernel(const Posit
 #pragma unroll
   for (int u = 0; u < kPosRows / kPosThreads; ++u) {
     const long long r = first + u * kPosThreads + tid;
-    if (r < front || r >= behind) continue;
+    if (r < front || r >= behind) {
+      none(r);
+      continue;
+    }
     const int b = request_of(p.row_start, lo, hi, r);
     const int p0 = p.pos0[b], start = p.row_start[b], n = p.row_start[b + 1] - start;
     const bool bad = p0 < 0 || (long long)p0 + n - 1 > 0x7fffffffLL;
