@@ -738,8 +738,8 @@ spec_status spec_prompt_attention(const spec_prompt_attn_args* args, void* works
 /* The attention weight that each key gets from the last `window` rows of its own request (all of them
  * where there are fewer), summed over these rows and over the query heads that share the key's head:
  *   weight[g][j] = sum_{i >= j, i in window} sum_{h in group g} exp(scale * q[i][h] . k[j][g] - lse[i][h])
- * in float32, the terms added in an order of their own that does not change from call to call; rows
- * outside of the requests keep what they hold.  lse is spec_prompt_attention's; only the window's rows
+ * in float32, the terms added in an order of their own that goes by the request's length, the window and the heads of
+ * a group alone, whatever else the batch holds; rows outside of the requests keep what they hold.  lse is spec_prompt_attention's; only the window's rows
  * of q and lse are read.
  * Host errors and workspace as for spec_prompt_attention (pieces of 128 rows), and window < 1. */
 typedef struct spec_key_weights_args {

@@ -85,9 +85,13 @@ __device__ __forceinline__ Chunks chunks_of(const KeyWeightsParams& p, const Wor
   c.end = (pass + 1) * w.per < w.chunks ? (pass + 1) * w.per : w.chunks;
   return c;
 }
-// The chunk that group a takes as its u.  The second group goes backwards: a short last chunk of one beside a whole one of the
-// other, as two groups in step would want the exponentials' unit at the same time (8 prompts 91.2 us in step, 89.0 so).
-__device__ __forceinline__ int turned(const Chunks& c, int u, int a) { return a ? c.first + c.end - 1 - u : u; }
+// The chunk that comes as the u-th for tile `i`.  Every other tile of a request takes them backwards, and so one of the two
+// groups does: a short last chunk of one beside a whole one of the other, as two groups in step would want the exponentials'
+// unit at the same time (8 prompts 91.2 us in step, 89.0 so).  By the request's own tiles, not by the group, which depends
+// on the batch: a key's terms are added in one order whatever comes with it.
+__device__ __forceinline__ int turned(const Work& w, const Chunks& c, int u, int i) {
+  return (w.key / kKeys + i) & 1 ? c.first + c.end - 1 - u : u;
+}
 // Rows of chunk c in the window.
 __device__ __forceinline__ int chunk_rows(const KeyWeightsParams& p, const Work& w, int c) {
   const int left = w.n - w.q0 - c * p.tc;
@@ -233,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = mbar_wait_bounded(&kfull[ks], k_phase, &s_abort);
             const uint32_t k_lo = k_lo0 + ks * (C::kK >> 4);
             for (int u = c.first; u < c.end; ++u) {
-              const int ch = turned(c, u, a);
+              const int ch = turned(w, c, u, i);
               const int buf = a * 2 + (s_n & 1);
               ok = ok && mbar_wait_bounded(&sfree[buf], ((s_n >> 1) & 1) ^ 1, &s_abort);
               if (!ok) break;
@@ -321,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if ((int)(k_n++ & 1) != a) continue;
           float sum_w = pass > 0 && key < w.n ? weight[key] : 0.f;
           for (int u = c.first; u < c.end; ++u) {
-            const int ch = turned(c, u, a);
+            const int ch = turned(w, c, u, i);
             const int buf = a * 2 + (s_n & 1);
             ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sfull[buf], (s_n >> 1) & 1, &s_abort));
             if (!ok) break;
