@@ -620,7 +620,7 @@ spec_status spec_tree_attention_kv8(const spec_attn_kv8_args* args, void* worksp
  *           length: theta for r >= high, theta / factor for r <= low, in between the two weighted by
  *           (r - low) / (high - low)
  *   RAMP    theta and theta / factor weighted linearly in i: theta up to the (real) index i_high at which r = high,
- *           theta / factor from the index i_low at which r = low on, both held to [0, rot_dim / 2 - 1]
+ *           theta / factor from the index i_low at which r = low on, both held to [0, rot_dim - 1]
  *           after rounding i_high down and i_low up (i_low at least 0.001 behind i_high)
  * SPEC_ERR_INVALID_ARGUMENT: turns NULL, rot_dim < 2 or odd, base <= 1, factor <= 0, and for BANDS and
  * RAMP original_len < 1 or not 0 < low < high; numbers that are not finite.  SPEC_ERR_UNSUPPORTED:

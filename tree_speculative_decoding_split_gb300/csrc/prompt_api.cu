@@ -192,8 +192,9 @@ spec_status spec_rope_table(int32_t rot_dim, double base, int32_t kind, double f
   auto index_of = [&](double r) { return rot_dim * std::log((double)original_len / (r * two_pi)) / (2.0 * std::log(base)); };
   double i_high = 0.0, i_low = 0.0;
   if (kind == SPEC_ROPE_RAMP) {
-    i_high = std::fmin(std::fmax(std::floor(index_of(high)), 0.0), half - 1.0);
-    i_low = std::fmin(std::fmax(std::ceil(index_of(low)), 0.0), half - 1.0);
+    // (the ramp may end, or lie, behind the last index: after a long trained length no frequency is scaled in full, or at all)
+    i_high = std::fmin(std::fmax(std::floor(index_of(high)), 0.0), rot_dim - 1.0);
+    i_low = std::fmin(std::fmax(std::ceil(index_of(low)), 0.0), rot_dim - 1.0);
     if (i_low < i_high + 0.001) i_low = i_high + 0.001;
   }
   for (int pass = 0; pass < 2; ++pass)  // (nothing is written before every frequency is known to fit)
