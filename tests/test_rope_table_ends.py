@@ -37,3 +37,22 @@ def test_a_ramp_that_ends_behind_the_last_frequency(rot, base, length, low, high
     for i, g in enumerate(got):
         t, x = base ** (-2 * i / rot), min(max((i - hi) / (lo - hi), 0), 1)
         assert _near(g, t * (1 - x) + t / 4 * x)
+
+
+@pytest.mark.parametrize("rot", [2 ** 32 + 64, 2 ** 33, -2 ** 32 + 64])
+def test_sizes_past_32_bits_are_refused(rot):
+    """(and not cut to their lower bits)"""
+    with pytest.raises(st.SpecError) as e:
+        st.rope_table(rot)
+    assert e.value.code == 1
+
+
+@pytest.mark.parametrize("length", [2 ** 64 + 8192, -2 ** 64 + 8192])
+def test_lengths_past_64_bits(length):
+    if length < 0:
+        with pytest.raises(st.SpecError) as e:
+            st.rope_table(64, scaling="bands", factor=8.0, original_len=length)
+        assert e.value.code == 1
+    else:  # (all frequencies turn often enough to be kept)
+        got = st.rope_table(64, scaling="bands", factor=8.0, original_len=length)
+        assert got.tolist() == st.rope_table(64).tolist()

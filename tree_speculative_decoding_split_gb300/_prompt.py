@@ -99,9 +99,9 @@ def _rows(t, name, dtype, dev):
     return t.data_ptr(), rows, H, d, H * d if step is None else step
 
 
-def _clip(x):
-    """x for a 32-bit field: what lies outside is as good as its nearer end (and would be cut to its lower bits)."""
-    return max(-2 ** 31, min(int(x), 2 ** 31 - 1))
+def _clip(x, bits=32):
+    """x for a field of 32 (64) bits: what lies outside is as good as its nearer end (and would be cut to its lower bits)."""
+    return max(-2 ** (bits - 1), min(int(x), 2 ** (bits - 1) - 1))
 
 
 def _on(dev, fn, *args):
@@ -115,8 +115,9 @@ def rope_table(rot_dim, base=10000.0, scaling="none", factor=1.0, original_len=0
     """Rotary frequencies as 2^-64 turns per position (see spec_rope_table): an int64 CPU tensor [rot_dim / 2].
     ``scaling``: "none", "linear", "base", "bands" or "ramp"."""
     torch = _torch()
-    turns = torch.empty(max(int(rot_dim) // 2, 1), dtype=torch.int64)
-    code = lib().spec_rope_table(int(rot_dim), float(base), ROPE_KINDS[scaling], float(factor), int(original_len), float(low),
+    rot = _clip(rot_dim)  # (odd where it was past 32 bits: refused, with nothing to hold)
+    turns = torch.empty(1 if rot % 2 else max(rot // 2, 1), dtype=torch.int64)
+    code = lib().spec_rope_table(rot, float(base), ROPE_KINDS[scaling], float(factor), _clip(original_len, 64), float(low),
                                  float(high), ctypes.cast(turns.data_ptr(), ctypes.POINTER(_i64)))
     _check(code, "spec_rope_table")
     return turns
