@@ -623,7 +623,7 @@ spec_status spec_tree_attention_kv8(const spec_attn_kv8_args* args, void* worksp
  *           theta / factor from the index i_low at which r = low on, both held to [0, rot_dim - 1]
  *           after rounding i_high down and i_low up (i_low at least 0.001 behind i_high)
  * SPEC_ERR_INVALID_ARGUMENT: turns NULL, rot_dim < 2 or odd, base <= 1, factor <= 0, and for BANDS and
- * RAMP original_len < 1 or not 0 < low < high; numbers that are not finite.  SPEC_ERR_UNSUPPORTED:
+ * RAMP original_len < 1 or not 0 < low < high; numbers, or a scaled base, that are not finite.  SPEC_ERR_UNSUPPORTED:
  * an unknown kind, a frequency of half a turn or more. */
 #define SPEC_ROPE_NONE 0
 #define SPEC_ROPE_LINEAR 1

@@ -56,3 +56,10 @@ def test_lengths_past_64_bits(length):
     else:  # (all frequencies turn often enough to be kept)
         got = st.rope_table(64, scaling="bands", factor=8.0, original_len=length)
         assert got.tolist() == st.rope_table(64).tolist()
+
+
+@pytest.mark.parametrize("base,factor", [(1e300, 1e10), (10000.0, 1e308)])
+def test_a_scaled_base_that_is_not_finite_is_refused(base, factor):
+    with pytest.raises(st.SpecError) as e:
+        st.rope_table(64, base, "base", factor)
+    assert e.value.code == 1

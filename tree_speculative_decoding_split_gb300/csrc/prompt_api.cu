@@ -187,7 +187,10 @@ spec_status spec_rope_table(int32_t rot_dim, double base, int32_t kind, double f
   if (kind == SPEC_ROPE_BASE && rot_dim == 2) return SPEC_ERR_INVALID_ARGUMENT;
   const double two_pi = 6.283185307179586476925;
   const int half = rot_dim / 2;
-  if (kind == SPEC_ROPE_BASE) base *= std::pow(factor, (double)rot_dim / (rot_dim - 2));
+  if (kind == SPEC_ROPE_BASE) {
+    base *= std::pow(factor, (double)rot_dim / (rot_dim - 2));
+    if (!std::isfinite(base)) return SPEC_ERR_INVALID_ARGUMENT;
+  }
   // the (real) index whose frequency makes r turns over the original length
   auto index_of = [&](double r) { return rot_dim * std::log((double)original_len / (r * two_pi)) / (2.0 * std::log(base)); };
   double i_high = 0.0, i_low = 0.0;
