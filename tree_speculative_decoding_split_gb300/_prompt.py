@@ -326,6 +326,8 @@ def kv_keep_args(k, v, weight, row_start, budget, first=0, last=0, rows_out=None
     if k_out.shape != (n_out, Hkv, d) or v_out.shape != k_out.shape or index.shape != (n_out, Hkv) or \
             keep_start.numel() != B + 1 or n_keep.numel() != B:
         raise ValueError("k_out and v_out must be [rows_out][Hkv][d], index [rows_out][Hkv], keep_start [B + 1], n_keep [B]")
+    if rows_out is not None and int(rows_out) != n_out:
+        raise ValueError("rows_out is the number of rows of the outputs")
     a = KvKeepArgs(code, B, Hkv, d, _clip(budget), _clip(first), _clip(last), 0, rows, n_out, k_step, v_step, k_ptr, v_ptr, w_ptr,
                    start, *ptr)
     return a, outputs
@@ -335,7 +337,7 @@ def kv_keep(k, v, weight, row_start, budget, first=0, last=0, rows_out=None, out
             stream=None):
     """The rows of each prompt that ``budget`` leaves, per KV head: its first ``first`` and last ``last`` rows and those with
     the largest weights, in the prompt's order (see spec_kv_keep).  ``rows_out`` bounds the rows kept in all (default: the
-    rows there are, or the budgets' sum).  Returns (k_out, v_out, index, keep_start, n_keep); keep_start and n_keep are the
+    rows there are, or the budgets' sum; the rows of ``outputs`` where these are given).  Returns (k_out, v_out, index, keep_start, n_keep); keep_start and n_keep are the
     row_start and n_new with which kv_reserve and kv8_append admit the rows."""
     if stream is None and workspace is None:
         r = _native().keep(k, v, weight, row_start, budget, first, last, rows_out, outputs, dev_status)
