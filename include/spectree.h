@@ -664,8 +664,8 @@ spec_status spec_rope_positions(const spec_rope_positions_args* args, int32_t* d
  * HALF pairs channel i with i + rot_dim / 2, INTERLEAVED 2 i with 2 i + 1.  Channels from rot_dim on
  * are passed on as they are.  The angle's fraction of a turn is exact in 32 bits at any position; cos,
  * sin and the products are float32, rounded once to the rows' type.  Rows with a negative
- * position are not written.  q_out == q (k_out == k) with equal strides works in place; outputs
- * that overlap an input in another way are not supported.
+ * position are not written (outputs of their own hold there what they held).  q_out == q (k_out == k) with equal
+ * strides works in place; outputs that overlap an input in another way are not supported.
  * Host errors: SPEC_ERR_INVALID_ARGUMENT (sizes < 1, NULL pointers, strides or addresses that are no
  * multiple of 16 bytes or too short, an amplitude that is not finite), SPEC_ERR_UNSUPPORTED (dtype,
  * layout, head_dim or rot_dim no multiple of 16, head_dim > 256, rot_dim > head_dim, n_rows >= 2^31,
@@ -739,8 +739,8 @@ spec_status spec_prompt_attention(const spec_prompt_attn_args* args, void* works
  * where there are fewer), summed over these rows and over the query heads that share the key's head:
  *   weight[g][j] = sum_{i >= j, i in window} sum_{h in group g} exp(scale * q[i][h] . k[j][g] - lse[i][h])
  * in float32, the terms added in an order of their own that goes by the request's length, the window and the heads of
- * a group alone, whatever else the batch holds; rows outside of the requests keep what they hold.  lse is spec_prompt_attention's; only the window's rows
- * of q and lse are read.
+ * a group alone, whatever else the batch holds; rows outside of the requests keep what they hold.  lse is
+ * spec_prompt_attention's; only the window's rows of q and lse are read.
  * Host errors and workspace as for spec_prompt_attention (pieces of 128 rows), and window < 1. */
 typedef struct spec_key_weights_args {
   int32_t dtype;            /* SPEC_DTYPE_BF16 */
@@ -772,14 +772,15 @@ spec_status spec_prompt_key_weights(const spec_key_weights_args* args, void* wor
  * +0; NaN ranks below -inf).  They are written in the prompt's order:
  *   keep_start[b] = sum of n_keep before b;  for s < n_keep[b], at row keep_start[b] + s and head g:
  *   index = the row's number within its request, k_out / v_out = its K and V.
- * Rows of the outputs behind keep_start[B] keep what they hold.  n_keep and keep_start are the n_new and
- * row_start with which spec_kv_reserve and spec_kv8_append admit the rows; rows behind the budget never
+ * Rows of the outputs behind keep_start[B] keep what they hold; outputs must not overlap the inputs.  n_keep and
+ * keep_start are the n_new and row_start with which spec_kv_reserve and spec_kv8_append admit the rows; rows behind the budget never
  * reach the cache.  (K rows carry their positions, so what follows goes on from the prompt's full length.)
  * Data errors: a bad row_start, or more than rows_out rows kept (SPEC_ERR_CAPACITY): n_keep and
  * keep_start are then 0 and no row is written.
  * Host errors: SPEC_ERR_INVALID_ARGUMENT (sizes < 1, first or last < 0, first + last > budget, NULL
  * pointers, strides or addresses that are no multiple of 16 bytes or too short), SPEC_ERR_UNSUPPORTED (dtype,
- * head_dim, n_rows >= 2^31 - 16384, rows_out >= 2^31, rows_out * Hkv >= 2^33, B > SPEC_MAX_RESERVE_BATCH, B * Hkv >= 2^27), SPEC_ERR_WORKSPACE_TOO_SMALL. */
+ * head_dim, n_rows >= 2^31 - 16384, rows_out >= 2^31, rows_out * Hkv >= 2^33, B > SPEC_MAX_RESERVE_BATCH,
+ * B * Hkv >= 2^27), SPEC_ERR_WORKSPACE_TOO_SMALL. */
 typedef struct spec_kv_keep_args {
   int32_t dtype;            /* of k, v: SPEC_DTYPE_BF16 or SPEC_DTYPE_F32 */
   int32_t batch;            /* B */

@@ -16,8 +16,10 @@
 //
 // What bounds it: the choice by its chain of passes and meetings of the cluster (two a pass), 10 to 14 us whatever the
 // bytes; the copy by memory.  16 prompts of up to 8192 rows at a budget of 1024: 29.1 us; one of 131072 rows on 8 heads, a
-// cluster of 8 each: 22.3 us (before its last copy, 36.1 with every CTA adding up all the bins, 29.0 with every CTA adding up a
-// slice, a third meeting and the last walk in steps of 128 keys a warp, 22.9 as it is).
+// cluster of 8 each: 22.6 us (with an earlier copy, 36.1 with every CTA adding up all the bins, 29.0 with every CTA adding up
+// a slice, a third meeting and the last walk in steps of 128 keys a warp, 22.9 as it is).  These are graph replays over the
+// same outputs; Python calls, which make new ones, take 33.6 and 24.0.  512 prompts of 200 rows at a budget of 64 take 233 us
+// where their bytes take 40: a CTA of the choice per request and head, one to an SM, cleared and walked for 200 keys.
 
 #include "pdl.cuh"
 #include "prompt.cuh"

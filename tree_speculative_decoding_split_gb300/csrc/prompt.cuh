@@ -58,8 +58,8 @@ cudaError_t launch_prompt_plan(const PlanParams& p, cudaStream_t stream);
 
 // What a kernel reads of its plan.  Without a list (items == nullptr) it finds the pieces in row_start itself, which saves
 // the 3 to 4 us of another kernel ahead: those of a single request in order or (by_work) the last first and, in a kernel of the
-// key weights' own (FEW), those of up to kPlanInKernel requests in order (8 prompts 95.9 to 91.9 us; code that does both
-// takes 0.4 us longer for a single one, and 1.1 us in the attention).
+// key weights' own (FEW), those of up to kPlanInKernel requests in order (8 prompts 93.2 to 89.1 us; code that does both
+// took 0.4 us longer for a single one, and 1.1 us in the attention).
 constexpr int kPlanInKernel = 32;
 struct PlanView {
   const PromptItem* items;

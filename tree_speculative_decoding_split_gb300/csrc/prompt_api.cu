@@ -296,8 +296,8 @@ spec_status spec_prompt_key_weights(const spec_key_weights_args* a, void* worksp
     return SPEC_ERR_CUDA;
   const spec_status ps = plan(a->n_rows, a->batch, kWeightKeys, 0, a->row_start, l, &p.plan, dev_status, stream);
   if (ps != SPEC_OK || a->n_rows == 0) return ps;
-  // Every head has as many CTAs of its own, where that idles an eighth of the SMs at most (8 prompts of 0.5K to 32K: 97.0 us,
-  // 98.0 with shares over heads)
+  // Every head has as many CTAs of its own, where that idles an eighth of the SMs at most (8 prompts of 0.5K to 32K: 89.1 us,
+  // 89.6 with shares over heads; one of 16K 13.2 and 14.2)
   int grid = grid_for(plan_items(a->n_rows, a->batch, kWeightKeys), p.Hkv);
   p.per_head = grid % p.Hkv * 8 <= grid ? grid / p.Hkv : 0;
   if (p.per_head) grid = p.per_head * p.Hkv;

@@ -13,7 +13,7 @@
 // turns that run back and forth (the CTA that took the longest of one turn takes the shortest of the next).
 //
 // Roles (12 warps):
-//   warp 0      TMA: Q of each group, then K and V tiles of 128 keys through one ring of 32 KB stages
+//   warp 0      TMA: Q of each group, then K and V tiles of 128 keys through one ring (5 stages of 32 KB, at d 64 8 of 16 KB)
 //   warps 1, 2  MMA issuers, one for each group, in turns.  A turn is O += P V of a tile and S of the next one; the
 //               commit behind S also tells that P V is done.  Tensor instructions keep their order for sure only where
 //               they have one accumulator and one shape, so S may not overwrite a P that P V has yet to read: at d 64
@@ -27,17 +27,20 @@
 //               to it.  O is rescaled only where a row's weights of a tile sum up to more than 2^8 (until then P and
 //               the sum use an older maximum); its row leaves through the same thread at the end.
 // P's completion and the turns go through named barriers, which wait without a limit: the tensor cores' reading slows
-// every access to shared memory, mbarriers included, to some 180 cycles (3250 cycles a tile of both groups against
-// 2900).  So a warp whose other waits gave up does no more work but meets these barriers up to its last item.
+// every access to shared memory, mbarriers included, to some 180 cycles (when they came in, 3250 cycles a tile of both
+// groups became 2900).  So a warp whose other waits gave up does no more work but meets these barriers up to its last item.
 // Tensor memory: 2 x (S 128 + O d) columns, and 2 x 64 for P at d 64.
 //
-// What bounds it: a tile of both groups is 2048 cycles of MMA at d 128 and takes 2750; the rest is the way from S to P and
-// back (1000 cycles of softmax, 600 of hand-offs), which two groups do not hide in full and for more tensor memory is
-// too small.  16384 rows of 64 heads on 8: 2720 us, 1617 TFLOP/s.  At d 64 the MMAs of S halve in number, those of P V (64
-// columns of output) take as long as with 128, and that way does not change: 2620 cycles a tile, and 3600 to go from one item to
-// the next, which weighs where prompts are short.  48 prompts of up to 1800 rows, 16 heads on 8: 190 us.
-// Weights go into P as bf16, off by 2^-8 of each at most: the tensor cores take 16-bit operands at twice the rate of wider
-// ones.  The sum, the maximum and O stay in fp32, and the sum adds the weights before that rounding.
+// What bounds it: a tile of both groups is 2048 cycles of MMA at d 128 and takes 2920; the rest is the way from S to P and
+// back (1000 cycles of softmax, 600 of hand-offs, 150 of the wait for P V), which two groups do not hide in full and for more
+// tensor memory is too small.  16384 rows of 64 heads on 8: 2850 us, 1545 TFLOP/s, at the power limit.  At d 64 the MMAs of S
+// halve in number, those of P V (64 columns of output) take as long as with 128, and that way does not change: 2650 cycles a
+// tile, and 3600 to go from one item to the next, which weighs where prompts are short.  48 prompts of up to 1800 rows, 16
+// heads on 8: 186 us.  (Graph replays; a Python call takes 2890 and 187.)
+// Weights go into P as bf16, off by 2^-8 of each at most, so that out is 0.0020 to 0.0022 from 64 bits where its own rounding
+// alone leaves 0.0016.  As a pair of bf16 numbers they leave no more than that, at half as many MMAs again and more to store:
+// 4450 us at the rows above (2770 then), 307 for the 48 prompts (184), 18.3 for one of 500 rows (12.4).  The sum, the maximum
+// and O stay in fp32, and the sum adds the weights before that rounding.
 
 #include "pdl.cuh"
 #include "prompt.cuh"
@@ -525,8 +528,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool edge = t * kKeys + kKeys - 1 > first;  // some row does not see all of the tile's keys
         // Weights are taken by the reference there is, the first tile's maximum at first.  Their sum tells where scores have
         // outgrown it (no weight is larger than the sum, so V of up to 2^-8 of float32's range stays within it; what overflows
-        // shows as well): tile_again then does the tile once more, by its maximum, after which 128 weights sum up to 2^7.  (So does a row that has seen nothing but -inf, whose reference is none yet.)  No
-        // other tile needs one, which is a pass less on the way from S to P.
+        // shows as well): tile_again then does the tile once more, by its maximum, after which 128 weights sum up to 2^7.  (So
+        // does a row that has seen nothing but -inf, whose reference is none yet.)  No other tile needs one, which is a pass
+        // less on the way from S to P.
         bool mine = false, again = false;
         if (ok) {
           uint32_t s[4][32];

@@ -17,10 +17,11 @@
 // two groups of four warps take every other key tile, each with two score buffers of 128 columns, so that products run
 // while sums are taken; warps 1 and 2 issue their MMAs.
 //
-// What bounds it: 8 prompts of 512 to 32768 rows, 64 heads on 8, window 37: 89.0 us where the bytes take 41.5; loads and
+// What bounds it: 8 prompts of 512 to 32768 rows, 64 heads on 8, window 37: 89.1 us where the bytes take 41.5; loads and
 // hand-offs alone 59, with the MMAs 77, and exponentials fill in only as far as two groups overlap (three groups 148 us, four
-// with one buffer each 122: less room for keys and queries).  One prompt of 16384 rows, 32 heads on 8, window 64: 13.2 us, of
-// which a launch, a start and seven tiles one behind the other.
+// with one buffer each 122: less room for keys and queries).  One prompt of 16384 rows, window 64: 13.2 us with 32 heads on 8
+// (of which a launch, a start and seven tiles one behind the other), 20.6 with 40 on 8, where no chunk is a whole one; 9.3 with
+// 32 on 8 and window 16.
 
 #include "pdl.cuh"
 #include "prompt.cuh"
@@ -87,7 +88,7 @@ __device__ __forceinline__ Chunks chunks_of(const KeyWeightsParams& p, const Wor
 }
 // The chunk that comes as the u-th for tile `i`.  Every other tile of a request takes them backwards, and so one of the two
 // groups does: a short last chunk of one beside a whole one of the other, as two groups in step would want the exponentials'
-// unit at the same time (8 prompts 91.2 us in step, 89.0 so).  By the request's own tiles, not by the group, which depends
+// unit at the same time (8 prompts 90.9 us in step, 89.1 so).  By the request's own tiles, not by the group, which depends
 // on the batch: a key's terms are added in one order whatever comes with it.
 __device__ __forceinline__ int turned(const Work& w, const Chunks& c, int u, int i) {
   return (w.key / kKeys + i) & 1 ? c.first + c.end - 1 - u : u;
@@ -152,7 +153,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (p.per_head) {  // neighbouring CTAs take the same keys of neighbouring heads, which lie together in memory
     const int head = blockIdx.x % p.Hkv;
     const long long i = blockIdx.x / p.Hkv;
-    // (the last tile, at the window's edge, counts twice: one prompt of 16K 14.8 us without, 13.4 so)
+    // (one tile more than there are: the batch's last one, at its window's edge, counts twice.  One prompt of 16K 14.6 us
+    // without, 13.2 so)
     begin = (int)((plan.count + 1) * i / p.per_head);
     end = (int)((plan.count + 1) * (i + 1) / p.per_head);
     begin = head * plan.count + (begin < plan.count ? begin : plan.count);
@@ -340,8 +342,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
             const uint32_t tS = tmem + buf * kCols + lane_off;
             if (cols == kCols && !edge) {
-              // a whole chunk: its 128 columns in one go, their lse eight reads ahead (left to the compiler, all reads
-              // come first and registers run out: 166 us where this takes 113; in blocks of 64 columns 123)
+              // a whole chunk: its 128 columns in one go, their lse eight reads ahead (in blocks of 64 columns, as below,
+              // 8 prompts take 108 us instead of 89; reads that the compiler may move came first, all of them, and
+              // registers ran out, in an earlier form of this loop)
               uint32_t s[4][32];
 #pragma unroll
               for (int b = 0; b < 4; ++b) tmem_ld_x32(tS + b * 32, s[b]);

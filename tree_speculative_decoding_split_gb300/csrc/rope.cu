@@ -15,7 +15,8 @@
 // many pairs (four in bf16 took 9.8 us at the trees below, as more blocks no longer fit an SM; loads ahead of the
 // angles took 80.4 us at the prompts).
 //
-// Measured: 4 fp32 prompts of 4096 to 16384 rows, 24 heads of 64, 76.9 us (0.96 of a plain copy's rate); 32 trees of 63
+// Measured: 4 fp32 prompts of 4096 to 16384 rows, 24 heads of 64, 76.7 us (0.97 of a plain copy's rate), as bf16 with 40
+// heads of 128 132 us (0.93); 32 trees of 63
 // bf16 nodes, 8.8 us of which 6.1 are the bytes'; one token 2.3 us, a launch.  Positions take a launch: 1.9 us for 32
 // trees, and 4.7 us for 512 prompts, where every block looks row_start over and searches it.
 
