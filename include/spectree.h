@@ -702,8 +702,8 @@ spec_status spec_rope(const spec_rope_args* args, void* stream);
  *   lse[i][h] = ln sum_{j <= i} exp(scale * q[i][h] . k[j][g])        (j over the same request's rows)
  * Products of bf16 numbers, sums in float32; the softmax weights enter the second product as bf16 (off
  * by 2^-8 of themselves at most, as the output's own rounding), their sum as float32.  Weights are relative to
- * one of the row's scores, the largest of its first 128 keys to begin with, and 2^8 at most, as is the sum
- * of those of 128 keys side by side: scores, and a row's sums of such weights times V, have to lie within
+ * 2^12 times that of the largest of the row's first 128 keys, or of later ones that pass it, and 2^8 at most, as is the
+ * sum of those of 128 keys side by side: scores, and a row's sums of such weights times V, have to lie within
  * float32.  out and lse must not overlap the inputs.  Keys that a row does not see have no influence on it, NaN
  * and infinities included.
  * Host errors: SPEC_ERR_INVALID_ARGUMENT, SPEC_ERR_UNSUPPORTED (dtype other than bf16, head_dim other

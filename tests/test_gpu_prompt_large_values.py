@@ -1,4 +1,4 @@
-"""Prompt attention with V near the ends of float32."""
+"""Prompt attention with V near the ends of float32, and scores that grow."""
 
 import math
 
@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import tree_speculative_decoding_split_gb300 as st
-from prompt_helpers import check_attention, starts
+from prompt_helpers import EPS, attention, check_attention, fused, score_error, starts
 
 pytestmark = pytest.mark.gpu
 
@@ -31,3 +31,29 @@ def test_large_values_behind_grown_scores(d, octaves):
     got = st.prompt_attention(q, k, v, start, scale=1.0)
     assert torch.isfinite(got[0]).all()
     check_attention(got, q, k, v, start, 1.0)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("power", [-100, -118, -126, -130])
+def test_small_values(d, power):
+    """V down to bf16's smallest numbers.  Beside the bound of ordinary ones: half a step of bf16's smallest numbers (2^-134),
+    and a step of float32's (2^-149) for each of n sums, of weights 2^-12 times their own."""
+    n, start = 300, starts([300])
+    q, k, v = fused(_gen(-power), n, 4, 2, d)
+    v = (v.float() * 2.0 ** power).bfloat16()
+    out, _ = st.prompt_attention(q, k, v, start)
+    want, _, mag, size = attention(q, k, v, start)
+    err = score_error(size, 1 / math.sqrt(d), d)[..., None]
+    bound = (1 + EPS) * mag * (EPS + 2 * err + (n + 8) * 2.0 ** -23) + EPS * want.abs() + 2.0 ** -134 + n * 2.0 ** -137
+    assert ((out.double() - want).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(8, 2, 128), (2, 2, 64)])
+@pytest.mark.parametrize("rise", [5.0, 10.0, 40.0, 200.0])
+def test_scores_that_rise_along_the_prompt(hq, hkv, d, rise):
+    """Rows whose reference moves now and then, each at its own tile."""
+    n, start = 1500, starts([1500])
+    q, k, v = (x.clone() for x in fused(_gen(int(rise)), n, hq, hkv, d))
+    q[..., 0] = 8.0
+    k[..., 0] = (torch.arange(n, device="cuda") / n * rise * math.sqrt(d) / 8.0)[:, None].bfloat16()
+    check_attention(st.prompt_attention(q, k, v, start), q, k, v, start)

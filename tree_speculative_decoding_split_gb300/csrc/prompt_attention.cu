@@ -103,14 +103,14 @@ __device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&a)[4][32]) {
 
 // A tile's weights in two passes over its scores, of which a row sees those up to key `lim`: the maximum, with what is
 // there brought to it where it has grown (with_o: O holds something; the commit behind the scores says
-// that it is complete), then P over the scores that have been read.  Where the maximum is so large that its product
+// that it is complete), then P over the scores that have been read.  Where the reference is so large that its product
 // with the scale would be rounded by whole units, differences are taken ahead of the scale.  The whole warp comes here
 // where one of its rows has to (`mine`); the others take the steps, and the order of additions, of the ordinary way, so that
-// a row's bits do not tell what lies beside it.  Returns the row's maximum (in the scores' units) and sum.  Out of line
+// a row's bits do not tell what lies beside it.  Returns the row's reference (in the scores' units) and sum.  Out of line
 // and in loops: it runs once or twice an item, and cold code costs more than its instructions.
 template <int D>
 __device__ __noinline__ float2 tile_again(uint32_t tS, uint32_t tP, uint32_t tO, int lim, bool mine, bool with_o, float2 ml,
-                                          float scale_log2) {
+                                          float head, float scale_log2) {
   float top = -INFINITY;
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
@@ -121,6 +121,7 @@ __device__ __noinline__ float2 tile_again(uint32_t tS, uint32_t tP, uint32_t tO,
     for (int j = 0; j < 32; ++j)
       if (c * 32 + j <= lim) top = fmaxf(top, __uint_as_float(s[j]));
   }
+  top += head;
   const bool need = mine && top > ml.x;  // (the first finite maximum among them)
   if (__any_sync(0xffffffffu, need)) {
     const float f = need ? exp2f((ml.x - top) * scale_log2) : 1.f;
@@ -517,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int first = w.tok + a * p.tg;   // the group's first row
       const int row = first + my_tok;
       const bool valid = rl < p.tg * p.G && row < w.n;  // (rows behind the last head, or of the next request, count for nothing)
-      float m_run = -INFINITY, l_run = 0.f;  // the maximum in the scores' own units
+      float m_run = -INFINITY, l_run = 0.f;  // the reference, in the scores' own units, and the weights' sum
       for (int t = 0; t < w.tiles[a]; ++t) {
         // (a warp whose wait gave up goes on to its last tile: the issuer waits for it without a limit)
         ok = __all_sync(0xffffffffu, ok && mbar_wait_bounded(&sfull[a], s_n++ & 1, &s_abort));
@@ -528,9 +529,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool edge = t * kKeys + kKeys - 1 > first;  // some row does not see all of the tile's keys
         // Weights are taken by the reference there is, the first tile's maximum at first.  Their sum tells where scores have
         // outgrown it (no weight is larger than the sum, so V of up to 2^-8 of float32's range stays within it; what overflows
-        // shows as well): tile_again then does the tile once more, by its maximum, after which 128 weights sum up to 2^7.  (So
-        // does a row that has seen nothing but -inf, whose reference is none yet.)  No other tile needs one, which is a pass
-        // less on the way from S to P.
+        // shows as well): tile_again then does the tile once more, by its maximum.  (So does a row that has seen nothing but
+        // -inf, whose reference is none yet.)  No other tile needs one, which is a pass less on the way from S to P.  The
+        // reference lies kPromptHead above that maximum, so that a tile's scores have to grow by e^9 before it moves (on the
+        // maximum itself by 2, and then some row of a warp goes through its tile again nearly every time: prompts whose scores
+        // rise by e^10 from their first row to their last take 58 us so, 33 as it is; 2048 rows, 32 heads on 8).
         bool mine = false, again = false;
         if (ok) {
           uint32_t s[4][32];
@@ -557,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 first_mx[c] = max3(first_mx[c], __uint_as_float(s[c][j]), __uint_as_float(s[c][j + 1]));
             }
             // (128 is no multiple of every G: rows behind the last head have a reference all the same)
-            m_run = rl < p.tg * p.G ? max3(fmaxf(first_mx[0], first_mx[1]), first_mx[2], first_mx[3]) : 0.f;
+            m_run = rl < p.tg * p.G ? max3(fmaxf(first_mx[0], first_mx[1]), first_mx[2], first_mx[3]) + p.head : 0.f;
           }
           // (without a reference: weights that do not count, and tile_again)
           const float shift = (m_run == -INFINITY ? INFINITY : m_run) * p.scale_log2;
@@ -584,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (ok && again) {
           const float2 ml = tile_again<D>(tS, tP, tO, edge ? row - t * kKeys : kKeys, mine, t > 0, make_float2(m_run, l_run),
-                                          p.scale_log2);
+                                          p.head, p.scale_log2);
           m_run = ml.x;
           l_run = ml.y;
         }
