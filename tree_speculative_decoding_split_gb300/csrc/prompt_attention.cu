@@ -33,10 +33,10 @@
 //
 // What bounds it: a tile of both groups is 2048 cycles of MMA at d 128 and takes 2920; the rest is the way from S to P and
 // back (1000 cycles of softmax, 600 of hand-offs, 150 of the wait for P V), which two groups do not hide in full and for more
-// tensor memory is too small.  16384 rows of 64 heads on 8: 2850 us, 1545 TFLOP/s, at the power limit.  At d 64 the MMAs of S
+// tensor memory is too small.  16384 rows of 64 heads on 8: 2825 us, 1557 TFLOP/s, at the power limit.  At d 64 the MMAs of S
 // halve in number, those of P V (64 columns of output) take as long as with 128, and that way does not change: 2650 cycles a
 // tile, and 3600 to go from one item to the next, which weighs where prompts are short.  48 prompts of up to 1800 rows, 16
-// heads on 8: 186 us.  (Graph replays; a Python call takes 2890 and 187.)
+// heads on 8: 185 us.  (Graph replays; a Python call takes 2880 and 186.)
 // Weights go into P as bf16, off by 2^-8 of each at most, so that out is 0.0020 to 0.0022 from 64 bits where its own rounding
 // alone leaves 0.0016.  As a pair of bf16 numbers they leave no more than that, at half as many MMAs again and more to store:
 // 4450 us at the rows above (2770 then), 307 for the 48 prompts (184), 18.3 for one of 500 rows (12.4).  The sum, the maximum
