@@ -135,7 +135,7 @@ struct PlanReader {
 constexpr float kPromptHead = 12.f;
 struct PromptAttnParams {
   int Hq, Hkv, G, tg;       // tg: rows of a request per 128-row group (128 / G)
-  float scale, scale_log2;
+  float scale_log2;
   float head;               // how far a row's reference lies above its maximum, in the scores' units (kPromptHead)
   PlanView plan;
   const uint16_t* v;        // for keys with infinities

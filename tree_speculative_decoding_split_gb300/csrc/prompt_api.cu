@@ -255,8 +255,7 @@ spec_status spec_prompt_attention(const spec_prompt_attn_args* a, void* workspac
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
   PromptAttnParams p;
   p.Hq = a->num_q_heads; p.Hkv = a->num_kv_heads; p.G = p.Hq / p.Hkv; p.tg = step / 2;
-  p.scale = scale_of(a->scale, a->head_dim);
-  p.scale_log2 = p.scale * 1.4426950408889634f;
+  p.scale_log2 = scale_of(a->scale, a->head_dim) * 1.4426950408889634f;
   p.head = p.scale_log2 > 1e-30f ? kPromptHead / p.scale_log2 : 0.f;  // (none where it might leave float32)
   p.v = static_cast<const uint16_t*>(a->v); p.v_stride = a->v_stride;
   p.out = static_cast<uint16_t*>(a->out); p.out32 = (reinterpret_cast<uintptr_t>(a->out) & 31u) == 0;

@@ -637,7 +637,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           store_64(p.out + orow * D + c * 32, y, p.out32);
         }
       }
-      if (valid && p.lse) p.lse[orow] = m_run * p.scale + logf(l_run);
+      // (from the rounded product that the weights were taken by, and near the maximum, so that what the head adds is not rounded)
+      if (valid && p.lse)
+        p.lse[orow] = fmaf(m_run * p.scale_log2 - kPromptHead, 0.69314718f, logf(l_run * (float)(1 << (int)kPromptHead)));
     }
     if (!ok && lane == 0) {
       s_abort = 1;
