@@ -15,8 +15,8 @@
 //
 // One CTA owns (request, KV head, key split, NG x 128 rows).  Bound: per 128-key tile and 128 rows the
 // tensor pipe takes 512 (S) + 512 (P V) cycles; the two groups fill each other's softmax.  TMEM: O 128
-// columns and S 128 per group, 512 in all with two; P lies over the S it came from, so the issue order per
-// group is  P V(t), S(t + 1)  back to back.  (With one group S has two buffers.)
+// columns and S 128 per group, 512 in all with two; P lies over the S it came from, so a group's S(t + 1) is
+// issued when its P V(t) is done.  (With one group S has two buffers.)
 //   warp 0     TMA producer: K and V rings of 128-key tiles (one box per block and tensor, issued by as many
 //              lanes), the tile's scales; first of all it works out the CTA's share of the batch;
 //   warp 1     MMA issuer;
@@ -25,10 +25,10 @@
 //              Both use the row's reference; whether one has to move is one barrier's OR per tile.  Moving it
 //              and masking the tile that ends the prefix have loops of their own, which leaves the tiles' own short
 //              (4 trees of 255 nodes 1880 -> 1861 us).
-// Measured (graph replay): 4 trees of 255 nodes, 64 query heads on 8, lengths up to 128K, 1861 us = 1471 TFLOP/s,
-// 0.77 of a large bf16 product's rate; a tile of both groups takes 3.2 K cycles for 2 K of tensor work.  32 trees of
-// 63 nodes at 4K 142 us = 954 TFLOP/s: 256 CTAs on 152 SMs are 1.7 rounds, and about 30 K of a CTA's 140 K cycles go
-// to its first two tiles and its last rows, which nothing overlaps.  8 trees of 127 nodes, d 64, 62 us.
+// Measured (graph replay): 4 trees of 255 nodes, 64 query heads on 8, lengths up to 128K, 1906 us = 1437 TFLOP/s,
+// 0.74 of a large bf16 product's rate; a tile of both groups takes 3.3 K cycles for 2 K of tensor work.  32 trees of
+// 63 nodes at 4K 140 us = 966 TFLOP/s: 256 CTAs on 152 SMs are 1.7 rounds, and about 30 K of a CTA's 140 K cycles go
+// to its first two tiles and its last rows, which nothing overlaps.  8 trees of 127 nodes, d 64, 58 us.
 // Tried and slower (63-node trees, batch 32 at 4K, when this stood at 160 us): P as e4m3 pairs with 128 keys a
 // thread, four warps per group and a row maximum ahead of the weights, 238 us; with one S buffer shared by both groups
 // and all descriptors in uniform registers, 203 us; with two threads per row, 211 us.  Four trees of 255 nodes, at
@@ -182,6 +182,7 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
   __shared__ float s_x[NG][2][kGR8];  // a row's threads tell each other their largest score; at the end, their sums
   __shared__ uint32_t s_w[NG][2][4];  // ... and which of the warp's rows move
   __shared__ uint64_t s_drained;
+  __shared__ uint64_t s_pread[NG];  // P read by its product
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort, s_bad, s_kissued, s_vissued;
   __shared__ int s_par[kMaxNodes];
@@ -206,6 +207,7 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
         // a tile's weights are there; for group 0 also its V, and the keys of the scores that follow
         for (int i = 0; i < 2; ++i) mbar_init(&pfull[g][i], g == 0 ? 10 : 8);
         mbar_init(&ofull[g], 1);
+        mbar_init(&s_pread[g], 1);
       }
       mbar_init(&s_drained, 1);
       s_abort = 0;
@@ -529,14 +531,20 @@ __global__ void __launch_bounds__(TcCfg<D, NG>::kThreads, 1)
         }
       }
     };
-    // P V(t), then the buffer's next scores: MMAs of one thread run in their order
+    // P V(t), and when that is done the buffer's next scores, which overwrite P: tensor instructions keep their order for
+    // sure only where they have one accumulator and one shape (4 trees of 255 nodes 1862 us without the wait, 1906 with it; 32
+    // of 63 nodes 136 and 140, 8 of 127 nodes with d 64 60.5 and 58.5)
     auto step = [&](auto pv_tree, auto s_tree, int t) -> bool {
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         if (!wait(&pfull[g][t & 1], (t >> 1) & 1)) return false;
         tc_fence_after();
         issue_pv(pv_tree, t, g);
-        if (t + C::kNB < T) issue_s(s_tree, t + C::kNB, g);
+        if (t + C::kNB < T) {
+          if (leader) umma_commit(&s_pread[g]);
+          if (!wait(&s_pread[g], t & 1)) return false;
+          issue_s(s_tree, t + C::kNB, g);
+        }
       }
       return true;
     };
