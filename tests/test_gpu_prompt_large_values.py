@@ -57,3 +57,13 @@ def test_scores_that_rise_along_the_prompt(hq, hkv, d, rise):
     q[..., 0] = 8.0
     k[..., 0] = (torch.arange(n, device="cuda") / n * rise * math.sqrt(d) / 8.0)[:, None].bfloat16()
     check_attention(st.prompt_attention(q, k, v, start), q, k, v, start)
+
+
+@pytest.mark.parametrize("scale", [1e-38, 1e-31, 1e-29, 1e-10])
+def test_small_scales(scale):
+    """A reference above the maximum in the scores' units, which are large where the scale is small."""
+    start = starts([300, 1, 130])
+    q, k, v = fused(_gen(3), 431, 4, 2, 64)
+    check_attention(st.prompt_attention(q, k, v, start, scale=scale), q, k, v, start, scale)
+    big = (q.float() * 2.0 ** 60).bfloat16()  # scores of up to 1e20
+    check_attention(st.prompt_attention(big, k, v, start, scale=scale), big, k, v, start, scale)

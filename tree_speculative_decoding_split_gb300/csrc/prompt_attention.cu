@@ -33,7 +33,7 @@
 //
 // What bounds it: a tile of both groups is 2048 cycles of MMA at d 128 and takes 2920; the rest is the way from S to P and
 // back (1000 cycles of softmax, 600 of hand-offs, 150 of the wait for P V), which two groups do not hide in full and for more
-// tensor memory is too small.  16384 rows of 64 heads on 8: 2825 us, 1557 TFLOP/s, at the power limit.  At d 64 the MMAs of S
+// tensor memory is too small.  16384 rows of 64 heads on 8: 2840 us, 1549 TFLOP/s, at the power limit.  At d 64 the MMAs of S
 // halve in number, those of P V (64 columns of output) take as long as with 128, and that way does not change: 2650 cycles a
 // tile, and 3600 to go from one item to the next, which weighs where prompts are short.  48 prompts of up to 1800 rows, 16
 // heads on 8: 185 us.  (Graph replays; a Python call takes 2880 and 186.)
@@ -605,6 +605,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) continue;
       tc_fence_after();
       const size_t orow = valid ? (size_t)(w.r0 + row) * p.Hq + w.g * p.G + my_head : 0;
+      // (from the rounded product that the weights were taken by, and near the maximum, so that what the head adds is not rounded)
+      const float lse =
+          fmaf(__fmul_rn(m_run, p.scale_log2) - kPromptHead, 0.69314718f, logf(l_run * (float)(1 << (int)kPromptHead)));
       const float inv = l_run > 0.f ? 1.f / l_run : (l_run == 0.f ? 0.f : l_run);  // (a NaN sum stays NaN)
       const bool special = *static_cast<volatile int*>(&s_special) != 0;
 #pragma unroll 1
@@ -637,9 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           store_64(p.out + orow * D + c * 32, y, p.out32);
         }
       }
-      // (from the rounded product that the weights were taken by, and near the maximum, so that what the head adds is not rounded)
-      if (valid && p.lse)
-        p.lse[orow] = fmaf(m_run * p.scale_log2 - kPromptHead, 0.69314718f, logf(l_run * (float)(1 << (int)kPromptHead)));
+      if (valid && p.lse) p.lse[orow] = lse;
     }
     if (!ok && lane == 0) {
       s_abort = 1;
